@@ -11,6 +11,7 @@ Entry points (same names as the C ABI):
     rlk_attn_prefill_states, rlk_attn_merge_states, rlk_attn_merge_states_noalloc,
     rlk_attn_prefill, rlk_attn_prefill_rope,
     rlk_attn_decode_paged, rlk_attn_backward, rlk_attn_workspace_size,
+    rlk_attn_qcache_write, rlk_attn_qcache_read, rlk_attn_decode_qcache,
     rlk_attn_check_device_error, rlk_attn_last_error, rlk_attn_core_id
 """
 from __future__ import annotations
@@ -97,6 +98,9 @@ def load():
             "rlk_attn_rope_qk": [PP, P, P, P, P, P, P, P, i32, P],
             "rlk_attn_decode_paged_rope": [PP, P, P, P, i32, i32, P, i32, P, P, i32, P, P, P, P],
             "rlk_attn_decode_paged_splitk_rope": [PP, P, P, P, i32, i32, P, i32, P, i32, P, i32, P, P, P, P, sz, P],
+            "rlk_attn_qcache_write": [PP, P, P, P, P, P, i32, P, P, P, P, i32, i32, P, i32, P],
+            "rlk_attn_qcache_read": [PP, P, P, P, P, i32, i32, P, i32, P, P, P, P, P],
+            "rlk_attn_decode_qcache": [PP, P, P, P, P, P, i32, i32, P, i32, P, i32, P, i32, P, P, P, P, sz, P],
             "rlk_attn_backward": [PP, P, P, P, P, P, P, P, i32, P, P, P, P, sz, P],
             "rlk_attn_workspace_size": [PP, i32, P, P],
             "rlk_attn_check_device_error": [P],
@@ -321,6 +325,67 @@ def rlk_attn_decode_paged_splitk_rope(params, q, k_pool, v_pool, n_pages, page_s
                                                     _ptr(out_f32), _ptr(out_bf16), _ptr(lse), _ptr(workspace),
                                                     int(workspace_bytes), _stream(stream)),
            "rlk_attn_decode_paged_splitk_rope")
+
+
+def _dev(x, *dtypes):
+    """_ptr of a device tensor the 8-bit cache's kernels read or write: refuses
+    one that is not contiguous, not on the current CUDA device or of another
+    type (a pointer value passes as it is)."""
+    if x is None or isinstance(x, int):
+        return _ptr(x)
+    import torch
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError("expected a tensor on the current CUDA device")
+    if not x.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    if str(x.dtype)[6:] not in dtypes:
+        raise ValueError(f"expected {' or '.join(dtypes)}, got {x.dtype}")
+    return _ptr(x)
+
+
+_E4M3 = ("float8_e4m3fn", "uint8")
+
+
+def _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages):
+    return (_dev(k_pool, *_E4M3), _dev(v_pool, *_E4M3), _dev(k_scale, "float32"), _dev(v_scale, "float32"),
+            int(n_pages), int(page_size), _dev(page_table, "int32"), int(max_pages))
+
+
+def rlk_attn_qcache_write(params, k, v, cu_seqlens, pos_offset, rope_table, rope_max_pos, k_pool, v_pool, k_scale,
+                          v_scale, n_pages, page_size, page_table, max_pages, stream=None):
+    """Quantise new BF16 K/V rows into the 8-bit pages (rope_table: rotate K
+    at its positions first, or None)."""
+    cu = _i32_host(cu_seqlens)
+    po = None if pos_offset is None else _i32_host(pos_offset)
+    pool = _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages)
+    _check(load().rlk_attn_qcache_write(ctypes.byref(params), _dev(k, "bfloat16"), _dev(v, "bfloat16"), _ptr(cu),
+                                        _ptr(po), _dev(rope_table, "float32"), int(rope_max_pos), *pool,
+                                        _stream(stream)), "rlk_attn_qcache_write")
+
+
+def rlk_attn_qcache_read(params, k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages,
+                         cu_seqlens, pos_offset, k, v, stream=None):
+    """Read token ranges of the 8-bit pages back as packed BF16 K/V rows."""
+    cu = _i32_host(cu_seqlens)
+    po = None if pos_offset is None else _i32_host(pos_offset)
+    pool = _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages)
+    _check(load().rlk_attn_qcache_read(ctypes.byref(params), *pool, _ptr(cu), _ptr(po), _dev(k, "bfloat16"),
+                                       _dev(v, "bfloat16"), _stream(stream)), "rlk_attn_qcache_read")
+
+
+def rlk_attn_decode_qcache(params, q, k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages,
+                           seqlens, split_k, rope_table, rope_max_pos, out_f32, out_bf16, lse, workspace=None,
+                           workspace_bytes=None, stream=None):
+    """Decode over the 8-bit pages (split_k: 1 single pass, 0 the library
+    picks; rope_table: rotate the query rows, or None)."""
+    sl = _i32_host(seqlens)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    pool = _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages)
+    _check(load().rlk_attn_decode_qcache(ctypes.byref(params), _dev(q, "bfloat16"), *pool, _ptr(sl), int(split_k),
+                                         _dev(rope_table, "float32"), int(rope_max_pos), _dev(out_f32, "float32"),
+                                         _dev(out_bf16, "bfloat16"), _dev(lse, "float32"), _ptr(workspace),
+                                         int(workspace_bytes), _stream(stream)), "rlk_attn_decode_qcache")
 
 
 def rlk_attn_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,

@@ -1,0 +1,47 @@
+// qcache_internal.h -- launch parameter blocks of the 8-bit paged KV cache
+// (write, read, decode).  Not part of the public interface.
+#pragma once
+#include "rlk_internal.h"
+
+namespace rlk {
+
+// The pages: E4M3 codes [n_pages][hkv][page_size][128] and FP32 scales
+// [n_pages][hkv], for K and for V, under one page table.
+struct QCachePools {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;  // device [num_seqs][max_pages]
+  int32_t n_pages, page_size, max_pages, hkv;
+};
+
+// Write and read: tokens pos0[s] .. pos0[s] + n - 1 of sequence s, packed
+// rows cu[s] .. cu[s + 1] - 1 of k / v [T, hkv, 128] BF16.
+struct QCacheParams {
+  ErrWord* err;
+  QCachePools c;
+  const uint16_t* k_in;  // write
+  const uint16_t* v_in;
+  uint16_t* k_out;  // read
+  uint16_t* v_out;
+  const float* rope_table;  // write: rotates K at its positions, or null
+  int32_t num_seqs;
+  int32_t cu[kMaxSeqs + 1];
+  int32_t pos0[kMaxSeqs];
+  int32_t page0[kMaxSeqs + 1];  // prefix sum of the pages the sequences touch
+};
+cudaError_t launch_qcache_write(const QCacheParams& p, cudaStream_t stream);
+cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
+
+// Decode over the 8-bit pages: the BF16 decode's parameters (items, contexts,
+// outputs, state table), the query rows and the pages' scales.
+struct QDecodeParams {
+  FwdParams f;
+  const uint16_t* q;  // [num_seqs, hq, 128] BF16
+  const float* k_scale;
+  const float* v_scale;
+};
+cudaError_t configure_qdecode_kernels();
+
+}  // namespace rlk

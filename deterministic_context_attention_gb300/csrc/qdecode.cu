@@ -1,0 +1,759 @@
+// qdecode.cu -- paged decode over the 8-bit KV cache for sm_103a.
+//
+// The transposed decode of the BF16 pools (keys, then head dimensions, on the
+// MMA's M side; block states of 128 keys folded in ascending order) with the
+// pages' E4M3 codes as they are: TMA brings them to shared memory and
+// tcgen05.mma kind::f8f6f4 reads them there, so no code is ever converted.
+// The other operand is split into E4M3 pieces, each 2^5 below the one before
+// (a rounding to 4 bits of a value in [2^E, 2^(E+1)) leaves at most 2^(E-4),
+// which times 32 fills the same range again), which ride in the N columns the
+// few query heads leave free:
+//   S^T = K_b [q0 | q1 | q2]^T        q 2^x = q0 + q1 / 32 + q2 / 1024
+//   O^T = V_b^T [p0 | p1 | p2 | p3]^T  w 2^7 = p0 + p1 / 32 + p2 / 1024 + p3 / 32768
+// q 2^x has its row maximum in [128, 256): a BF16 query's 8 significant bits
+// are q0 + q1 / 32 exactly, q2 serves elements 2^13 and more below the row's
+// maximum.  w_c = p_c sv_c / A, with sv_c the V scale of key c's page and A
+// the block's largest of them (as a power of two): four pieces leave at most
+// 2^-19 of w_c.  The K scale multiplies the FP32 score of its key,
+//   s_c = (q . code_c) sk_c,
+// and from there every step is the one numerics.cuh defines: the block
+// maximum, p = 2^fma(s, scale_log2, -m scale_log2), the canonical row sum
+// (of the unsplit FP32 p), o_b = PV / l, the fold in ascending block order.
+// A result depends on the cached codes, scales and the query alone, not on
+// the batch, the order of the pages or the split.
+//
+// What bounds it: HBM, 32 KB of codes per (KV head, 128-key block) and 4 heads
+// of 4 x 128 x 128 flops against them.  Per block the tensor core issues 4 + 4
+// MMAs (K = 32 codes each; the BF16 decode needs 8 + 16), and the 8 warps of
+// the softmax run two blocks at a time.
+//
+// Warp roles (544 threads):
+//   warps 0-3   correction / epilogue: thread d owns head dimension d
+//   warps 4-7   softmax of the even blocks, warps 8-11 of the odd ones:
+//               thread t owns key t of the block and fetches its page's scales
+//   warp  12    TMA producer of the K pages, warp 13 of the V pages
+//   warp  14    TMEM allocator and issuer of the S^T products
+//   warp  15    issuer of the O^T products
+//   warp  16    the query rows: loads them (rotating them first where asked),
+//               splits them and keeps one item ahead
+// Split decode writes block states to the state table; with the fold on chip
+// the CTAs past the items fold them as they land (decode_common.cuh).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "decode_common.cuh"
+#include "numerics.cuh"
+#include "ptx.cuh"
+#include "qcache_internal.h"
+
+namespace rlk {
+namespace {
+
+constexpr int kQDThreads = 544;
+constexpr int kQPieces = 3, kPPieces = 4;
+
+// N: MMA columns, the pieces of up to MG query heads, at column piece * MG + head
+template <int MG>
+struct QDecLayout {
+  static constexpr int B = kDecBlock;
+  static constexpr int N = MG <= 4 ? 16 : 32;
+  static_assert(kPPieces * MG <= N && kQPieces * MG <= N, "the pieces fit the MMA's columns");
+  static constexpr int kSK = 6, kSV = 5;  // K and V rings
+  static constexpr int kPS = 2;           // P^T operand slots
+  static constexpr int kQS = 2;           // query slots (the next item's rows are prepared ahead)
+  static constexpr int kSS = 4, kOS = 4;  // TMEM rings of S^T and O^T
+  static constexpr int kSR = 8;           // statistics ring
+  static constexpr int kKVBytes = B * 128;
+  static constexpr int kTBytes = N * 128;  // an N-row operand tile of 128 codes
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kQOff + kQS * kTBytes;
+  static constexpr int kKOff = (kPOff + kPS * kTBytes + 1023) / 1024 * 1024;
+  static constexpr int kVOff = kKOff + kSK * kKVBytes;
+  // per softmax group, double-buffered by block: maxima of 4 warps (MG heads
+  // and the V scale) and the probabilities for the row sums
+  static constexpr int kRedBytes = 2 * 4 * (MG + 1) * 4;
+  static constexpr int kPartBytes = 2 * 4 * MG * 32 * 4;
+  static constexpr int kPartOff = kVOff + kSV * kKVBytes;
+  static constexpr int kRedOff = kPartOff + 2 * kPartBytes;
+  static constexpr int kStatsOff = (kRedOff + 2 * kRedBytes + 7) / 8 * 8;  // float2 [kSR][MG]
+  static constexpr int kQsOff = kStatsOff + kSR * MG * 8;                  // float [kQS][MG]
+  static constexpr int kBarOff = (kQsOff + kQS * MG * 4 + 7) / 8 * 8;
+  static constexpr int kQFull = 0, kQEmpty = kQFull + kQS, kKFull = kQEmpty + kQS, kKEmpty = kKFull + kSK,
+                       kVFull = kKEmpty + kSK, kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV,
+                       kSEmpty = kSFull + kSS, kPFull = kSEmpty + kSS, kPEmpty = kPFull + kPS,
+                       kOFull = kPEmpty + kPS, kOEmpty = kOFull + kOS, kStatsFull = kOEmpty + kOS,
+                       kSyncMax = kStatsFull + kSR, kSyncPart = kSyncMax + 4, kFillDone = kSyncPart + 4,
+                       kNumBars = kFillDone + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort (i32)
+  static constexpr int kPageWin = 512;                     // page ids cached per window (one per producer)
+  static constexpr int kPageOff = (kMiscOff + 16 + 15) / 16 * 16;
+  static constexpr int kTotal = kPageOff + 2 * kPageWin * 4;
+  static constexpr int kAlloc = kTotal + 1024;
+  static constexpr int kTmemCols = N * (kSS + kOS);
+  static_assert(kAlloc <= 232448, "decode shared memory");
+  static_assert(kTmemCols == 128 || kTmemCols == 256, "TMEM columns are allocated in powers of two");
+};
+
+// Byte offset of (row, code column) of a K-major operand tile of 128-byte rows
+// in the 128-byte swizzle (what a TMA load with that swizzle produces).
+__device__ __forceinline__ uint32_t tile8_off(int row, int col) {
+  return static_cast<uint32_t>(row * 128) + ((static_cast<uint32_t>(col >> 4) ^ static_cast<uint32_t>(row & 7)) << 4) +
+         static_cast<uint32_t>(col & 15);
+}
+
+// Instruction descriptor, kind::f8f6f4 with E4M3 A and B and FP32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// One K = 32 step of D[tmem] (+)= A B^T, both from shared memory.
+template <int ACC>
+__device__ __forceinline__ void mma8_ss(uint32_t d_tmem, Desc a, uint32_t a_off, Desc b, uint32_t b_off,
+                                        uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t.reg .b32 la, lb;\n\t"
+      "add.u32 la, %1, %3;\n\tadd.u32 lb, %4, %6;\n\t"
+      "mov.b64 da, {la, %2};\n\tmov.b64 db, {lb, %5};\n\t"
+      "setp.ne.b32 p, %8, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %7, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo), "r"(a.hi), "r"(a_off), "r"(b.lo), "r"(b.hi), "r"(b_off), "r"(idesc), "n"(ACC)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {  // a in the low byte
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3_pair_value(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+  float2 f;
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+// The next piece of a and b (packed, a low), which keep what it leaves times
+// 32 (both steps exact: the residual of a rounding to 4 bits is a multiple of
+// the value's last place).
+__device__ __forceinline__ uint32_t next_piece(float& a, float& b) {
+  const uint32_t c = e4m3_pair(a, b);
+  const float2 f = e4m3_pair_value(c);
+  a = __fmul_rn(__fsub_rn(a, f.x), 32.0f);
+  b = __fmul_rn(__fsub_rn(b, f.y), 32.0f);
+  return c;
+}
+
+__device__ __forceinline__ float pow2_bits(int biased) { return __uint_as_float(static_cast<uint32_t>(biased) << 23); }
+
+template <int N>
+struct TmemRow;
+template <>
+struct TmemRow<16> {
+  static __device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[16]) { tmem_ld16(a, r); }
+};
+template <>
+struct TmemRow<32> {
+  static __device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[32]) { tmem_ld32(a, r); }
+};
+
+// One arrival for the whole warp, after every lane's earlier writes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+template <int MG, bool FOLD>
+__global__ void __launch_bounds__(kQDThreads, 1)
+    rlk_qdecode_kernel(const __grid_constant__ QDecodeParams qp, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v) {
+  using L = QDecLayout<MG>;
+  constexpr int B = L::B, N = L::N, SK = L::kSK, SV = L::kSV, PS = L::kPS, QS = L::kQS, SS = L::kSS, OS = L::kOS,
+                SR = L::kSR;
+  static_assert(MG <= kDecodeMaxGroup && PS == 2 && QS == 2, "decode layout");
+  const FwdParams& p = qp.f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  float2* stats = reinterpret_cast<float2*>(smem + L::kStatsOff);
+  float* qscale = reinterpret_cast<float*>(smem + L::kQsOff);
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int G = p.group;
+
+  // operand rows of no head's piece are never written: they must read as zero
+  for (int i = tid; i < (QS + PS) * L::kTBytes / 16; i += kQDThreads)
+    reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (tid == 0) {
+    for (int s = 0; s < QS; ++s) {
+      mbar_init(&bars[L::kQFull + s], 1);
+      mbar_init(&bars[L::kQEmpty + s], 1 + 8);  // the S products' commit and the softmax warps
+    }
+    for (int s = 0; s < SK; ++s) {
+      mbar_init(&bars[L::kKFull + s], 1);
+      mbar_init(&bars[L::kKEmpty + s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(&bars[L::kVFull + s], 1);
+      mbar_init(&bars[L::kVEmpty + s], 1);
+    }
+    for (int s = 0; s < SS; ++s) {
+      mbar_init(&bars[L::kSFull + s], 1);
+      mbar_init(&bars[L::kSEmpty + s], 4);
+    }
+    for (int s = 0; s < PS; ++s) {
+      mbar_init(&bars[L::kPFull + s], 4);
+      mbar_init(&bars[L::kPEmpty + s], 1);
+    }
+    for (int s = 0; s < OS; ++s) {
+      mbar_init(&bars[L::kOFull + s], 1);
+      mbar_init(&bars[L::kOEmpty + s], 4);
+    }
+    for (int s = 0; s < SR; ++s) mbar_init(&bars[L::kStatsFull + s], 4);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars[L::kSyncMax + s], 4);
+      mbar_init(&bars[L::kSyncPart + s], 4);
+    }
+    mbar_init(&bars[L::kFillDone], kFillThreads);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 14) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm_s = *tmem_slot;       // S^T slots: + N * slot
+  const uint32_t tm_o = tm_s + N * SS;    // O^T slots: + N * slot
+  uint8_t* q_base = smem + L::kQOff;
+  uint8_t* p_base = smem + L::kPOff;
+  uint8_t* k_base = smem + L::kKOff;
+  uint8_t* v_base = smem + L::kVOff;
+
+  if (FOLD && static_cast<int>(blockIdx.x) >= p.num_items) {
+    // ------------------------------------------------------------ fold CTA
+    const int chain = (static_cast<int>(blockIdx.x) - p.num_items) * 16 + warp;
+    const int per_seq = p.hkv * G;
+    if (warp < 16 && p.split_stride > 0 && chain < p.fold_seqs * per_seq) {
+      const int seq = chain / per_seq, g = (chain % per_seq) / G, q = chain % G;
+      fold_chain_on_chip(p, seq, g, q, lane, abort);
+    }
+  } else if (warp == 12 || warp == 13) {
+    // ------------------------------------------------------------ producers
+    const bool is_v = warp == 13;
+    const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+    if (lane == 0) tma_prefetch_desc(map);
+    const int S = is_v ? SV : SK;
+    uint64_t* full_b = &bars[is_v ? L::kVFull : L::kKFull];
+    uint64_t* empty_b = &bars[is_v ? L::kVEmpty : L::kKEmpty];
+    uint8_t* ring = is_v ? v_base : k_base;
+    int32_t* wc = reinterpret_cast<int32_t*>(smem + L::kPageOff) + (is_v ? L::kPageWin : 0);
+    const int ps = p.page_size;
+    const int lg = 31 - __clz(B / ps);  // log2 of the pages per block
+    uint32_t stage = 0, par = 1;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = dec_snake_item(round);
+      if (item >= p.num_items) continue;
+      const DecItem di = dec_item(p, item);
+      const int seq = di.seq, g = di.g, kv_len = di.kv_len, nb = di.nb;
+      const int seq_pages = (kv_len + ps - 1) / ps;
+      const int32_t* prow = p.page_table + static_cast<int64_t>(seq) * p.max_pages;
+      int cached = -1;  // a new sequence's page ids
+      bool fail = false;
+      for (int j = 0; j < nb; ++j) {
+        const int b = di.b0 + j * di.stride;  // global block
+        bool ok = mbar_wait(empty_b + stage, par, abort, p.err, is_v ? 0xb03 : 0xb02);
+        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        uint8_t* dst = ring + stage * L::kKVBytes;
+        const int n_tok = min(B, kv_len - b * B);
+        const int n_pg = (n_tok + ps - 1) / ps;
+        // the window holds the pages of 2^(9 - lg) consecutive blocks of the
+        // item, all 16 loads of a lane in flight before the first store
+        const int win = j >> (9 - lg);
+        if (cached != win) {
+          int32_t pg[L::kPageWin / 32];
+#pragma unroll
+          for (int t = 0; t < L::kPageWin / 32; ++t) {
+            const int i = lane + 32 * t;
+            const int jj = (win << (9 - lg)) + (i >> lg);  // block of the item
+            const int gp = ((di.b0 + jj * di.stride) << lg) + (i & ((1 << lg) - 1));
+            pg[t] = (jj < nb && gp < seq_pages) ? __ldg(prow + gp) : -1;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int t = 0; t < L::kPageWin / 32; ++t) wc[lane + 32 * t] = pg[t];
+          __syncwarp();
+          cached = win;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full_b + stage, n_pg * ps * 128);
+        __syncwarp();
+        if (lane < n_pg) {
+          int32_t pe = wc[((j & ((1 << (9 - lg)) - 1)) << lg) + lane];
+          if (pe < 0 || pe >= p.n_pages) {
+            report_error(p.err, kErrBadPage, 0xb04);
+            pe = p.n_pages;  // out of range: the copy reads the zero fill
+          }
+          tma_load_3d(dst + lane * ps * 128, map, full_b + stage, 0, 0, pe * p.hkv + g);
+        }
+        if (++stage == static_cast<uint32_t>(S)) {
+          stage = 0;
+          par ^= 1;
+        }
+      }
+      if (fail || *abort) break;
+    }
+  } else if (warp == 14) {
+    // ------------------------------------------------------------ S issuer
+    constexpr uint32_t kIdS = idesc_e4m3(128, N, false);  // A = K (K-major), B = Q pieces (K-major)
+    const uint32_t leader = elect_one_sync();
+    uint32_t stage = 0, kpar = 0, s_it = 0, q_it = 0;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = dec_snake_item(round);
+      if (item >= p.num_items) continue;
+      const DecItem di = dec_item(p, item);
+      const uint32_t qslot = q_it & 1;
+      bool ok = mbar_wait(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb11);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++q_it;
+      const Desc qd = make_desc(smem_u32(q_base + qslot * L::kTBytes), 16, 1024);
+      bool fail = false;
+      for (int j = 0; j < di.nb; ++j, ++s_it) {
+        const uint32_t slot = s_it % SS;
+        bool w = mbar_wait(&bars[L::kKFull + stage], kpar, abort, p.err, 0xb12);
+        w = w && mbar_wait(&bars[L::kSEmpty + slot], ((s_it / SS) & 1) ^ 1, abort, p.err, 0xb13);
+        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        tc_fence_after();
+        const Desc kd = make_desc(smem_u32(k_base + stage * L::kKVBytes), 16, 1024);
+        const uint32_t d = tm_s + slot * N;
+        if (leader) {
+          mma8_ss<0>(d, kd, 0, qd, 0, kIdS);
+#pragma unroll
+          for (int s = 1; s < kHeadDim / 32; ++s) mma8_ss<1>(d, kd, s * 2, qd, s * 2, kIdS);
+          umma_commit(&bars[L::kSFull + slot]);
+          umma_commit(&bars[L::kKEmpty + stage]);
+          if (j + 1 == di.nb) umma_commit(&bars[L::kQEmpty + qslot]);
+        }
+        __syncwarp();
+        if (++stage == SK) {
+          stage = 0;
+          kpar ^= 1;
+        }
+      }
+      if (fail) break;
+    }
+  } else if (warp == 15) {
+    // ------------------------------------------------------------ PV issuer
+    constexpr uint32_t kIdO = idesc_e4m3(128, N, true);  // A = V^T (dims contiguous), B = P^T pieces
+    const uint32_t leader = elect_one_sync();
+    uint32_t stage = 0, vpar = 0, o_it = 0;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = dec_snake_item(round);
+      if (item >= p.num_items) continue;
+      const DecItem di = dec_item(p, item);
+      bool fail = false;
+      for (int j = 0; j < di.nb; ++j, ++o_it) {
+        const uint32_t oslot = o_it % OS, pslot = o_it % PS;
+        bool w = mbar_wait(&bars[L::kVFull + stage], vpar, abort, p.err, 0xb22);
+        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        uint8_t* vd = v_base + stage * L::kKVBytes;
+        // V rows past the context may hold anything, NaN codes among it; P is
+        // exactly 0 there, so zero them (0 * NaN = NaN)
+        const int valid = min(B, di.kv_len - (di.b0 + j * di.stride) * B);
+        if (valid < B) {
+          for (int i = lane; i < (B - valid) * 8; i += 32)
+            *reinterpret_cast<uint4*>(vd + valid * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        w = mbar_wait(&bars[L::kPFull + pslot], (o_it / PS) & 1, abort, p.err, 0xb21);
+        w = w && mbar_wait(&bars[L::kOEmpty + oslot], ((o_it / OS) & 1) ^ 1, abort, p.err, 0xb23);
+        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        tc_fence_after();
+        // K-step s covers keys 32 s .. 32 s + 31: V rows 4096 B a step, P^T
+        // columns 32 B a step
+        const Desc vdd = make_desc(smem_u32(vd), 16, 1024);
+        const Desc pd = make_desc(smem_u32(p_base + pslot * L::kTBytes), 16, 1024);
+        const uint32_t d = tm_o + oslot * N;
+        if (leader) {
+          mma8_ss<0>(d, vdd, 0, pd, 0, kIdO);
+#pragma unroll
+          for (int s = 1; s < B / 32; ++s) mma8_ss<1>(d, vdd, s * 256, pd, s * 2, kIdO);
+          umma_commit(&bars[L::kOFull + oslot]);
+          umma_commit(&bars[L::kVEmpty + stage]);
+          umma_commit(&bars[L::kPEmpty + pslot]);
+        }
+        __syncwarp();
+        if (++stage == SV) {
+          stage = 0;
+          vpar ^= 1;
+        }
+      }
+      if (fail) break;
+    }
+  } else if (warp == 16) {
+    // ------------------------------------------------------------ query rows
+    uint32_t q_it = 0;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = dec_snake_item(round);
+      if (item >= p.num_items) continue;
+      const DecItem di = dec_item(p, item);
+      const uint32_t qslot = q_it & 1;
+      // lane l holds elements 4 l .. 4 l + 3 of every row
+      uint2 x[MG];
+#pragma unroll
+      for (int i = 0; i < MG; ++i)
+        if (i < G)
+          x[i] = __ldg(reinterpret_cast<const uint2*>(
+                           qp.q + (static_cast<int64_t>(di.seq) * p.hq + di.g * G + i) * kHeadDim) + lane);
+      float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
+      if (p.rope_table) {
+        const float* trow = p.rope_table + static_cast<int64_t>(di.kv_len - 1) * kHeadDim;
+        c = __ldg(reinterpret_cast<const float4*>(trow) + (lane & 15));
+        s = __ldg(reinterpret_cast<const float4*>(trow + 64) + (lane & 15));
+      }
+      bool ok = mbar_wait(&bars[L::kQEmpty + qslot], ((q_it >> 1) & 1) ^ 1, abort, p.err, 0xb31);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++q_it;
+      uint8_t* tile = q_base + qslot * L::kTBytes;
+#pragma unroll
+      for (int i = 0; i < MG; ++i) {
+        if (i >= G) continue;
+        uint32_t w[2] = {x[i].x, x[i].y};
+        if (p.rope_table) {
+          // the pair of element e is e +- 64, 16 lanes away
+          const uint32_t o[2] = {__shfl_xor_sync(0xffffffffu, w[0], 16), __shfl_xor_sync(0xffffffffu, w[1], 16)};
+          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float xe = (e & 1) ? bf16_hi_as_f32(w[e >> 1]) : bf16_lo_as_f32(w[e >> 1]);
+            const float oe = (e & 1) ? bf16_hi_as_f32(o[e >> 1]) : bf16_lo_as_f32(o[e >> 1]);
+            float y0, y1;
+            rope_pair(lane < 16 ? xe : oe, lane < 16 ? oe : xe, cc[e], ss[e], y0, y1);
+            y[e] = lane < 16 ? y0 : y1;
+          }
+          w[0] = pack_bf16x2(y[0], y[1]);
+          w[1] = pack_bf16x2(y[2], y[3]);
+        }
+        float v[4] = {bf16_lo_as_f32(w[0]), bf16_hi_as_f32(w[0]), bf16_lo_as_f32(w[1]), bf16_hi_as_f32(w[1])};
+        // the row's largest finite magnitude to [128, 256)
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = fabsf(v[e]);
+          if (a <= 3.4028234e38f) m = fmaxf(m, a);
+          else v[e] = __uint_as_float(0x7FC00000u);  // Inf and NaN queries give NaN rows
+        }
+        m = warp_max(m);
+        const int up = min(261 - static_cast<int>(__float_as_uint(m) >> 23), 253);
+        const float f = pow2_bits(up);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], f);
+#pragma unroll
+        for (int k = 0; k < kQPieces; ++k) {
+          const uint32_t lo = next_piece(v[0], v[1]);
+          const uint32_t hi = next_piece(v[2], v[3]);
+          *reinterpret_cast<uint32_t*>(tile + tile8_off(k * MG + i, 4 * lane)) = lo | (hi << 16);
+        }
+        if (lane == 0) qscale[qslot * MG + i] = pow2_bits(254 - up);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bars[L::kQFull + qslot], lane);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int grp = warp >= 8 ? 1 : 0;
+    const int t = tid - (grp ? 256 : 128);  // key lane
+    const int w = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(w * 32) << 16;
+    float* red = reinterpret_cast<float*>(smem + L::kRedOff + grp * L::kRedBytes);
+    float* part = reinterpret_cast<float*>(smem + L::kPartOff + grp * L::kPartBytes);
+    const float sl = p.scale_log2;
+    const int lps = 31 - __clz(p.page_size);
+    uint32_t s_base = 0, sy_it = 0, q_it = 0;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = dec_snake_item(round);
+      if (item >= p.num_items) continue;
+      const DecItem di = dec_item(p, item);
+      const int kv_len = di.kv_len, nb = di.nb;
+      // the scales of this thread's key: page ids two own blocks ahead, the
+      // scales themselves one ahead
+      const int32_t* prow = p.page_table + static_cast<int64_t>(di.seq) * p.max_pages;
+      auto page_of = [&](int j) -> int {
+        const int key = (di.b0 + j * di.stride) * B + t;
+        return (j < nb && key < kv_len) ? __ldg(prow + (key >> lps)) : -1;
+      };
+      auto scales_of = [&](int pg, float& sk, float& sv) {
+        sk = sv = 1.0f;
+        if (pg >= 0 && pg < p.n_pages) {
+          const int64_t i = static_cast<int64_t>(pg) * p.hkv + di.g;
+          sk = __ldg(qp.k_scale + i);
+          sv = __ldg(qp.v_scale + i);
+        }
+      };
+      const int j0 = static_cast<int>(s_base & 1) == grp ? 0 : 1;
+      float sk, sv;
+      int pg_next = page_of(j0 + 2);
+      scales_of(page_of(j0), sk, sv);
+      if (FOLD && p.state_o && p.fill_flag) {
+        // their share of the item's table fill, released to the correction warps
+        fill_item_slots(p, di, G, tid);
+        mbar_arrive(&bars[L::kFillDone]);
+      }
+      const uint32_t qslot = q_it & 1;
+      bool ok = mbar_wait(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb41);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++q_it;
+      float qs[MG];
+#pragma unroll
+      for (int q = 0; q < MG; ++q) qs[q] = q < G ? qscale[qslot * MG + q] : 0.0f;
+      warp_arrive(&bars[L::kQEmpty + qslot], lane);
+      bool fail = false;
+      for (int j = j0; j < nb; j += 2) {
+        const uint32_t s_it = s_base + j;
+        const uint32_t slot = s_it % SS;
+        float sk_next, sv_next;
+        scales_of(pg_next, sk_next, sv_next);
+        pg_next = page_of(j + 4);
+        ok = mbar_wait(&bars[L::kSFull + slot], (s_it / SS) & 1, abort, p.err, 0xb42);
+        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        tc_fence_after();
+        uint32_t raw[N];
+        TmemRow<N>::ld(tm_s + lane_off + slot * N, raw);
+        tmem_ld_wait(raw);
+        tc_fence_before();
+        warp_arrive(&bars[L::kSEmpty + slot], lane);
+        const bool vis = (di.b0 + j * di.stride) * B + t < kv_len;
+        const int rb = static_cast<int>(sy_it & 1);
+        const uint32_t sy_par = (sy_it >> 1) & 1;
+        // scores, and the block maxima over the visible keys (exact)
+        float sc[MG];
+#pragma unroll
+        for (int q = 0; q < MG; ++q) {
+          const float a = __fmaf_rn(__uint_as_float(raw[2 * MG + q]), 0x1p-10f,
+                                    __fmaf_rn(__uint_as_float(raw[MG + q]), 0x1p-5f, __uint_as_float(raw[q])));
+          sc[q] = (q < G && vis) ? __fmul_rn(__fmul_rn(a, qs[q]), sk) : -INFINITY;
+          const float m = warp_max(sc[q]);
+          if (lane == 0) red[(rb * 4 + w) * (MG + 1) + q] = m;
+        }
+        {
+          const float m = warp_max(vis ? sv : 0.0f);
+          if (lane == 0) red[(rb * 4 + w) * (MG + 1) + MG] = m;
+        }
+        warp_arrive(&bars[L::kSyncMax + grp * 2 + rb], lane);
+        ok = mbar_wait(&bars[L::kSyncMax + grp * 2 + rb], sy_par, abort, p.err, 0xb43);
+        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        const float* r4 = red + rb * 4 * (MG + 1);
+        auto max4 = [&](int q) {
+          return fmaxf(fmaxf(fmaxf(r4[q], r4[MG + 1 + q]), r4[2 * (MG + 1) + q]), r4[3 * (MG + 1) + q]);
+        };
+        float mc[MG], pr[MG];
+#pragma unroll
+        for (int q = 0; q < MG; ++q) {
+          mc[q] = __fmul_rn(max4(q), sl);
+          pr[q] = (q < G && vis) ? prob(sc[q], sl, -mc[q]) : 0.0f;
+        }
+        // the block's V anchor A = 2^(ae - 127); w = p (sv 2^7 / A)
+        const int ae = max(static_cast<int>(__float_as_uint(max4(MG)) >> 23), 8);
+        const float wf = vis ? __fmul_rn(sv, pow2_bits(261 - ae)) : 0.0f;
+        ok = mbar_wait(&bars[L::kPEmpty + grp], ((s_it / PS) & 1) ^ 1, abort, p.err, 0xb44);
+        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        uint8_t* pt = p_base + (s_it % PS) * L::kTBytes;
+#pragma unroll
+        for (int q = 0; q < MG; q += 2) {
+          float a = __fmul_rn(pr[q], wf), b = q + 1 < MG ? __fmul_rn(pr[q + 1 < MG ? q + 1 : q], wf) : 0.0f;
+#pragma unroll
+          for (int k = 0; k < kPPieces; ++k) {
+            const uint32_t c = k + 1 < kPPieces ? next_piece(a, b) : e4m3_pair(a, b);
+            if (q < G) pt[tile8_off(k * MG + q, t)] = static_cast<uint8_t>(c);
+            if (q + 1 < G) pt[tile8_off(k * MG + q + 1, t)] = static_cast<uint8_t>(c >> 8);
+          }
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&bars[L::kPFull + (s_it % PS)], lane);
+        // canonical row sums (numerics.cuh): warp w sums query heads w, w + 4
+#pragma unroll
+        for (int q = 0; q < MG; ++q) part[((rb * 4 + w) * MG + q) * 32 + lane] = pr[q];
+        warp_arrive(&bars[L::kSyncPart + grp * 2 + rb], lane);
+        ok = mbar_wait(&bars[L::kSyncPart + grp * 2 + rb], sy_par, abort, p.err, 0xb45);
+        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        const uint32_t sslot = s_it % SR;
+#pragma unroll
+        for (int q = 0; q < MG; ++q) {
+          if (q >= G || (q & 3) != w) continue;
+          const float* pw = part + (rb * 4 * MG + q) * 32 + (lane & 15);
+          float a = __fadd_rn(__fadd_rn(__fadd_rn(pw[0], pw[16]), pw[MG * 32]), pw[MG * 32 + 16]);
+          float a1 = __fadd_rn(__fadd_rn(__fadd_rn(pw[2 * MG * 32], pw[2 * MG * 32 + 16]), pw[3 * MG * 32]),
+                               pw[3 * MG * 32 + 16]);
+#pragma unroll
+          for (int off = 8; off >= 1; off >>= 1) {
+            a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
+            a1 = __fadd_rn(a1, __shfl_xor_sync(0xffffffffu, a1, off));
+          }
+          a = __fadd_rn(a, a1);
+          if (lane == 0) {
+            float lse_b, rcp;
+            block_stats(mc[q], a, lse_b, rcp);
+            // PV carries 2^7 / A: fold its inverse into 1 / l (exact)
+            stats[sslot * MG + q] = make_float2(lse_b, __fmul_rn(rcp, pow2_bits(ae - 7)));
+          }
+        }
+        warp_arrive(&bars[L::kStatsFull + sslot], lane);
+        ++sy_it;
+        sk = sk_next;
+        sv = sv_next;
+      }
+      if (fail) break;
+      s_base += nb;
+    }
+  } else {
+    // ------------------------------------------------------------ correction / epilogue
+    const int d = tid;  // head dimension lane
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t o_it = 0, fill_it = 0;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = dec_snake_item(round);
+      if (item >= p.num_items) continue;
+      const DecItem di = dec_item(p, item);
+      const int seq = di.seq, g = di.g, nb = di.nb;
+      const bool split = p.state_o != nullptr;
+      if (FOLD && split && p.fill_flag) {
+        // the item's slots of the state table hold kUnwritten before any of
+        // its states can land; the fill barrier orders every fill store (the
+        // softmax warps write a share) before every state store
+        fill_item_slots(p, di, G, tid);
+        mbar_arrive(&bars[L::kFillDone]);
+        const bool ok = mbar_wait(&bars[L::kFillDone], fill_it & 1, abort, p.err, 0xb53);
+        ++fill_it;
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
+      float O[MG];
+#pragma unroll
+      for (int q = 0; q < MG; ++q) O[q] = 0.0f;
+      float Lrun = -INFINITY;  // lane q: running lse of query head q
+      bool fail = false;
+      for (int j = 0; j < nb; ++j) {
+        const uint32_t sslot = o_it % SR, oslot = o_it % OS;
+        bool ok = mbar_wait(&bars[L::kStatsFull + sslot], (o_it / SR) & 1, abort, p.err, 0xb51);
+        ok = ok && mbar_wait(&bars[L::kOFull + oslot], (o_it / OS) & 1, abort, p.err, 0xb52);
+        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        tc_fence_after();
+        uint32_t raw[N];
+        TmemRow<N>::ld(tm_o + lane_off + oslot * N, raw);
+        // fold coefficients of query head `lane` (overlap the TMEM load)
+        float lb = -INFINITY, rc = 0.0f, al = 0.0f, be = 0.0f, Lp = 0.0f;
+        if (lane < G) {
+          const float2 st = stats[sslot * MG + lane];
+          lb = st.x;
+          rc = st.y;
+          if (j > 0 && !split) fold_coeffs(Lrun, lb, Lp, al, be);
+        }
+        tmem_ld_wait(raw);
+        tc_fence_before();
+        warp_arrive(&bars[L::kOEmpty + oslot], lane);
+        const int64_t blk = p.cu_q[seq] + di.b0 + j * di.stride;  // state-table block
+        const int64_t pair_b = blk * p.hq + g * G;
+#pragma unroll
+        for (int q = 0; q < MG; ++q) {
+          const float rq = __shfl_sync(0xffffffffu, rc, q);
+          const float aq = __shfl_sync(0xffffffffu, al, q);
+          const float bq = __shfl_sync(0xffffffffu, be, q);
+          if (q < G) {
+            float pv = __uint_as_float(raw[(kPPieces - 1) * MG + q]);
+#pragma unroll
+            for (int k = kPPieces - 2; k >= 0; --k) pv = __fmaf_rn(pv, 0x1p-5f, __uint_as_float(raw[k * MG + q]));
+            const float oa = state_elem(pv, rq);
+            if (split) p.state_o[(pair_b + q) * kHeadDim + d] = oa;
+            else O[q] = (j == 0) ? oa : fold_elem(O[q], oa, aq, bq);
+          }
+        }
+        if (split) {
+          if (warp == 0 && lane < G) p.state_lse[pair_b + lane] = lb;
+          if (FOLD && p.fill_flag && j == 0 && tid == 0)
+            st_release_u64(p.fill_flag + (static_cast<int64_t>(seq) * p.hkv + g) * kMaxSplitK + di.b0, p.fill_nonce);
+        } else if (lane < G) {
+          Lrun = (j == 0) ? lb : Lp;
+        }
+        ++o_it;
+      }
+      if (fail) break;
+      if (split) continue;
+      // epilogue: O and L are final
+#pragma unroll
+      for (int q = 0; q < MG; ++q) {
+        if (q < G) {
+          const int64_t row = static_cast<int64_t>(seq) * p.hq + g * G + q;
+          if (p.out_f32) p.out_f32[row * kHeadDim + d] = O[q];
+          if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(O[q]);
+        }
+      }
+      if (warp == 0 && lane < G && p.lse) p.lse[static_cast<int64_t>(seq) * p.hq + g * G + lane] = Lrun;
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 14) {
+    if (*abort) {
+      // let copies already in flight land before the CTA's memory is released
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+    tc_fence_after();
+    tmem_dealloc(tm_s, L::kTmemCols);
+  }
+}
+
+template <int MG>
+cudaError_t launch_qdecode_t(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                             bool cooperative, cudaStream_t stream) {
+  if (!cooperative) {
+    rlk_qdecode_kernel<MG, false><<<grid, kQDThreads, QDecLayout<MG>::kAlloc, stream>>>(p, tk, tv);
+    return cudaGetLastError();
+  }
+  // the fold warps wait for states that other CTAs of the launch publish:
+  // every CTA must be resident at once
+  void* args[] = {const_cast<QDecodeParams*>(&p), const_cast<CUtensorMap*>(&tk), const_cast<CUtensorMap*>(&tv)};
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(&rlk_qdecode_kernel<MG, true>), dim3(grid),
+                                     dim3(kQDThreads), args, QDecLayout<MG>::kAlloc, stream);
+}
+
+template <int MG>
+cudaError_t configure_qdecode_mg() {
+  cudaError_t e = cudaFuncSetAttribute(rlk_qdecode_kernel<MG, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       QDecLayout<MG>::kAlloc);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(rlk_qdecode_kernel<MG, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              QDecLayout<MG>::kAlloc);
+}
+
+}  // namespace
+
+cudaError_t configure_qdecode_kernels() {
+  cudaError_t e;
+  if ((e = configure_qdecode_mg<1>())) return e;
+  if ((e = configure_qdecode_mg<2>())) return e;
+  if ((e = configure_qdecode_mg<4>())) return e;
+  return configure_qdecode_mg<8>();
+}
+
+cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                           bool cooperative, cudaStream_t stream) {
+  if (p.f.group <= 1) return launch_qdecode_t<1>(p, tk, tv, grid, cooperative, stream);
+  if (p.f.group <= 2) return launch_qdecode_t<2>(p, tk, tv, grid, cooperative, stream);
+  if (p.f.group <= 4) return launch_qdecode_t<4>(p, tk, tv, grid, cooperative, stream);
+  return launch_qdecode_t<8>(p, tk, tv, grid, cooperative, stream);
+}
+
+}  // namespace rlk

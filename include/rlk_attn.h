@@ -379,6 +379,106 @@ rlk_status rlk_attn_decode_paged_splitk_rope(const rlk_attn_params* params, cons
 int32_t rlk_attn_decode_auto_split(const rlk_attn_params* params, const int32_t* seqlens, int32_t num_sms);
 
 /*
+ * 8-bit paged KV cache: K and V as E4M3 codes (1 byte each) with one FP32
+ * scale per (page, KV head), half the bytes of the BF16 pools a decode step
+ * reads.  All three calls below share
+ *   k_pool, v_pool: device E4M3 [n_pages, Hkv, page_size, 128] -- the head
+ *     before the slot, unlike the BF16 pools, so one head's page is one run of
+ *     page_size * 128 bytes under one scale;
+ *   k_scale, v_scale: device FP32 [n_pages, Hkv]; an element is code * scale;
+ *   page_table: device int32 [num_seqs, max_pages] as in
+ *     rlk_attn_decode_paged: token t of sequence s is slot t % page_size of
+ *     page page_table[s * max_pages + t / page_size].
+ * page_size divides kv_block_size and is >= 8.  16-byte aligned pools, 4-byte
+ * aligned scales.  A page id outside [0, n_pages) sets RLK_ERR_BAD_PAGE on
+ * the device error word; it is read as zeros and never written.
+ *
+ * Quantisation.  A BF16 value x is first rounded to 4 significant bits, q4(x)
+ * (nearest, ties to even; BF16 subnormals count as 0, and a value that would
+ * overflow stays at 1.875 * 2^127).  The scale of a (page, head) is 2^e with
+ *     e = max(-120, floor(log2 max |q4|) - 7)
+ * over the finite elements of the page's tokens so far, and a code is
+ * q4 / 2^e, or +0 where that is below 2^-6 in magnitude; Inf and NaN become
+ * the NaN code.  Codes use E4M3's normal numbers up to 240 alone.  So
+ *   - a page's codes and scales depend on its tokens, not on the calls that
+ *     wrote them: appending token by token, in chunks, or all at once gives
+ *     the same bytes (a later token that raises e moves the page's earlier
+ *     codes to the new scale, exactly);
+ *   - code * scale is a BF16 number: reading back rounds nothing.
+ * The relative error of an element is at most 2^-4 (half a step of 3
+ * mantissa bits), or the whole element where it is below 2^-13 of its page's
+ * largest.
+ */
+
+/*
+ * Quantises new K and V rows into the pages: row i of sequence s is the token
+ * at position pos_offset[s] + i.  Tokens of a sequence are written in order
+ * and each once: a page's slots below the first written one hold earlier
+ * tokens, those from the last written one on are left as they are.  (Writing
+ * the latest tokens again is a no-op only if they are the same ones: a page's
+ * scale never shrinks while it holds tokens.)
+ *   k, v: device BF16 [T, Hkv, 128], T = cu_seqlens[num_seqs];
+ *   cu_seqlens: HOST [num_seqs + 1] (a sequence may have no new token);
+ *   pos_offset: HOST [num_seqs] tokens already cached, or NULL (0);
+ *   rope_table: NULL (k is stored as given), or device, from
+ *     rlk_attn_rope_table: k is pre-RoPE and each row is rotated at its
+ *     position in the form of rlk_attn_rope before it is quantised (the same
+ *     bytes as rlk_attn_rope on k first); every position < rope_max_pos.
+ * The pages written by one call must differ from each other and from those
+ * that other calls in flight read or write.  params: num_seqs, num_kv_heads,
+ * kv_block_size (and head_dim) are read.
+ */
+rlk_status rlk_attn_qcache_write(const rlk_attn_params* params, const void* k, const void* v,
+                                 const int32_t* cu_seqlens, const int32_t* pos_offset, const float* rope_table,
+                                 int32_t rope_max_pos, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                 int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
+                                 rlk_stream_t stream);
+
+/*
+ * Reads tokens pos_offset[s] .. pos_offset[s] + len_s - 1 of every sequence
+ * back as packed BF16 rows (what rlk_attn_prefill takes as k and v: chunked
+ * prefill over the 8-bit cache reads each sequence's tokens 0 .. kv_len - 1).
+ *   cu_seqlens: HOST [num_seqs + 1], prefix sums of len_s; pos_offset: HOST
+ *     [num_seqs] or NULL (0); k, v: device BF16 [T, Hkv, 128] outputs,
+ *     T = cu_seqlens[num_seqs], bf16_rn(code * scale) (exact for the scales
+ *     rlk_attn_qcache_write sets; any finite FP32 scale is taken).
+ */
+rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_pool, const void* v_pool,
+                                const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
+                                const int32_t* page_table, int32_t max_pages, const int32_t* cu_seqlens,
+                                const int32_t* pos_offset, void* k, void* v, rlk_stream_t stream);
+
+/*
+ * Decode over the 8-bit cache: one query token per sequence, at the last
+ * position of its context, against the pages' values code * scale -- the
+ * counterpart of rlk_attn_decode_paged, _splitk and _rope in one call.
+ *   q: device BF16 [num_seqs, Hq, 128]; seqlens: HOST [num_seqs], context
+ *     lengths 1 .. max_pages * page_size; outputs as rlk_attn_decode_paged;
+ *   split_k: 1 = single pass; 2 .. 64 items per (sequence, KV head); 0 = the
+ *     library picks (as rlk_attn_decode_paged_splitk; the same result for
+ *     every value);
+ *   rope_table: NULL, or device: q is pre-RoPE and rotated at position
+ *     seqlens[s] - 1 (< rope_max_pos) as in rlk_attn_decode_paged_rope;
+ *   workspace: for split_k != 1, device, 16-byte aligned,
+ *     >= rlk_attn_workspace_size(params, RLK_OP_DECODE_SPLIT, NULL, seqlens)
+ *     bytes, not shared by calls that overlap; unused for split_k == 1.
+ * The pages' codes go to the tensor core as they are; the query and the
+ * probabilities are split into 3 and 4 E4M3 pieces, so neither loses
+ * precision to 8 bits: scores, softmax and sums are FP32, and out / lse stay
+ * within 2e-5 / 1e-5 of the exact attention over the cached values at unit
+ * scale.  Scales must be positive, finite and >= 2^-120.  A query row that
+ * holds Inf or NaN gives a NaN row.  The result does not depend on the batch,
+ * the page order, split_k or repetition (bit for bit).  Needs kv_block_size
+ * 128 and at most 8 query heads per KV head (RLK_ERR_UNSUPPORTED otherwise).
+ */
+rlk_status rlk_attn_decode_qcache(const rlk_attn_params* params, const void* q, const void* k_pool,
+                                  const void* v_pool, const float* k_scale, const float* v_scale, int32_t n_pages,
+                                  int32_t page_size, const int32_t* page_table, int32_t max_pages,
+                                  const int32_t* seqlens, int32_t split_k, const float* rope_table,
+                                  int32_t rope_max_pos, float* out_f32, void* out_bf16, float* lse, void* workspace,
+                                  size_t workspace_bytes, rlk_stream_t stream);
+
+/*
  * Deterministic backward of causal prefill (q_len == kv_len per sequence):
  *   q, k, v, dout: device BF16; out_f32: device FP32 forward output;
  *   lse: device FP32 forward lse; cu_seqlens: HOST [num_seqs + 1];
