@@ -31,7 +31,7 @@ STATUS_NAMES = {
     3: "RLK_ERR_WORKSPACE_TOO_SMALL", 4: "RLK_ERR_DUPLICATE_BLOCK", 5: "RLK_ERR_MISSING_BLOCK",
     6: "RLK_ERR_DEVICE_TIMEOUT", 7: "RLK_ERR_CUDA", 8: "RLK_ERR_BAD_PAGE", 9: "RLK_ERR_BAD_STATE_TABLE",
 }
-RLK_OP_MERGE, RLK_OP_BACKWARD, RLK_OP_DECODE_SPLIT = 1, 2, 3
+RLK_OP_MERGE, RLK_OP_BACKWARD, RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE = 1, 2, 3, 4
 CONTIGUOUS, ZIGZAG = 0, 1
 
 
@@ -182,8 +182,8 @@ def rlk_attn_block_manifest_hash(params, cu_seqlens_q, cu_seqlens_k) -> int:
 
 
 def rlk_attn_workspace_size(params, op, cu_seqlens_q, cu_seqlens_k=None) -> int:
-    """RLK_OP_DECODE_SPLIT: pass the decode context lengths as cu_seqlens_k
-    (cu_seqlens_q may be None)."""
+    """RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE: pass the decode context
+    lengths as cu_seqlens_k (cu_seqlens_q may be None)."""
     cq = None if cu_seqlens_q is None else _i32_host(cu_seqlens_q)
     ck = _i32_host(cu_seqlens_k if cu_seqlens_k is not None else cu_seqlens_q)
     return int(load().rlk_attn_workspace_size(ctypes.byref(params), int(op), _ptr(cq), _ptr(ck)))

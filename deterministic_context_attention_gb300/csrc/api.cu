@@ -36,8 +36,6 @@ cudaError_t launch_decode(const FwdParams& p, const CUtensorMap& tq, const CUten
                           int grid, cudaStream_t stream);
 cudaError_t launch_decode_cooperative(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                       const CUtensorMap& tv, int grid, cudaStream_t stream);
-cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                           bool cooperative, cudaStream_t stream);
 rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k, const void* v,
                         const float* out_f32, const void* dout, const float* lse,
                         const int32_t* cu, int32_t cp_rank, float* dq, float* dk, float* dv,
@@ -48,9 +46,9 @@ size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu);
 
 static_assert(sizeof(rlk::FwdParams) + 3 * sizeof(CUtensorMap) + 256 <= 32764,
               "forward kernel parameters exceed the 32 KB launch limit");
-static_assert(sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) + 256 <= 32764,
-              "8-bit decode kernel parameters exceed the 32 KB launch limit");
 static_assert(sizeof(rlk::MergeParams) <= 4096, "merge parameters");
+static_assert(sizeof(rlk::QCacheParams) <= 4096 && sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) <= 4096,
+              "8-bit cache parameters");
 static_assert(sizeof(rlk_attn_slab) == sizeof(rlk::Slab), "slab layout");
 
 // The device error word.  Host code reaches it through its device address,
@@ -639,108 +637,36 @@ rlk_status rlk_attn_prefill_rope(const rlk_attn_params* params, const void* q, c
 
 namespace {
 
-// The paged cache a decode reads: BF16 pools [n_pages][page_size][hkv][128],
-// or (scales set) 8-bit pools [n_pages][hkv][page_size][128] with one FP32
-// scale per (page, KV head).
-struct DecodeCache {
-  const void* k_pool;
-  const void* v_pool;
-  const float* k_scale;
-  const float* v_scale;
-  int32_t n_pages, page_size;
-  const int32_t* page_table;
-  int32_t max_pages;
-  bool coded() const { return k_scale != nullptr; }
-  // the cache seen from sequence s0 on
-  DecodeCache from(int s0) const {
-    DecodeCache c = *this;
-    c.page_table += static_cast<int64_t>(s0) * max_pages;
-    return c;
-  }
-};
-
-rlk_status check_page_size(const rlk_attn_params* params, int32_t page_size) {
-  const int B = params->kv_block_size;
-  if (page_size < 8 || page_size > B || B % page_size)
-    return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
-  return RLK_OK;
-}
-
-rlk_status check_pages(const rlk_attn_params* params, const DecodeCache& c, const int32_t* seqlens) {
-  if (rlk_status st = check_page_size(params, c.page_size)) return st;
-  if (c.n_pages < 1 || c.max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
-  if (!c.coded() && (static_cast<int64_t>(c.n_pages) + 1) * c.page_size >= (int64_t(1) << 31))
-    return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit token coordinates");
-  if (c.coded() && (static_cast<int64_t>(c.n_pages) + 1) * params->num_kv_heads >= (int64_t(1) << 31))
-    return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit (page, head) coordinates");
-  for (int s = 0; s < params->num_seqs; ++s)
-    if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(c.max_pages) * c.page_size)
-      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: context length %d not in 1..max_pages*page_size", s,
-                  seqlens[s]);
-  return RLK_OK;
-}
-
-// The tensor maps of a decode over either cache (q: BF16 pools only, the
-// 8-bit kernel loads the query rows itself).
-struct DecodeMaps {
-  CUtensorMap q, k, v;
-};
-rlk_status make_decode_maps(const rlk_attn_params* params, const void* q, const DecodeCache& c, DecodeMaps* m) {
-  rlk_status st;
-  if (c.coded()) {
-    if ((st = make_code_map(&m->k, c.k_pool, c.n_pages, params->num_kv_heads, c.page_size))) return st;
-    return make_code_map(&m->v, c.v_pool, c.n_pages, params->num_kv_heads, c.page_size);
-  }
-  // one query head per TMA box: the kernel places each head in its own operand row
-  if ((st = make_map(&m->q, q, params->num_q_heads, params->num_seqs, 1, 1))) return st;
-  const uint64_t tokens = static_cast<uint64_t>(c.n_pages) * c.page_size;
-  if ((st = make_map(&m->k, c.k_pool, params->num_kv_heads, tokens, 1, c.page_size))) return st;
-  return make_map(&m->v, c.v_pool, params->num_kv_heads, tokens, 1, c.page_size);
-}
-
-// One decode launch over fp.tiles (the transposed kernels).
-cudaError_t launch_decode_kernel(const rlk::QDecodeParams& dp, const DecodeCache& c, const DecodeMaps& m, int grid,
-                                 bool cooperative, cudaStream_t stream) {
-  if (c.coded()) return rlk::launch_qdecode(dp, m.k, m.v, grid, cooperative, stream);
-  return cooperative ? rlk::launch_decode_cooperative(dp.f, m.q, m.k, m.v, grid, stream)
-                     : rlk::launch_decode(dp.f, m.q, m.k, m.v, grid, stream);
-}
-
-std::unique_ptr<rlk::QDecodeParams> decode_params(const rlk_attn_params* params, const DeviceInfo* dev,
-                                                  const void* q, const DecodeCache& c, const float* rope_table) {
-  auto dp = std::make_unique<rlk::QDecodeParams>();
-  base_fwd(&dp->f, params, dev, rlk::kModeDecode);
-  dp->f.page_table = c.page_table;
-  dp->f.max_pages = c.max_pages;
-  dp->f.page_size = c.page_size;
-  dp->f.n_pages = c.n_pages;
-  dp->f.rope_table = rope_table;
-  dp->q = static_cast<const uint16_t*>(q);
-  dp->k_scale = c.k_scale;
-  dp->v_scale = c.v_scale;
-  return dp;
-}
-
-rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const DecodeCache& cache,
+rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const void* k_pool, const void* v_pool,
+                             int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                              const int32_t* seqlens, const float* rope_table, int32_t rope_max_pos,
                              float* out_f32, void* out_bf16, float* lse, cudaStream_t stream) {
   rlk_status st = check_params(params);
   if (st) return st;
-  if (!q || !cache.k_pool || !cache.v_pool || !cache.page_table || !seqlens)
-    return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
+  if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
   if (!out_f32 && !out_bf16) return fail(RLK_ERR_INVALID_ARGUMENT, "out_f32 and out_bf16 are both NULL");
-  if (!aligned16(q) || !aligned16(cache.k_pool) || !aligned16(cache.v_pool) || (out_f32 && !aligned16(out_f32)) ||
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || (out_f32 && !aligned16(out_f32)) ||
       (out_bf16 && !aligned16(out_bf16)))
     return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
   if (params->num_seqs > rlk::kMaxSeqs)
     return over_ranges(params->num_seqs, [&](int s0, int s1) {
       const rlk_attn_params rp = range_params(params, s0, s1);
       const int64_t o = static_cast<int64_t>(s0) * params->num_q_heads;
-      return decode_paged_impl(&rp, adv(q, o * 128, 2), cache.from(s0), seqlens + s0, rope_table, rope_max_pos,
-                               adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4), stream);
+      return decode_paged_impl(&rp, adv(q, o * 128, 2), k_pool, v_pool, n_pages, page_size,
+                               page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, rope_table,
+                               rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4),
+                               stream);
     });
   const int B = params->kv_block_size;
-  if ((st = check_pages(params, cache, seqlens))) return st;
+  if (page_size < 8 || page_size > B || B % page_size)
+    return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
+  if (n_pages < 1 || max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
+  if (static_cast<int64_t>(n_pages + 1) * page_size >= (int64_t(1) << 31))
+    return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit token coordinates");
+  for (int s = 0; s < params->num_seqs; ++s)
+    if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(max_pages) * page_size)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: context length %d not in 1..max_pages*page_size", s,
+                  seqlens[s]);
   if (rope_table) {
     if (!aligned16(rope_table)) return fail(RLK_ERR_INVALID_ARGUMENT, "rope table must be 16-byte aligned");
     if (B != 128 || params->num_q_heads / params->num_kv_heads > rlk::kDecodeMaxGroup)
@@ -772,27 +698,37 @@ rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const
                    });
   std::vector<rlk::FwdTile> tiles;
   for (auto& c : costed) tiles.push_back(c.second);
-  DecodeMaps maps;
-  if ((st = make_decode_maps(params, q, cache, &maps))) return st;
-  auto dp = decode_params(params, dev, q, cache, rope_table);
-  rlk::FwdParams* fp = &dp->f;
+  CUtensorMap mq, mk, mv;
+  // one query head per TMA box: the kernel places each head in its own lane quadrant
+  if ((st = make_map(&mq, q, params->num_q_heads, params->num_seqs, 1, 1))) return st;
+  if ((st = make_map(&mk, k_pool, params->num_kv_heads, static_cast<uint64_t>(n_pages) * page_size, 1, page_size)))
+    return st;
+  if ((st = make_map(&mv, v_pool, params->num_kv_heads, static_cast<uint64_t>(n_pages) * page_size, 1, page_size)))
+    return st;
+  auto fp = std::make_unique<rlk::FwdParams>();
+  base_fwd(fp.get(), params, dev, rlk::kModeDecode);
   for (int s = 0; s < params->num_seqs; ++s) fp->cu_k[s] = seqlens[s];
   fp->out_f32 = out_f32;
   fp->out_bf16 = static_cast<uint16_t*>(out_bf16);
   fp->lse = lse;
-  if (!cache.coded() && !rlk::decode_transposed_supported(*fp)) {
-    if ((st = launch_fwd_tiles(fp, tiles, 1, maps.q, maps.k, maps.v, dev, stream))) return st;
+  fp->page_table = page_table;
+  fp->max_pages = max_pages;
+  fp->page_size = page_size;
+  fp->n_pages = n_pages;
+  fp->rope_table = rope_table;
+  if (!rlk::decode_transposed_supported(*fp)) {
+    if ((st = launch_fwd_tiles(fp.get(), tiles, 1, mq, mk, mv, dev, stream))) return st;
     return ok();
   }
   // KV blocks of 128 keys and up to 8 query heads per KV head: the
-  // transposed decode kernels (keys on the MMA's M side)
+  // transposed decode kernel (keys on the MMA's M side)
   for (size_t t0 = 0; t0 < tiles.size(); t0 += rlk::kMaxTilesPerLaunch) {
     const size_t n = std::min(tiles.size() - t0, static_cast<size_t>(rlk::kMaxTilesPerLaunch));
     std::copy(tiles.begin() + t0, tiles.begin() + t0 + n, fp->tiles);
     fp->num_tiles = static_cast<int32_t>(n);
     fp->num_items = static_cast<int32_t>(n);
     const int grid = std::min(fp->num_items, dev->num_sms);
-    cudaError_t e = launch_decode_kernel(*dp, cache, maps, grid, false, stream);
+    cudaError_t e = rlk::launch_decode(*fp, mq, mk, mv, grid, stream);
     if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
   }
   return ok();
@@ -804,8 +740,8 @@ rlk_status rlk_attn_decode_paged(const rlk_attn_params* params, const void* q, c
                                  const void* v_pool, int32_t n_pages, int32_t page_size,
                                  const int32_t* page_table, int32_t max_pages, const int32_t* seqlens,
                                  float* out_f32, void* out_bf16, float* lse, rlk_stream_t stream) {
-  const DecodeCache cache{k_pool, v_pool, nullptr, nullptr, n_pages, page_size, page_table, max_pages};
-  return decode_paged_impl(params, q, cache, seqlens, nullptr, 0, out_f32, out_bf16, lse, stream);
+  return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, nullptr, 0,
+                           out_f32, out_bf16, lse, stream);
 }
 
 rlk_status rlk_attn_decode_paged_rope(const rlk_attn_params* params, const void* q, const void* k_pool,
@@ -814,8 +750,8 @@ rlk_status rlk_attn_decode_paged_rope(const rlk_attn_params* params, const void*
                                       const float* rope_table, int32_t rope_max_pos, float* out_f32,
                                       void* out_bf16, float* lse, rlk_stream_t stream) {
   if (!rope_table) return fail(RLK_ERR_INVALID_ARGUMENT, "rope table is NULL");
-  const DecodeCache cache{k_pool, v_pool, nullptr, nullptr, n_pages, page_size, page_table, max_pages};
-  return decode_paged_impl(params, q, cache, seqlens, rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
+  return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens,
+                           rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
 }
 
 rlk_status rlk_attn_rope_table(double theta, int32_t max_pos, float* table) {
@@ -1022,14 +958,14 @@ int32_t rlk_attn_decode_auto_split(const rlk_attn_params* params, const int32_t*
 
 namespace {
 
-rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, const DecodeCache& cache,
+rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, const void* k_pool, const void* v_pool,
+                              int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                               const int32_t* seqlens, int32_t split_k, const float* rope_table,
                               int32_t rope_max_pos, float* out_f32, void* out_bf16, float* lse, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
   rlk_status st = check_params(params);
   if (st) return st;
-  if (!q || !cache.k_pool || !cache.v_pool || !cache.page_table || !seqlens)
-    return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
+  if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
   if (!out_f32 && !out_bf16) return fail(RLK_ERR_INVALID_ARGUMENT, "out_f32 and out_bf16 are both NULL");
   if (split_k < 0 || split_k > 64) return fail(RLK_ERR_INVALID_ARGUMENT, "split_k %d not in 0..64", split_k);
   if (params->num_seqs > rlk::kMaxSeqs)
@@ -1039,11 +975,12 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     return over_ranges(params->num_seqs, [&](int s0, int s1) {
       const rlk_attn_params rp = range_params(params, s0, s1);
       const int64_t o = static_cast<int64_t>(s0) * params->num_q_heads;
-      return decode_splitk_impl(&rp, adv(q, o * 128, 2), cache.from(s0), seqlens + s0, split_k, rope_table,
-                                rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4),
-                                workspace, workspace_bytes, stream);
+      return decode_splitk_impl(&rp, adv(q, o * 128, 2), k_pool, v_pool, n_pages, page_size,
+                                page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, split_k,
+                                rope_table, rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2),
+                                adv(lse, o, 4), workspace, workspace_bytes, stream);
     });
-  if (!aligned16(q) || !aligned16(cache.k_pool) || !aligned16(cache.v_pool) || (out_f32 && !aligned16(out_f32)) ||
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || (out_f32 && !aligned16(out_f32)) ||
       (out_bf16 && !aligned16(out_bf16)) || !aligned16(workspace))
     return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
   const int B = params->kv_block_size;
@@ -1051,7 +988,15 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
   if (B != 128 || group > rlk::kDecodeMaxGroup)
     return fail(RLK_ERR_UNSUPPORTED, "split decode needs kv_block_size 128 and at most %d query heads per KV head",
                 rlk::kDecodeMaxGroup);
-  if ((st = check_pages(params, cache, seqlens))) return st;
+  if (page_size < 8 || page_size > B || B % page_size)
+    return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
+  if (n_pages < 1 || max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
+  if (static_cast<int64_t>(n_pages + 1) * page_size >= (int64_t(1) << 31))
+    return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit token coordinates");
+  for (int s = 0; s < params->num_seqs; ++s)
+    if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(max_pages) * page_size)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: context length %d not in 1..max_pages*page_size", s,
+                  seqlens[s]);
   if (rope_table) {
     if (!aligned16(rope_table)) return fail(RLK_ERR_INVALID_ARGUMENT, "rope table must be 16-byte aligned");
     for (int s = 0; s < params->num_seqs; ++s)
@@ -1069,7 +1014,8 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     split_k = choose_split(seqlens, params->num_seqs, params->num_kv_heads, params->num_q_heads, B, dev->num_sms);
     // one range per sequence is the single-pass decode, which needs no state table
     if (split_k == 1)
-      return decode_paged_impl(params, q, cache, seqlens, rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
+      return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens,
+                               rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
   }
   // state table: pair (block_base[s] + b) * Hq + head; o_b FP32 [pair][128], then lse_b [pair]
   std::vector<int32_t> block_base(params->num_seqs + 1, 0);
@@ -1122,16 +1068,26 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
                      });
   };
   if (!on_chip) contiguous_items();
-  DecodeMaps maps;
-  if ((st = make_decode_maps(params, q, cache, &maps))) return st;
-  auto dp = decode_params(params, dev, q, cache, rope_table);
-  rlk::FwdParams* fp = &dp->f;
+  CUtensorMap mq, mk, mv;
+  // one query head per TMA box: the kernel places each head in its own operand row
+  if ((st = make_map(&mq, q, params->num_q_heads, params->num_seqs, 1, 1))) return st;
+  if ((st = make_map(&mk, k_pool, params->num_kv_heads, static_cast<uint64_t>(n_pages) * page_size, 1, page_size)))
+    return st;
+  if ((st = make_map(&mv, v_pool, params->num_kv_heads, static_cast<uint64_t>(n_pages) * page_size, 1, page_size)))
+    return st;
+  auto fp = std::make_unique<rlk::FwdParams>();
+  base_fwd(fp.get(), params, dev, rlk::kModeDecode);
   for (int s = 0; s < params->num_seqs; ++s) {
     fp->cu_k[s] = seqlens[s];
     fp->cu_q[s] = block_base[s];
   }
   fp->state_o = static_cast<float*>(workspace);
   fp->state_lse = static_cast<float*>(workspace) + pairs * rlk::kHeadDim;
+  fp->rope_table = rope_table;
+  fp->page_table = page_table;
+  fp->max_pages = max_pages;
+  fp->page_size = page_size;
+  fp->n_pages = n_pages;
   if (on_chip) {
     // the fold warps take a state as landed once it differs from the fill;
     // each item fills its own slots and publishes a flag, except inside a
@@ -1158,7 +1114,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     static_assert(rlk::kUnwritten == 0xFFFFFFFFu, "the table fill is all-ones bytes");
     cudaError_t e = self_fill ? cudaSuccess : cudaMemsetAsync(workspace, 0xFF, state_bytes, stream);
     const int grid = fp->num_items + fold_ctas(params->num_seqs, params->num_q_heads);
-    if (e == cudaSuccess) e = launch_decode_kernel(*dp, cache, maps, grid, true, stream);
+    if (e == cudaSuccess) e = rlk::launch_decode_cooperative(*fp, mq, mk, mv, grid, stream);
     if (e == cudaSuccess) return ok();
     if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported)
       return fail(RLK_ERR_CUDA, "split decode launch: %s", cudaGetErrorString(e));
@@ -1178,7 +1134,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     fp->num_tiles = static_cast<int32_t>(n);
     fp->num_items = static_cast<int32_t>(n);
     const int grid = std::min(fp->num_items, dev->num_sms);
-    cudaError_t e = launch_decode_kernel(*dp, cache, maps, grid, false, stream);
+    cudaError_t e = rlk::launch_decode(*fp, mq, mk, mv, grid, stream);
     if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "split decode launch: %s", cudaGetErrorString(e));
   }
   // fold: num_tiles carries the sequence count for the merge
@@ -1199,9 +1155,8 @@ rlk_status rlk_attn_decode_paged_splitk(const rlk_attn_params* params, const voi
                                         const int32_t* seqlens, int32_t split_k, float* out_f32,
                                         void* out_bf16, float* lse, void* workspace,
                                         size_t workspace_bytes, rlk_stream_t stream) {
-  const DecodeCache cache{k_pool, v_pool, nullptr, nullptr, n_pages, page_size, page_table, max_pages};
-  return decode_splitk_impl(params, q, cache, seqlens, split_k, nullptr, 0, out_f32, out_bf16, lse, workspace,
-                            workspace_bytes, stream);
+  return decode_splitk_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, split_k,
+                            nullptr, 0, out_f32, out_bf16, lse, workspace, workspace_bytes, stream);
 }
 
 rlk_status rlk_attn_decode_paged_splitk_rope(const rlk_attn_params* params, const void* q, const void* k_pool,
@@ -1211,9 +1166,8 @@ rlk_status rlk_attn_decode_paged_splitk_rope(const rlk_attn_params* params, cons
                                              int32_t rope_max_pos, float* out_f32, void* out_bf16, float* lse,
                                              void* workspace, size_t workspace_bytes, rlk_stream_t stream) {
   if (!rope_table) return fail(RLK_ERR_INVALID_ARGUMENT, "rope table is NULL");
-  const DecodeCache cache{k_pool, v_pool, nullptr, nullptr, n_pages, page_size, page_table, max_pages};
-  return decode_splitk_impl(params, q, cache, seqlens, split_k, rope_table, rope_max_pos, out_f32, out_bf16, lse,
-                            workspace, workspace_bytes, stream);
+  return decode_splitk_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, split_k,
+                            rope_table, rope_max_pos, out_f32, out_bf16, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
@@ -1234,7 +1188,25 @@ rlk_status guarded(Fn&& call) {
   }
 }
 
-rlk_status check_qcache(const rlk_attn_params* params, const DecodeCache& c) {
+// The 8-bit pages: codes [n_pages][hkv][page_size][128] and FP32 scales
+// [n_pages][hkv] of K and V.
+struct QCache {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  int32_t n_pages, page_size;
+  const int32_t* page_table;
+  int32_t max_pages;
+  // the cache seen from sequence s0 on
+  QCache from(int s0) const {
+    QCache c = *this;
+    c.page_table += static_cast<int64_t>(s0) * max_pages;
+    return c;
+  }
+};
+
+rlk_status check_qcache(const rlk_attn_params* params, const QCache& c) {
   if (!c.k_pool || !c.v_pool || !c.k_scale || !c.v_scale || !c.page_table)
     return fail(RLK_ERR_INVALID_ARGUMENT, "NULL cache argument");
   if (!aligned16(c.k_pool) || !aligned16(c.v_pool))
@@ -1242,7 +1214,9 @@ rlk_status check_qcache(const rlk_attn_params* params, const DecodeCache& c) {
   if ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale) |
        reinterpret_cast<uintptr_t>(c.page_table)) & 3u)
     return fail(RLK_ERR_INVALID_ARGUMENT, "scales and page table must be 4-byte aligned");
-  if (rlk_status st = check_page_size(params, c.page_size)) return st;
+  const int B = params->kv_block_size;
+  if (c.page_size < 8 || c.page_size > B || B % c.page_size)
+    return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", c.page_size, B);
   if (c.n_pages < 1 || c.max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
   return RLK_OK;
 }
@@ -1251,7 +1225,7 @@ rlk_status check_qcache(const rlk_attn_params* params, const DecodeCache& c) {
 // pos_offset[s] + 0 .. len - 1 of every sequence.
 rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const void* v_in, void* k_out, void* v_out,
                        const int32_t* cu_seqlens, const int32_t* pos_offset, const float* rope_table,
-                       int32_t rope_max_pos, const DecodeCache& cache, cudaStream_t stream) {
+                       int32_t rope_max_pos, const QCache& cache, cudaStream_t stream) {
   rlk_status st = check_params(params);
   if (st) return st;
   const bool write = k_in != nullptr;
@@ -1299,10 +1273,10 @@ rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const vo
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
   qp->err = dev->err;
-  qp->c.k = static_cast<uint8_t*>(const_cast<void*>(cache.k_pool));
-  qp->c.v = static_cast<uint8_t*>(const_cast<void*>(cache.v_pool));
-  qp->c.k_scale = const_cast<float*>(cache.k_scale);
-  qp->c.v_scale = const_cast<float*>(cache.v_scale);
+  qp->c.k = static_cast<uint8_t*>(cache.k_pool);
+  qp->c.v = static_cast<uint8_t*>(cache.v_pool);
+  qp->c.k_scale = cache.k_scale;
+  qp->c.v_scale = cache.v_scale;
   qp->c.page_table = cache.page_table;
   qp->c.n_pages = cache.n_pages;
   qp->c.page_size = ps;
@@ -1319,6 +1293,124 @@ rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const vo
   return ok();
 }
 
+// Decode workspace: the segment states (O then (m, l)) of every (sequence,
+// segment, query head), then one 8-byte count per (sequence, KV head).
+int64_t qdecode_segments(const int32_t* seqlens, int num_seqs) {
+  int64_t n = 0;
+  for (int s = 0; s < num_seqs; ++s)
+    n += (static_cast<int64_t>(seqlens[s]) + rlk::kQSegKeys - 1) / rlk::kQSegKeys;
+  return n;
+}
+size_t qdecode_state_bytes(int64_t segments, int hq) {
+  return static_cast<size_t>(segments) * hq * (rlk::kHeadDim + 2) * sizeof(float);
+}
+
+rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCache& cache, const int32_t* seqlens,
+                        int32_t split_k, const float* rope_table, int32_t rope_max_pos, float* out_f32,
+                        void* out_bf16, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  rlk_status st = check_params(params);
+  if (st) return st;
+  if (!q || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
+  if (!out_f32 && !out_bf16) return fail(RLK_ERR_INVALID_ARGUMENT, "out_f32 and out_bf16 are both NULL");
+  if (split_k < 0 || split_k > rlk::kMaxSplitK) return fail(RLK_ERR_INVALID_ARGUMENT, "split_k %d not in 0..64", split_k);
+  if (!aligned16(q) || !aligned16(out_f32) || !aligned16(out_bf16) || !aligned16(rope_table) ||
+      (split_k != 1 && !aligned16(workspace)))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+  if ((st = check_qcache(params, cache))) return st;
+  const int hq = params->num_q_heads, hkv = params->num_kv_heads, B = params->kv_block_size;
+  if (B != 128 || hq / hkv > rlk::kDecodeMaxGroup)
+    return fail(RLK_ERR_UNSUPPORTED, "8-bit decode needs kv_block_size 128 and at most %d query heads per KV head",
+                rlk::kDecodeMaxGroup);
+  if ((static_cast<int64_t>(cache.n_pages) + 1) * hkv > INT32_MAX)
+    return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit (page, head) coordinates");
+  if (params->num_seqs > rlk::kMaxSeqs)
+    // each range reuses the workspace from its start (the ranges run in order
+    // on the stream, and a range needs no more than the whole call)
+    return over_ranges(params->num_seqs, [&](int s0, int s1) {
+      const rlk_attn_params rp = range_params(params, s0, s1);
+      const int64_t o = static_cast<int64_t>(s0) * hq;
+      return qdecode_impl(&rp, adv(q, o * 128, 2), cache.from(s0), seqlens + s0, split_k, rope_table, rope_max_pos,
+                          adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4), workspace,
+                          workspace_bytes, stream);
+    });
+  rlk::QDecodeParams dp;
+  std::memset(&dp, 0, sizeof(dp));
+  int64_t blocks = 0, segments = 0, pair_segments = 0;
+  for (int s = 0; s < params->num_seqs; ++s) {
+    if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(cache.max_pages) * cache.page_size ||
+        seqlens[s] > INT32_MAX - 1024)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: context length %d not in 1..max_pages*page_size", s,
+                  seqlens[s]);
+    if (rope_table && seqlens[s] > rope_max_pos)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: position %d is past the RoPE table (%d positions)", s,
+                  seqlens[s] - 1, rope_max_pos);
+    dp.ctx[s] = seqlens[s];
+    blocks += (static_cast<int64_t>(seqlens[s]) + B - 1) / B * hkv;
+    segments += qdecode_segments(seqlens + s, 1);
+    if (blocks > INT32_MAX - 1024 || segments * hq > INT32_MAX)
+      return fail(RLK_ERR_UNSUPPORTED, "more than 2^31 (block, KV head) or (segment, query head) pairs in one launch");
+    dp.blk0[s + 1] = static_cast<int32_t>(blocks);
+    dp.seg0[s + 1] = static_cast<int32_t>(segments);
+  }
+  pair_segments = segments * hkv;
+  const int64_t items = static_cast<int64_t>(params->num_seqs) * hkv * std::max(split_k, 1);
+  if (items > INT32_MAX - 1024) return fail(RLK_ERR_UNSUPPORTED, "more than 2^31 work items in one launch");
+  const size_t state_bytes = qdecode_state_bytes(segments, hq);
+  const size_t count_bytes = static_cast<size_t>(params->num_seqs) * hkv * sizeof(uint64_t);
+  if (split_k != 1 && (!workspace || workspace_bytes < state_bytes + count_bytes))
+    return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes,
+                state_bytes + count_bytes);
+  if (g_dry_run) return ok();
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev))) return st;
+  CUtensorMap mk, mv;
+  if ((st = make_code_map(&mk, cache.k_pool, cache.n_pages, hkv, cache.page_size))) return st;
+  if ((st = make_code_map(&mv, cache.v_pool, cache.n_pages, hkv, cache.page_size))) return st;
+  const int grid = static_cast<int>(std::min<int64_t>(dev->num_sms, split_k == 0 ? pair_segments : items));
+  dp.err = dev->err;
+  dp.num_seqs = params->num_seqs;
+  dp.hq = hq;
+  dp.hkv = hkv;
+  dp.group = hq / hkv;
+  dp.scale_log2 = scale_log2(params);
+  dp.q = static_cast<const uint16_t*>(q);
+  dp.k_scale = cache.k_scale;
+  dp.v_scale = cache.v_scale;
+  dp.page_table = cache.page_table;
+  dp.n_pages = cache.n_pages;
+  dp.page_size = cache.page_size;
+  dp.max_pages = cache.max_pages;
+  dp.split_k = split_k;
+  dp.part_q = static_cast<int32_t>(blocks / grid);
+  dp.part_r = static_cast<int32_t>(blocks % grid);
+  dp.rope_table = rope_table;
+  dp.out_f32 = out_f32;
+  dp.out_bf16 = static_cast<uint16_t*>(out_bf16);
+  dp.lse = lse;
+  if (split_k != 1) {
+    dp.state_o = static_cast<float*>(workspace);
+    dp.state_ml = dp.state_o + segments * hq * rlk::kHeadDim;
+    dp.counts = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + state_bytes);
+    // the counts' nonce, new to every call, stands for their being zero;
+    // inside a graph capture, where replays repeat it (and other graphs may
+    // use the workspace in between), a fill precedes the launch
+    dp.nonce = next_fill_nonce() >> 24;
+    if (dp.nonce == 0) dp.nonce = 1;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+      (void)cudaGetLastError();
+      cap = cudaStreamCaptureStatusActive;  // unknown: take the form that is safe in both
+    }
+    if (cap != cudaStreamCaptureStatusNone) {
+      cudaError_t e = cudaMemsetAsync(dp.counts, 0, count_bytes, stream);
+      if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "8-bit decode count fill: %s", cudaGetErrorString(e));
+    }
+  }
+  cudaError_t e = rlk::launch_qdecode(dp, mk, mv, grid, stream);
+  if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "8-bit decode launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -1330,7 +1422,7 @@ rlk_status rlk_attn_qcache_write(const rlk_attn_params* params, const void* k, c
                                  rlk_stream_t stream) {
   return guarded([&]() -> rlk_status {
     if (!k || !v) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
-    const DecodeCache cache{k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages};
+    const QCache cache{k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages};
     return qcache_impl(params, k, v, nullptr, nullptr, cu_seqlens, pos_offset, rope_table, rope_max_pos, cache,
                        stream);
   });
@@ -1342,7 +1434,8 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
                                 const int32_t* pos_offset, void* k, void* v, rlk_stream_t stream) {
   return guarded([&]() -> rlk_status {
     if (!k || !v) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
-    const DecodeCache cache{k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages};
+    const QCache cache{const_cast<void*>(k_pool), const_cast<void*>(v_pool), const_cast<float*>(k_scale),
+                       const_cast<float*>(v_scale), n_pages, page_size, page_table, max_pages};
     return qcache_impl(params, nullptr, nullptr, k, v, cu_seqlens, pos_offset, nullptr, 0, cache, stream);
   });
 }
@@ -1354,18 +1447,10 @@ rlk_status rlk_attn_decode_qcache(const rlk_attn_params* params, const void* q, 
                                   int32_t rope_max_pos, float* out_f32, void* out_bf16, float* lse, void* workspace,
                                   size_t workspace_bytes, rlk_stream_t stream) {
   return guarded([&]() -> rlk_status {
-    rlk_status st = check_params(params);
-    if (st) return st;
-    const DecodeCache cache{k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages};
-    if (!q || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
-    if ((st = check_qcache(params, cache))) return st;
-    if (params->kv_block_size != 128 || params->num_q_heads / params->num_kv_heads > rlk::kDecodeMaxGroup)
-      return fail(RLK_ERR_UNSUPPORTED, "8-bit decode needs kv_block_size 128 and at most %d query heads per KV head",
-                  rlk::kDecodeMaxGroup);
-    if (split_k == 1)
-      return decode_paged_impl(params, q, cache, seqlens, rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
-    return decode_splitk_impl(params, q, cache, seqlens, split_k, rope_table, rope_max_pos, out_f32, out_bf16, lse,
-                              workspace, workspace_bytes, stream);
+    const QCache cache{const_cast<void*>(k_pool), const_cast<void*>(v_pool), const_cast<float*>(k_scale),
+                       const_cast<float*>(v_scale), n_pages, page_size, page_table, max_pages};
+    return qdecode_impl(params, q, cache, seqlens, split_k, rope_table, rope_max_pos, out_f32, out_bf16, lse,
+                        workspace, workspace_bytes, stream);
   });
 }
 
@@ -1381,6 +1466,13 @@ size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op, const 
     }
     const int64_t pairs = blocks * params->num_q_heads;
     return split_table_bytes(pairs) + split_flag_bytes(params->num_seqs, params->num_kv_heads);
+  }
+  if (op == RLK_OP_DECODE_QCACHE) {
+    if (!cu_seqlens_k) return 0;
+    for (int s = 0; s < params->num_seqs; ++s)
+      if (cu_seqlens_k[s] < 1) return 0;
+    return qdecode_state_bytes(qdecode_segments(cu_seqlens_k, params->num_seqs), params->num_q_heads) +
+           static_cast<size_t>(params->num_seqs) * params->num_kv_heads * sizeof(uint64_t);
   }
   if (op == RLK_OP_MERGE) {
     if (check_cu(params, cu_seqlens_q, cu_seqlens_k) != RLK_OK) return 0;

@@ -1,6 +1,8 @@
 // qcache_internal.h -- launch parameter blocks of the 8-bit paged KV cache
 // (write, read, decode).  Not part of the public interface.
 #pragma once
+#include <cuda.h>
+
 #include "rlk_internal.h"
 
 namespace rlk {
@@ -34,14 +36,37 @@ struct QCacheParams {
 cudaError_t launch_qcache_write(const QCacheParams& p, cudaStream_t stream);
 cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
 
-// Decode over the 8-bit pages: the BF16 decode's parameters (items, contexts,
-// outputs, state table), the query rows and the pages' scales.
+// Decode over the 8-bit pages.  The keys of a sequence are cut into segments
+// of kQSegKeys, whatever CTAs take them (qdecode.cu).
+constexpr int kQSegKeys = 512;
 struct QDecodeParams {
-  FwdParams f;
+  ErrWord* err;
+  int32_t num_seqs, hq, hkv, group;
+  float scale_log2;
   const uint16_t* q;  // [num_seqs, hq, 128] BF16
   const float* k_scale;
   const float* v_scale;
+  const int32_t* page_table;
+  int32_t n_pages, page_size, max_pages;
+  int32_t split_k;          // items per (sequence, KV head), or 0: the blocks cut evenly over the grid
+  const float* rope_table;  // rotates the query at ctx - 1, or null
+  float* out_f32;
+  uint16_t* out_bf16;
+  float* lse;
+  // segment states of the pairs several CTAs share: row (seg0[s] + segment) *
+  // hq + head of state_o [.., 128] and state_ml [.., 2] (m in log2, l), and
+  // one count of finished segments per (sequence, KV head)
+  float* state_o;
+  float* state_ml;
+  unsigned long long* counts;
+  uint64_t nonce;              // 40 bits, new to every call
+  int32_t ctx[kMaxSeqs];
+  int32_t seg0[kMaxSeqs + 1];  // prefix sums of the sequences' segments
+  int32_t blk0[kMaxSeqs + 1];  // prefix sums of the sequences' blocks x hkv
+  int32_t part_q, part_r;      // split_k 0: blocks / grid and the rest
 };
 cudaError_t configure_qdecode_kernels();
+cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                           cudaStream_t stream);
 
 }  // namespace rlk

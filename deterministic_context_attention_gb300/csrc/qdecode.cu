@@ -1,8 +1,7 @@
 // qdecode.cu -- paged decode over the 8-bit KV cache for sm_103a.
 //
-// The transposed decode of the BF16 pools (keys, then head dimensions, on the
-// MMA's M side; block states of 128 keys folded in ascending order) with the
-// pages' E4M3 codes as they are: TMA brings them to shared memory and
+// A transposed decode (keys, then head dimensions, on the MMA's M side) over
+// the pages' E4M3 codes as they are: TMA brings them to shared memory and
 // tcgen05.mma kind::f8f6f4 reads them there, so no code is ever converted.
 // The other operand is split into E4M3 pieces, each 2^5 below the one before
 // (a rounding to 4 bits of a value in [2^E, 2^(E+1)) leaves at most 2^(E-4),
@@ -15,35 +14,44 @@
 // maximum.  w_c = p_c sv_c / A, with sv_c the V scale of key c's page and A
 // the block's largest of them (as a power of two): four pieces leave at most
 // 2^-19 of w_c.  The K scale multiplies the FP32 score of its key,
-//   s_c = (q . code_c) sk_c,
-// and from there every step is the one numerics.cuh defines: the block
-// maximum, p = 2^fma(s, scale_log2, -m scale_log2), the canonical row sum
-// (of the unsplit FP32 p), o_b = PV / l, the fold in ascending block order.
-// A result depends on the cached codes, scales and the query alone, not on
-// the batch, the order of the pages or the split.
+//   x_c = (q . code_c) sk_c scale log2(e).
+//
+// Softmax, all in FP32.  A block b of 128 keys gives m_b = max x, p = 2^(x -
+// m_b), l_b = sum p and O_b = sum p v.  Blocks are folded left to right into
+// the segment (kSegBlocks blocks, a fixed cut of the sequence) they lie in,
+// and segments left to right into the sequence, both by
+//   M = max(m, m'),  O = O' 2^(m' - M) + O 2^(m - M),  l likewise,
+// so the arithmetic is the same whichever CTAs take which segments: a result
+// depends on the cached codes, scales and the query alone, not on the batch,
+// the order of the pages or the split.  (Two levels, because the fold is a
+// chain: one over every block of a 32768-token sequence, on states written
+// out per block, took 125 us for 4 sequences where the pages take 40.)
+//
+// Work split.  The blocks of all (sequence, KV head) pairs in order form one
+// line; CTA c of g takes its c-th g-th part, cut at segment boundaries, so the
+// SMs' loads differ by a segment at the most and no plan is built on the host.
+// A CTA that holds a whole pair writes its output; otherwise each segment's
+// state goes to the workspace and the CTA that adds the last segment of a pair
+// (an atomic count; which one it is changes nothing in the result) folds them.
 //
 // What bounds it: HBM, 32 KB of codes per (KV head, 128-key block) and 4 heads
 // of 4 x 128 x 128 flops against them.  Per block the tensor core issues 4 + 4
 // MMAs (K = 32 codes each; the BF16 decode needs 8 + 16), and the 8 warps of
 // the softmax run two blocks at a time.
 //
-// Warp roles (544 threads):
+// Warp roles (512 threads):
 //   warps 0-3   correction / epilogue: thread d owns head dimension d
 //   warps 4-7   softmax of the even blocks, warps 8-11 of the odd ones:
 //               thread t owns key t of the block and fetches its page's scales
 //   warp  12    TMA producer of the K pages, warp 13 of the V pages
-//   warp  14    TMEM allocator and issuer of the S^T products
-//   warp  15    issuer of the O^T products
-//   warp  16    the query rows: loads them (rotating them first where asked),
-//               splits them and keeps one item ahead
-// Split decode writes block states to the state table; with the fold on chip
-// the CTAs past the items fold them as they land (decode_common.cuh).
+//   warp  14    the query rows (loads them, rotates them where asked, splits
+//               them) and the S^T products; up to 4 blocks ahead of the softmax
+//   warp  15    the O^T products
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "decode_common.cuh"
 #include "numerics.cuh"
 #include "ptx.cuh"
 #include "qcache_internal.h"
@@ -51,13 +59,15 @@
 namespace rlk {
 namespace {
 
-constexpr int kQDThreads = 544;
+constexpr int kQDThreads = 512;
 constexpr int kQPieces = 3, kPPieces = 4;
+constexpr int kSegBlocks = kQSegKeys / 128;
+constexpr float kLUnit = 0x1p26f;  // block sums of p: fixed point, 26 fraction bits
 
 // N: MMA columns, the pieces of up to MG query heads, at column piece * MG + head
 template <int MG>
 struct QDecLayout {
-  static constexpr int B = kDecBlock;
+  static constexpr int B = 128;           // keys per block
   static constexpr int N = MG <= 4 ? 16 : 32;
   static_assert(kPPieces * MG <= N && kQPieces * MG <= N, "the pieces fit the MMA's columns");
   static constexpr int kSK = 6, kSV = 5;  // K and V rings
@@ -72,21 +82,21 @@ struct QDecLayout {
   static constexpr int kKOff = (kPOff + kPS * kTBytes + 1023) / 1024 * 1024;
   static constexpr int kVOff = kKOff + kSK * kKVBytes;
   // per softmax group, double-buffered by block: maxima of 4 warps (MG heads
-  // and the V scale) and the probabilities for the row sums
+  // and the V scale)
   static constexpr int kRedBytes = 2 * 4 * (MG + 1) * 4;
-  static constexpr int kPartBytes = 2 * 4 * MG * 32 * 4;
-  static constexpr int kPartOff = kVOff + kSV * kKVBytes;
-  static constexpr int kRedOff = kPartOff + 2 * kPartBytes;
-  static constexpr int kStatsOff = (kRedOff + 2 * kRedBytes + 7) / 8 * 8;  // float2 [kSR][MG]
-  static constexpr int kQsOff = kStatsOff + kSR * MG * 8;                  // float [kQS][MG]
+  static constexpr int kRedOff = kVOff + kSV * kKVBytes;
+  // per block: float m[MG], then the V factor, then uint32 l[4 warps][MG]
+  static constexpr int kStatWords = MG + 1 + 4 * MG;
+  static constexpr int kStatsOff = kRedOff + 2 * kRedBytes;
+  static constexpr int kQsOff = kStatsOff + kSR * kStatWords * 4;  // float [kQS][MG]
   static constexpr int kBarOff = (kQsOff + kQS * MG * 4 + 7) / 8 * 8;
   static constexpr int kQFull = 0, kQEmpty = kQFull + kQS, kKFull = kQEmpty + kQS, kKEmpty = kKFull + kSK,
                        kVFull = kKEmpty + kSK, kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV,
                        kSEmpty = kSFull + kSS, kPFull = kSEmpty + kSS, kPEmpty = kPFull + kPS,
                        kOFull = kPEmpty + kPS, kOEmpty = kOFull + kOS, kStatsFull = kOEmpty + kOS,
-                       kSyncMax = kStatsFull + kSR, kSyncPart = kSyncMax + 4, kFillDone = kSyncPart + 4,
-                       kNumBars = kFillDone + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort (i32)
+                       kSyncMax = kStatsFull + kSR, kStored = kSyncMax + 4, kCounted = kStored + 1,
+                       kNumBars = kCounted + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort (i32), last (i32)
   static constexpr int kPageWin = 512;                     // page ids cached per window (one per producer)
   static constexpr int kPageOff = (kMiscOff + 16 + 15) / 16 * 16;
   static constexpr int kTotal = kPageOff + 2 * kPageWin * 4;
@@ -166,21 +176,190 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-template <int MG, bool FOLD>
+// Row maximum of the 32 lanes of a warp (exact; every lane receives it).
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// The same, NaN where any lane holds one, and the maximum of two like it: a NaN
+// score makes its row's maximum, and from there the whole row, NaN.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float m;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// A piece of work: segments [s0, s1) of the ns of (sequence, KV head g).
+struct QPiece {
+  int seq, g, kv_len, nb, s0, s1, ns;
+  __device__ int block0() const { return s0 * kSegBlocks; }
+  __device__ int block1() const { return min(s1 * kSegBlocks, nb); }
+  __device__ bool whole() const { return s0 == 0 && s1 == ns; }
+};
+
+// The pieces of this CTA, in order; every role walks them on its own.
+struct QWalk {
+  int at, end;  // balanced: blocks of the line [at, end); otherwise items at, at + grid, ...
+  __device__ explicit QWalk(const QDecodeParams& p) {
+    if (p.split_k == 0) {
+      at = cut(p, blockIdx.x);
+      end = cut(p, blockIdx.x + 1);
+    } else {
+      at = blockIdx.x;
+      end = p.num_seqs * p.hkv * p.split_k;
+    }
+  }
+  static __device__ int seq_of(const QDecodeParams& p, int x) {
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.blk0[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+  // the c-th part's start: part_q blocks a part and one more for the first
+  // part_r, from there on to the next segment
+  static __device__ int cut(const QDecodeParams& p, int c) {
+    const int x = c * p.part_q + min(c, p.part_r);
+    if (x >= p.blk0[p.num_seqs]) return p.blk0[p.num_seqs];
+    const int s = seq_of(p, x);
+    const int nb = (p.ctx[s] + 127) / 128;
+    const int b = (x - p.blk0[s]) % nb;
+    return x - b + min((b + kSegBlocks - 1) / kSegBlocks * kSegBlocks, nb);
+  }
+  __device__ bool next(const QDecodeParams& p, QPiece* q) {
+    if (p.split_k == 0) {
+      if (at >= end) return false;
+      q->seq = seq_of(p, at);
+      set(p, q);
+      const int r = at - p.blk0[q->seq];
+      q->g = r / q->nb;
+      const int b = r - q->g * q->nb;
+      const int stop = min(end - at, q->nb - b);
+      q->s0 = b / kSegBlocks;
+      q->s1 = (b + stop + kSegBlocks - 1) / kSegBlocks;
+      at += stop;
+      return true;
+    }
+    while (at < end) {
+      const int pair = at / p.split_k, r = at - pair * p.split_k;
+      q->seq = pair / p.hkv;
+      q->g = pair - q->seq * p.hkv;
+      set(p, q);
+      q->s0 = static_cast<int>(static_cast<int64_t>(r) * q->ns / p.split_k);
+      q->s1 = static_cast<int>(static_cast<int64_t>(r + 1) * q->ns / p.split_k);
+      at += gridDim.x;
+      if (q->s1 > q->s0) return true;
+    }
+    return false;
+  }
+  static __device__ void set(const QDecodeParams& p, QPiece* q) {
+    q->kv_len = p.ctx[q->seq];
+    q->nb = (q->kv_len + 127) / 128;
+    q->ns = (q->nb + kSegBlocks - 1) / kSegBlocks;
+  }
+};
+
+// (O, m, l) folded with a later state: the factors of the two, and m.
+__device__ __forceinline__ void fold_factors(float m, float mb, float& mn, float& a, float& b) {
+  mn = fmaxf(m, mb);
+  a = ex2_hw(__fsub_rn(m, mn));
+  b = ex2_hw(__fsub_rn(mb, mn));
+}
+
+// Counts n finished segments of a pair; true for the call that brings the
+// count to ns.  A word holds the call's nonce (40 bits) over the count (24);
+// another nonce means no segment of this call has been counted yet.  The last
+// one clears the word, so a replayed launch starts over.
+__device__ __forceinline__ bool count_segments(unsigned long long* word, uint64_t nonce, int n, int ns) {
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  for (;;) {
+    const uint64_t have = (old >> 24) == nonce ? (old & 0xFFFFFFu) : 0u;
+    const bool last = have + n == static_cast<uint64_t>(ns);
+    const unsigned long long seen = atomicCAS(word, old, last ? 0ull : (nonce << 24) | (have + n));
+    if (seen == old) return last;
+    old = seen;
+  }
+}
+
+// The fold of a cut pair's segment states, one warp a query head: lane l
+// takes head dimensions 4 l .. 4 l + 3; chunks of C segments, the next chunk's
+// reads in flight while one folds.
+__device__ __noinline__ void fold_pair(const QDecodeParams& p, const QPiece& pc, int h, int lane) {
+  constexpr int C = 8;
+  const int64_t base = static_cast<int64_t>(p.seg0[pc.seq]) * p.hq + h;
+  auto load = [&](int c0, float2& ml, float4 (&v)[C]) {
+    const int64_t r = base + static_cast<int64_t>(min(c0 + (lane & (C - 1)), pc.ns - 1)) * p.hq;
+    ml = __ldcg(reinterpret_cast<const float2*>(p.state_ml) + r);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      v[i] = __ldcg(reinterpret_cast<const float4*>(
+                        p.state_o + (base + static_cast<int64_t>(min(c0 + i, pc.ns - 1)) * p.hq) * kHeadDim) +
+                    lane);
+  };
+  float4 v[C], vn[C];
+  float2 ml, mln = make_float2(0.f, 0.f);
+  load(0, ml, v);
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = 0.f, l = 0.f;
+  for (int c0 = 0; c0 < pc.ns; c0 += C) {
+    if (c0 + C < pc.ns) load(c0 + C, mln, vn);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const float mb = __shfl_sync(0xffffffffu, ml.x, i), lb = __shfl_sync(0xffffffffu, ml.y, i);
+      if (c0 + i >= pc.ns) continue;
+      if (c0 + i == 0) {
+        O = v[0];
+        m = mb;
+        l = lb;
+      } else {
+        float mn, a, b;
+        fold_factors(m, mb, mn, a, b);
+        O.x = __fmaf_rn(v[i].x, b, __fmul_rn(O.x, a));
+        O.y = __fmaf_rn(v[i].y, b, __fmul_rn(O.y, a));
+        O.z = __fmaf_rn(v[i].z, b, __fmul_rn(O.z, a));
+        O.w = __fmaf_rn(v[i].w, b, __fmul_rn(O.w, a));
+        l = __fmaf_rn(lb, b, __fmul_rn(l, a));
+        m = mn;
+      }
+    }
+    ml = mln;
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = vn[i];
+  }
+  const float r = __frcp_rn(l);
+  O = make_float4(__fmul_rn(O.x, r), __fmul_rn(O.y, r), __fmul_rn(O.z, r), __fmul_rn(O.w, r));
+  const int64_t row = static_cast<int64_t>(pc.seq) * p.hq + h;
+  if (p.out_f32) *(reinterpret_cast<float4*>(p.out_f32 + row * kHeadDim) + lane) = O;
+  if (p.out_bf16)
+    *(reinterpret_cast<uint2*>(p.out_bf16 + row * kHeadDim) + lane) =
+        make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
+  if (p.lse && lane == 0) p.lse[row] = __fmaf_rn(m, kLn2f, logf(l));
+}
+
+template <int MG>
 __global__ void __launch_bounds__(kQDThreads, 1)
-    rlk_qdecode_kernel(const __grid_constant__ QDecodeParams qp, const __grid_constant__ CUtensorMap tm_k,
+    rlk_qdecode_kernel(const __grid_constant__ QDecodeParams p, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v) {
   using L = QDecLayout<MG>;
   constexpr int B = L::B, N = L::N, SK = L::kSK, SV = L::kSV, PS = L::kPS, QS = L::kQS, SS = L::kSS, OS = L::kOS,
                 SR = L::kSR;
   static_assert(MG <= kDecodeMaxGroup && PS == 2 && QS == 2, "decode layout");
-  const FwdParams& p = qp.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  float2* stats = reinterpret_cast<float2*>(smem + L::kStatsOff);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
+  uint32_t* stats = reinterpret_cast<uint32_t*>(smem + L::kStatsOff);
   float* qscale = reinterpret_cast<float*>(smem + L::kQsOff);
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -217,11 +396,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       mbar_init(&bars[L::kOEmpty + s], 4);
     }
     for (int s = 0; s < SR; ++s) mbar_init(&bars[L::kStatsFull + s], 4);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&bars[L::kSyncMax + s], 4);
-      mbar_init(&bars[L::kSyncPart + s], 4);
-    }
-    mbar_init(&bars[L::kFillDone], kFillThreads);
+    for (int s = 0; s < 4; ++s) mbar_init(&bars[L::kSyncMax + s], 4);
+    mbar_init(&bars[L::kStored], 4);
+    mbar_init(&bars[L::kCounted], 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -239,15 +416,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
   uint8_t* k_base = smem + L::kKOff;
   uint8_t* v_base = smem + L::kVOff;
 
-  if (FOLD && static_cast<int>(blockIdx.x) >= p.num_items) {
-    // ------------------------------------------------------------ fold CTA
-    const int chain = (static_cast<int>(blockIdx.x) - p.num_items) * 16 + warp;
-    const int per_seq = p.hkv * G;
-    if (warp < 16 && p.split_stride > 0 && chain < p.fold_seqs * per_seq) {
-      const int seq = chain / per_seq, g = (chain % per_seq) / G, q = chain % G;
-      fold_chain_on_chip(p, seq, g, q, lane, abort);
-    }
-  } else if (warp == 12 || warp == 13) {
+  QWalk walk(p);
+  QPiece pc;
+  if (warp == 12 || warp == 13) {
     // ------------------------------------------------------------ producers
     const bool is_v = warp == 13;
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
@@ -260,33 +431,26 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const int ps = p.page_size;
     const int lg = 31 - __clz(B / ps);  // log2 of the pages per block
     uint32_t stage = 0, par = 1;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = dec_snake_item(round);
-      if (item >= p.num_items) continue;
-      const DecItem di = dec_item(p, item);
-      const int seq = di.seq, g = di.g, kv_len = di.kv_len, nb = di.nb;
-      const int seq_pages = (kv_len + ps - 1) / ps;
-      const int32_t* prow = p.page_table + static_cast<int64_t>(seq) * p.max_pages;
+    while (walk.next(p, &pc)) {
+      const int seq_pages = (pc.kv_len + ps - 1) / ps;
+      const int32_t* prow = p.page_table + static_cast<int64_t>(pc.seq) * p.max_pages;
       int cached = -1;  // a new sequence's page ids
       bool fail = false;
-      for (int j = 0; j < nb; ++j) {
-        const int b = di.b0 + j * di.stride;  // global block
+      for (int b = pc.block0(); b < pc.block1(); ++b) {
         bool ok = mbar_wait(empty_b + stage, par, abort, p.err, is_v ? 0xb03 : 0xb02);
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
         uint8_t* dst = ring + stage * L::kKVBytes;
-        const int n_tok = min(B, kv_len - b * B);
+        const int n_tok = min(B, pc.kv_len - b * B);
         const int n_pg = (n_tok + ps - 1) / ps;
-        // the window holds the pages of 2^(9 - lg) consecutive blocks of the
-        // item, all 16 loads of a lane in flight before the first store
-        const int win = j >> (9 - lg);
+        // the window holds the pages of 2^(9 - lg) consecutive blocks, all 16
+        // loads of a lane in flight before the first store
+        const int win = b >> (9 - lg);
         if (cached != win) {
           int32_t pg[L::kPageWin / 32];
 #pragma unroll
           for (int t = 0; t < L::kPageWin / 32; ++t) {
-            const int i = lane + 32 * t;
-            const int jj = (win << (9 - lg)) + (i >> lg);  // block of the item
-            const int gp = ((di.b0 + jj * di.stride) << lg) + (i & ((1 << lg) - 1));
-            pg[t] = (jj < nb && gp < seq_pages) ? __ldg(prow + gp) : -1;
+            const int gp = (win << 9) + lane + 32 * t;
+            pg[t] = (gp < seq_pages && (gp >> lg) < pc.block1()) ? __ldg(prow + gp) : -1;
           }
           __syncwarp();
 #pragma unroll
@@ -297,12 +461,12 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(full_b + stage, n_pg * ps * 128);
         __syncwarp();
         if (lane < n_pg) {
-          int32_t pe = wc[((j & ((1 << (9 - lg)) - 1)) << lg) + lane];
+          int32_t pe = wc[((b << lg) & (L::kPageWin - 1)) + lane];
           if (pe < 0 || pe >= p.n_pages) {
             report_error(p.err, kErrBadPage, 0xb04);
             pe = p.n_pages;  // out of range: the copy reads the zero fill
           }
-          tma_load_3d(dst + lane * ps * 128, map, full_b + stage, 0, 0, pe * p.hkv + g);
+          tma_load_3d(dst + lane * ps * 128, map, full_b + stage, 0, 0, pe * p.hkv + pc.g);
         }
         if (++stage == static_cast<uint32_t>(S)) {
           stage = 0;
@@ -312,100 +476,12 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       if (fail || *abort) break;
     }
   } else if (warp == 14) {
-    // ------------------------------------------------------------ S issuer
+    // ------------------------------------------------------------ queries, S issuer
     constexpr uint32_t kIdS = idesc_e4m3(128, N, false);  // A = K (K-major), B = Q pieces (K-major)
     const uint32_t leader = elect_one_sync();
     uint32_t stage = 0, kpar = 0, s_it = 0, q_it = 0;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = dec_snake_item(round);
-      if (item >= p.num_items) continue;
-      const DecItem di = dec_item(p, item);
-      const uint32_t qslot = q_it & 1;
-      bool ok = mbar_wait(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb11);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      ++q_it;
-      const Desc qd = make_desc(smem_u32(q_base + qslot * L::kTBytes), 16, 1024);
-      bool fail = false;
-      for (int j = 0; j < di.nb; ++j, ++s_it) {
-        const uint32_t slot = s_it % SS;
-        bool w = mbar_wait(&bars[L::kKFull + stage], kpar, abort, p.err, 0xb12);
-        w = w && mbar_wait(&bars[L::kSEmpty + slot], ((s_it / SS) & 1) ^ 1, abort, p.err, 0xb13);
-        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
-        tc_fence_after();
-        const Desc kd = make_desc(smem_u32(k_base + stage * L::kKVBytes), 16, 1024);
-        const uint32_t d = tm_s + slot * N;
-        if (leader) {
-          mma8_ss<0>(d, kd, 0, qd, 0, kIdS);
-#pragma unroll
-          for (int s = 1; s < kHeadDim / 32; ++s) mma8_ss<1>(d, kd, s * 2, qd, s * 2, kIdS);
-          umma_commit(&bars[L::kSFull + slot]);
-          umma_commit(&bars[L::kKEmpty + stage]);
-          if (j + 1 == di.nb) umma_commit(&bars[L::kQEmpty + qslot]);
-        }
-        __syncwarp();
-        if (++stage == SK) {
-          stage = 0;
-          kpar ^= 1;
-        }
-      }
-      if (fail) break;
-    }
-  } else if (warp == 15) {
-    // ------------------------------------------------------------ PV issuer
-    constexpr uint32_t kIdO = idesc_e4m3(128, N, true);  // A = V^T (dims contiguous), B = P^T pieces
-    const uint32_t leader = elect_one_sync();
-    uint32_t stage = 0, vpar = 0, o_it = 0;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = dec_snake_item(round);
-      if (item >= p.num_items) continue;
-      const DecItem di = dec_item(p, item);
-      bool fail = false;
-      for (int j = 0; j < di.nb; ++j, ++o_it) {
-        const uint32_t oslot = o_it % OS, pslot = o_it % PS;
-        bool w = mbar_wait(&bars[L::kVFull + stage], vpar, abort, p.err, 0xb22);
-        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
-        uint8_t* vd = v_base + stage * L::kKVBytes;
-        // V rows past the context may hold anything, NaN codes among it; P is
-        // exactly 0 there, so zero them (0 * NaN = NaN)
-        const int valid = min(B, di.kv_len - (di.b0 + j * di.stride) * B);
-        if (valid < B) {
-          for (int i = lane; i < (B - valid) * 8; i += 32)
-            *reinterpret_cast<uint4*>(vd + valid * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        w = mbar_wait(&bars[L::kPFull + pslot], (o_it / PS) & 1, abort, p.err, 0xb21);
-        w = w && mbar_wait(&bars[L::kOEmpty + oslot], ((o_it / OS) & 1) ^ 1, abort, p.err, 0xb23);
-        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
-        tc_fence_after();
-        // K-step s covers keys 32 s .. 32 s + 31: V rows 4096 B a step, P^T
-        // columns 32 B a step
-        const Desc vdd = make_desc(smem_u32(vd), 16, 1024);
-        const Desc pd = make_desc(smem_u32(p_base + pslot * L::kTBytes), 16, 1024);
-        const uint32_t d = tm_o + oslot * N;
-        if (leader) {
-          mma8_ss<0>(d, vdd, 0, pd, 0, kIdO);
-#pragma unroll
-          for (int s = 1; s < B / 32; ++s) mma8_ss<1>(d, vdd, s * 256, pd, s * 2, kIdO);
-          umma_commit(&bars[L::kOFull + oslot]);
-          umma_commit(&bars[L::kVEmpty + stage]);
-          umma_commit(&bars[L::kPEmpty + pslot]);
-        }
-        __syncwarp();
-        if (++stage == SV) {
-          stage = 0;
-          vpar ^= 1;
-        }
-      }
-      if (fail) break;
-    }
-  } else if (warp == 16) {
-    // ------------------------------------------------------------ query rows
-    uint32_t q_it = 0;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = dec_snake_item(round);
-      if (item >= p.num_items) continue;
-      const DecItem di = dec_item(p, item);
+    while (walk.next(p, &pc)) {
+      // ---- the query rows
       const uint32_t qslot = q_it & 1;
       // lane l holds elements 4 l .. 4 l + 3 of every row
       uint2 x[MG];
@@ -413,14 +489,14 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       for (int i = 0; i < MG; ++i)
         if (i < G)
           x[i] = __ldg(reinterpret_cast<const uint2*>(
-                           qp.q + (static_cast<int64_t>(di.seq) * p.hq + di.g * G + i) * kHeadDim) + lane);
+                           p.q + (static_cast<int64_t>(pc.seq) * p.hq + pc.g * G + i) * kHeadDim) + lane);
       float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
       if (p.rope_table) {
-        const float* trow = p.rope_table + static_cast<int64_t>(di.kv_len - 1) * kHeadDim;
+        const float* trow = p.rope_table + static_cast<int64_t>(pc.kv_len - 1) * kHeadDim;
         c = __ldg(reinterpret_cast<const float4*>(trow) + (lane & 15));
         s = __ldg(reinterpret_cast<const float4*>(trow + 64) + (lane & 15));
       }
-      bool ok = mbar_wait(&bars[L::kQEmpty + qslot], ((q_it >> 1) & 1) ^ 1, abort, p.err, 0xb31);
+      bool ok = mbar_wait(&bars[L::kQEmpty + qslot], ((q_it >> 1) & 1) ^ 1, abort, p.err, 0xb11);
       if (!__all_sync(0xffffffffu, ok)) break;
       ++q_it;
       uint8_t* tile = q_base + qslot * L::kTBytes;
@@ -468,6 +544,80 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       }
       fence_proxy_async_smem();
       warp_arrive(&bars[L::kQFull + qslot], lane);
+      // ---- the products
+      const Desc qd = make_desc(smem_u32(q_base + qslot * L::kTBytes), 16, 1024);
+      bool fail = false;
+      const int b1 = pc.block1();
+      for (int b = pc.block0(); b < b1; ++b, ++s_it) {
+        const uint32_t slot = s_it % SS;
+        bool w = mbar_wait(&bars[L::kKFull + stage], kpar, abort, p.err, 0xb12);
+        w = w && mbar_wait(&bars[L::kSEmpty + slot], ((s_it / SS) & 1) ^ 1, abort, p.err, 0xb13);
+        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        tc_fence_after();
+        const Desc kd = make_desc(smem_u32(k_base + stage * L::kKVBytes), 16, 1024);
+        const uint32_t d = tm_s + slot * N;
+        if (leader) {
+          mma8_ss<0>(d, kd, 0, qd, 0, kIdS);
+#pragma unroll
+          for (int s = 1; s < kHeadDim / 32; ++s) mma8_ss<1>(d, kd, s * 2, qd, s * 2, kIdS);
+          umma_commit(&bars[L::kSFull + slot]);
+          umma_commit(&bars[L::kKEmpty + stage]);
+          if (b + 1 == b1) umma_commit(&bars[L::kQEmpty + qslot]);
+        }
+        __syncwarp();
+        if (++stage == SK) {
+          stage = 0;
+          kpar ^= 1;
+        }
+      }
+      if (fail) break;
+    }
+  } else if (warp == 15) {
+    // ------------------------------------------------------------ PV issuer
+    constexpr uint32_t kIdO = idesc_e4m3(128, N, true);  // A = V^T (dims contiguous), B = P^T pieces
+    const uint32_t leader = elect_one_sync();
+    uint32_t stage = 0, vpar = 0, o_it = 0;
+    while (walk.next(p, &pc)) {
+      bool fail = false;
+      const int b1 = pc.block1();
+      for (int b = pc.block0(); b < b1; ++b, ++o_it) {
+        const uint32_t oslot = o_it % OS, pslot = o_it % PS;
+        bool w = mbar_wait(&bars[L::kVFull + stage], vpar, abort, p.err, 0xb22);
+        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        uint8_t* vd = v_base + stage * L::kKVBytes;
+        // V rows past the context may hold anything, NaN codes among it; P is
+        // exactly 0 there, so zero them (0 * NaN = NaN)
+        const int valid = min(B, pc.kv_len - b * B);
+        if (valid < B) {
+          for (int i = lane; i < (B - valid) * 8; i += 32)
+            *reinterpret_cast<uint4*>(vd + valid * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        w = mbar_wait(&bars[L::kPFull + pslot], (o_it / PS) & 1, abort, p.err, 0xb21);
+        w = w && mbar_wait(&bars[L::kOEmpty + oslot], ((o_it / OS) & 1) ^ 1, abort, p.err, 0xb23);
+        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        tc_fence_after();
+        // K-step s covers keys 32 s .. 32 s + 31: V rows 4096 B a step, P^T
+        // columns 32 B a step
+        const Desc vdd = make_desc(smem_u32(vd), 16, 1024);
+        const Desc pd = make_desc(smem_u32(p_base + pslot * L::kTBytes), 16, 1024);
+        const uint32_t d = tm_o + oslot * N;
+        if (leader) {
+          mma8_ss<0>(d, vdd, 0, pd, 0, kIdO);
+#pragma unroll
+          for (int s = 1; s < B / 32; ++s) mma8_ss<1>(d, vdd, s * 256, pd, s * 2, kIdO);
+          umma_commit(&bars[L::kOFull + oslot]);
+          umma_commit(&bars[L::kVEmpty + stage]);
+          umma_commit(&bars[L::kPEmpty + pslot]);
+        }
+        __syncwarp();
+        if (++stage == SV) {
+          stage = 0;
+          vpar ^= 1;
+        }
+      }
+      if (fail) break;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
@@ -476,39 +626,30 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const int w = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(w * 32) << 16;
     float* red = reinterpret_cast<float*>(smem + L::kRedOff + grp * L::kRedBytes);
-    float* part = reinterpret_cast<float*>(smem + L::kPartOff + grp * L::kPartBytes);
     const float sl = p.scale_log2;
     const int lps = 31 - __clz(p.page_size);
     uint32_t s_base = 0, sy_it = 0, q_it = 0;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = dec_snake_item(round);
-      if (item >= p.num_items) continue;
-      const DecItem di = dec_item(p, item);
-      const int kv_len = di.kv_len, nb = di.nb;
+    while (walk.next(p, &pc)) {
+      const int kv_len = pc.kv_len, b0 = pc.block0(), nb = pc.block1() - b0;
       // the scales of this thread's key: page ids two own blocks ahead, the
       // scales themselves one ahead
-      const int32_t* prow = p.page_table + static_cast<int64_t>(di.seq) * p.max_pages;
+      const int32_t* prow = p.page_table + static_cast<int64_t>(pc.seq) * p.max_pages;
       auto page_of = [&](int j) -> int {
-        const int key = (di.b0 + j * di.stride) * B + t;
+        const int key = (b0 + j) * B + t;
         return (j < nb && key < kv_len) ? __ldg(prow + (key >> lps)) : -1;
       };
       auto scales_of = [&](int pg, float& sk, float& sv) {
         sk = sv = 1.0f;
         if (pg >= 0 && pg < p.n_pages) {
-          const int64_t i = static_cast<int64_t>(pg) * p.hkv + di.g;
-          sk = __ldg(qp.k_scale + i);
-          sv = __ldg(qp.v_scale + i);
+          const int64_t i = static_cast<int64_t>(pg) * p.hkv + pc.g;
+          sk = __ldg(p.k_scale + i);
+          sv = __ldg(p.v_scale + i);
         }
       };
       const int j0 = static_cast<int>(s_base & 1) == grp ? 0 : 1;
       float sk, sv;
       int pg_next = page_of(j0 + 2);
       scales_of(page_of(j0), sk, sv);
-      if (FOLD && p.state_o && p.fill_flag) {
-        // their share of the item's table fill, released to the correction warps
-        fill_item_slots(p, di, G, tid);
-        mbar_arrive(&bars[L::kFillDone]);
-      }
       const uint32_t qslot = q_it & 1;
       bool ok = mbar_wait(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb41);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -532,9 +673,8 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         tmem_ld_wait(raw);
         tc_fence_before();
         warp_arrive(&bars[L::kSEmpty + slot], lane);
-        const bool vis = (di.b0 + j * di.stride) * B + t < kv_len;
+        const bool vis = (b0 + j) * B + t < kv_len;
         const int rb = static_cast<int>(sy_it & 1);
-        const uint32_t sy_par = (sy_it >> 1) & 1;
         // scores, and the block maxima over the visible keys (exact)
         float sc[MG];
 #pragma unroll
@@ -542,7 +682,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           const float a = __fmaf_rn(__uint_as_float(raw[2 * MG + q]), 0x1p-10f,
                                     __fmaf_rn(__uint_as_float(raw[MG + q]), 0x1p-5f, __uint_as_float(raw[q])));
           sc[q] = (q < G && vis) ? __fmul_rn(__fmul_rn(a, qs[q]), sk) : -INFINITY;
-          const float m = warp_max(sc[q]);
+          const float m = warp_max_nan(sc[q]);
           if (lane == 0) red[(rb * 4 + w) * (MG + 1) + q] = m;
         }
         {
@@ -550,11 +690,12 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           if (lane == 0) red[(rb * 4 + w) * (MG + 1) + MG] = m;
         }
         warp_arrive(&bars[L::kSyncMax + grp * 2 + rb], lane);
-        ok = mbar_wait(&bars[L::kSyncMax + grp * 2 + rb], sy_par, abort, p.err, 0xb43);
+        ok = mbar_wait(&bars[L::kSyncMax + grp * 2 + rb], (sy_it >> 1) & 1, abort, p.err, 0xb43);
+        ++sy_it;
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
         const float* r4 = red + rb * 4 * (MG + 1);
         auto max4 = [&](int q) {
-          return fmaxf(fmaxf(fmaxf(r4[q], r4[MG + 1 + q]), r4[2 * (MG + 1) + q]), r4[3 * (MG + 1) + q]);
+          return max_nan(max_nan(r4[q], r4[MG + 1 + q]), max_nan(r4[2 * (MG + 1) + q], r4[3 * (MG + 1) + q]));
         };
         float mc[MG], pr[MG];
 #pragma unroll
@@ -567,7 +708,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         const float wf = vis ? __fmul_rn(sv, pow2_bits(261 - ae)) : 0.0f;
         ok = mbar_wait(&bars[L::kPEmpty + grp], ((s_it / PS) & 1) ^ 1, abort, p.err, 0xb44);
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
-        uint8_t* pt = p_base + (s_it % PS) * L::kTBytes;
+        uint8_t* pt = p_base + grp * L::kTBytes;
 #pragma unroll
         for (int q = 0; q < MG; q += 2) {
           float a = __fmul_rn(pr[q], wf), b = q + 1 < MG ? __fmul_rn(pr[q + 1 < MG ? q + 1 : q], wf) : 0.0f;
@@ -579,36 +720,21 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        warp_arrive(&bars[L::kPFull + (s_it % PS)], lane);
-        // canonical row sums (numerics.cuh): warp w sums query heads w, w + 4
-#pragma unroll
-        for (int q = 0; q < MG; ++q) part[((rb * 4 + w) * MG + q) * 32 + lane] = pr[q];
-        warp_arrive(&bars[L::kSyncPart + grp * 2 + rb], lane);
-        ok = mbar_wait(&bars[L::kSyncPart + grp * 2 + rb], sy_par, abort, p.err, 0xb45);
-        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
-        const uint32_t sslot = s_it % SR;
+        warp_arrive(&bars[L::kPFull + grp], lane);
+        // the warp's part of the block sums: p <= 1 (and a block's largest is
+        // 1), so 26 fraction bits of fixed point lose less than FP32 sums
+        // would, in one instruction and in no order
+        uint32_t* st = stats + (s_it % SR) * L::kStatWords;
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
-          if (q >= G || (q & 3) != w) continue;
-          const float* pw = part + (rb * 4 * MG + q) * 32 + (lane & 15);
-          float a = __fadd_rn(__fadd_rn(__fadd_rn(pw[0], pw[16]), pw[MG * 32]), pw[MG * 32 + 16]);
-          float a1 = __fadd_rn(__fadd_rn(__fadd_rn(pw[2 * MG * 32], pw[2 * MG * 32 + 16]), pw[3 * MG * 32]),
-                               pw[3 * MG * 32 + 16]);
-#pragma unroll
-          for (int off = 8; off >= 1; off >>= 1) {
-            a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
-            a1 = __fadd_rn(a1, __shfl_xor_sync(0xffffffffu, a1, off));
-          }
-          a = __fadd_rn(a, a1);
+          const uint32_t l = __reduce_add_sync(0xffffffffu, __float2uint_rn(__fmul_rn(pr[q], kLUnit)));
           if (lane == 0) {
-            float lse_b, rcp;
-            block_stats(mc[q], a, lse_b, rcp);
-            // PV carries 2^7 / A: fold its inverse into 1 / l (exact)
-            stats[sslot * MG + q] = make_float2(lse_b, __fmul_rn(rcp, pow2_bits(ae - 7)));
+            st[MG + 1 + w * MG + q] = l;
+            if (w == 0) st[q] = __float_as_uint(mc[q]);
           }
         }
-        warp_arrive(&bars[L::kStatsFull + sslot], lane);
-        ++sy_it;
+        if (w == 0 && lane == 0) st[MG] = __float_as_uint(pow2_bits(ae - 7));  // PV carries 2^7 / A
+        warp_arrive(&bars[L::kStatsFull + (s_it % SR)], lane);
         sk = sk_next;
         sv = sv_next;
       }
@@ -619,29 +745,18 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     // ------------------------------------------------------------ correction / epilogue
     const int d = tid;  // head dimension lane
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    uint32_t o_it = 0, fill_it = 0;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = dec_snake_item(round);
-      if (item >= p.num_items) continue;
-      const DecItem di = dec_item(p, item);
-      const int seq = di.seq, g = di.g, nb = di.nb;
-      const bool split = p.state_o != nullptr;
-      if (FOLD && split && p.fill_flag) {
-        // the item's slots of the state table hold kUnwritten before any of
-        // its states can land; the fill barrier orders every fill store (the
-        // softmax warps write a share) before every state store
-        fill_item_slots(p, di, G, tid);
-        mbar_arrive(&bars[L::kFillDone]);
-        const bool ok = mbar_wait(&bars[L::kFillDone], fill_it & 1, abort, p.err, 0xb53);
-        ++fill_it;
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-      float O[MG];
+    uint32_t o_it = 0, cut_it = 0;
+    while (walk.next(p, &pc)) {
+      const bool whole = pc.whole();
+      // O: the segment's, T: the sequence's (whole pairs); lane q holds m and
+      // l of query head q
+      float O[MG], T[MG];
 #pragma unroll
-      for (int q = 0; q < MG; ++q) O[q] = 0.0f;
-      float Lrun = -INFINITY;  // lane q: running lse of query head q
+      for (int q = 0; q < MG; ++q) O[q] = T[q] = 0.0f;
+      float m = 0.0f, l = 0.0f, mt = 0.0f, lt = 0.0f;
+      const int b1 = pc.block1();
       bool fail = false;
-      for (int j = 0; j < nb; ++j) {
+      for (int b = pc.block0(); b < b1; ++b) {
         const uint32_t sslot = o_it % SR, oslot = o_it % OS;
         bool ok = mbar_wait(&bars[L::kStatsFull + sslot], (o_it / SR) & 1, abort, p.err, 0xb51);
         ok = ok && mbar_wait(&bars[L::kOFull + oslot], (o_it / OS) & 1, abort, p.err, 0xb52);
@@ -649,54 +764,108 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         tc_fence_after();
         uint32_t raw[N];
         TmemRow<N>::ld(tm_o + lane_off + oslot * N, raw);
-        // fold coefficients of query head `lane` (overlap the TMEM load)
-        float lb = -INFINITY, rc = 0.0f, al = 0.0f, be = 0.0f, Lp = 0.0f;
-        if (lane < G) {
-          const float2 st = stats[sslot * MG + lane];
-          lb = st.x;
-          rc = st.y;
-          if (j > 0 && !split) fold_coeffs(Lrun, lb, Lp, al, be);
+        // fold factors of query head `lane` (overlap the TMEM load)
+        const uint32_t* st = stats + sslot * L::kStatWords;
+        const bool first = b % kSegBlocks == 0;
+        const float vf = __uint_as_float(st[MG]);
+        float fa = 0.0f, fb = 1.0f;
+        if (lane < MG) {
+          const float mb = __uint_as_float(st[lane]);
+          const uint32_t* ls = st + MG + 1 + lane;
+          const float lb = __fmul_rn(__fadd_rn(__fadd_rn(__uint2float_rn(ls[0]), __uint2float_rn(ls[MG])),
+                                               __fadd_rn(__uint2float_rn(ls[2 * MG]), __uint2float_rn(ls[3 * MG]))),
+                                     1.0f / kLUnit);
+          if (first) {
+            m = mb;
+            l = lb;
+          } else {
+            float mn;
+            fold_factors(m, mb, mn, fa, fb);
+            l = __fmaf_rn(lb, fb, __fmul_rn(l, fa));
+            m = mn;
+          }
         }
         tmem_ld_wait(raw);
         tc_fence_before();
         warp_arrive(&bars[L::kOEmpty + oslot], lane);
-        const int64_t blk = p.cu_q[seq] + di.b0 + j * di.stride;  // state-table block
-        const int64_t pair_b = blk * p.hq + g * G;
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
-          const float rq = __shfl_sync(0xffffffffu, rc, q);
-          const float aq = __shfl_sync(0xffffffffu, al, q);
-          const float bq = __shfl_sync(0xffffffffu, be, q);
-          if (q < G) {
-            float pv = __uint_as_float(raw[(kPPieces - 1) * MG + q]);
+          const float aq = __shfl_sync(0xffffffffu, fa, q);
+          const float bq = __shfl_sync(0xffffffffu, fb, q);
+          float pv = __uint_as_float(raw[(kPPieces - 1) * MG + q]);
 #pragma unroll
-            for (int k = kPPieces - 2; k >= 0; --k) pv = __fmaf_rn(pv, 0x1p-5f, __uint_as_float(raw[k * MG + q]));
-            const float oa = state_elem(pv, rq);
-            if (split) p.state_o[(pair_b + q) * kHeadDim + d] = oa;
-            else O[q] = (j == 0) ? oa : fold_elem(O[q], oa, aq, bq);
-          }
-        }
-        if (split) {
-          if (warp == 0 && lane < G) p.state_lse[pair_b + lane] = lb;
-          if (FOLD && p.fill_flag && j == 0 && tid == 0)
-            st_release_u64(p.fill_flag + (static_cast<int64_t>(seq) * p.hkv + g) * kMaxSplitK + di.b0, p.fill_nonce);
-        } else if (lane < G) {
-          Lrun = (j == 0) ? lb : Lp;
+          for (int k = kPPieces - 2; k >= 0; --k) pv = __fmaf_rn(pv, 0x1p-5f, __uint_as_float(raw[k * MG + q]));
+          pv = __fmul_rn(pv, vf);
+          O[q] = first ? pv : __fmaf_rn(pv, bq, __fmul_rn(O[q], aq));
         }
         ++o_it;
-      }
-      if (fail) break;
-      if (split) continue;
-      // epilogue: O and L are final
+        if ((b + 1) % kSegBlocks != 0 && b + 1 != pc.nb) continue;
+        // the segment is complete
+        const int seg = b / kSegBlocks;
+        if (whole) {
+          float ta = 0.0f, tb = 1.0f;
+          if (seg == 0) {
+            mt = m;
+            lt = l;
+          } else {
+            float mn;
+            fold_factors(mt, m, mn, ta, tb);
+            lt = __fmaf_rn(l, tb, __fmul_rn(lt, ta));
+            mt = mn;
+          }
 #pragma unroll
-      for (int q = 0; q < MG; ++q) {
-        if (q < G) {
-          const int64_t row = static_cast<int64_t>(seq) * p.hq + g * G + q;
-          if (p.out_f32) p.out_f32[row * kHeadDim + d] = O[q];
-          if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(O[q]);
+          for (int q = 0; q < MG; ++q) {
+            const float aq = __shfl_sync(0xffffffffu, ta, q);
+            const float bq = __shfl_sync(0xffffffffu, tb, q);
+            T[q] = seg == 0 ? O[q] : __fmaf_rn(O[q], bq, __fmul_rn(T[q], aq));
+          }
+        } else {
+          const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + seg) * p.hq + pc.g * G;
+#pragma unroll
+          for (int q = 0; q < MG; ++q)
+            if (q < G) p.state_o[(r + q) * kHeadDim + d] = O[q];
+          if (warp == 0 && lane < G) reinterpret_cast<float2*>(p.state_ml)[r + lane] = make_float2(m, l);
         }
       }
-      if (warp == 0 && lane < G && p.lse) p.lse[static_cast<int64_t>(seq) * p.hq + g * G + lane] = Lrun;
+      if (fail) break;
+      if (whole) {
+        const float rl = __frcp_rn(lt);
+#pragma unroll
+        for (int q = 0; q < MG; ++q) {
+          const float rq = __shfl_sync(0xffffffffu, rl, q);
+          if (q < G) {
+            const int64_t row = static_cast<int64_t>(pc.seq) * p.hq + pc.g * G + q;
+            const float o = __fmul_rn(T[q], rq);
+            if (p.out_f32) p.out_f32[row * kHeadDim + d] = o;
+            if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(o);
+          }
+        }
+        if (warp == 0 && lane < G && p.lse)
+          p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * G + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
+        continue;
+      }
+      // a part of a pair: every thread's states are in device memory before
+      // the segments are counted; the CTA that counts the last one folds
+      __threadfence();
+      warp_arrive(&bars[L::kStored], lane);
+      if (warp == 0) {
+        bool ok = mbar_wait(&bars[L::kStored], cut_it & 1, abort, p.err, 0xb54);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          *last_flag = count_segments(p.counts + static_cast<int64_t>(pc.seq) * p.hkv + pc.g, p.nonce, pc.s1 - pc.s0,
+                                      pc.ns);
+          __threadfence();
+          mbar_arrive(&bars[L::kCounted]);
+        }
+        __syncwarp();
+      }
+      bool ok = mbar_wait(&bars[L::kCounted], cut_it & 1, abort, p.err, 0xb55);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      ++cut_it;
+      if (*last_flag) {
+        __threadfence();
+        for (int q = warp; q < G; q += 4) fold_pair(p, pc, pc.g * G + q, lane);
+      }
     }
   }
 
@@ -717,24 +886,14 @@ __global__ void __launch_bounds__(kQDThreads, 1)
 
 template <int MG>
 cudaError_t launch_qdecode_t(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                             bool cooperative, cudaStream_t stream) {
-  if (!cooperative) {
-    rlk_qdecode_kernel<MG, false><<<grid, kQDThreads, QDecLayout<MG>::kAlloc, stream>>>(p, tk, tv);
-    return cudaGetLastError();
-  }
-  // the fold warps wait for states that other CTAs of the launch publish:
-  // every CTA must be resident at once
-  void* args[] = {const_cast<QDecodeParams*>(&p), const_cast<CUtensorMap*>(&tk), const_cast<CUtensorMap*>(&tv)};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(&rlk_qdecode_kernel<MG, true>), dim3(grid),
-                                     dim3(kQDThreads), args, QDecLayout<MG>::kAlloc, stream);
+                             cudaStream_t stream) {
+  rlk_qdecode_kernel<MG><<<grid, kQDThreads, QDecLayout<MG>::kAlloc, stream>>>(p, tk, tv);
+  return cudaGetLastError();
 }
 
 template <int MG>
 cudaError_t configure_qdecode_mg() {
-  cudaError_t e = cudaFuncSetAttribute(rlk_qdecode_kernel<MG, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       QDecLayout<MG>::kAlloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(rlk_qdecode_kernel<MG, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(rlk_qdecode_kernel<MG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               QDecLayout<MG>::kAlloc);
 }
 
@@ -749,11 +908,11 @@ cudaError_t configure_qdecode_kernels() {
 }
 
 cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                           bool cooperative, cudaStream_t stream) {
-  if (p.f.group <= 1) return launch_qdecode_t<1>(p, tk, tv, grid, cooperative, stream);
-  if (p.f.group <= 2) return launch_qdecode_t<2>(p, tk, tv, grid, cooperative, stream);
-  if (p.f.group <= 4) return launch_qdecode_t<4>(p, tk, tv, grid, cooperative, stream);
-  return launch_qdecode_t<8>(p, tk, tv, grid, cooperative, stream);
+                           cudaStream_t stream) {
+  if (p.group <= 1) return launch_qdecode_t<1>(p, tk, tv, grid, stream);
+  if (p.group <= 2) return launch_qdecode_t<2>(p, tk, tv, grid, stream);
+  if (p.group <= 4) return launch_qdecode_t<4>(p, tk, tv, grid, stream);
+  return launch_qdecode_t<8>(p, tk, tv, grid, stream);
 }
 
 }  // namespace rlk

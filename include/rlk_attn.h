@@ -454,22 +454,25 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
  * counterpart of rlk_attn_decode_paged, _splitk and _rope in one call.
  *   q: device BF16 [num_seqs, Hq, 128]; seqlens: HOST [num_seqs], context
  *     lengths 1 .. max_pages * page_size; outputs as rlk_attn_decode_paged;
- *   split_k: 1 = single pass; 2 .. 64 items per (sequence, KV head); 0 = the
- *     library picks (as rlk_attn_decode_paged_splitk; the same result for
- *     every value);
+ *   split_k: how the work is spread over the SMs, never what it computes:
+ *     0 = the blocks of all sequences and KV heads, cut evenly (the choice
+ *     for speed); k = 1 .. 64 = k items per (sequence, KV head);
  *   rope_table: NULL, or device: q is pre-RoPE and rotated at position
  *     seqlens[s] - 1 (< rope_max_pos) as in rlk_attn_decode_paged_rope;
  *   workspace: for split_k != 1, device, 16-byte aligned,
- *     >= rlk_attn_workspace_size(params, RLK_OP_DECODE_SPLIT, NULL, seqlens)
- *     bytes, not shared by calls that overlap; unused for split_k == 1.
+ *     >= rlk_attn_workspace_size(params, RLK_OP_DECODE_QCACHE, NULL, seqlens)
+ *     bytes (520 per (512 keys, query head) and 8 per (sequence, KV head)), not
+ *     shared by calls that overlap; its contents need no initialisation.
+ *     Unused for split_k == 1.
  * The pages' codes go to the tensor core as they are; the query and the
  * probabilities are split into 3 and 4 E4M3 pieces, so neither loses
- * precision to 8 bits: scores, softmax and sums are FP32, and out / lse stay
- * within 2e-5 / 1e-5 of the exact attention over the cached values at unit
- * scale.  Scales must be positive, finite and >= 2^-120.  A query row that
- * holds Inf or NaN gives a NaN row.  The result does not depend on the batch,
- * the page order, split_k or repetition (bit for bit).  Needs kv_block_size
- * 128 and at most 8 query heads per KV head (RLK_ERR_UNSUPPORTED otherwise).
+ * precision to 8 bits (a probability 2^-19 of itself).  Scores, softmax and
+ * sums are FP32: blocks of 128 keys are folded left to right into segments of
+ * 512 keys, those left to right into the row, with a running maximum.
+ * Scales must be positive, finite and >= 2^-120.  A query row that holds Inf
+ * or NaN gives a NaN row.  The result does not depend on the batch, the page
+ * order, split_k or repetition (bit for bit).  Needs kv_block_size 128 and at
+ * most 8 query heads per KV head (RLK_ERR_UNSUPPORTED otherwise).
  */
 rlk_status rlk_attn_decode_qcache(const rlk_attn_params* params, const void* q, const void* k_pool,
                                   const void* v_pool, const float* k_scale, const float* v_scale, int32_t n_pages,
@@ -525,11 +528,11 @@ rlk_status rlk_attn_merge_states_noalloc(const rlk_attn_params* params, const in
                                          int64_t n_state_pairs, float* out_f32, void* out_bf16, float* lse,
                                          rlk_stream_t stream);
 
-enum { RLK_OP_MERGE = 1, RLK_OP_BACKWARD = 2, RLK_OP_DECODE_SPLIT = 3 };
+enum { RLK_OP_MERGE = 1, RLK_OP_BACKWARD = 2, RLK_OP_DECODE_SPLIT = 3, RLK_OP_DECODE_QCACHE = 4 };
 
 /* Workspace bytes an entry point needs (HOST cu_seqlens; 0 on bad input).
- * RLK_OP_DECODE_SPLIT takes the decode context lengths (seqlens) as
- * cu_seqlens_k and ignores cu_seqlens_q. */
+ * RLK_OP_DECODE_SPLIT and RLK_OP_DECODE_QCACHE take the decode context
+ * lengths (seqlens) as cu_seqlens_k and ignore cu_seqlens_q. */
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op,
                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k);
 

@@ -104,7 +104,7 @@ def decode(rlk, torch, c, q, ctx, hq, split_k=1, seqs=None, rope=None, max_pos=0
     p = rlk.make_params(n, hq, hkv, 128, softmax_scale=scale)
     ws = None
     if split_k != 1:
-        ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_SPLIT, None, ctx), dtype=torch.uint8,
+        ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx), dtype=torch.uint8,
                          device="cuda")
     rlk.rlk_attn_decode_qcache(p, to_bf16(torch, q[seqs]), kd, vd, ksd, vsd, c.n_pages, c.page, td, td.shape[1], ctx,
                                split_k, rope, max_pos, out, outb, lse, ws)

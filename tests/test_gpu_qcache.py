@@ -448,7 +448,7 @@ def test_serving_loop_against_the_definition():
         to = [a + 1 for a in at]
         append(at, to)
         ctx = np.array(to, np.int32)
-        ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_SPLIT, None, ctx), dtype=torch.uint8,
+        ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx), dtype=torch.uint8,
                          device="cuda")
         q = qh.to_bf16(torch, np.stack([qs[s][at[s]] for s in range(n)]))
         rlk.rlk_attn_decode_qcache(p, q, *pool, ctx, 0, table, 200, out, outb, lse, ws)
@@ -478,7 +478,7 @@ def test_other_stream_and_graph_replay():
     qd, kd, vd = (qh.to_bf16(torch, x) for x in (q, k, v))
     out, outb = torch.empty((4, hq, 128), device="cuda"), torch.empty((4, hq, 128), dtype=torch.bfloat16, device="cuda")
     lse = torch.empty((4, hq), device="cuda")
-    ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_SPLIT, None, ctx), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx), dtype=torch.uint8, device="cuda")
 
     def step():
         rlk.rlk_attn_qcache_write(p, kd, vd, [0, 1, 2, 3, 4], pos, None, 0, *pool)
@@ -531,7 +531,7 @@ def test_two_streams_at_once():
             p = rlk.make_params(len(ctx), 8, 2)
             with torch.cuda.stream(s):
                 out = torch.empty((len(ctx), 8, 128), device="cuda")
-                ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_SPLIT, None, ctx), dtype=torch.uint8,
+                ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx), dtype=torch.uint8,
                                  device="cuda")
                 rlk.rlk_attn_decode_qcache(p, qd, *dev[:4], c.n_pages, 16, dev[4], dev[4].shape[1], ctx, 2, None, 0,
                                            out, None, None, ws, stream=s)
