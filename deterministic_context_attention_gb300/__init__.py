@@ -17,6 +17,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -57,7 +58,7 @@ SLAB_DTYPE = np.dtype([("seq", "<i4"), ("block", "<i4"), ("row_begin", "<i4"), (
 def make_params(num_seqs, num_q_heads=32, num_kv_heads=8, kv_block_size=128, cp_size=1,
                 cp_layout=ZIGZAG, softmax_scale=None, head_dim=128) -> rlk_attn_params:
     if softmax_scale is None:
-        softmax_scale = 1.0 / float(np.sqrt(head_dim))
+        softmax_scale = 1.0 / math.sqrt(head_dim)
     return rlk_attn_params(int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim),
                            float(softmax_scale), 1, int(kv_block_size), int(cp_size), int(cp_layout))
 
@@ -327,65 +328,95 @@ def rlk_attn_decode_paged_splitk_rope(params, q, k_pool, v_pool, n_pages, page_s
            "rlk_attn_decode_paged_splitk_rope")
 
 
-def _dev(x, *dtypes):
-    """_ptr of a device tensor the 8-bit cache's kernels read or write: refuses
-    one that is not contiguous, not on the current CUDA device or of another
-    type (a pointer value passes as it is)."""
-    if x is None or isinstance(x, int):
-        return _ptr(x)
+_dtypes = {}  # what the 8-bit cache's arguments may be, by name (filled once torch is there)
+
+
+def _kinds():
     import torch
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device.index != torch.cuda.current_device():
-        raise ValueError("expected a tensor on the current CUDA device")
-    if not x.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    if str(x.dtype)[6:] not in dtypes:
-        raise ValueError(f"expected {' or '.join(dtypes)}, got {x.dtype}")
-    return _ptr(x)
+    _dtypes.update(codes=(torch.float8_e4m3fn, torch.uint8), bf16=(torch.bfloat16,), f32=(torch.float32,),
+                   i32=(torch.int32,))
+    _dtypes["cuda"] = torch.cuda
+    return _dtypes
 
 
-_E4M3 = ("float8_e4m3fn", "uint8")
+def _dev_args(stream, *args):
+    """Addresses of the tensors an 8-bit cache call reads or writes and its
+    stream, as ``(kind, tensor), ...`` of the kinds above: refuses a tensor that
+    is not contiguous, not on the current CUDA device or of another type (a
+    pointer value or None passes as it is)."""
+    kinds = _dtypes or _kinds()
+    out, dev = [], None
+    for kind, x in args:
+        if x is not None and not isinstance(x, int):
+            if not hasattr(x, "data_ptr") or not x.is_cuda:
+                raise ValueError("expected a tensor on the current CUDA device")
+            if dev is None:
+                dev = kinds["cuda"].current_device()
+            if x.get_device() != dev:
+                raise ValueError("expected a tensor on the current CUDA device")
+            if not x.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+            if kind is not None and x.dtype not in kinds[kind]:
+                raise ValueError(f"expected {' or '.join(str(t) for t in kinds[kind])}, got {x.dtype}")
+            x = x.data_ptr()
+        out.append(x)
+    if stream is None:
+        stream = kinds["cuda"].current_stream().cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    out.append(stream)
+    return out
 
 
-def _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages):
-    return (_dev(k_pool, *_E4M3), _dev(v_pool, *_E4M3), _dev(k_scale, "float32"), _dev(v_scale, "float32"),
-            int(n_pages), int(page_size), _dev(page_table, "int32"), int(max_pages))
+def _i32_addr(a):
+    """A host int32 array and its address (keep the array until the call returns)."""
+    if a is None:
+        return None, None
+    a = a if isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous else _i32_host(a)
+    return a, a.ctypes.data
 
 
 def rlk_attn_qcache_write(params, k, v, cu_seqlens, pos_offset, rope_table, rope_max_pos, k_pool, v_pool, k_scale,
                           v_scale, n_pages, page_size, page_table, max_pages, stream=None):
     """Quantise new BF16 K/V rows into the 8-bit pages (rope_table: rotate K
     at its positions first, or None)."""
-    cu = _i32_host(cu_seqlens)
-    po = None if pos_offset is None else _i32_host(pos_offset)
-    pool = _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages)
-    _check(load().rlk_attn_qcache_write(ctypes.byref(params), _dev(k, "bfloat16"), _dev(v, "bfloat16"), _ptr(cu),
-                                        _ptr(po), _dev(rope_table, "float32"), int(rope_max_pos), *pool,
-                                        _stream(stream)), "rlk_attn_qcache_write")
+    cu, cu_p = _i32_addr(cu_seqlens)
+    po, po_p = _i32_addr(pos_offset)
+    k, v, rt, kp, vp, ks, vs, pt, st = _dev_args(
+        stream, ("bf16", k), ("bf16", v), ("f32", rope_table), ("codes", k_pool), ("codes", v_pool), ("f32", k_scale),
+        ("f32", v_scale), ("i32", page_table))
+    _check(load().rlk_attn_qcache_write(params, k, v, cu_p, po_p, rt, rope_max_pos, kp, vp, ks, vs, n_pages, page_size,
+                                        pt, max_pages, st), "rlk_attn_qcache_write")
 
 
 def rlk_attn_qcache_read(params, k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages,
                          cu_seqlens, pos_offset, k, v, stream=None):
     """Read token ranges of the 8-bit pages back as packed BF16 K/V rows."""
-    cu = _i32_host(cu_seqlens)
-    po = None if pos_offset is None else _i32_host(pos_offset)
-    pool = _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages)
-    _check(load().rlk_attn_qcache_read(ctypes.byref(params), *pool, _ptr(cu), _ptr(po), _dev(k, "bfloat16"),
-                                       _dev(v, "bfloat16"), _stream(stream)), "rlk_attn_qcache_read")
+    cu, cu_p = _i32_addr(cu_seqlens)
+    po, po_p = _i32_addr(pos_offset)
+    kp, vp, ks, vs, pt, k, v, st = _dev_args(
+        stream, ("codes", k_pool), ("codes", v_pool), ("f32", k_scale), ("f32", v_scale), ("i32", page_table),
+        ("bf16", k), ("bf16", v))
+    _check(load().rlk_attn_qcache_read(params, kp, vp, ks, vs, n_pages, page_size, pt, max_pages, cu_p, po_p, k, v, st),
+           "rlk_attn_qcache_read")
 
 
 def rlk_attn_decode_qcache(params, q, k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages,
                            seqlens, split_k, rope_table, rope_max_pos, out_f32, out_bf16, lse, workspace=None,
                            workspace_bytes=None, stream=None):
-    """Decode over the 8-bit pages (split_k: 1 single pass, 0 the library
-    picks; rope_table: rotate the query rows, or None)."""
-    sl = _i32_host(seqlens)
+    """Decode over the 8-bit pages (split_k: 0 spreads the work evenly, k items
+    per (sequence, KV head) otherwise; rope_table: rotate the query rows, or
+    None)."""
+    sl, sl_p = _i32_addr(seqlens)
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    pool = _qcache(k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages)
-    _check(load().rlk_attn_decode_qcache(ctypes.byref(params), _dev(q, "bfloat16"), *pool, _ptr(sl), int(split_k),
-                                         _dev(rope_table, "float32"), int(rope_max_pos), _dev(out_f32, "float32"),
-                                         _dev(out_bf16, "bfloat16"), _dev(lse, "float32"), _ptr(workspace),
-                                         int(workspace_bytes), _stream(stream)), "rlk_attn_decode_qcache")
+    q, kp, vp, ks, vs, pt, rt, of, ob, ls, ws, st = _dev_args(
+        stream, ("bf16", q), ("codes", k_pool), ("codes", v_pool), ("f32", k_scale), ("f32", v_scale),
+        ("i32", page_table), ("f32", rope_table), ("f32", out_f32), ("bf16", out_bf16), ("f32", lse),
+        (None, workspace))
+    _check(load().rlk_attn_decode_qcache(params, q, kp, vp, ks, vs, n_pages, page_size, pt, max_pages, sl_p, split_k,
+                                         rt, rope_max_pos, of, ob, ls, ws, workspace_bytes, st),
+           "rlk_attn_decode_qcache")
 
 
 def rlk_attn_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,

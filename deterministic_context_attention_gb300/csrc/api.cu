@@ -1371,7 +1371,6 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   dp.num_seqs = params->num_seqs;
   dp.hq = hq;
   dp.hkv = hkv;
-  dp.group = hq / hkv;
   dp.scale_log2 = scale_log2(params);
   dp.q = static_cast<const uint16_t*>(q);
   dp.k_scale = cache.k_scale;

@@ -41,7 +41,7 @@ cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
 constexpr int kQSegKeys = 512;
 struct QDecodeParams {
   ErrWord* err;
-  int32_t num_seqs, hq, hkv, group;
+  int32_t num_seqs, hq, hkv;
   float scale_log2;
   const uint16_t* q;  // [num_seqs, hq, 128] BF16
   const float* k_scale;

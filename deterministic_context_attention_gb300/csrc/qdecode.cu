@@ -64,7 +64,8 @@ constexpr int kQPieces = 3, kPPieces = 4;
 constexpr int kSegBlocks = kQSegKeys / 128;
 constexpr float kLUnit = 0x1p26f;  // block sums of p: fixed point, 26 fraction bits
 
-// N: MMA columns, the pieces of up to MG query heads, at column piece * MG + head
+// MG: query heads per KV head.  N: MMA columns, their pieces (of Q at column
+// piece * MG + head, of P at p_col)
 template <int MG>
 struct QDecLayout {
   static constexpr int B = 128;           // keys per block
@@ -76,17 +77,17 @@ struct QDecLayout {
   static constexpr int kSS = 4, kOS = 4;  // TMEM rings of S^T and O^T
   static constexpr int kSR = 8;           // statistics ring
   static constexpr int kKVBytes = B * 128;
-  static constexpr int kTBytes = N * 128;  // an N-row operand tile of 128 codes
+  static constexpr int kTBytes = N * 128;  // an operand tile: N x 128 codes
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + kQS * kTBytes;
   static constexpr int kKOff = (kPOff + kPS * kTBytes + 1023) / 1024 * 1024;
   static constexpr int kVOff = kKOff + kSK * kKVBytes;
-  // per softmax group, double-buffered by block: maxima of 4 warps (MG heads
-  // and the V scale)
-  static constexpr int kRedBytes = 2 * 4 * (MG + 1) * 4;
+  // per softmax group, double-buffered by block: float [MG heads, V scale][4
+  // warps] maxima
+  static constexpr int kRedBytes = 2 * (MG + 1) * 16;
   static constexpr int kRedOff = kVOff + kSV * kKVBytes;
-  // per block: float m[MG], then the V factor, then uint32 l[4 warps][MG]
-  static constexpr int kStatWords = MG + 1 + 4 * MG;
+  // per block: uint32 l[MG][4 warps], then float m[MG] and the V factor
+  static constexpr int kStatWords = (5 * MG + 1 + 3) / 4 * 4;
   static constexpr int kStatsOff = kRedOff + 2 * kRedBytes;
   static constexpr int kQsOff = kStatsOff + kSR * kStatWords * 4;  // float [kQS][MG]
   static constexpr int kBarOff = (kQsOff + kQS * MG * 4 + 7) / 8 * 8;
@@ -113,10 +114,34 @@ __device__ __forceinline__ uint32_t tile8_off(int row, int col) {
          static_cast<uint32_t>(col & 15);
 }
 
+// P^T is stored N-major: the N pieces of key t are one run of bytes, which
+// the key's thread writes whole, 16 bytes a store.  N = 16: runs of 16 bytes,
+// no swizzle; N = 32: runs of 32 bytes in the 32-byte swizzle (its two halves
+// swapped for keys with bit 2 set).  The piece k of head q is column
+// 8 (q / 2) + 2 k + q mod 2, so that the pairs next_piece makes pack as they
+// are.
+__host__ __device__ constexpr int p_col(int q, int k) { return 8 * (q >> 1) + 2 * k + (q & 1); }
+template <int N>
+__device__ __forceinline__ Desc p_desc(uint32_t saddr) {
+  // 8 keys are N * 8 bytes apart; no second group along N
+  const uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(N * 8 >> 4) << 16) |
+                     (static_cast<uint64_t>(N * 8 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+                     (static_cast<uint64_t>(N == 32 ? 6 : 0) << 61);
+  return Desc{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+template <int N>
+__device__ __forceinline__ void p_store(uint8_t* tile, int t, const uint32_t (&w)[N / 4]) {
+#pragma unroll
+  for (int h = 0; h < N / 16; ++h) {
+    const int at = N == 32 ? t * 32 + ((h ^ ((t >> 2) & 1)) << 4) : t * 16;
+    *reinterpret_cast<uint4*>(tile + at) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+  }
+}
+
 // Instruction descriptor, kind::f8f6f4 with E4M3 A and B and FP32 accumulation.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // One K = 32 step of D[tmem] (+)= A B^T, both from shared memory.
 template <int ACC>
@@ -364,10 +389,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int G = p.group;
 
-  // operand rows of no head's piece are never written: they must read as zero
-  for (int i = tid; i < (QS + PS) * L::kTBytes / 16; i += kQDThreads)
+  // query rows of no head's piece are never written: they must read as zero
+  for (int i = tid; i < QS * L::kTBytes / 16; i += kQDThreads)
     reinterpret_cast<uint4*>(smem + L::kQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (tid == 0) {
@@ -431,32 +455,45 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const int ps = p.page_size;
     const int lg = 31 - __clz(B / ps);  // log2 of the pages per block
     uint32_t stage = 0, par = 1;
-    while (walk.next(p, &pc)) {
-      const int seq_pages = (pc.kv_len + ps - 1) / ps;
-      const int32_t* prow = p.page_table + static_cast<int64_t>(pc.seq) * p.max_pages;
-      int cached = -1;  // a new sequence's page ids
+    // a window holds the page ids of 2^(9 - lg) consecutive blocks, all 16
+    // loads of a lane in flight at once; the next piece's first window is
+    // fetched while the current piece runs
+    int32_t pg[L::kPageWin / 32];
+    auto fetch = [&](const QPiece& q, int win) {
+      const int seq_pages = (q.kv_len + ps - 1) / ps;
+      const int32_t* prow = p.page_table + static_cast<int64_t>(q.seq) * p.max_pages;
+#pragma unroll
+      for (int t = 0; t < L::kPageWin / 32; ++t) {
+        const int gp = (win << 9) + lane + 32 * t;
+        pg[t] = (gp < seq_pages && (gp >> lg) < q.block1()) ? __ldg(prow + gp) : -1;
+      }
+    };
+    bool more = walk.next(p, &pc);
+    if (more) fetch(pc, pc.block0() >> (9 - lg));
+    while (more) {
+      const QPiece cur = pc;
+      int cached = -1;
+      bool fetched = false;  // the next piece's window is in pg
       bool fail = false;
-      for (int b = pc.block0(); b < pc.block1(); ++b) {
+      for (int b = cur.block0(); b < cur.block1(); ++b) {
         bool ok = mbar_wait(empty_b + stage, par, abort, p.err, is_v ? 0xb03 : 0xb02);
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
         uint8_t* dst = ring + stage * L::kKVBytes;
-        const int n_tok = min(B, pc.kv_len - b * B);
+        const int n_tok = min(B, cur.kv_len - b * B);
         const int n_pg = (n_tok + ps - 1) / ps;
-        // the window holds the pages of 2^(9 - lg) consecutive blocks, all 16
-        // loads of a lane in flight before the first store
         const int win = b >> (9 - lg);
         if (cached != win) {
-          int32_t pg[L::kPageWin / 32];
-#pragma unroll
-          for (int t = 0; t < L::kPageWin / 32; ++t) {
-            const int gp = (win << 9) + lane + 32 * t;
-            pg[t] = (gp < seq_pages && (gp >> lg) < pc.block1()) ? __ldg(prow + gp) : -1;
-          }
+          if (cached >= 0) fetch(cur, win);
           __syncwarp();
 #pragma unroll
           for (int t = 0; t < L::kPageWin / 32; ++t) wc[lane + 32 * t] = pg[t];
           __syncwarp();
           cached = win;
+          if ((cur.block1() - 1) >> (9 - lg) == win) {  // the last window of this piece
+            more = walk.next(p, &pc);
+            if (more) fetch(pc, pc.block0() >> (9 - lg));
+            fetched = true;
+          }
         }
         if (lane == 0) mbar_arrive_expect_tx(full_b + stage, n_pg * ps * 128);
         __syncwarp();
@@ -466,18 +503,18 @@ __global__ void __launch_bounds__(kQDThreads, 1)
             report_error(p.err, kErrBadPage, 0xb04);
             pe = p.n_pages;  // out of range: the copy reads the zero fill
           }
-          tma_load_3d(dst + lane * ps * 128, map, full_b + stage, 0, 0, pe * p.hkv + pc.g);
+          tma_load_3d(dst + lane * ps * 128, map, full_b + stage, 0, 0, pe * p.hkv + cur.g);
         }
         if (++stage == static_cast<uint32_t>(S)) {
           stage = 0;
           par ^= 1;
         }
       }
-      if (fail || *abort) break;
+      if (fail || *abort || !fetched) break;
     }
   } else if (warp == 14) {
     // ------------------------------------------------------------ queries, S issuer
-    constexpr uint32_t kIdS = idesc_e4m3(128, N, false);  // A = K (K-major), B = Q pieces (K-major)
+    constexpr uint32_t kIdS = idesc_e4m3(128, N, false, false);  // A = K (K-major), B = Q pieces (K-major)
     const uint32_t leader = elect_one_sync();
     uint32_t stage = 0, kpar = 0, s_it = 0, q_it = 0;
     while (walk.next(p, &pc)) {
@@ -487,9 +524,8 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       uint2 x[MG];
 #pragma unroll
       for (int i = 0; i < MG; ++i)
-        if (i < G)
-          x[i] = __ldg(reinterpret_cast<const uint2*>(
-                           p.q + (static_cast<int64_t>(pc.seq) * p.hq + pc.g * G + i) * kHeadDim) + lane);
+        x[i] = __ldg(reinterpret_cast<const uint2*>(
+                         p.q + (static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + i) * kHeadDim) + lane);
       float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
       if (p.rope_table) {
         const float* trow = p.rope_table + static_cast<int64_t>(pc.kv_len - 1) * kHeadDim;
@@ -502,7 +538,6 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       uint8_t* tile = q_base + qslot * L::kTBytes;
 #pragma unroll
       for (int i = 0; i < MG; ++i) {
-        if (i >= G) continue;
         uint32_t w[2] = {x[i].x, x[i].y};
         if (p.rope_table) {
           // the pair of element e is e +- 64, 16 lanes away
@@ -574,7 +609,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     }
   } else if (warp == 15) {
     // ------------------------------------------------------------ PV issuer
-    constexpr uint32_t kIdO = idesc_e4m3(128, N, true);  // A = V^T (dims contiguous), B = P^T pieces
+    constexpr uint32_t kIdO = idesc_e4m3(128, N, true, true);  // A = V^T (dims contiguous), B = P^T (pieces contiguous)
     const uint32_t leader = elect_one_sync();
     uint32_t stage = 0, vpar = 0, o_it = 0;
     while (walk.next(p, &pc)) {
@@ -599,14 +634,14 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
         tc_fence_after();
         // K-step s covers keys 32 s .. 32 s + 31: V rows 4096 B a step, P^T
-        // columns 32 B a step
+        // 32 N B a step
         const Desc vdd = make_desc(smem_u32(vd), 16, 1024);
-        const Desc pd = make_desc(smem_u32(p_base + pslot * L::kTBytes), 16, 1024);
+        const Desc pd = p_desc<N>(smem_u32(p_base + pslot * L::kTBytes));
         const uint32_t d = tm_o + oslot * N;
         if (leader) {
           mma8_ss<0>(d, vdd, 0, pd, 0, kIdO);
 #pragma unroll
-          for (int s = 1; s < B / 32; ++s) mma8_ss<1>(d, vdd, s * 256, pd, s * 2, kIdO);
+          for (int s = 1; s < B / 32; ++s) mma8_ss<1>(d, vdd, s * 256, pd, s * 2 * N, kIdO);
           umma_commit(&bars[L::kOFull + oslot]);
           umma_commit(&bars[L::kVEmpty + stage]);
           umma_commit(&bars[L::kPEmpty + pslot]);
@@ -629,42 +664,59 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const float sl = p.scale_log2;
     const int lps = 31 - __clz(p.page_size);
     uint32_t s_base = 0, sy_it = 0, q_it = 0;
-    while (walk.next(p, &pc)) {
-      const int kv_len = pc.kv_len, b0 = pc.block0(), nb = pc.block1() - b0;
-      // the scales of this thread's key: page ids two own blocks ahead, the
-      // scales themselves one ahead
-      const int32_t* prow = p.page_table + static_cast<int64_t>(pc.seq) * p.max_pages;
-      auto page_of = [&](int j) -> int {
-        const int key = (b0 + j) * B + t;
-        return (j < nb && key < kv_len) ? __ldg(prow + (key >> lps)) : -1;
-      };
-      auto scales_of = [&](int pg, float& sk, float& sv) {
-        sk = sv = 1.0f;
-        if (pg >= 0 && pg < p.n_pages) {
-          const int64_t i = static_cast<int64_t>(pg) * p.hkv + pc.g;
-          sk = __ldg(p.k_scale + i);
-          sv = __ldg(p.v_scale + i);
-        }
-      };
+    // the scales of this thread's key: page ids two own blocks ahead, the
+    // scales themselves one ahead, across pieces too
+    auto page_of = [&](const QPiece& q, int j) -> int {
+      const int key = (q.block0() + j) * B + t;
+      return (q.block0() + j < q.block1() && key < q.kv_len)
+                 ? __ldg(p.page_table + static_cast<int64_t>(q.seq) * p.max_pages + (key >> lps))
+                 : -1;
+    };
+    auto scales_of = [&](const QPiece& q, int pg, float& sk, float& sv) {
+      sk = sv = 1.0f;
+      if (pg >= 0 && pg < p.n_pages) {
+        const int64_t i = static_cast<int64_t>(pg) * p.hkv + q.g;
+        sk = __ldg(p.k_scale + i);
+        sv = __ldg(p.v_scale + i);
+      }
+    };
+    float sk, sv, sk0 = 1.0f, sv0 = 1.0f;
+    int pg0 = -1, pg1 = -1;
+    bool more = walk.next(p, &pc);
+    if (more) {
+      pg0 = page_of(pc, grp);
+      pg1 = page_of(pc, grp + 2);
+      scales_of(pc, pg0, sk0, sv0);
+    }
+    while (more) {
+      const QPiece cur = pc;
+      const int kv_len = cur.kv_len, b0 = cur.block0(), nb = cur.block1() - b0;
       const int j0 = static_cast<int>(s_base & 1) == grp ? 0 : 1;
-      float sk, sv;
-      int pg_next = page_of(j0 + 2);
-      scales_of(page_of(j0), sk, sv);
+      sk = sk0;
+      sv = sv0;
+      int pg_next = pg1;
+      more = walk.next(p, &pc);
+      if (more) {
+        const int j0n = static_cast<int>((s_base + nb) & 1) == grp ? 0 : 1;
+        pg0 = page_of(pc, j0n);
+        pg1 = page_of(pc, j0n + 2);
+      }
+      bool ahead = false;
       const uint32_t qslot = q_it & 1;
       bool ok = mbar_wait(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb41);
       if (!__all_sync(0xffffffffu, ok)) break;
       ++q_it;
       float qs[MG];
 #pragma unroll
-      for (int q = 0; q < MG; ++q) qs[q] = q < G ? qscale[qslot * MG + q] : 0.0f;
+      for (int q = 0; q < MG; ++q) qs[q] = qscale[qslot * MG + q];
       warp_arrive(&bars[L::kQEmpty + qslot], lane);
       bool fail = false;
       for (int j = j0; j < nb; j += 2) {
         const uint32_t s_it = s_base + j;
         const uint32_t slot = s_it % SS;
         float sk_next, sv_next;
-        scales_of(pg_next, sk_next, sv_next);
-        pg_next = page_of(j + 4);
+        scales_of(cur, pg_next, sk_next, sv_next);
+        pg_next = page_of(cur, j + 4);
         ok = mbar_wait(&bars[L::kSFull + slot], (s_it / SS) & 1, abort, p.err, 0xb42);
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
         tc_fence_after();
@@ -681,44 +733,45 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         for (int q = 0; q < MG; ++q) {
           const float a = __fmaf_rn(__uint_as_float(raw[2 * MG + q]), 0x1p-10f,
                                     __fmaf_rn(__uint_as_float(raw[MG + q]), 0x1p-5f, __uint_as_float(raw[q])));
-          sc[q] = (q < G && vis) ? __fmul_rn(__fmul_rn(a, qs[q]), sk) : -INFINITY;
+          sc[q] = vis ? __fmul_rn(__fmul_rn(a, qs[q]), sk) : -INFINITY;
           const float m = warp_max_nan(sc[q]);
-          if (lane == 0) red[(rb * 4 + w) * (MG + 1) + q] = m;
+          if (lane == 0) red[(rb * (MG + 1) + q) * 4 + w] = m;
         }
         {
           const float m = warp_max(vis ? sv : 0.0f);
-          if (lane == 0) red[(rb * 4 + w) * (MG + 1) + MG] = m;
+          if (lane == 0) red[(rb * (MG + 1) + MG) * 4 + w] = m;
         }
         warp_arrive(&bars[L::kSyncMax + grp * 2 + rb], lane);
         ok = mbar_wait(&bars[L::kSyncMax + grp * 2 + rb], (sy_it >> 1) & 1, abort, p.err, 0xb43);
         ++sy_it;
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
-        const float* r4 = red + rb * 4 * (MG + 1);
         auto max4 = [&](int q) {
-          return max_nan(max_nan(r4[q], r4[MG + 1 + q]), max_nan(r4[2 * (MG + 1) + q], r4[3 * (MG + 1) + q]));
+          const float4 r = *reinterpret_cast<const float4*>(red + (rb * (MG + 1) + q) * 4);
+          return max_nan(max_nan(r.x, r.y), max_nan(r.z, r.w));
         };
         float mc[MG], pr[MG];
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
           mc[q] = __fmul_rn(max4(q), sl);
-          pr[q] = (q < G && vis) ? prob(sc[q], sl, -mc[q]) : 0.0f;
+          pr[q] = vis ? prob(sc[q], sl, -mc[q]) : 0.0f;
         }
         // the block's V anchor A = 2^(ae - 127); w = p (sv 2^7 / A)
         const int ae = max(static_cast<int>(__float_as_uint(max4(MG)) >> 23), 8);
         const float wf = vis ? __fmul_rn(sv, pow2_bits(261 - ae)) : 0.0f;
         ok = mbar_wait(&bars[L::kPEmpty + grp], ((s_it / PS) & 1) ^ 1, abort, p.err, 0xb44);
         if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
-        uint8_t* pt = p_base + grp * L::kTBytes;
+        uint32_t pw[N / 4];
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) pw[i] = 0u;
 #pragma unroll
         for (int q = 0; q < MG; q += 2) {
           float a = __fmul_rn(pr[q], wf), b = q + 1 < MG ? __fmul_rn(pr[q + 1 < MG ? q + 1 : q], wf) : 0.0f;
-#pragma unroll
-          for (int k = 0; k < kPPieces; ++k) {
-            const uint32_t c = k + 1 < kPPieces ? next_piece(a, b) : e4m3_pair(a, b);
-            if (q < G) pt[tile8_off(k * MG + q, t)] = static_cast<uint8_t>(c);
-            if (q + 1 < G) pt[tile8_off(k * MG + q + 1, t)] = static_cast<uint8_t>(c >> 8);
-          }
+          static_assert(kPPieces == 4 && p_col(2, 0) == 8 && p_col(1, 3) == 7, "a pair's pieces are two words");
+          const uint32_t c0 = next_piece(a, b), c1 = next_piece(a, b), c2 = next_piece(a, b);
+          pw[q] = __byte_perm(c0, c1, 0x5410);
+          pw[q + 1] = __byte_perm(c2, e4m3_pair(a, b), 0x5410);
         }
+        p_store<N>(p_base + grp * L::kTBytes, t, pw);
         fence_proxy_async_smem();
         warp_arrive(&bars[L::kPFull + grp], lane);
         // the warp's part of the block sums: p <= 1 (and a block's largest is
@@ -729,16 +782,21 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         for (int q = 0; q < MG; ++q) {
           const uint32_t l = __reduce_add_sync(0xffffffffu, __float2uint_rn(__fmul_rn(pr[q], kLUnit)));
           if (lane == 0) {
-            st[MG + 1 + w * MG + q] = l;
-            if (w == 0) st[q] = __float_as_uint(mc[q]);
+            st[q * 4 + w] = l;
+            if (w == 0) st[4 * MG + q] = __float_as_uint(mc[q]);
           }
         }
-        if (w == 0 && lane == 0) st[MG] = __float_as_uint(pow2_bits(ae - 7));  // PV carries 2^7 / A
+        if (w == 0 && lane == 0) st[5 * MG] = __float_as_uint(pow2_bits(ae - 7));  // PV carries 2^7 / A
         warp_arrive(&bars[L::kStatsFull + (s_it % SR)], lane);
+        if (!ahead) {  // the page ids have landed meanwhile
+          if (more) scales_of(pc, pg0, sk0, sv0);
+          ahead = true;
+        }
         sk = sk_next;
         sv = sv_next;
       }
       if (fail) break;
+      if (!ahead && more) scales_of(pc, pg0, sk0, sv0);
       s_base += nb;
     }
   } else {
@@ -767,13 +825,13 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // fold factors of query head `lane` (overlap the TMEM load)
         const uint32_t* st = stats + sslot * L::kStatWords;
         const bool first = b % kSegBlocks == 0;
-        const float vf = __uint_as_float(st[MG]);
+        const float vf = __uint_as_float(st[5 * MG]);
         float fa = 0.0f, fb = 1.0f;
         if (lane < MG) {
-          const float mb = __uint_as_float(st[lane]);
-          const uint32_t* ls = st + MG + 1 + lane;
-          const float lb = __fmul_rn(__fadd_rn(__fadd_rn(__uint2float_rn(ls[0]), __uint2float_rn(ls[MG])),
-                                               __fadd_rn(__uint2float_rn(ls[2 * MG]), __uint2float_rn(ls[3 * MG]))),
+          const float mb = __uint_as_float(st[4 * MG + lane]);
+          const uint4 ls = *reinterpret_cast<const uint4*>(st + 4 * lane);
+          const float lb = __fmul_rn(__fadd_rn(__fadd_rn(__uint2float_rn(ls.x), __uint2float_rn(ls.y)),
+                                               __fadd_rn(__uint2float_rn(ls.z), __uint2float_rn(ls.w))),
                                      1.0f / kLUnit);
           if (first) {
             m = mb;
@@ -792,9 +850,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         for (int q = 0; q < MG; ++q) {
           const float aq = __shfl_sync(0xffffffffu, fa, q);
           const float bq = __shfl_sync(0xffffffffu, fb, q);
-          float pv = __uint_as_float(raw[(kPPieces - 1) * MG + q]);
+          float pv = __uint_as_float(raw[p_col(q, kPPieces - 1)]);
 #pragma unroll
-          for (int k = kPPieces - 2; k >= 0; --k) pv = __fmaf_rn(pv, 0x1p-5f, __uint_as_float(raw[k * MG + q]));
+          for (int k = kPPieces - 2; k >= 0; --k) pv = __fmaf_rn(pv, 0x1p-5f, __uint_as_float(raw[p_col(q, k)]));
           pv = __fmul_rn(pv, vf);
           O[q] = first ? pv : __fmaf_rn(pv, bq, __fmul_rn(O[q], aq));
         }
@@ -820,11 +878,11 @@ __global__ void __launch_bounds__(kQDThreads, 1)
             T[q] = seg == 0 ? O[q] : __fmaf_rn(O[q], bq, __fmul_rn(T[q], aq));
           }
         } else {
-          const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + seg) * p.hq + pc.g * G;
+          const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + seg) * p.hq + pc.g * MG;
 #pragma unroll
           for (int q = 0; q < MG; ++q)
-            if (q < G) p.state_o[(r + q) * kHeadDim + d] = O[q];
-          if (warp == 0 && lane < G) reinterpret_cast<float2*>(p.state_ml)[r + lane] = make_float2(m, l);
+            p.state_o[(r + q) * kHeadDim + d] = O[q];
+          if (warp == 0 && lane < MG) reinterpret_cast<float2*>(p.state_ml)[r + lane] = make_float2(m, l);
         }
       }
       if (fail) break;
@@ -833,15 +891,13 @@ __global__ void __launch_bounds__(kQDThreads, 1)
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
           const float rq = __shfl_sync(0xffffffffu, rl, q);
-          if (q < G) {
-            const int64_t row = static_cast<int64_t>(pc.seq) * p.hq + pc.g * G + q;
-            const float o = __fmul_rn(T[q], rq);
-            if (p.out_f32) p.out_f32[row * kHeadDim + d] = o;
-            if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(o);
-          }
+          const int64_t row = static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + q;
+          const float o = __fmul_rn(T[q], rq);
+          if (p.out_f32) p.out_f32[row * kHeadDim + d] = o;
+          if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(o);
         }
-        if (warp == 0 && lane < G && p.lse)
-          p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * G + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
+        if (warp == 0 && lane < MG && p.lse)
+          p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
         continue;
       }
       // a part of a pair: every thread's states are in device memory before
@@ -864,7 +920,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       ++cut_it;
       if (*last_flag) {
         __threadfence();
-        for (int q = warp; q < G; q += 4) fold_pair(p, pc, pc.g * G + q, lane);
+        for (int q = warp; q < MG; q += 4) fold_pair(p, pc, pc.g * MG + q, lane);
       }
     }
   }
@@ -901,18 +957,25 @@ cudaError_t configure_qdecode_mg() {
 
 cudaError_t configure_qdecode_kernels() {
   cudaError_t e;
-  if ((e = configure_qdecode_mg<1>())) return e;
-  if ((e = configure_qdecode_mg<2>())) return e;
-  if ((e = configure_qdecode_mg<4>())) return e;
+  if ((e = configure_qdecode_mg<1>()) || (e = configure_qdecode_mg<2>()) || (e = configure_qdecode_mg<3>()) ||
+      (e = configure_qdecode_mg<4>()) || (e = configure_qdecode_mg<5>()) || (e = configure_qdecode_mg<6>()) ||
+      (e = configure_qdecode_mg<7>()))
+    return e;
   return configure_qdecode_mg<8>();
 }
 
 cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                            cudaStream_t stream) {
-  if (p.group <= 1) return launch_qdecode_t<1>(p, tk, tv, grid, stream);
-  if (p.group <= 2) return launch_qdecode_t<2>(p, tk, tv, grid, stream);
-  if (p.group <= 4) return launch_qdecode_t<4>(p, tk, tv, grid, stream);
-  return launch_qdecode_t<8>(p, tk, tv, grid, stream);
+  switch (p.hq / p.hkv) {
+    case 1: return launch_qdecode_t<1>(p, tk, tv, grid, stream);
+    case 2: return launch_qdecode_t<2>(p, tk, tv, grid, stream);
+    case 3: return launch_qdecode_t<3>(p, tk, tv, grid, stream);
+    case 4: return launch_qdecode_t<4>(p, tk, tv, grid, stream);
+    case 5: return launch_qdecode_t<5>(p, tk, tv, grid, stream);
+    case 6: return launch_qdecode_t<6>(p, tk, tv, grid, stream);
+    case 7: return launch_qdecode_t<7>(p, tk, tv, grid, stream);
+    default: return launch_qdecode_t<8>(p, tk, tv, grid, stream);
+  }
 }
 
 }  // namespace rlk
