@@ -1335,7 +1335,7 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
     });
   rlk::QDecodeParams dp;
   std::memset(&dp, 0, sizeof(dp));
-  int64_t blocks = 0, segments = 0, pair_segments = 0;
+  int64_t blocks = 0, segments = 0;
   for (int s = 0; s < params->num_seqs; ++s) {
     if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(cache.max_pages) * cache.page_size ||
         seqlens[s] > INT32_MAX - 1024)
@@ -1352,9 +1352,6 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
     dp.blk0[s + 1] = static_cast<int32_t>(blocks);
     dp.seg0[s + 1] = static_cast<int32_t>(segments);
   }
-  pair_segments = segments * hkv;
-  const int64_t items = static_cast<int64_t>(params->num_seqs) * hkv * std::max(split_k, 1);
-  if (items > INT32_MAX - 1024) return fail(RLK_ERR_UNSUPPORTED, "more than 2^31 work items in one launch");
   const size_t state_bytes = qdecode_state_bytes(segments, hq);
   const size_t count_bytes = static_cast<size_t>(params->num_seqs) * hkv * sizeof(uint64_t);
   if (split_k != 1 && (!workspace || workspace_bytes < state_bytes + count_bytes))
@@ -1366,7 +1363,7 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   CUtensorMap mk, mv;
   if ((st = make_code_map(&mk, cache.k_pool, cache.n_pages, hkv, cache.page_size))) return st;
   if ((st = make_code_map(&mv, cache.v_pool, cache.n_pages, hkv, cache.page_size))) return st;
-  const int grid = static_cast<int>(std::min<int64_t>(dev->num_sms, split_k == 0 ? pair_segments : items));
+  const int grid = static_cast<int>(std::min<int64_t>(dev->num_sms, segments * hkv));
   dp.err = dev->err;
   dp.num_seqs = params->num_seqs;
   dp.hq = hq;

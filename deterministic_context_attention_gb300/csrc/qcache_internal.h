@@ -48,7 +48,7 @@ struct QDecodeParams {
   const float* v_scale;
   const int32_t* page_table;
   int32_t n_pages, page_size, max_pages;
-  int32_t split_k;          // items per (sequence, KV head), or 0: the blocks cut evenly over the grid
+  int32_t split_k;          // most parts a (sequence, KV head) is cut into, or 0: any
   const float* rope_table;  // rotates the query at ctx - 1, or null
   float* out_f32;
   uint16_t* out_bf16;
@@ -63,7 +63,7 @@ struct QDecodeParams {
   int32_t ctx[kMaxSeqs];
   int32_t seg0[kMaxSeqs + 1];  // prefix sums of the sequences' segments
   int32_t blk0[kMaxSeqs + 1];  // prefix sums of the sequences' blocks x hkv
-  int32_t part_q, part_r;      // split_k 0: blocks / grid and the rest
+  int32_t part_q, part_r;      // all blocks / grid, and the rest
 };
 cudaError_t configure_qdecode_kernels();
 cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,

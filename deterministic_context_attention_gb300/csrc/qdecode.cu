@@ -42,11 +42,12 @@
 // Warp roles (512 threads):
 //   warps 0-3   correction / epilogue: thread d owns head dimension d
 //   warps 4-7   softmax of the even blocks, warps 8-11 of the odd ones:
-//               thread t owns key t of the block and fetches its page's scales
-//   warp  12    TMA producer of the K pages, warp 13 of the V pages
-//   warp  14    the query rows (loads them, rotates them where asked, splits
-//               them) and the S^T products; up to 4 blocks ahead of the softmax
-//   warp  15    the O^T products
+//               thread t owns key t of the block
+//   warp  12    producer of the K pages (TMA) and of both scales (cp.async: it
+//               runs ahead of the softmax, the V ring follows it)
+//   warp  13    producer of the V pages; loads the query rows, rotates them
+//               where asked and splits them, a piece of work ahead
+//   warp  14    the S^T products, warp 15 the O^T products
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -76,6 +77,10 @@ struct QDecLayout {
   static constexpr int kQS = 2;           // query slots (the next item's rows are prepared ahead)
   static constexpr int kSS = 4, kOS = 4;  // TMEM rings of S^T and O^T
   static constexpr int kSR = 8;           // statistics ring
+  // scales ring: fetched with the K codes, in groups of up to 4 blocks; the
+  // softmax reads a block's scales before it frees the block's S slot
+  static constexpr int kScRing = 16;
+  static_assert(kScRing >= kSK + kSS + 4, "scales ring");
   static constexpr int kKVBytes = B * 128;
   static constexpr int kTBytes = N * 128;  // an operand tile: N x 128 codes
   static constexpr int kQOff = 0;
@@ -96,11 +101,12 @@ struct QDecLayout {
                        kSEmpty = kSFull + kSS, kPFull = kSEmpty + kSS, kPEmpty = kPFull + kPS,
                        kOFull = kPEmpty + kPS, kOEmpty = kOFull + kOS, kStatsFull = kOEmpty + kOS,
                        kSyncMax = kStatsFull + kSR, kStored = kSyncMax + 4, kCounted = kStored + 1,
-                       kNumBars = kCounted + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort (i32), last (i32)
-  static constexpr int kPageWin = 512;                     // page ids cached per window (one per producer)
-  static constexpr int kPageOff = (kMiscOff + 16 + 15) / 16 * 16;
-  static constexpr int kTotal = kPageOff + 2 * kPageWin * 4;
+                       kScales = kCounted + 1, kNumBars = kScales + kScRing;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort, last [2] (i32)
+  static constexpr int kScOff = (kMiscOff + 16 + 15) / 16 * 16;  // float [K, V][kScRing][16 pages]
+  static constexpr int kRowOff = kScOff + 2 * kScRing * 16 * 4;  // staged query rows and RoPE table row
+  static constexpr int kRowBytes = MG * 256 + 512;
+  static constexpr int kTotal = kRowOff + kQS * kRowBytes;
   static constexpr int kAlloc = kTotal + 1024;
   static constexpr int kTmemCols = N * (kSS + kOS);
   static_assert(kAlloc <= 232448, "decode shared memory");
@@ -195,6 +201,19 @@ struct TmemRow<32> {
   static __device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[32]) { tmem_ld32(a, r); }
 };
 
+// A warp's wait on a barrier (bounded, mbar_wait): one test and one vote when
+// the phase is complete already, the rest out of line (the roles' code
+// competes for the instruction cache).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrWord* err,
+                                       unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, ErrWord* err,
+                                          unsigned int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_slow(bar, parity, abort, err, site);
+}
+
 // One arrival for the whole warp, after every lane's earlier writes.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
@@ -231,15 +250,17 @@ struct QPiece {
 
 // The pieces of this CTA, in order; every role walks them on its own.
 struct QWalk {
-  int at, end;  // balanced: blocks of the line [at, end); otherwise items at, at + grid, ...
+  int left;       // blocks still to take
+  int seq, g, b;  // where the next piece starts
   __device__ explicit QWalk(const QDecodeParams& p) {
-    if (p.split_k == 0) {
-      at = cut(p, blockIdx.x);
-      end = cut(p, blockIdx.x + 1);
-    } else {
-      at = blockIdx.x;
-      end = p.num_seqs * p.hkv * p.split_k;
-    }
+    seq = g = b = 0;
+    const int at = cut(p, blockIdx.x);
+    left = cut(p, blockIdx.x + 1) - at;
+    if (left <= 0) return;
+    seq = seq_of(p, at);
+    const int nb = (p.ctx[seq] + 127) / 128, r = at - p.blk0[seq];
+    g = r / nb;
+    b = r - g * nb;
   }
   static __device__ int seq_of(const QDecodeParams& p, int x) {
     int lo = 0, hi = p.num_seqs - 1;
@@ -251,47 +272,78 @@ struct QWalk {
     return lo;
   }
   // the c-th part's start: part_q blocks a part and one more for the first
-  // part_r, from there on to the next segment
+  // part_r, from there on to the next segment, or (split_k) the next of the
+  // at most split_k equal runs of segments a pair may be cut into
   static __device__ int cut(const QDecodeParams& p, int c) {
     const int x = c * p.part_q + min(c, p.part_r);
     if (x >= p.blk0[p.num_seqs]) return p.blk0[p.num_seqs];
     const int s = seq_of(p, x);
     const int nb = (p.ctx[s] + 127) / 128;
     const int b = (x - p.blk0[s]) % nb;
-    return x - b + min((b + kSegBlocks - 1) / kSegBlocks * kSegBlocks, nb);
+    int step = kSegBlocks;
+    if (p.split_k) step *= ((nb + kSegBlocks - 1) / kSegBlocks + p.split_k - 1) / p.split_k;
+    return x - b + min((b + step - 1) / step * step, nb);
   }
   __device__ bool next(const QDecodeParams& p, QPiece* q) {
-    if (p.split_k == 0) {
-      if (at >= end) return false;
-      q->seq = seq_of(p, at);
-      set(p, q);
-      const int r = at - p.blk0[q->seq];
-      q->g = r / q->nb;
-      const int b = r - q->g * q->nb;
-      const int stop = min(end - at, q->nb - b);
-      q->s0 = b / kSegBlocks;
-      q->s1 = (b + stop + kSegBlocks - 1) / kSegBlocks;
-      at += stop;
-      return true;
-    }
-    while (at < end) {
-      const int pair = at / p.split_k, r = at - pair * p.split_k;
-      q->seq = pair / p.hkv;
-      q->g = pair - q->seq * p.hkv;
-      set(p, q);
-      q->s0 = static_cast<int>(static_cast<int64_t>(r) * q->ns / p.split_k);
-      q->s1 = static_cast<int>(static_cast<int64_t>(r + 1) * q->ns / p.split_k);
-      at += gridDim.x;
-      if (q->s1 > q->s0) return true;
-    }
-    return false;
-  }
-  static __device__ void set(const QDecodeParams& p, QPiece* q) {
-    q->kv_len = p.ctx[q->seq];
+    if (left <= 0) return false;
+    q->seq = seq;
+    q->g = g;
+    q->kv_len = p.ctx[seq];
     q->nb = (q->kv_len + 127) / 128;
     q->ns = (q->nb + kSegBlocks - 1) / kSegBlocks;
+    const int stop = min(left, q->nb - b);
+    q->s0 = b / kSegBlocks;
+    q->s1 = (b + stop + kSegBlocks - 1) / kSegBlocks;
+    left -= stop;
+    b = 0;
+    if (++g == p.hkv) {
+      g = 0;
+      ++seq;
+    }
+    return true;
   }
 };
+
+// The blocks of those pieces in groups of up to 4 consecutive ones of a piece
+// whose page ids fill a warp (32 pages: 2 blocks of 8-token pages, 4 of larger).
+struct QGroups {
+  QWalk walk;
+  QPiece pc;
+  int b, n;  // first block, blocks
+  bool ok;
+  __device__ QGroups(const QDecodeParams& p, int lg) : walk(p) {
+    b = n = 0;
+    ok = walk.next(p, &pc);
+    if (ok) begin(pc.block0(), lg);
+  }
+  __device__ void begin(int first, int lg) {
+    b = first;
+    n = min(1 << min(5 - lg, 2), pc.block1() - b);
+  }
+  __device__ void step(const QDecodeParams& p, int lg) {
+    if (!ok) return;
+    if (b + n >= pc.block1()) {
+      ok = walk.next(p, &pc);
+      if (ok) begin(pc.block0(), lg);
+    } else {
+      begin(b + n, lg);
+    }
+  }
+  // lane l: the id of page l of the group (-1: none)
+  __device__ int page_id(const QDecodeParams& p, int lg, int lane) const {
+    const int gp = (b << lg) + lane;
+    if (!ok || lane >= (n << lg) || gp * (128 >> lg) >= pc.kv_len) return -1;
+    return __ldg(p.page_table + static_cast<int64_t>(pc.seq) * p.max_pages + gp);
+  }
+};
+
+__device__ const float g_unit_scale = 1.0f;  // the scale of a page id out of range
+
+// Arrives on bar once this thread's earlier cp.async copies have landed (the
+// arrival is one of the barrier's count).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // (O, m, l) folded with a later state: the factors of the two, and m.
 __device__ __forceinline__ void fold_factors(float m, float mb, float& mn, float& a, float& b) {
@@ -318,16 +370,16 @@ __device__ __forceinline__ bool count_segments(unsigned long long* word, uint64_
 // The fold of a cut pair's segment states, one warp a query head: lane l
 // takes head dimensions 4 l .. 4 l + 3; chunks of C segments, the next chunk's
 // reads in flight while one folds.
-__device__ __noinline__ void fold_pair(const QDecodeParams& p, const QPiece& pc, int h, int lane) {
+__device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, int h, int lane) {
   constexpr int C = 8;
-  const int64_t base = static_cast<int64_t>(p.seg0[pc.seq]) * p.hq + h;
+  const int64_t base = static_cast<int64_t>(p.seg0[seq]) * p.hq + h;
   auto load = [&](int c0, float2& ml, float4 (&v)[C]) {
-    const int64_t r = base + static_cast<int64_t>(min(c0 + (lane & (C - 1)), pc.ns - 1)) * p.hq;
+    const int64_t r = base + static_cast<int64_t>(min(c0 + (lane & (C - 1)), ns - 1)) * p.hq;
     ml = __ldcg(reinterpret_cast<const float2*>(p.state_ml) + r);
 #pragma unroll
     for (int i = 0; i < C; ++i)
       v[i] = __ldcg(reinterpret_cast<const float4*>(
-                        p.state_o + (base + static_cast<int64_t>(min(c0 + i, pc.ns - 1)) * p.hq) * kHeadDim) +
+                        p.state_o + (base + static_cast<int64_t>(min(c0 + i, ns - 1)) * p.hq) * kHeadDim) +
                     lane);
   };
   float4 v[C], vn[C];
@@ -335,12 +387,12 @@ __device__ __noinline__ void fold_pair(const QDecodeParams& p, const QPiece& pc,
   load(0, ml, v);
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = 0.f, l = 0.f;
-  for (int c0 = 0; c0 < pc.ns; c0 += C) {
-    if (c0 + C < pc.ns) load(c0 + C, mln, vn);
+  for (int c0 = 0; c0 < ns; c0 += C) {
+    if (c0 + C < ns) load(c0 + C, mln, vn);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const float mb = __shfl_sync(0xffffffffu, ml.x, i), lb = __shfl_sync(0xffffffffu, ml.y, i);
-      if (c0 + i >= pc.ns) continue;
+      if (c0 + i >= ns) continue;
       if (c0 + i == 0) {
         O = v[0];
         m = mb;
@@ -362,7 +414,7 @@ __device__ __noinline__ void fold_pair(const QDecodeParams& p, const QPiece& pc,
   }
   const float r = __frcp_rn(l);
   O = make_float4(__fmul_rn(O.x, r), __fmul_rn(O.y, r), __fmul_rn(O.z, r), __fmul_rn(O.w, r));
-  const int64_t row = static_cast<int64_t>(pc.seq) * p.hq + h;
+  const int64_t row = static_cast<int64_t>(seq) * p.hq + h;
   if (p.out_f32) *(reinterpret_cast<float4*>(p.out_f32 + row * kHeadDim) + lane) = O;
   if (p.out_bf16)
     *(reinterpret_cast<uint2*>(p.out_bf16 + row * kHeadDim) + lane) =
@@ -421,6 +473,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     }
     for (int s = 0; s < SR; ++s) mbar_init(&bars[L::kStatsFull + s], 4);
     for (int s = 0; s < 4; ++s) mbar_init(&bars[L::kSyncMax + s], 4);
+    for (int s = 0; s < L::kScRing; ++s) mbar_init(&bars[L::kScales + s], 32);
     mbar_init(&bars[L::kStored], 4);
     mbar_init(&bars[L::kCounted], 1);
     *abort = 0;
@@ -440,122 +493,76 @@ __global__ void __launch_bounds__(kQDThreads, 1)
   uint8_t* k_base = smem + L::kKOff;
   uint8_t* v_base = smem + L::kVOff;
 
-  QWalk walk(p);
-  QPiece pc;
   if (warp == 12 || warp == 13) {
     // ------------------------------------------------------------ producers
     const bool is_v = warp == 13;
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     if (lane == 0) tma_prefetch_desc(map);
+    const uint32_t leader = elect_one_sync();
     const int S = is_v ? SV : SK;
     uint64_t* full_b = &bars[is_v ? L::kVFull : L::kKFull];
     uint64_t* empty_b = &bars[is_v ? L::kVEmpty : L::kKEmpty];
     uint8_t* ring = is_v ? v_base : k_base;
-    int32_t* wc = reinterpret_cast<int32_t*>(smem + L::kPageOff) + (is_v ? L::kPageWin : 0);
-    const int ps = p.page_size;
-    const int lg = 31 - __clz(B / ps);  // log2 of the pages per block
-    uint32_t stage = 0, par = 1;
-    // a window holds the page ids of 2^(9 - lg) consecutive blocks, all 16
-    // loads of a lane in flight at once; the next piece's first window is
-    // fetched while the current piece runs
-    int32_t pg[L::kPageWin / 32];
-    auto fetch = [&](const QPiece& q, int win) {
-      const int seq_pages = (q.kv_len + ps - 1) / ps;
-      const int32_t* prow = p.page_table + static_cast<int64_t>(q.seq) * p.max_pages;
-#pragma unroll
-      for (int t = 0; t < L::kPageWin / 32; ++t) {
-        const int gp = (win << 9) + lane + 32 * t;
-        pg[t] = (gp < seq_pages && (gp >> lg) < q.block1()) ? __ldg(prow + gp) : -1;
+    const int lps = 31 - __clz(p.page_size), lg = 7 - lps;  // log2 of a page's tokens, of a block's pages
+    // page ids: two groups of blocks ahead, across pieces
+    QGroups cur(p, lg), ahead(p, lg);
+    int id = ahead.page_id(p, lg, lane);
+    ahead.step(p, lg);
+    int id1 = ahead.page_id(p, lg, lane);
+    ahead.step(p, lg);
+    float* scales = reinterpret_cast<float*>(smem + L::kScOff);
+    uint32_t stage = 0, par = 1, n = 0;
+    bool fail = false;
+    // The query rows, by the V warp (whose ring is the slower one to free): of
+    // the first piece before its first page, of each later one once the first
+    // pages of the piece before it are on their way.  Rows and RoPE table row land in shared memory a piece
+    // earlier still.  Rolled loops: a piece runs this code once, and unrolled
+    // it took 3 us, most of it fetching instructions.
+    uint8_t* row_stage = smem + L::kRowOff;
+    QWalk qwalk(p);
+    uint32_t q_it = 0;
+    bool q_more = false;
+    auto fetch_rows = [&]() {
+      QPiece q;
+      q_more = qwalk.next(p, &q);
+      if (q_more) {
+        uint8_t* to = row_stage + (q_it & 1) * L::kRowBytes;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+            p.q + (static_cast<int64_t>(q.seq) * p.hq + q.g * MG) * kHeadDim);
+        for (int i = lane; i < MG * 16; i += 32) cp_async16(to + i * 16, src + i * 16);
+        if (p.rope_table)
+          cp_async16(to + MG * 256 + lane * 16,
+                     p.rope_table + static_cast<int64_t>(q.kv_len - 1) * kHeadDim + lane * 4);
       }
+      cp_async_commit();
     };
-    bool more = walk.next(p, &pc);
-    if (more) fetch(pc, pc.block0() >> (9 - lg));
-    while (more) {
-      const QPiece cur = pc;
-      int cached = -1;
-      bool fetched = false;  // the next piece's window is in pg
-      bool fail = false;
-      for (int b = cur.block0(); b < cur.block1(); ++b) {
-        bool ok = mbar_wait(empty_b + stage, par, abort, p.err, is_v ? 0xb03 : 0xb02);
-        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
-        uint8_t* dst = ring + stage * L::kKVBytes;
-        const int n_tok = min(B, cur.kv_len - b * B);
-        const int n_pg = (n_tok + ps - 1) / ps;
-        const int win = b >> (9 - lg);
-        if (cached != win) {
-          if (cached >= 0) fetch(cur, win);
-          __syncwarp();
-#pragma unroll
-          for (int t = 0; t < L::kPageWin / 32; ++t) wc[lane + 32 * t] = pg[t];
-          __syncwarp();
-          cached = win;
-          if ((cur.block1() - 1) >> (9 - lg) == win) {  // the last window of this piece
-            more = walk.next(p, &pc);
-            if (more) fetch(pc, pc.block0() >> (9 - lg));
-            fetched = true;
-          }
-        }
-        if (lane == 0) mbar_arrive_expect_tx(full_b + stage, n_pg * ps * 128);
-        __syncwarp();
-        if (lane < n_pg) {
-          int32_t pe = wc[((b << lg) & (L::kPageWin - 1)) + lane];
-          if (pe < 0 || pe >= p.n_pages) {
-            report_error(p.err, kErrBadPage, 0xb04);
-            pe = p.n_pages;  // out of range: the copy reads the zero fill
-          }
-          tma_load_3d(dst + lane * ps * 128, map, full_b + stage, 0, 0, pe * p.hkv + cur.g);
-        }
-        if (++stage == static_cast<uint32_t>(S)) {
-          stage = 0;
-          par ^= 1;
-        }
-      }
-      if (fail || *abort || !fetched) break;
-    }
-  } else if (warp == 14) {
-    // ------------------------------------------------------------ queries, S issuer
-    constexpr uint32_t kIdS = idesc_e4m3(128, N, false, false);  // A = K (K-major), B = Q pieces (K-major)
-    const uint32_t leader = elect_one_sync();
-    uint32_t stage = 0, kpar = 0, s_it = 0, q_it = 0;
-    while (walk.next(p, &pc)) {
-      // ---- the query rows
+    auto split_rows = [&]() -> bool {  // of the piece fetch_rows took
+      if (!q_more) return true;
       const uint32_t qslot = q_it & 1;
-      // lane l holds elements 4 l .. 4 l + 3 of every row
-      uint2 x[MG];
-#pragma unroll
-      for (int i = 0; i < MG; ++i)
-        x[i] = __ldg(reinterpret_cast<const uint2*>(
-                         p.q + (static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + i) * kHeadDim) + lane);
-      float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
-      if (p.rope_table) {
-        const float* trow = p.rope_table + static_cast<int64_t>(pc.kv_len - 1) * kHeadDim;
-        c = __ldg(reinterpret_cast<const float4*>(trow) + (lane & 15));
-        s = __ldg(reinterpret_cast<const float4*>(trow + 64) + (lane & 15));
-      }
-      bool ok = mbar_wait(&bars[L::kQEmpty + qslot], ((q_it >> 1) & 1) ^ 1, abort, p.err, 0xb11);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      ++q_it;
+      cp_async_wait<0>();
+      __syncwarp();
+      if (!wait_warp(&bars[L::kQEmpty + qslot], ((q_it >> 1) & 1) ^ 1, abort, p.err, 0xb31)) return false;
+      const uint8_t* rows = row_stage + qslot * L::kRowBytes;
       uint8_t* tile = q_base + qslot * L::kTBytes;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < MG; ++i) {
-        uint32_t w[2] = {x[i].x, x[i].y};
+        // lane l: elements 4 l .. 4 l + 3
+        const uint2 x = *reinterpret_cast<const uint2*>(rows + i * 256 + lane * 8);
+        float v[4] = {bf16_lo_as_f32(x.x), bf16_hi_as_f32(x.x), bf16_lo_as_f32(x.y), bf16_hi_as_f32(x.y)};
         if (p.rope_table) {
           // the pair of element e is e +- 64, 16 lanes away
-          const uint32_t o[2] = {__shfl_xor_sync(0xffffffffu, w[0], 16), __shfl_xor_sync(0xffffffffu, w[1], 16)};
+          const uint2 o = *reinterpret_cast<const uint2*>(rows + i * 256 + (lane ^ 16) * 8);
+          const float4 c = *reinterpret_cast<const float4*>(rows + MG * 256 + (lane & 15) * 16);
+          const float4 s = *reinterpret_cast<const float4*>(rows + MG * 256 + 256 + (lane & 15) * 16);
+          const float w[4] = {bf16_lo_as_f32(o.x), bf16_hi_as_f32(o.x), bf16_lo_as_f32(o.y), bf16_hi_as_f32(o.y)};
           const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-          float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float xe = (e & 1) ? bf16_hi_as_f32(w[e >> 1]) : bf16_lo_as_f32(w[e >> 1]);
-            const float oe = (e & 1) ? bf16_hi_as_f32(o[e >> 1]) : bf16_lo_as_f32(o[e >> 1]);
             float y0, y1;
-            rope_pair(lane < 16 ? xe : oe, lane < 16 ? oe : xe, cc[e], ss[e], y0, y1);
-            y[e] = lane < 16 ? y0 : y1;
+            rope_pair(lane < 16 ? v[e] : w[e], lane < 16 ? w[e] : v[e], cc[e], ss[e], y0, y1);
+            v[e] = __uint_as_float(static_cast<uint32_t>(f32_to_bf16_rn(lane < 16 ? y0 : y1)) << 16);
           }
-          w[0] = pack_bf16x2(y[0], y[1]);
-          w[1] = pack_bf16x2(y[2], y[3]);
         }
-        float v[4] = {bf16_lo_as_f32(w[0]), bf16_hi_as_f32(w[0]), bf16_lo_as_f32(w[1]), bf16_hi_as_f32(w[1])};
         // the row's largest finite magnitude to [128, 256)
         float m = 0.0f;
 #pragma unroll
@@ -579,15 +586,81 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       }
       fence_proxy_async_smem();
       warp_arrive(&bars[L::kQFull + qslot], lane);
-      // ---- the products
+      ++q_it;
+      fetch_rows();
+      return true;
+    };
+    if (is_v) {
+      fetch_rows();
+      fail = !split_rows();
+    }
+    while (cur.ok && !fail) {
+      const int id2 = ahead.page_id(p, lg, lane);
+      ahead.step(p, lg);
+      // the (page, head) row of the codes; out of range: past the last one,
+      // where the copy reads the zero fill
+      int row = id * p.hkv + cur.pc.g;
+      const bool bad = static_cast<unsigned>(id) >= static_cast<unsigned>(p.n_pages);
+      const bool real = lane < cur.n << lg && ((cur.b << lg) + lane) << lps < cur.pc.kv_len;  // a page of the group
+      if (bad) row = p.n_pages * p.hkv;
+      if (bad && real) report_error(p.err, kErrBadPage, 0xb04);
+      for (int i = 0; i < cur.n; ++i) {
+        const bool ok = wait_warp(empty_b + stage, par, abort, p.err, is_v ? 0xb03 : 0xb02);
+        if (!ok) { fail = true; break; }
+        if (!is_v && i == 0) {
+          // the group's scales, with its first block's codes: by now the
+          // softmax has read those of block n - kSK - kSS, so the ring has room
+          if (real) {
+            float* to = scales + ((n + (lane >> lg)) % L::kScRing) * 16 + (lane & ((1 << lg) - 1));
+            cp_async4(to, bad ? &g_unit_scale : p.k_scale + row);
+            cp_async4(to + L::kScRing * 16, bad ? &g_unit_scale : p.v_scale + row);
+          }
+          for (int k = 0; k < cur.n; ++k) cp_async_arrive(&bars[L::kScales + (n + k) % L::kScRing]);
+          n += cur.n;
+        }
+        uint8_t* dst = ring + stage * L::kKVBytes;
+        const int n_pg = (min(B, cur.pc.kv_len - (cur.b + i) * B) + (1 << lps) - 1) >> lps;
+        if (lane == 0) mbar_arrive_expect_tx(full_b + stage, (n_pg << lps) * 128);
+        __syncwarp();
+        // one copy a page, issued by one lane in a loop the whole warp walks
+        // (issued by the lanes that hold the page ids, one lane after another,
+        // they took more than a block's time at HBM rate)
+#pragma unroll 4
+        for (int k = 0; k < n_pg; ++k) {
+          const int r = __shfl_sync(0xffffffffu, row, (i << lg) + k);
+          if (leader) tma_load_3d(dst + ((k << lps) * 128), map, full_b + stage, 0, 0, r);
+        }
+        if (++stage == static_cast<uint32_t>(S)) {
+          stage = 0;
+          par ^= 1;
+        }
+      }
+      if (is_v && !fail && cur.b == cur.pc.block0()) fail = !split_rows();
+      cur.step(p, lg);
+      id = id1;
+      id1 = id2;
+    }
+    cp_async_wait<0>();
+  } else if (warp == 14) {
+    // ------------------------------------------------------------ S issuer
+    constexpr uint32_t kIdS = idesc_e4m3(128, N, false, false);  // A = K (K-major), B = Q pieces (K-major)
+    const uint32_t leader = elect_one_sync();
+    uint32_t stage = 0, kpar = 0, s_it = 0, q_it = 0;
+    QWalk walk(p);
+    QPiece pc;
+    while (walk.next(p, &pc)) {
+      const uint32_t qslot = q_it & 1;
+      const bool ok = wait_warp(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb11);
+      if (!ok) break;
+      ++q_it;
       const Desc qd = make_desc(smem_u32(q_base + qslot * L::kTBytes), 16, 1024);
       bool fail = false;
       const int b1 = pc.block1();
       for (int b = pc.block0(); b < b1; ++b, ++s_it) {
         const uint32_t slot = s_it % SS;
-        bool w = mbar_wait(&bars[L::kKFull + stage], kpar, abort, p.err, 0xb12);
-        w = w && mbar_wait(&bars[L::kSEmpty + slot], ((s_it / SS) & 1) ^ 1, abort, p.err, 0xb13);
-        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        bool w = wait_warp(&bars[L::kKFull + stage], kpar, abort, p.err, 0xb12);
+        w = w && wait_warp(&bars[L::kSEmpty + slot], ((s_it / SS) & 1) ^ 1, abort, p.err, 0xb13);
+        if (!w) { fail = true; break; }
         tc_fence_after();
         const Desc kd = make_desc(smem_u32(k_base + stage * L::kKVBytes), 16, 1024);
         const uint32_t d = tm_s + slot * N;
@@ -612,13 +685,15 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     constexpr uint32_t kIdO = idesc_e4m3(128, N, true, true);  // A = V^T (dims contiguous), B = P^T (pieces contiguous)
     const uint32_t leader = elect_one_sync();
     uint32_t stage = 0, vpar = 0, o_it = 0;
+    QWalk walk(p);
+    QPiece pc;
     while (walk.next(p, &pc)) {
       bool fail = false;
       const int b1 = pc.block1();
       for (int b = pc.block0(); b < b1; ++b, ++o_it) {
         const uint32_t oslot = o_it % OS, pslot = o_it % PS;
-        bool w = mbar_wait(&bars[L::kVFull + stage], vpar, abort, p.err, 0xb22);
-        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        bool w = wait_warp(&bars[L::kVFull + stage], vpar, abort, p.err, 0xb22);
+        if (!w) { fail = true; break; }
         uint8_t* vd = v_base + stage * L::kKVBytes;
         // V rows past the context may hold anything, NaN codes among it; P is
         // exactly 0 there, so zero them (0 * NaN = NaN)
@@ -629,9 +704,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        w = mbar_wait(&bars[L::kPFull + pslot], (o_it / PS) & 1, abort, p.err, 0xb21);
-        w = w && mbar_wait(&bars[L::kOEmpty + oslot], ((o_it / OS) & 1) ^ 1, abort, p.err, 0xb23);
-        if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+        w = wait_warp(&bars[L::kPFull + pslot], (o_it / PS) & 1, abort, p.err, 0xb21);
+        w = w && wait_warp(&bars[L::kOEmpty + oslot], ((o_it / OS) & 1) ^ 1, abort, p.err, 0xb23);
+        if (!w) { fail = true; break; }
         tc_fence_after();
         // K-step s covers keys 32 s .. 32 s + 31: V rows 4096 B a step, P^T
         // 32 N B a step
@@ -664,47 +739,16 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const float sl = p.scale_log2;
     const int lps = 31 - __clz(p.page_size);
     uint32_t s_base = 0, sy_it = 0, q_it = 0;
-    // the scales of this thread's key: page ids two own blocks ahead, the
-    // scales themselves one ahead, across pieces too
-    auto page_of = [&](const QPiece& q, int j) -> int {
-      const int key = (q.block0() + j) * B + t;
-      return (q.block0() + j < q.block1() && key < q.kv_len)
-                 ? __ldg(p.page_table + static_cast<int64_t>(q.seq) * p.max_pages + (key >> lps))
-                 : -1;
-    };
-    auto scales_of = [&](const QPiece& q, int pg, float& sk, float& sv) {
-      sk = sv = 1.0f;
-      if (pg >= 0 && pg < p.n_pages) {
-        const int64_t i = static_cast<int64_t>(pg) * p.hkv + q.g;
-        sk = __ldg(p.k_scale + i);
-        sv = __ldg(p.v_scale + i);
-      }
-    };
-    float sk, sv, sk0 = 1.0f, sv0 = 1.0f;
-    int pg0 = -1, pg1 = -1;
-    bool more = walk.next(p, &pc);
-    if (more) {
-      pg0 = page_of(pc, grp);
-      pg1 = page_of(pc, grp + 2);
-      scales_of(pc, pg0, sk0, sv0);
-    }
-    while (more) {
-      const QPiece cur = pc;
-      const int kv_len = cur.kv_len, b0 = cur.block0(), nb = cur.block1() - b0;
+    const float* k_scales = reinterpret_cast<const float*>(smem + L::kScOff) + (t >> lps);
+    const float* v_scales = k_scales + L::kScRing * 16;
+    QWalk walk(p);
+    QPiece pc;
+    while (walk.next(p, &pc)) {
+      const int kv_len = pc.kv_len, b0 = pc.block0(), nb = pc.block1() - b0;
       const int j0 = static_cast<int>(s_base & 1) == grp ? 0 : 1;
-      sk = sk0;
-      sv = sv0;
-      int pg_next = pg1;
-      more = walk.next(p, &pc);
-      if (more) {
-        const int j0n = static_cast<int>((s_base + nb) & 1) == grp ? 0 : 1;
-        pg0 = page_of(pc, j0n);
-        pg1 = page_of(pc, j0n + 2);
-      }
-      bool ahead = false;
       const uint32_t qslot = q_it & 1;
-      bool ok = mbar_wait(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb41);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      bool ok = wait_warp(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb41);
+      if (!ok) break;
       ++q_it;
       float qs[MG];
 #pragma unroll
@@ -714,11 +758,12 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       for (int j = j0; j < nb; j += 2) {
         const uint32_t s_it = s_base + j;
         const uint32_t slot = s_it % SS;
-        float sk_next, sv_next;
-        scales_of(cur, pg_next, sk_next, sv_next);
-        pg_next = page_of(cur, j + 4);
-        ok = mbar_wait(&bars[L::kSFull + slot], (s_it / SS) & 1, abort, p.err, 0xb42);
-        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        // the scales of this thread's key
+        const uint32_t isl = s_it % L::kScRing;
+        ok = wait_warp(&bars[L::kScales + isl], (s_it / L::kScRing) & 1, abort, p.err, 0xb46);
+        const float sk = k_scales[isl * 16], sv = v_scales[isl * 16];
+        ok = ok && wait_warp(&bars[L::kSFull + slot], (s_it / SS) & 1, abort, p.err, 0xb42);
+        if (!ok) { fail = true; break; }
         tc_fence_after();
         uint32_t raw[N];
         TmemRow<N>::ld(tm_s + lane_off + slot * N, raw);
@@ -742,9 +787,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           if (lane == 0) red[(rb * (MG + 1) + MG) * 4 + w] = m;
         }
         warp_arrive(&bars[L::kSyncMax + grp * 2 + rb], lane);
-        ok = mbar_wait(&bars[L::kSyncMax + grp * 2 + rb], (sy_it >> 1) & 1, abort, p.err, 0xb43);
+        ok = wait_warp(&bars[L::kSyncMax + grp * 2 + rb], (sy_it >> 1) & 1, abort, p.err, 0xb43);
         ++sy_it;
-        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        if (!ok) { fail = true; break; }
         auto max4 = [&](int q) {
           const float4 r = *reinterpret_cast<const float4*>(red + (rb * (MG + 1) + q) * 4);
           return max_nan(max_nan(r.x, r.y), max_nan(r.z, r.w));
@@ -758,8 +803,8 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // the block's V anchor A = 2^(ae - 127); w = p (sv 2^7 / A)
         const int ae = max(static_cast<int>(__float_as_uint(max4(MG)) >> 23), 8);
         const float wf = vis ? __fmul_rn(sv, pow2_bits(261 - ae)) : 0.0f;
-        ok = mbar_wait(&bars[L::kPEmpty + grp], ((s_it / PS) & 1) ^ 1, abort, p.err, 0xb44);
-        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        ok = wait_warp(&bars[L::kPEmpty + grp], ((s_it / PS) & 1) ^ 1, abort, p.err, 0xb44);
+        if (!ok) { fail = true; break; }
         uint32_t pw[N / 4];
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) pw[i] = 0u;
@@ -778,25 +823,22 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // 1), so 26 fraction bits of fixed point lose less than FP32 sums
         // would, in one instruction and in no order
         uint32_t* st = stats + (s_it % SR) * L::kStatWords;
+        uint32_t l_mine = 0;  // lane q: query head q's
+        float m_mine = 0.0f;
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
           const uint32_t l = __reduce_add_sync(0xffffffffu, __float2uint_rn(__fmul_rn(pr[q], kLUnit)));
-          if (lane == 0) {
-            st[q * 4 + w] = l;
-            if (w == 0) st[4 * MG + q] = __float_as_uint(mc[q]);
-          }
+          l_mine = lane == q ? l : l_mine;
+          m_mine = lane == q ? mc[q] : m_mine;
         }
-        if (w == 0 && lane == 0) st[5 * MG] = __float_as_uint(pow2_bits(ae - 7));  // PV carries 2^7 / A
+        if (lane < MG) st[lane * 4 + w] = l_mine;
+        if (w == 0) {
+          if (lane == MG) m_mine = pow2_bits(ae - 7);  // PV carries 2^7 / A
+          if (lane <= MG) st[4 * MG + lane] = __float_as_uint(m_mine);
+        }
         warp_arrive(&bars[L::kStatsFull + (s_it % SR)], lane);
-        if (!ahead) {  // the page ids have landed meanwhile
-          if (more) scales_of(pc, pg0, sk0, sv0);
-          ahead = true;
-        }
-        sk = sk_next;
-        sv = sv_next;
       }
       if (fail) break;
-      if (!ahead && more) scales_of(pc, pg0, sk0, sv0);
       s_base += nb;
     }
   } else {
@@ -804,6 +846,42 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const int d = tid;  // head dimension lane
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     uint32_t o_it = 0, cut_it = 0;
+    struct Cut {
+      int seq, g, n, ns;
+    } cut0 = {}, cut1 = {};
+    int n_cut = 0;
+    bool fail = false;
+    // Counts the cut pieces and folds the pairs they complete: every
+    // thread's states are in device memory before the count, and the CTA that
+    // counts a pair's last segment reads them after it.
+    auto flush = [&]() -> bool {
+      __threadfence();
+      warp_arrive(&bars[L::kStored], lane);
+      if (warp == 0) {
+        const bool ok = wait_warp(&bars[L::kStored], cut_it & 1, abort, p.err, 0xb54);
+        if (!ok) return false;
+        if (lane < n_cut) {
+          const Cut q = lane == 0 ? cut0 : cut1;
+          last_flag[lane] = count_segments(p.counts + static_cast<int64_t>(q.seq) * p.hkv + q.g, p.nonce, q.n, q.ns);
+          __threadfence();
+        }
+        warp_arrive(&bars[L::kCounted], lane);
+      }
+      const bool ok = wait_warp(&bars[L::kCounted], cut_it & 1, abort, p.err, 0xb55);
+      if (!ok) return false;
+      ++cut_it;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        if (i >= n_cut || !last_flag[i]) continue;
+        __threadfence();
+        const Cut c = i == 0 ? cut0 : cut1;
+        for (int q = warp; q < MG; q += 4) fold_pair(p, c.seq, c.ns, c.g * MG + q, lane);
+      }
+      n_cut = 0;
+      return true;
+    };
+    QWalk walk(p);
+    QPiece pc;
     while (walk.next(p, &pc)) {
       const bool whole = pc.whole();
       // O: the segment's, T: the sequence's (whole pairs); lane q holds m and
@@ -813,12 +891,11 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       for (int q = 0; q < MG; ++q) O[q] = T[q] = 0.0f;
       float m = 0.0f, l = 0.0f, mt = 0.0f, lt = 0.0f;
       const int b1 = pc.block1();
-      bool fail = false;
       for (int b = pc.block0(); b < b1; ++b) {
         const uint32_t sslot = o_it % SR, oslot = o_it % OS;
-        bool ok = mbar_wait(&bars[L::kStatsFull + sslot], (o_it / SR) & 1, abort, p.err, 0xb51);
-        ok = ok && mbar_wait(&bars[L::kOFull + oslot], (o_it / OS) & 1, abort, p.err, 0xb52);
-        if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
+        bool ok = wait_warp(&bars[L::kStatsFull + sslot], (o_it / SR) & 1, abort, p.err, 0xb51);
+        ok = ok && wait_warp(&bars[L::kOFull + oslot], (o_it / OS) & 1, abort, p.err, 0xb52);
+        if (!ok) { fail = true; break; }
         tc_fence_after();
         uint32_t raw[N];
         TmemRow<N>::ld(tm_o + lane_off + oslot * N, raw);
@@ -898,31 +975,16 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         }
         if (warp == 0 && lane < MG && p.lse)
           p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
+        if (n_cut > 0 && !flush()) break;
         continue;
       }
-      // a part of a pair: every thread's states are in device memory before
-      // the segments are counted; the CTA that counts the last one folds
-      __threadfence();
-      warp_arrive(&bars[L::kStored], lane);
-      if (warp == 0) {
-        bool ok = mbar_wait(&bars[L::kStored], cut_it & 1, abort, p.err, 0xb54);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (lane == 0) {
-          *last_flag = count_segments(p.counts + static_cast<int64_t>(pc.seq) * p.hkv + pc.g, p.nonce, pc.s1 - pc.s0,
-                                      pc.ns);
-          __threadfence();
-          mbar_arrive(&bars[L::kCounted]);
-        }
-        __syncwarp();
-      }
-      bool ok = mbar_wait(&bars[L::kCounted], cut_it & 1, abort, p.err, 0xb55);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      ++cut_it;
-      if (*last_flag) {
-        __threadfence();
-        for (int q = warp; q < MG; q += 4) fold_pair(p, pc, pc.g * MG + q, lane);
-      }
+      // a part of a pair: counted once the next piece is done too (waiting
+      // here for the stores and the count would hold up the blocks behind)
+      cut1 = cut0;
+      cut0 = {pc.seq, pc.g, pc.s1 - pc.s0, pc.ns};
+      if (++n_cut == 2 && !flush()) break;
     }
+    if (!fail && n_cut > 0) flush();
   }
 
   // ---------------------------------------------------------------- teardown

@@ -454,9 +454,10 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
  * counterpart of rlk_attn_decode_paged, _splitk and _rope in one call.
  *   q: device BF16 [num_seqs, Hq, 128]; seqlens: HOST [num_seqs], context
  *     lengths 1 .. max_pages * page_size; outputs as rlk_attn_decode_paged;
- *   split_k: how the work is spread over the SMs, never what it computes:
- *     0 = the blocks of all sequences and KV heads, cut evenly (the choice
- *     for speed); k = 1 .. 64 = k items per (sequence, KV head);
+ *   split_k: how the work is spread over the SMs, never what it computes: the
+ *     blocks of all sequences and KV heads are cut evenly over the SMs, a
+ *     (sequence, KV head) into at most split_k (1 .. 64) equal parts, or into
+ *     as many as even the load (0, the choice for speed);
  *   rope_table: NULL, or device: q is pre-RoPE and rotated at position
  *     seqlens[s] - 1 (< rope_max_pos) as in rlk_attn_decode_paged_rope;
  *   workspace: for split_k != 1, device, 16-byte aligned,
