@@ -1347,8 +1347,9 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
     dp.ctx[s] = seqlens[s];
     blocks += (static_cast<int64_t>(seqlens[s]) + B - 1) / B * hkv;
     segments += qdecode_segments(seqlens + s, 1);
-    if (blocks > INT32_MAX - 1024 || segments * hq > INT32_MAX)
-      return fail(RLK_ERR_UNSUPPORTED, "more than 2^31 (block, KV head) or (segment, query head) pairs in one launch");
+    if (4 * blocks + static_cast<int64_t>(rlk::kPairCost) * hkv * params->num_seqs > INT32_MAX - 1024 ||
+        segments * hq > INT32_MAX)
+      return fail(RLK_ERR_UNSUPPORTED, "more than 2^29 (block, KV head) or 2^31 (segment, query head) pairs in one launch");
     dp.blk0[s + 1] = static_cast<int32_t>(blocks);
     dp.seg0[s + 1] = static_cast<int32_t>(segments);
   }
@@ -1377,8 +1378,9 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   dp.page_size = cache.page_size;
   dp.max_pages = cache.max_pages;
   dp.split_k = split_k;
-  dp.part_q = static_cast<int32_t>(blocks / grid);
-  dp.part_r = static_cast<int32_t>(blocks % grid);
+  const int64_t cost = 4 * blocks + static_cast<int64_t>(rlk::kPairCost) * hkv * params->num_seqs;
+  dp.part_q = static_cast<int32_t>(cost / grid);
+  dp.part_r = static_cast<int32_t>(cost % grid);
   dp.rope_table = rope_table;
   dp.out_f32 = out_f32;
   dp.out_bf16 = static_cast<uint16_t*>(out_bf16);

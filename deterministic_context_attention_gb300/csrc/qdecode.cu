@@ -28,8 +28,9 @@
 // out per block, took 125 us for 4 sequences where the pages take 40.)
 //
 // Work split.  The blocks of all (sequence, KV head) pairs in order form one
-// line; CTA c of g takes its c-th g-th part, cut at segment boundaries, so the
-// SMs' loads differ by a segment at the most and no plan is built on the host.
+// line; CTA c of g takes its c-th g-th part by cost (a pair counts 1.5 blocks
+// more than it has), cut at segment boundaries, so the SMs' loads differ by a
+// segment at the most and no plan is built on the host.
 // A CTA that holds a whole pair writes its output; otherwise each segment's
 // state goes to the workspace and the CTA that adds the last segment of a pair
 // (an atomic count; which one it is changes nothing in the result) folds them.
@@ -106,7 +107,9 @@ struct QDecLayout {
   static constexpr int kScOff = (kMiscOff + 16 + 15) / 16 * 16;  // float [K, V][kScRing][16 pages]
   static constexpr int kRowOff = kScOff + 2 * kScRing * 16 * 4;  // staged query rows and RoPE table row
   static constexpr int kRowBytes = MG * 256 + 512;
-  static constexpr int kTotal = kRowOff + kQS * kRowBytes;
+  static constexpr int kFoldGroups = N == 16 ? 4 : 3;  // per correction warp: segment states being folded
+  static constexpr int kFoldOff = kRowOff + kQS * kRowBytes;
+  static constexpr int kTotal = kFoldOff + 4 * kFoldGroups * 4 * 512;
   static constexpr int kAlloc = kTotal + 1024;
   static constexpr int kTmemCols = N * (kSS + kOS);
   static_assert(kAlloc <= 232448, "decode shared memory");
@@ -257,32 +260,37 @@ struct QWalk {
     const int at = cut(p, blockIdx.x);
     left = cut(p, blockIdx.x + 1) - at;
     if (left <= 0) return;
-    seq = seq_of(p, at);
+    int hi = p.num_seqs - 1;
+    while (seq < hi) {
+      const int mid = (seq + hi + 1) >> 1;
+      if (p.blk0[mid] <= at) seq = mid;
+      else hi = mid - 1;
+    }
     const int nb = (p.ctx[seq] + 127) / 128, r = at - p.blk0[seq];
     g = r / nb;
     b = r - g * nb;
   }
-  static __device__ int seq_of(const QDecodeParams& p, int x) {
+  // the line's place where sequence s begins, in quarters of a block
+  static __device__ int cost0(const QDecodeParams& p, int s) { return 4 * p.blk0[s] + kPairCost * p.hkv * s; }
+  // the c-th part's start, as a block of the line: part_q of its cost a part
+  // and one more for the first part_r, from there on to the next segment, or
+  // (split_k) the next of the at most split_k equal runs of segments a pair
+  // may be cut into
+  static __device__ int cut(const QDecodeParams& p, int c) {
+    const int x = c * p.part_q + min(c, p.part_r);
+    if (x >= cost0(p, p.num_seqs)) return p.blk0[p.num_seqs];
     int lo = 0, hi = p.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.blk0[mid] <= x) lo = mid;
+      if (cost0(p, mid) <= x) lo = mid;
       else hi = mid - 1;
     }
-    return lo;
-  }
-  // the c-th part's start: part_q blocks a part and one more for the first
-  // part_r, from there on to the next segment, or (split_k) the next of the
-  // at most split_k equal runs of segments a pair may be cut into
-  static __device__ int cut(const QDecodeParams& p, int c) {
-    const int x = c * p.part_q + min(c, p.part_r);
-    if (x >= p.blk0[p.num_seqs]) return p.blk0[p.num_seqs];
-    const int s = seq_of(p, x);
-    const int nb = (p.ctx[s] + 127) / 128;
-    const int b = (x - p.blk0[s]) % nb;
+    const int nb = (p.ctx[lo] + 127) / 128;
+    const int r = x - cost0(p, lo), pair = r / (4 * nb + kPairCost);
+    const int b = max(r - pair * (4 * nb + kPairCost) - kPairCost + 3, 0) / 4;
     int step = kSegBlocks;
     if (p.split_k) step *= ((nb + kSegBlocks - 1) / kSegBlocks + p.split_k - 1) / p.split_k;
-    return x - b + min((b + step - 1) / step * step, nb);
+    return p.blk0[lo] + pair * nb + min((b + step - 1) / step * step, nb);
   }
   __device__ bool next(const QDecodeParams& p, QPiece* q) {
     if (left <= 0) return false;
@@ -368,50 +376,72 @@ __device__ __forceinline__ bool count_segments(unsigned long long* word, uint64_
 }
 
 // The fold of a cut pair's segment states, one warp a query head: lane l
-// takes head dimensions 4 l .. 4 l + 3; chunks of C segments, the next chunk's
-// reads in flight while one folds.
-__device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, int h, int lane) {
-  constexpr int C = 8;
+// takes head dimensions 4 l .. 4 l + 3.  Groups of 4 segments are copied ahead
+// into the warp's ring (a lane reads what it copied itself); lane i's (m, l)
+// are those of segment 32 k + i.  One warp a scheduler, so what costs is the
+// chain of dependent steps: the maxima of a group first, then its factors side
+// by side, then the sums; past the last segment m = -inf (a factor of 0).
+template <int GROUPS>
+__device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, int h, int lane, float4* ring) {
+  constexpr int C = 4;
   const int64_t base = static_cast<int64_t>(p.seg0[seq]) * p.hq + h;
-  auto load = [&](int c0, float2& ml, float4 (&v)[C]) {
-    const int64_t r = base + static_cast<int64_t>(min(c0 + (lane & (C - 1)), ns - 1)) * p.hq;
-    ml = __ldcg(reinterpret_cast<const float2*>(p.state_ml) + r);
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      v[i] = __ldcg(reinterpret_cast<const float4*>(
-                        p.state_o + (base + static_cast<int64_t>(min(c0 + i, ns - 1)) * p.hq) * kHeadDim) +
-                    lane);
+  const int64_t pitch = static_cast<int64_t>(p.hq) * kHeadDim;
+  const float* src = p.state_o + base * kHeadDim + 4 * lane;
+  const float2* sml = reinterpret_cast<const float2*>(p.state_ml) + base;
+  auto load_ml = [&](int c0) {
+    return c0 + lane < ns ? __ldcg(sml + static_cast<int64_t>(c0 + lane) * p.hq) : make_float2(-INFINITY, 0.f);
   };
-  float4 v[C], vn[C];
-  float2 ml, mln = make_float2(0.f, 0.f);
-  load(0, ml, v);
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = 0.f, l = 0.f;
-  for (int c0 = 0; c0 < ns; c0 += C) {
-    if (c0 + C < ns) load(c0 + C, mln, vn);
+  int next = 0;  // the next segment to copy
+  float4* to = ring + lane;
+  auto copy = [&]() {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const float mb = __shfl_sync(0xffffffffu, ml.x, i), lb = __shfl_sync(0xffffffffu, ml.y, i);
-      if (c0 + i >= ns) continue;
-      if (c0 + i == 0) {
-        O = v[0];
-        m = mb;
-        l = lb;
-      } else {
-        float mn, a, b;
-        fold_factors(m, mb, mn, a, b);
-        O.x = __fmaf_rn(v[i].x, b, __fmul_rn(O.x, a));
-        O.y = __fmaf_rn(v[i].y, b, __fmul_rn(O.y, a));
-        O.z = __fmaf_rn(v[i].z, b, __fmul_rn(O.z, a));
-        O.w = __fmaf_rn(v[i].w, b, __fmul_rn(O.w, a));
-        l = __fmaf_rn(lb, b, __fmul_rn(l, a));
-        m = mn;
-      }
+      if (next + i < ns) cp_async16(to + i * 32, src + i * pitch);
+      else to[i * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    ml = mln;
+    cp_async_commit();
+    next += C;
+    src += C * pitch;
+    to = to + C * 32 == ring + lane + GROUPS * C * 32 ? ring + lane : to + C * 32;
+  };
+  float2 ml = load_ml(0), ml_next = load_ml(32);
+#pragma unroll 1
+  for (int c = 0; c < GROUPS; ++c) copy();
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int s = 0; s < ns; s += C) {
+    float mb[C], lb[C], a[C], b[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = vn[i];
+    for (int i = 0; i < C; ++i) {
+      mb[i] = __shfl_sync(0xffffffffu, ml.x, (s + i) & 31);
+      lb[i] = __shfl_sync(0xffffffffu, ml.y, (s + i) & 31);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float mn;
+      fold_factors(m, mb[i], mn, a[i], b[i]);
+      m = mn;
+    }
+    cp_async_wait<GROUPS - 1>();
+    float4 v[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = to[i * 32];  // the slot the next copy fills is the oldest one
+    copy();
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      O.x = __fmaf_rn(v[i].x, b[i], __fmul_rn(O.x, a[i]));
+      O.y = __fmaf_rn(v[i].y, b[i], __fmul_rn(O.y, a[i]));
+      O.z = __fmaf_rn(v[i].z, b[i], __fmul_rn(O.z, a[i]));
+      O.w = __fmaf_rn(v[i].w, b[i], __fmul_rn(O.w, a[i]));
+      l = __fmaf_rn(lb[i], b[i], __fmul_rn(l, a[i]));
+    }
+    if (((s + C) & 31) == 0) {
+      ml = ml_next;
+      ml_next = load_ml(s + C + 32);
+    }
   }
+  cp_async_wait<0>();
   const float r = __frcp_rn(l);
   O = make_float4(__fmul_rn(O.x, r), __fmul_rn(O.y, r), __fmul_rn(O.z, r), __fmul_rn(O.w, r));
   const int64_t row = static_cast<int64_t>(seq) * p.hq + h;
@@ -875,7 +905,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         if (i >= n_cut || !last_flag[i]) continue;
         __threadfence();
         const Cut c = i == 0 ? cut0 : cut1;
-        for (int q = warp; q < MG; q += 4) fold_pair(p, c.seq, c.ns, c.g * MG + q, lane);
+        for (int q = warp; q < MG; q += 4)
+          fold_pair<L::kFoldGroups>(p, c.seq, c.ns, c.g * MG + q, lane,
+                                    reinterpret_cast<float4*>(smem + L::kFoldOff) + warp * L::kFoldGroups * 4 * 32);
       }
       n_cut = 0;
       return true;
@@ -889,7 +921,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       float O[MG], T[MG];
 #pragma unroll
       for (int q = 0; q < MG; ++q) O[q] = T[q] = 0.0f;
-      float m = 0.0f, l = 0.0f, mt = 0.0f, lt = 0.0f;
+      float m = 0.0f, l = 0.0f, mt = -INFINITY, lt = 0.0f;
       const int b1 = pc.block1();
       for (int b = pc.block0(); b < b1; ++b) {
         const uint32_t sslot = o_it % SR, oslot = o_it % OS;
@@ -938,21 +970,15 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // the segment is complete
         const int seg = b / kSegBlocks;
         if (whole) {
-          float ta = 0.0f, tb = 1.0f;
-          if (seg == 0) {
-            mt = m;
-            lt = l;
-          } else {
-            float mn;
-            fold_factors(mt, m, mn, ta, tb);
-            lt = __fmaf_rn(l, tb, __fmul_rn(lt, ta));
-            mt = mn;
-          }
+          float mn, ta, tb;
+          fold_factors(mt, m, mn, ta, tb);
+          lt = __fmaf_rn(l, tb, __fmul_rn(lt, ta));
+          mt = mn;
 #pragma unroll
           for (int q = 0; q < MG; ++q) {
             const float aq = __shfl_sync(0xffffffffu, ta, q);
             const float bq = __shfl_sync(0xffffffffu, tb, q);
-            T[q] = seg == 0 ? O[q] : __fmaf_rn(O[q], bq, __fmul_rn(T[q], aq));
+            T[q] = __fmaf_rn(O[q], bq, __fmul_rn(T[q], aq));
           }
         } else {
           const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + seg) * p.hq + pc.g * MG;
