@@ -217,18 +217,18 @@ rlk_status check_cu(const rlk_attn_params* p, const int32_t* cu_q, const int32_t
 // device work), then the ranges launch in order on the caller's stream, so a
 // bad argument anywhere still fails the call before its first launch.
 template <class Fn>
-rlk_status over_ranges(int num_seqs, Fn&& range_call) {
+rlk_status over_ranges(int num_seqs, Fn&& range_call, int per_launch = rlk::kMaxSeqs) {
   g_dry_run = true;
-  for (int s0 = 0; s0 < num_seqs; s0 += rlk::kMaxSeqs) {
-    const rlk_status st = range_call(s0, std::min(num_seqs, s0 + rlk::kMaxSeqs));
+  for (int s0 = 0; s0 < num_seqs; s0 += per_launch) {
+    const rlk_status st = range_call(s0, std::min(num_seqs, s0 + per_launch));
     if (st) {
       g_dry_run = false;
       return st;
     }
   }
   g_dry_run = false;
-  for (int s0 = 0; s0 < num_seqs; s0 += rlk::kMaxSeqs) {
-    const rlk_status st = range_call(s0, std::min(num_seqs, s0 + rlk::kMaxSeqs));
+  for (int s0 = 0; s0 < num_seqs; s0 += per_launch) {
+    const rlk_status st = range_call(s0, std::min(num_seqs, s0 + per_launch));
     if (st) return st;
   }
   return ok();
@@ -1323,7 +1323,7 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
                 rlk::kDecodeMaxGroup);
   if ((static_cast<int64_t>(cache.n_pages) + 1) * hkv > INT32_MAX)
     return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit (page, head) coordinates");
-  if (params->num_seqs > rlk::kMaxSeqs)
+  if (params->num_seqs > rlk::kQMaxSeqs)
     // each range reuses the workspace from its start (the ranges run in order
     // on the stream, and a range needs no more than the whole call)
     return over_ranges(params->num_seqs, [&](int s0, int s1) {
@@ -1332,7 +1332,7 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
       return qdecode_impl(&rp, adv(q, o * 128, 2), cache.from(s0), seqlens + s0, split_k, rope_table, rope_max_pos,
                           adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4), workspace,
                           workspace_bytes, stream);
-    });
+    }, rlk::kQMaxSeqs);
   rlk::QDecodeParams dp;
   std::memset(&dp, 0, sizeof(dp));
   int64_t blocks = 0, segments = 0;

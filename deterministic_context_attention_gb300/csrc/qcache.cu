@@ -21,7 +21,8 @@
 //
 // Both passes move 3 bytes per element (2 BF16, 1 code) and are bound by
 // HBM; the arithmetic is kept to packed 16-bit integer steps on the BF16
-// words (write) and one multiply per element (read).  A unit of work is one
+// words (write, about 7 a element, where the integer pipe allows 16 at HBM
+// rate) and a multiply or two per element (read).  A unit of work is one
 // (page, head) of K or of V: a warp takes up to 16 of its rows, 16 bytes of
 // BF16 a lane, all loads in flight before the first use; neighbouring warps
 // take neighbouring heads, whose rows are contiguous in the packed tensors.
@@ -40,23 +41,28 @@ constexpr int kQThreads = 256;
 constexpr int kQWarps = kQThreads / 32;
 constexpr int kQEsMin = 14;  // the biased exponent of the smallest block maximum that sets a scale (e = -120)
 
-// One unit: head h of page `page` (of K or V) and its slots [slot0, slot1),
-// which hold the packed rows row0 + slot - slot0.
+// One unit: head `head` of a page (of K or V) and its slots [slot0, slot1),
+// which hold the packed rows row0 + slot - slot0; `part` is the warp's run of
+// R slots of it.
 struct QUnit {
   bool valid;
   bool is_v;
-  int head, slot0, slot1;
+  int head, slot0, slot1, part;
   int64_t row0;   // packed row of slot slot0
   int64_t entry;  // page-table entry
   int pos_slot0;  // position of slot 0's token
 };
-__device__ __forceinline__ QUnit q_unit(const QCacheParams& p, int64_t u) {
+template <int R>
+__device__ __forceinline__ QUnit q_unit(const QCacheParams& p, int warp) {
   QUnit r;
   const int hkv = p.c.hkv, ps = p.c.page_size;
-  const int64_t pk = u / hkv;
+  const int lw = __clz(R) - __clz(ps);  // log2 of the warps of a unit (1 .. 8)
+  const unsigned u = blockIdx.x * static_cast<unsigned>(kQWarps >> lw) + (warp >> lw);
+  r.part = warp & ((1 << lw) - 1);
+  const unsigned pk = u / hkv;
   r.head = static_cast<int>(u - pk * hkv);
   r.is_v = pk & 1;
-  const int64_t pg = pk >> 1;
+  const int pg = static_cast<int>(pk >> 1);
   r.valid = pg < p.page0[p.num_seqs];
   // the sequence of the touched page: the last s with page0[s] <= pg
   int lo = 0, hi = p.num_seqs - 1;
@@ -65,11 +71,12 @@ __device__ __forceinline__ QUnit q_unit(const QCacheParams& p, int64_t u) {
     if (p.page0[mid] <= pg) lo = mid;
     else hi = mid - 1;
   }
+  const int lps = 31 - __clz(ps);
   const int pos0 = p.pos0[lo], n = p.cu[lo + 1] - p.cu[lo];
-  const int logical = pos0 / ps + static_cast<int>(pg - p.page0[lo]);
-  r.pos_slot0 = logical * ps;
+  const int logical = (pos0 >> lps) + (pg - p.page0[lo]);
+  r.pos_slot0 = logical << lps;
   r.slot0 = max(pos0 - r.pos_slot0, 0);
-  r.slot1 = static_cast<int>(min(static_cast<int64_t>(ps), static_cast<int64_t>(pos0) + n - r.pos_slot0));
+  r.slot1 = min(ps, pos0 + n - r.pos_slot0);
   r.row0 = static_cast<int64_t>(p.cu[lo]) + (r.pos_slot0 + r.slot0 - pos0);
   r.entry = static_cast<int64_t>(lo) * p.c.max_pages + logical;
   return r;
@@ -77,32 +84,58 @@ __device__ __forceinline__ QUnit q_unit(const QCacheParams& p, int64_t u) {
 
 __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// Two BF16 magnitudes (sign bits cleared) rounded to 3 mantissa bits; a half
-// at or past 0x7F80 (overflow, Inf or NaN) is settled by fix_pair.
-__device__ __forceinline__ uint32_t round4_pair(uint32_t w) {
-  const uint32_t m = w & 0x7FFF7FFFu;
-  return (m + 0x00070007u + ((m >> 4) & 0x00010001u)) & 0xFFF0FFF0u;
-}
-// Non-finite inputs become 0x7FF0 (the NaN code, which sets no scale);
-// finite ones that rounded past the largest value are held at it; BF16
-// subnormals (which only count where they rounded to a normal) become 0.
-__device__ __forceinline__ uint32_t fix_half(uint32_t m, uint32_t r) {
-  if (m >= 0x7F80u) return 0x7FF0u;
-  if (r >= 0x7F80u) return 0x7F70u;
-  return m < 0x0080u ? 0u : r;
-}
-__device__ __forceinline__ uint32_t fix_pair(uint32_t w, uint32_t r) {
-  const uint32_t m = w & 0x7FFF7FFFu;
-  return fix_half(m & 0xFFFFu, r & 0xFFFFu) | (fix_half(m >> 16, r >> 16) << 16);
+// A BF16 magnitude rounded to 3 mantissa bits (nearest, ties to even).
+__device__ __forceinline__ uint32_t round4(uint32_t m) { return (m + 7u + ((m >> 4) & 1u)) & 0xFFF0u; }
+
+// Eight elements among which there may be what the packed steps do not take:
+// Inf and NaN (which become 0 here, a bit of `nan` each, and set no scale),
+// magnitudes that would round past the largest one (held at 1.875 * 2^127)
+// and subnormals (0).  mx: the largest magnitude of the result.  Out of line:
+// hardly any warp runs it.
+struct Settled {
+  uint4 x;
+  uint32_t mx, nan;
+};
+__device__ __noinline__ Settled settle(uint4 x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  Settled r;
+  r.mx = r.nan = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int sh = 16 * (k & 1);
+    uint32_t h = (w[k >> 1] >> sh) & 0xFFFFu;
+    const uint32_t m = h & 0x7FFFu;
+    if (m >= 0x7F80u) {
+      r.nan |= 1u << k;
+      h = 0;
+    } else if (m >= 0x7F78u) {
+      h = (h & 0x8000u) | 0x7F70u;
+    } else if (m < 0x0080u) {
+      h = 0;
+    }
+    r.mx = max(r.mx, h & 0x7FFFu);
+    w[k >> 1] = (w[k >> 1] & (0xFFFF0000u >> sh)) | (h << sh);
+  }
+  r.x = make_uint4(w[0], w[1], w[2], w[3]);
+  return r;
 }
 
-// Codes of a rounded pair (one in each half's low byte) under the anchor
-// `floor2` = ((es - 14) << 3) + 7 in both halves: exponent field E - es + 14,
-// 0 where that is below 1.
-__device__ __forceinline__ uint32_t encode_pair(uint32_t w, uint32_t r, uint32_t floor2) {
-  const uint32_t t = umax2(r >> 4, floor2) - floor2;  // 0: flushed; otherwise code - 7
-  const uint32_t one = __vminu2(t, 0x00010001u);
-  return (t + one * 7u) | ((w >> 8) & (one << 7));
+// Codes of four elements (two packed BF16 words) under the anchor floor2 =
+// (((es - 14) << 3) + 7) << 4 in both halves: the rounded magnitude less the
+// anchor is the code - 7, or at most 0 where the code's exponent field, E - es
+// + 14, is below 1.  Then, byte by byte: 7 more and the sign where it is not 0.
+__device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, uint32_t floor2) {
+  const uint32_t w[2] = {w0, w1};
+  uint32_t t[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t m = w[k] & 0x7FFF7FFFu;
+    const uint32_t r = (m + 0x00070007u + ((m >> 4) & 0x00010001u)) & 0xFFF0FFF0u;
+    t[k] = (umax2(r, floor2) - floor2) >> 4;
+  }
+  const uint32_t c = __byte_perm(t[0], t[1], 0x6420);
+  const uint32_t nz = (c + 0x7F7F7F7Fu) & 0x80808080u;  // c <= 112: no carry
+  return (c + (nz >> 7) * 7u) | (__byte_perm(w0, w1, 0x7531) & nz);
 }
 
 // An existing code under a scale 2^d times larger (d >= 0).
@@ -116,23 +149,26 @@ __device__ __forceinline__ uint32_t rescale_byte(uint32_t c, int d) {
 // R: rows a warp takes (8 for 8-token pages, else 16).  Lane l holds elements
 // 8 (l mod 16) .. + 7 of rows 2 i + l / 16.
 template <int R, bool ROPE>
-__global__ void __launch_bounds__(kQThreads) rlk_qcache_write_kernel(const __grid_constant__ QCacheParams p) {
+__global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
+    rlk_qcache_write_kernel(const __grid_constant__ QCacheParams p) {
   __shared__ uint32_t s_max[kQWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ps = p.c.page_size, hkv = p.c.hkv;
-  const int wpu = ps / R;  // warps per unit: a power of two up to 8
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kQWarps + warp;
-  const QUnit un = q_unit(p, gw / wpu);
-  const int part = static_cast<int>(gw % wpu);
+  const QUnit un = q_unit<R>(p, warp);
   const int c8 = lane & 15, sub = lane >> 4;
-  const uint16_t* in = un.is_v ? p.v_in : p.k_in;
+  // the warp's slots that are written, and this lane's first (slot of i = 0)
+  const int s_lo = un.valid ? max(un.slot0, un.part * R) : 0;
+  const int s_hi = un.valid ? min(un.slot1, un.part * R + R) : 0;
+  const int slot_a = un.part * R + sub;
+  const int i_lo = (s_lo - un.part * R) >> 1, i_hi = (s_hi - un.part * R + 1) >> 1;  // warp-uniform
+  const uint16_t* in = (un.is_v ? p.v_in : p.k_in) + ((un.row0 + slot_a - un.slot0) * hkv + un.head) * kHeadDim;
   uint4 x[R / 2];
 #pragma unroll
   for (int i = 0; i < R / 2; ++i) {
-    const int slot = part * R + 2 * i + sub;
+    const int slot = slot_a + 2 * i;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (un.valid && slot >= un.slot0 && slot < un.slot1)
-      x[i] = __ldcs(reinterpret_cast<const uint4*>(in + ((un.row0 + slot - un.slot0) * hkv + un.head) * kHeadDim) + c8);
+    if (slot >= s_lo && slot < s_hi)
+      x[i] = __ldcs(reinterpret_cast<const uint4*>(in + static_cast<int64_t>(2 * i) * hkv * kHeadDim) + c8);
   }
   int page = -1;
   if (un.valid) page = __ldg(p.c.page_table + un.entry);
@@ -146,13 +182,14 @@ __global__ void __launch_bounds__(kQThreads) rlk_qcache_write_kernel(const __gri
     // element 8 c + e is held by lane l xor 8
 #pragma unroll
     for (int i = 0; i < R / 2; ++i) {
-      const int slot = part * R + 2 * i + sub;
+      if (i < i_lo || i >= i_hi) continue;
+      const int slot = slot_a + 2 * i;
       uint4 o;
       o.x = __shfl_xor_sync(0xffffffffu, x[i].x, 8);
       o.y = __shfl_xor_sync(0xffffffffu, x[i].y, 8);
       o.z = __shfl_xor_sync(0xffffffffu, x[i].z, 8);
       o.w = __shfl_xor_sync(0xffffffffu, x[i].w, 8);
-      if (un.valid && slot >= un.slot0 && slot < un.slot1) {
+      if (slot >= s_lo && slot < s_hi) {
         const float4* t =
             reinterpret_cast<const float4*>(p.rope_table + static_cast<int64_t>(un.pos_slot0 + slot) * kHeadDim);
         const int j = c8 & 7;
@@ -160,58 +197,61 @@ __global__ void __launch_bounds__(kQThreads) rlk_qcache_write_kernel(const __gri
         const float4 sa = __ldg(t + 16 + 2 * j), sb = __ldg(t + 16 + 2 * j + 1);
         const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
         const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-        uint4 a = c8 < 8 ? x[i] : o, b = c8 < 8 ? o : x[i];
-        rope_words8(a, b, c, s);
-        x[i] = c8 < 8 ? a : b;
+        // the lane's own half of the pairs: y = x c -+ (pair s), the products
+        // with s rounded on their own
+        const uint32_t own[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, oth[4] = {o.x, o.y, o.z, o.w};
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float s0 = c8 < 8 ? -s[2 * k] : s[2 * k], s1 = c8 < 8 ? -s[2 * k + 1] : s[2 * k + 1];
+          y[k] = pack_bf16x2(__fmaf_rn(bf16_lo_as_f32(own[k]), c[2 * k], __fmul_rn(bf16_lo_as_f32(oth[k]), s0)),
+                             __fmaf_rn(bf16_hi_as_f32(own[k]), c[2 * k + 1], __fmul_rn(bf16_hi_as_f32(oth[k]), s1)));
+        }
+        x[i] = make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
   }
-  // 4 significant bits, and the largest magnitude (bit patterns order as the
-  // magnitudes do)
+  // the largest magnitude (bit patterns order as the magnitudes do, and
+  // rounding keeps their order, so it is rounded alone)
   uint32_t mx = 0;
 #pragma unroll
-  for (int i = 0; i < R / 2; ++i) {
-    mx = umax2(mx, umax2(umax2(round4_pair(x[i].x), round4_pair(x[i].y)),
-                         umax2(round4_pair(x[i].z), round4_pair(x[i].w))));
-  }
+  for (int i = 0; i < R / 2; ++i)
+    mx = umax2(mx, umax2(umax2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                         umax2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
   mx = max(mx & 0xFFFFu, mx >> 16);
-  // rare: a non-finite or overflowing value, or (where e may be at its lower
-  // bound) values next to the smallest normal: settle each element
-  const bool rare = mx >= 0x7F80u || mx < static_cast<uint32_t>((kQEsMin + 1) << 7);
-  if (rare) {
+  uint64_t nan = 0;  // bit 8 i + e: element e of x[i] is Inf or NaN
+  if (mx >= 0x7F78u || (mx > 0 && round4(mx) < static_cast<uint32_t>((kQEsMin + 1) << 7))) {
     mx = 0;
 #pragma unroll
     for (int i = 0; i < R / 2; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t r = fix_pair(w[k], round4_pair(w[k]));
-        const uint32_t lo = r & 0xFFFFu, hi = r >> 16;
-        if (lo < 0x7F80u) mx = max(mx, lo);
-        if (hi < 0x7F80u) mx = max(mx, hi);
-      }
+      const Settled r = settle(x[i]);
+      x[i] = r.x;
+      mx = max(mx, r.mx);
+      nan |= static_cast<uint64_t>(r.nan) << (8 * i);
     }
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
-  if (wpu > 1) {
+  if (ps > R) {
     if (lane == 0) s_max[warp] = mx;
     __syncthreads();
-    for (int i = 0; i < wpu; ++i) mx = max(mx, s_max[(warp / wpu) * wpu + i]);
+    const int wpu = ps / R;
+    for (int i = 0; i < wpu; ++i) mx = max(mx, s_max[(warp & ~(wpu - 1)) + i]);
   }
   if (!un.valid) return;
   if (!page_ok) {
-    if (lane == 0 && part == 0) report_error(p.err, kErrBadPage, 0xa01);
+    if (lane == 0 && un.part == 0) report_error(p.err, kErrBadPage, 0xa01);
     return;
   }
-  int es = max(static_cast<int>(mx >> 7), kQEsMin);
+  int es = max(static_cast<int>(round4(mx) >> 7), kQEsMin);
   const int es_old = static_cast<int>((old_bits >> 23) & 0xFFu) + 7;
   if (had) es = max(es, min(es_old, 254));
-  uint8_t* codes = (un.is_v ? p.c.v : p.c.k) + (static_cast<int64_t>(page) * hkv + un.head) * ps * kHeadDim;
+  uint8_t* codes = (un.is_v ? p.c.v : p.c.k) + (static_cast<int64_t>(page) * hkv + un.head) * ps * kHeadDim + c8 * 8;
   if (had && es > es_old) {
     // earlier tokens of the page: their codes under the larger scale
-    for (int slot = part * R + sub; slot < min((part + 1) * R, un.slot0); slot += 2) {
-      uint2* at = reinterpret_cast<uint2*>(codes + slot * kHeadDim) + c8;
-      uint2 v = *at;
+#pragma unroll 2
+    for (int slot = slot_a; slot < min((un.part + 1) * R, un.slot0); slot += 2) {
+      uint2* at = reinterpret_cast<uint2*>(codes + slot * kHeadDim);
+      const uint2 v = *at;
       uint32_t w[2] = {v.x, v.y};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -223,29 +263,21 @@ __global__ void __launch_bounds__(kQThreads) rlk_qcache_write_kernel(const __gri
       *at = make_uint2(w[0], w[1]);
     }
   }
-  const uint32_t floor1 = static_cast<uint32_t>((es - 14) << 3) + 7u;
+  const uint32_t floor1 = (static_cast<uint32_t>((es - 14) << 3) + 7u) << 4;
   const uint32_t floor2 = floor1 | (floor1 << 16);
 #pragma unroll
   for (int i = 0; i < R / 2; ++i) {
-    const int slot = part * R + 2 * i + sub;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t e[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t r = round4_pair(w[k]);
-      if (rare) r = fix_pair(w[k], r);
-      e[k] = encode_pair(w[k], r, floor2);
-      if (rare) {
-        // non-finite: the NaN code
-        if ((r & 0xFFFFu) == 0x7FF0u) e[k] = (e[k] & 0xFFFF0000u) | 0x7Fu;
-        if ((r >> 16) == 0x7FF0u) e[k] = (e[k] & 0xFFFFu) | 0x7F0000u;
-      }
-    }
-    if (slot >= un.slot0 && slot < un.slot1)
-      reinterpret_cast<uint2*>(codes + slot * kHeadDim)[c8] =
-          make_uint2(__byte_perm(e[0], e[1], 0x6420), __byte_perm(e[2], e[3], 0x6420));
+    if (i < i_lo || i >= i_hi) continue;
+    const int slot = slot_a + 2 * i;
+    const uint2 e = make_uint2(encode4(x[i].x, x[i].y, floor2), encode4(x[i].z, x[i].w, floor2));
+    if (slot >= s_lo && slot < s_hi) *reinterpret_cast<uint2*>(codes + slot * kHeadDim) = e;
   }
-  if (lane == 0 && part == 0) *scale_at = __uint_as_float(static_cast<uint32_t>(es - 7) << 23);
+  while (nan) {
+    const int b = __ffsll(static_cast<long long>(nan)) - 1;
+    nan &= nan - 1;
+    codes[(slot_a + 2 * (b >> 3)) * kHeadDim + (b & 7)] = 0x7F;
+  }
+  if (lane == 0 && un.part == 0) *scale_at = __uint_as_float(static_cast<uint32_t>(es - 7) << 23);
 }
 
 // The BF16 value of code byte b of word w under scale: the byte's magnitude
@@ -265,11 +297,9 @@ template <int R>
 __global__ void __launch_bounds__(kQThreads) rlk_qcache_read_kernel(const __grid_constant__ QCacheParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ps = p.c.page_size, hkv = p.c.hkv;
-  const int wpu = ps / R;
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kQWarps + warp;
-  const QUnit un = q_unit(p, gw / wpu);
+  const QUnit un = q_unit<R>(p, warp);
   if (!un.valid) return;
-  const int part = static_cast<int>(gw % wpu);
+  const int part = un.part;
   const int c8 = lane & 15, sub = lane >> 4;
   const int page = __ldg(p.c.page_table + un.entry);
   const bool page_ok = page >= 0 && page < p.c.n_pages;

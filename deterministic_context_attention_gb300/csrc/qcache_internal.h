@@ -39,6 +39,7 @@ cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
 // Decode over the 8-bit pages.  The keys of a sequence are cut into segments
 // of kQSegKeys, whatever CTAs take them (qdecode.cu).
 constexpr int kQSegKeys = 512;
+constexpr int kQMaxSeqs = 256;  // sequences per launch
 constexpr int kPairCost = 6;  // a (sequence, KV head)'s fixed cost in quarters of a 128-key block (1.2 us of 0.73)
 struct QDecodeParams {
   ErrWord* err;
@@ -61,9 +62,9 @@ struct QDecodeParams {
   float* state_ml;
   unsigned long long* counts;
   uint64_t nonce;              // 40 bits, new to every call
-  int32_t ctx[kMaxSeqs];
-  int32_t seg0[kMaxSeqs + 1];  // prefix sums of the sequences' segments
-  int32_t blk0[kMaxSeqs + 1];  // prefix sums of the sequences' blocks x hkv
+  int32_t ctx[kQMaxSeqs];
+  int32_t seg0[kQMaxSeqs + 1];  // prefix sums of the sequences' segments
+  int32_t blk0[kQMaxSeqs + 1];  // prefix sums of the sequences' blocks x hkv
   int32_t part_q, part_r;      // the line's cost / grid, and the rest
 };
 cudaError_t configure_qdecode_kernels();

@@ -108,6 +108,8 @@ struct QDecLayout {
   static constexpr int kRowOff = kScOff + 2 * kScRing * 16 * 4;  // staged query rows and RoPE table row
   static constexpr int kRowBytes = MG * 256 + 512;
   static constexpr int kFoldGroups = N == 16 ? 4 : 3;  // per correction warp: segment states being folded
+  static constexpr int kEndGroups = 20;
+  static_assert(4 * kEndGroups * 4 * 512 <= (kSK + kSV) * kKVBytes, "the rings hold them");
   static constexpr int kFoldOff = kRowOff + kQS * kRowBytes;
   static constexpr int kTotal = kFoldOff + 4 * kFoldGroups * 4 * 512;
   static constexpr int kAlloc = kTotal + 1024;
@@ -884,7 +886,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     // Counts the cut pieces and folds the pairs they complete: every
     // thread's states are in device memory before the count, and the CTA that
     // counts a pair's last segment reads them after it.
-    auto flush = [&]() -> bool {
+    auto flush = [&](bool end) -> bool {
       __threadfence();
       warp_arrive(&bars[L::kStored], lane);
       if (warp == 0) {
@@ -905,9 +907,16 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         if (i >= n_cut || !last_flag[i]) continue;
         __threadfence();
         const Cut c = i == 0 ? cut0 : cut1;
-        for (int q = warp; q < MG; q += 4)
-          fold_pair<L::kFoldGroups>(p, c.seq, c.ns, c.g * MG + q, lane,
-                                    reinterpret_cast<float4*>(smem + L::kFoldOff) + warp * L::kFoldGroups * 4 * 32);
+        // once all blocks are done the K and V rings are free: 80 rows a warp
+        // in flight instead of 12 or 16
+        for (int q = warp; q < MG; q += 4) {
+          if (end)
+            fold_pair<L::kEndGroups>(p, c.seq, c.ns, c.g * MG + q, lane,
+                                     reinterpret_cast<float4*>(k_base) + warp * L::kEndGroups * 4 * 32);
+          else
+            fold_pair<L::kFoldGroups>(p, c.seq, c.ns, c.g * MG + q, lane,
+                                      reinterpret_cast<float4*>(smem + L::kFoldOff) + warp * L::kFoldGroups * 4 * 32);
+        }
       }
       n_cut = 0;
       return true;
@@ -1001,16 +1010,16 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         }
         if (warp == 0 && lane < MG && p.lse)
           p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
-        if (n_cut > 0 && !flush()) break;
+        if (n_cut > 0 && !flush(false)) break;
         continue;
       }
       // a part of a pair: counted once the next piece is done too (waiting
       // here for the stores and the count would hold up the blocks behind)
       cut1 = cut0;
       cut0 = {pc.seq, pc.g, pc.s1 - pc.s0, pc.ns};
-      if (++n_cut == 2 && !flush()) break;
+      if (++n_cut == 2 && !flush(false)) break;
     }
-    if (!fail && n_cut > 0) flush();
+    if (!fail && n_cut > 0) flush(true);
   }
 
   // ---------------------------------------------------------------- teardown
