@@ -16,6 +16,7 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -375,6 +376,9 @@ def _i32_addr(a):
     """A host int32 array and its address (keep the array until the call returns)."""
     if a is None:
         return None, None
+    if isinstance(a, (list, tuple)):  # a fraction of what a numpy array of them costs
+        a = array.array("i", a)
+        return a, a.buffer_info()[0]
     a = a if isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous else _i32_host(a)
     return a, a.ctypes.data
 

@@ -20,9 +20,10 @@
 // of up to max * 2^-5 of the largest ones.
 //
 // Both passes move 3 bytes per element (2 BF16, 1 code) and are bound by
-// HBM; the arithmetic is kept to packed 16-bit integer steps on the BF16
-// words (write, about 7 a element, where the integer pipe allows 16 at HBM
-// rate) and a multiply or two per element (read).  A unit of work is one
+// HBM; what could bind the write instead is the integer pipe (half the rate of
+// the FP32 one), so its steps are packed: a maximum per pair of elements, three
+// integer steps per pair for the flush, a multiply per element and the
+// hardware's conversion.  A unit of work is one
 // (page, head) of K or of V: a warp takes up to 16 of its rows, 16 bytes of
 // BF16 a lane, all loads in flight before the first use; neighbouring warps
 // take neighbouring heads, whose rows are contiguous in the packed tensors.
@@ -82,7 +83,13 @@ __device__ __forceinline__ QUnit q_unit(const QCacheParams& p, int warp) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+// The larger magnitude of each half of two packed BF16 words, NaN if either
+// is one (the sign bits are of no use).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // A BF16 magnitude rounded to 3 mantissa bits (nearest, ties to even).
 __device__ __forceinline__ uint32_t round4(uint32_t m) { return (m + 7u + ((m >> 4) & 1u)) & 0xFFF0u; }
@@ -120,22 +127,25 @@ __device__ __noinline__ Settled settle(uint4 x) {
   return r;
 }
 
-// Codes of four elements (two packed BF16 words) under the anchor floor2 =
-// (((es - 14) << 3) + 7) << 4 in both halves: the rounded magnitude less the
-// anchor is the code - 7, or at most 0 where the code's exponent field, E - es
-// + 14, is below 1.  Then, byte by byte: 7 more and the sign where it is not 0.
-__device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, uint32_t floor2) {
+// Codes of four elements (two packed BF16 words).  above2: 0x8000 less the
+// smallest magnitude that does not become 0, in both halves -- that is 31/32 of
+// the smallest normal code's value, which 4 significant bits round up to it.
+// Past the flush the hardware's rounding to E4M3 is the one to 4 bits (it
+// rounds [31/32, 1) of the smallest normal number to that number too).
+__device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, uint32_t above2, float inv_scale) {
   const uint32_t w[2] = {w0, w1};
-  uint32_t t[2];
+  uint32_t c[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t m = w[k] & 0x7FFF7FFFu;
-    const uint32_t r = (m + 0x00070007u + ((m >> 4) & 0x00010001u)) & 0xFFF0FFF0u;
-    t[k] = (umax2(r, floor2) - floor2) >> 4;
+    uint32_t keep;  // each half's bit 15 of the sum, 16 times
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(keep) : "r"((w[k] & 0x7FFF7FFFu) + above2));
+    const uint32_t v = w[k] & keep;
+    const float lo = __fmul_rn(bf16_lo_as_f32(v), inv_scale), hi = __fmul_rn(bf16_hi_as_f32(v), inv_scale);
+    uint16_t e;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(hi), "f"(lo));
+    c[k] = e;
   }
-  const uint32_t c = __byte_perm(t[0], t[1], 0x6420);
-  const uint32_t nz = (c + 0x7F7F7F7Fu) & 0x80808080u;  // c <= 112: no carry
-  return (c + (nz >> 7) * 7u) | (__byte_perm(w0, w1, 0x7531) & nz);
+  return c[0] | (c[1] << 16);
 }
 
 // An existing code under a scale 2^d times larger (d >= 0).
@@ -147,28 +157,34 @@ __device__ __forceinline__ uint32_t rescale_byte(uint32_t c, int d) {
 }
 
 // R: rows a warp takes (8 for 8-token pages, else 16).  Lane l holds elements
-// 8 (l mod 16) .. + 7 of rows 2 i + l / 16.
+// 8 j .. 8 j + 7 and 64 + 8 j .. (j = l mod 8; the RoPE pairs of one another) of
+// rows 4 i + l / 8.
 template <int R, bool ROPE>
 __global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
     rlk_qcache_write_kernel(const __grid_constant__ QCacheParams p) {
   __shared__ uint32_t s_max[kQWarps];
+  constexpr int I = R / 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ps = p.c.page_size, hkv = p.c.hkv;
   const QUnit un = q_unit<R>(p, warp);
-  const int c8 = lane & 15, sub = lane >> 4;
-  // the warp's slots that are written, and this lane's first (slot of i = 0)
+  const int j = lane & 7, sub = lane >> 3;
+  // the warp's slots that are written, this lane's first (i = 0), and the i
+  // that have any (the same for the whole warp)
   const int s_lo = un.valid ? max(un.slot0, un.part * R) : 0;
   const int s_hi = un.valid ? min(un.slot1, un.part * R + R) : 0;
   const int slot_a = un.part * R + sub;
-  const int i_lo = (s_lo - un.part * R) >> 1, i_hi = (s_hi - un.part * R + 1) >> 1;  // warp-uniform
+  const int i_lo = (s_lo - un.part * R) >> 2, i_hi = (s_hi - un.part * R + 3) >> 2;
   const uint16_t* in = (un.is_v ? p.v_in : p.k_in) + ((un.row0 + slot_a - un.slot0) * hkv + un.head) * kHeadDim;
-  uint4 x[R / 2];
+  uint4 xa[I], xb[I];
 #pragma unroll
-  for (int i = 0; i < R / 2; ++i) {
-    const int slot = slot_a + 2 * i;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= s_lo && slot < s_hi)
-      x[i] = __ldcs(reinterpret_cast<const uint4*>(in + static_cast<int64_t>(2 * i) * hkv * kHeadDim) + c8);
+  for (int i = 0; i < I; ++i) {
+    const int slot = slot_a + 4 * i;
+    xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (slot >= s_lo && slot < s_hi) {
+      const uint4* row = reinterpret_cast<const uint4*>(in + static_cast<int64_t>(4 * i) * hkv * kHeadDim) + j;
+      xa[i] = __ldcs(row);
+      xb[i] = __ldcs(row + 8);
+    }
   }
   int page = -1;
   if (un.valid) page = __ldg(p.c.page_table + un.entry);
@@ -178,36 +194,18 @@ __global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
   uint32_t old_bits = 0;
   if (had) old_bits = __float_as_uint(*scale_at);
   if (ROPE && !un.is_v) {
-    // the canonical rotation of the rows at their positions; the pair of
-    // element 8 c + e is held by lane l xor 8
+    // the canonical rotation of the rows at their positions
 #pragma unroll
-    for (int i = 0; i < R / 2; ++i) {
-      if (i < i_lo || i >= i_hi) continue;
-      const int slot = slot_a + 2 * i;
-      uint4 o;
-      o.x = __shfl_xor_sync(0xffffffffu, x[i].x, 8);
-      o.y = __shfl_xor_sync(0xffffffffu, x[i].y, 8);
-      o.z = __shfl_xor_sync(0xffffffffu, x[i].z, 8);
-      o.w = __shfl_xor_sync(0xffffffffu, x[i].w, 8);
+    for (int i = 0; i < I; ++i) {
+      const int slot = slot_a + 4 * i;
       if (slot >= s_lo && slot < s_hi) {
         const float4* t =
             reinterpret_cast<const float4*>(p.rope_table + static_cast<int64_t>(un.pos_slot0 + slot) * kHeadDim);
-        const int j = c8 & 7;
         const float4 ca = __ldg(t + 2 * j), cb = __ldg(t + 2 * j + 1);
         const float4 sa = __ldg(t + 16 + 2 * j), sb = __ldg(t + 16 + 2 * j + 1);
         const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
         const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-        // the lane's own half of the pairs: y = x c -+ (pair s), the products
-        // with s rounded on their own
-        const uint32_t own[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, oth[4] = {o.x, o.y, o.z, o.w};
-        uint32_t y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float s0 = c8 < 8 ? -s[2 * k] : s[2 * k], s1 = c8 < 8 ? -s[2 * k + 1] : s[2 * k + 1];
-          y[k] = pack_bf16x2(__fmaf_rn(bf16_lo_as_f32(own[k]), c[2 * k], __fmul_rn(bf16_lo_as_f32(oth[k]), s0)),
-                             __fmaf_rn(bf16_hi_as_f32(own[k]), c[2 * k + 1], __fmul_rn(bf16_hi_as_f32(oth[k]), s1)));
-        }
-        x[i] = make_uint4(y[0], y[1], y[2], y[3]);
+        rope_words8(xa[i], xb[i], c, s);
       }
     }
   }
@@ -215,19 +213,22 @@ __global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
   // rounding keeps their order, so it is rounded alone)
   uint32_t mx = 0;
 #pragma unroll
-  for (int i = 0; i < R / 2; ++i)
-    mx = umax2(mx, umax2(umax2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                         umax2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+  for (int i = 0; i < I; ++i) {
+    mx = max_abs2(mx, max_abs2(max_abs2(xa[i].x, xa[i].y), max_abs2(xa[i].z, xa[i].w)));
+    mx = max_abs2(mx, max_abs2(max_abs2(xb[i].x, xb[i].y), max_abs2(xb[i].z, xb[i].w)));
+  }
+  mx &= 0x7FFF7FFFu;
   mx = max(mx & 0xFFFFu, mx >> 16);
-  uint64_t nan = 0;  // bit 8 i + e: element e of x[i] is Inf or NaN
+  uint64_t nan = 0;  // bit 16 i + e: element e (of xa, then xb) of row i is Inf or NaN
   if (mx >= 0x7F78u || (mx > 0 && round4(mx) < static_cast<uint32_t>((kQEsMin + 1) << 7))) {
     mx = 0;
 #pragma unroll
-    for (int i = 0; i < R / 2; ++i) {
-      const Settled r = settle(x[i]);
-      x[i] = r.x;
-      mx = max(mx, r.mx);
-      nan |= static_cast<uint64_t>(r.nan) << (8 * i);
+    for (int i = 0; i < I; ++i) {
+      const Settled ra = settle(xa[i]), rb = settle(xb[i]);
+      xa[i] = ra.x;
+      xb[i] = rb.x;
+      mx = max(mx, max(ra.mx, rb.mx));
+      nan |= static_cast<uint64_t>(ra.nan | (rb.nan << 8)) << (16 * i);
     }
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
@@ -245,13 +246,13 @@ __global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
   int es = max(static_cast<int>(round4(mx) >> 7), kQEsMin);
   const int es_old = static_cast<int>((old_bits >> 23) & 0xFFu) + 7;
   if (had) es = max(es, min(es_old, 254));
-  uint8_t* codes = (un.is_v ? p.c.v : p.c.k) + (static_cast<int64_t>(page) * hkv + un.head) * ps * kHeadDim + c8 * 8;
+  uint8_t* codes = (un.is_v ? p.c.v : p.c.k) + (static_cast<int64_t>(page) * hkv + un.head) * ps * kHeadDim + j * 8;
   if (had && es > es_old) {
     // earlier tokens of the page: their codes under the larger scale
-#pragma unroll 2
-    for (int slot = slot_a; slot < min((un.part + 1) * R, un.slot0); slot += 2) {
-      uint2* at = reinterpret_cast<uint2*>(codes + slot * kHeadDim);
-      const uint2 v = *at;
+#pragma unroll 1
+    for (int at = 2 * slot_a; at < 2 * min((un.part + 1) * R, un.slot0); at += (at & 1) ? 7 : 1) {
+      uint2* half = reinterpret_cast<uint2*>(codes + (at >> 1) * kHeadDim + (at & 1) * 64);
+      const uint2 v = *half;
       uint32_t w[2] = {v.x, v.y};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -260,22 +261,30 @@ __global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
         for (int b = 0; b < 32; b += 8) r |= rescale_byte((w[k] >> b) & 0xFFu, es - es_old) << b;
         w[k] = r;
       }
-      *at = make_uint2(w[0], w[1]);
+      *half = make_uint2(w[0], w[1]);
     }
   }
-  const uint32_t floor1 = (static_cast<uint32_t>((es - 14) << 3) + 7u) << 4;
-  const uint32_t floor2 = floor1 | (floor1 << 16);
+  const uint32_t above1 = 0x8000u - ((static_cast<uint32_t>(es - 14) << 7) | 0x78u);
+  const uint32_t above2 = above1 | (above1 << 16);
+  const float inv_scale = __uint_as_float(static_cast<uint32_t>(261 - es) << 23);  // 2^(134 - es)
 #pragma unroll
-  for (int i = 0; i < R / 2; ++i) {
+  for (int i = 0; i < I; ++i) {
     if (i < i_lo || i >= i_hi) continue;
-    const int slot = slot_a + 2 * i;
-    const uint2 e = make_uint2(encode4(x[i].x, x[i].y, floor2), encode4(x[i].z, x[i].w, floor2));
-    if (slot >= s_lo && slot < s_hi) *reinterpret_cast<uint2*>(codes + slot * kHeadDim) = e;
+    const int slot = slot_a + 4 * i;
+    const uint2 ea = make_uint2(encode4(xa[i].x, xa[i].y, above2, inv_scale),
+                                encode4(xa[i].z, xa[i].w, above2, inv_scale));
+    const uint2 eb = make_uint2(encode4(xb[i].x, xb[i].y, above2, inv_scale),
+                                encode4(xb[i].z, xb[i].w, above2, inv_scale));
+    if (slot >= s_lo && slot < s_hi) {
+      uint2* row = reinterpret_cast<uint2*>(codes + slot * kHeadDim);
+      row[0] = ea;
+      row[8] = eb;
+    }
   }
   while (nan) {
     const int b = __ffsll(static_cast<long long>(nan)) - 1;
     nan &= nan - 1;
-    codes[(slot_a + 2 * (b >> 3)) * kHeadDim + (b & 7)] = 0x7F;
+    codes[(slot_a + 4 * (b >> 4)) * kHeadDim + ((b >> 3) & 1) * 64 + (b & 7)] = 0x7F;
   }
   if (lane == 0 && un.part == 0) *scale_at = __uint_as_float(static_cast<uint32_t>(es - 7) << 23);
 }

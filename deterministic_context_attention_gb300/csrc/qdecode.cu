@@ -290,8 +290,8 @@ struct QWalk {
     const int nb = (p.ctx[lo] + 127) / 128;
     const int r = x - cost0(p, lo), pair = r / (4 * nb + kPairCost);
     const int b = max(r - pair * (4 * nb + kPairCost) - kPairCost + 3, 0) / 4;
-    int step = kSegBlocks;
-    if (p.split_k) step *= ((nb + kSegBlocks - 1) / kSegBlocks + p.split_k - 1) / p.split_k;
+    int step = nb > 2 * kSegBlocks ? kSegBlocks : nb;  // up to 2 segments: cutting (3 us) saves less than it costs
+    if (p.split_k) step = ((nb + kSegBlocks - 1) / kSegBlocks + p.split_k - 1) / p.split_k * kSegBlocks;
     return p.blk0[lo] + pair * nb + min((b + step - 1) / step * step, nb);
   }
   __device__ bool next(const QDecodeParams& p, QPiece* q) {
