@@ -47,7 +47,7 @@ size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu);
 static_assert(sizeof(rlk::FwdParams) + 3 * sizeof(CUtensorMap) + 256 <= 32764,
               "forward kernel parameters exceed the 32 KB launch limit");
 static_assert(sizeof(rlk::MergeParams) <= 4096, "merge parameters");
-static_assert(sizeof(rlk::QCacheParams) <= 4096 && sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) <= 4096,
+static_assert(sizeof(rlk::QCacheParams) <= 4096 && sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) <= 8192,
               "8-bit cache parameters");
 static_assert(sizeof(rlk_attn_slab) == sizeof(rlk::Slab), "slab layout");
 
@@ -1305,6 +1305,56 @@ size_t qdecode_state_bytes(int64_t segments, int hq) {
   return static_cast<size_t>(segments) * hq * (rlk::kHeadDim + 2) * sizeof(float);
 }
 
+// Where each of `grid` CTAs starts.  The blocks of all (sequence, KV head)
+// pairs in order form a line on which a pair costs its blocks and kPairCost
+// quarters of a block more; CTA c starts where the c-th of `grid` equal parts
+// does, moved up to the next segment of its pair, or (split_k) to the next of
+// the at most split_k equal runs of segments.  A pair of up to 2 segments is not
+// cut: counting and folding its parts (3 us) costs more than it evens out.
+void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int grid, rlk::QStart* start) {
+  constexpr int kSeg = rlk::kQSegKeys / 128;
+  auto blocks_of = [&](int s) { return (ctx[s] + 127) / 128; };
+  int64_t total = 0;
+  for (int s = 0; s < num_seqs; ++s) total += static_cast<int64_t>(hkv) * (4 * blocks_of(s) + rlk::kPairCost);
+  int s = 0;
+  int64_t cost0 = 0, blk0 = 0;  // where sequence s begins on the line, in cost and in blocks
+  int64_t before = 0;
+  for (int c = 0; c <= grid; ++c) {
+    const int64_t x = total / grid * c + std::min<int64_t>(c, total % grid);
+    int64_t at;
+    rlk::QStart st{0, 0, 0, 0};
+    for (; s < num_seqs; ++s) {
+      const int64_t cost = static_cast<int64_t>(hkv) * (4 * blocks_of(s) + rlk::kPairCost);
+      if (x < cost0 + cost) break;
+      cost0 += cost;
+      blk0 += static_cast<int64_t>(hkv) * blocks_of(s);
+    }
+    if (s == num_seqs) {
+      at = blk0;
+    } else {
+      const int nb = blocks_of(s), per = 4 * nb + rlk::kPairCost;
+      const int64_t pair = (x - cost0) / per;
+      const int rest = static_cast<int>(x - cost0 - pair * per);
+      const int b = std::max(rest - rlk::kPairCost + 3, 0) / 4;
+      int step = nb > 2 * kSeg ? kSeg : nb;
+      if (split_k) step = ((nb + kSeg - 1) / kSeg + split_k - 1) / split_k * kSeg;
+      const int up = std::min((b + step - 1) / step * step, nb);
+      at = blk0 + pair * nb + up;
+      st = {s, static_cast<int32_t>(pair), up, 0};
+      if (up == nb) {  // the next pair, of this sequence or the next
+        st.b = 0;
+        if (++st.g == hkv) {
+          st.g = 0;
+          ++st.seq;
+        }
+      }
+    }
+    if (c > 0) start[c - 1].left = static_cast<int32_t>(at - before);
+    if (c < grid) start[c] = st;
+    before = at;
+  }
+}
+
 rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCache& cache, const int32_t* seqlens,
                         int32_t split_k, const float* rope_table, int32_t rope_max_pos, float* out_f32,
                         void* out_bf16, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -1350,7 +1400,6 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
     if (4 * blocks + static_cast<int64_t>(rlk::kPairCost) * hkv * params->num_seqs > INT32_MAX - 1024 ||
         segments * hq > INT32_MAX)
       return fail(RLK_ERR_UNSUPPORTED, "more than 2^29 (block, KV head) or 2^31 (segment, query head) pairs in one launch");
-    dp.blk0[s + 1] = static_cast<int32_t>(blocks);
     dp.seg0[s + 1] = static_cast<int32_t>(segments);
   }
   const size_t state_bytes = qdecode_state_bytes(segments, hq);
@@ -1364,7 +1413,8 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   CUtensorMap mk, mv;
   if ((st = make_code_map(&mk, cache.k_pool, cache.n_pages, hkv, cache.page_size))) return st;
   if ((st = make_code_map(&mv, cache.v_pool, cache.n_pages, hkv, cache.page_size))) return st;
-  const int grid = static_cast<int>(std::min<int64_t>(dev->num_sms, segments * hkv));
+  const int grid = static_cast<int>(std::min<int64_t>({dev->num_sms, rlk::kQMaxParts, segments * hkv}));
+  plan_qdecode(dp.ctx, params->num_seqs, hkv, split_k, grid, dp.start);
   dp.err = dev->err;
   dp.num_seqs = params->num_seqs;
   dp.hq = hq;
@@ -1377,10 +1427,6 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   dp.n_pages = cache.n_pages;
   dp.page_size = cache.page_size;
   dp.max_pages = cache.max_pages;
-  dp.split_k = split_k;
-  const int64_t cost = 4 * blocks + static_cast<int64_t>(rlk::kPairCost) * hkv * params->num_seqs;
-  dp.part_q = static_cast<int32_t>(cost / grid);
-  dp.part_r = static_cast<int32_t>(cost % grid);
   dp.rope_table = rope_table;
   dp.out_f32 = out_f32;
   dp.out_bf16 = static_cast<uint16_t*>(out_bf16);

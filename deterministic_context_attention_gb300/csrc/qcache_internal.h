@@ -40,7 +40,11 @@ cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
 // of kQSegKeys, whatever CTAs take them (qdecode.cu).
 constexpr int kQSegKeys = 512;
 constexpr int kQMaxSeqs = 256;  // sequences per launch
+constexpr int kQMaxParts = 160;  // CTAs per launch
 constexpr int kPairCost = 6;  // a (sequence, KV head)'s fixed cost in quarters of a 128-key block (1.2 us of 0.73)
+struct alignas(16) QStart {  // where a CTA's work starts, and how many blocks it has
+  int32_t seq, g, b, left;
+};
 struct QDecodeParams {
   ErrWord* err;
   int32_t num_seqs, hq, hkv;
@@ -50,7 +54,6 @@ struct QDecodeParams {
   const float* v_scale;
   const int32_t* page_table;
   int32_t n_pages, page_size, max_pages;
-  int32_t split_k;          // most parts a (sequence, KV head) is cut into, or 0: any
   const float* rope_table;  // rotates the query at ctx - 1, or null
   float* out_f32;
   uint16_t* out_bf16;
@@ -64,8 +67,7 @@ struct QDecodeParams {
   uint64_t nonce;              // 40 bits, new to every call
   int32_t ctx[kQMaxSeqs];
   int32_t seg0[kQMaxSeqs + 1];  // prefix sums of the sequences' segments
-  int32_t blk0[kQMaxSeqs + 1];  // prefix sums of the sequences' blocks x hkv
-  int32_t part_q, part_r;      // the line's cost / grid, and the rest
+  QStart start[kQMaxParts];
 };
 cudaError_t configure_qdecode_kernels();
 cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,

@@ -30,7 +30,7 @@
 // Work split.  The blocks of all (sequence, KV head) pairs in order form one
 // line; CTA c of g takes its c-th g-th part by cost (a pair counts 1.5 blocks
 // more than it has), cut at segment boundaries, so the SMs' loads differ by a
-// segment at the most and no plan is built on the host.
+// segment at the most.
 // A CTA that holds a whole pair writes its output; otherwise each segment's
 // state goes to the workspace and the CTA that adds the last segment of a pair
 // (an atomic count; which one it is changes nothing in the result) folds them.
@@ -253,46 +253,19 @@ struct QPiece {
   __device__ bool whole() const { return s0 == 0 && s1 == ns; }
 };
 
-// The pieces of this CTA, in order; every role walks them on its own.
+// The pieces of this CTA, in order; every role walks them on its own from the
+// CTA's start, which the host worked out (found here, by searching the tables
+// in the parameters, it was the first 4 us of every CTA: each probe of a table
+// missed the constant cache).
 struct QWalk {
-  int left;       // blocks still to take
   int seq, g, b;  // where the next piece starts
+  int left;       // blocks still to take
   __device__ explicit QWalk(const QDecodeParams& p) {
-    seq = g = b = 0;
-    const int at = cut(p, blockIdx.x);
-    left = cut(p, blockIdx.x + 1) - at;
-    if (left <= 0) return;
-    int hi = p.num_seqs - 1;
-    while (seq < hi) {
-      const int mid = (seq + hi + 1) >> 1;
-      if (p.blk0[mid] <= at) seq = mid;
-      else hi = mid - 1;
-    }
-    const int nb = (p.ctx[seq] + 127) / 128, r = at - p.blk0[seq];
-    g = r / nb;
-    b = r - g * nb;
-  }
-  // the line's place where sequence s begins, in quarters of a block
-  static __device__ int cost0(const QDecodeParams& p, int s) { return 4 * p.blk0[s] + kPairCost * p.hkv * s; }
-  // the c-th part's start, as a block of the line: part_q of its cost a part
-  // and one more for the first part_r, from there on to the next segment, or
-  // (split_k) the next of the at most split_k equal runs of segments a pair
-  // may be cut into
-  static __device__ int cut(const QDecodeParams& p, int c) {
-    const int x = c * p.part_q + min(c, p.part_r);
-    if (x >= cost0(p, p.num_seqs)) return p.blk0[p.num_seqs];
-    int lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cost0(p, mid) <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    const int nb = (p.ctx[lo] + 127) / 128;
-    const int r = x - cost0(p, lo), pair = r / (4 * nb + kPairCost);
-    const int b = max(r - pair * (4 * nb + kPairCost) - kPairCost + 3, 0) / 4;
-    int step = nb > 2 * kSegBlocks ? kSegBlocks : nb;  // up to 2 segments: cutting (3 us) saves less than it costs
-    if (p.split_k) step = ((nb + kSegBlocks - 1) / kSegBlocks + p.split_k - 1) / p.split_k * kSegBlocks;
-    return p.blk0[lo] + pair * nb + min((b + step - 1) / step * step, nb);
+    const QStart s = p.start[blockIdx.x];
+    seq = s.seq;
+    g = s.g;
+    b = s.b;
+    left = s.left;
   }
   __device__ bool next(const QDecodeParams& p, QPiece* q) {
     if (left <= 0) return false;
@@ -362,19 +335,20 @@ __device__ __forceinline__ void fold_factors(float m, float mb, float& mn, float
   b = ex2_hw(__fsub_rn(mb, mn));
 }
 
-// Counts n finished segments of a pair; true for the call that brings the
-// count to ns.  A word holds the call's nonce (40 bits) over the count (24);
-// another nonce means no segment of this call has been counted yet.  The last
-// one clears the word, so a replayed launch starts over.
-__device__ __forceinline__ bool count_segments(unsigned long long* word, uint64_t nonce, int n, int ns) {
-  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
-  for (;;) {
-    const uint64_t have = (old >> 24) == nonce ? (old & 0xFFFFFFu) : 0u;
-    const bool last = have + n == static_cast<uint64_t>(ns);
-    const unsigned long long seen = atomicCAS(word, old, last ? 0ull : (nonce << 24) | (have + n));
-    if (seen == old) return last;
-    old = seen;
-  }
+// The count of a cut pair's finished segments: a word that holds the call's
+// nonce (40 bits) over the count (24).  Another nonce means that no segment of
+// this call has been counted yet; every CTA with a part of the pair sees to it
+// early (begin_count) that the word holds its nonce, so that counting is one
+// addition.  The CTA that counts the last segment clears the word.
+__device__ __forceinline__ void begin_count(unsigned long long* word, uint64_t nonce) {
+  const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  // where this fails, another CTA of the call has done it
+  if ((old >> 24) != nonce) atomicCAS(word, old, static_cast<unsigned long long>(nonce << 24));
+}
+__device__ __forceinline__ bool count_segments(unsigned long long* word, int n, int ns) {
+  const bool last = (atomicAdd(word, static_cast<unsigned long long>(n)) & 0xFFFFFFu) + n == static_cast<unsigned>(ns);
+  if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
+  return last;
 }
 
 // The fold of a cut pair's segment states, one warp a query head: lane l
@@ -894,7 +868,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         if (!ok) return false;
         if (lane < n_cut) {
           const Cut q = lane == 0 ? cut0 : cut1;
-          last_flag[lane] = count_segments(p.counts + static_cast<int64_t>(q.seq) * p.hkv + q.g, p.nonce, q.n, q.ns);
+          last_flag[lane] = count_segments(p.counts + static_cast<int64_t>(q.seq) * p.hkv + q.g, q.n, q.ns);
           __threadfence();
         }
         warp_arrive(&bars[L::kCounted], lane);
@@ -925,6 +899,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     QPiece pc;
     while (walk.next(p, &pc)) {
       const bool whole = pc.whole();
+      if (!whole && tid == 0) begin_count(p.counts + static_cast<int64_t>(pc.seq) * p.hkv + pc.g, p.nonce);
       // O: the segment's, T: the sequence's (whole pairs); lane q holds m and
       // l of query head q
       float O[MG], T[MG];
