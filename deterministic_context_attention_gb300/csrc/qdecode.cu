@@ -353,10 +353,11 @@ __device__ __forceinline__ bool count_segments(unsigned long long* word, int n, 
 
 // The fold of a cut pair's segment states, one warp a query head: lane l
 // takes head dimensions 4 l .. 4 l + 3.  Groups of 4 segments are copied ahead
-// into the warp's ring (a lane reads what it copied itself); lane i's (m, l)
-// are those of segment 32 k + i.  One warp a scheduler, so what costs is the
-// chain of dependent steps: the maxima of a group first, then its factors side
-// by side, then the sums; past the last segment m = -inf (a factor of 0).
+// into the warp's ring (a lane reads what it copied itself).  One warp a
+// scheduler, so what costs is the chain of dependent steps: for 32 segments at
+// a time the running maxima are a scan over the lanes and the factors come out
+// side by side (the same values as one after another: a maximum rounds
+// nothing), which leaves a multiply and an fma a segment on the chain.
 template <int GROUPS>
 __device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, int h, int lane, float4* ring) {
   constexpr int C = 4;
@@ -364,58 +365,62 @@ __device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, 
   const int64_t pitch = static_cast<int64_t>(p.hq) * kHeadDim;
   const float* src = p.state_o + base * kHeadDim + 4 * lane;
   const float2* sml = reinterpret_cast<const float2*>(p.state_ml) + base;
+  // past the last segment: m = -inf, a factor of 0
   auto load_ml = [&](int c0) {
     return c0 + lane < ns ? __ldcg(sml + static_cast<int64_t>(c0 + lane) * p.hq) : make_float2(-INFINITY, 0.f);
   };
   int next = 0;  // the next segment to copy
   float4* to = ring + lane;
   auto copy = [&]() {
+    if (next < ns) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      if (next + i < ns) cp_async16(to + i * 32, src + i * pitch);
-      else to[i * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < C; ++i) {
+        if (next + i < ns) cp_async16(to + i * 32, src + i * pitch);
+        else to[i * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
-    cp_async_commit();
+    cp_async_commit();  // empty groups keep the count uniform
     next += C;
     src += C * pitch;
     to = to + C * 32 == ring + lane + GROUPS * C * 32 ? ring + lane : to + C * 32;
   };
-  float2 ml = load_ml(0), ml_next = load_ml(32);
+  float2 ml = load_ml(0);
 #pragma unroll 1
   for (int c = 0; c < GROUPS; ++c) copy();
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-  for (int s = 0; s < ns; s += C) {
-    float mb[C], lb[C], a[C], b[C];
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    const float2 ml_next = load_ml(s0 + 32);
+    float run = fmaxf(m, ml.x);  // lane i: the maximum up to segment s0 + i
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      mb[i] = __shfl_sync(0xffffffffu, ml.x, (s + i) & 31);
-      lb[i] = __shfl_sync(0xffffffffu, ml.y, (s + i) & 31);
+    for (int off = 1; off < 32; off <<= 1) {
+      const float o = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run = fmaxf(run, o);
     }
+    float before = __shfl_up_sync(0xffffffffu, run, 1);
+    if (lane == 0) before = m;
+    const float fa = ex2_hw(__fsub_rn(before, run)), fb = ex2_hw(__fsub_rn(ml.x, run));
+    m = __shfl_sync(0xffffffffu, run, 31);
+#pragma unroll 1
+    for (int s = s0; s < min(s0 + 32, ns); s += C) {
+      cp_async_wait<GROUPS - 1>();
+      float4 v[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float mn;
-      fold_factors(m, mb[i], mn, a[i], b[i]);
-      m = mn;
-    }
-    cp_async_wait<GROUPS - 1>();
-    float4 v[C];
+      for (int i = 0; i < C; ++i) v[i] = to[i * 32];  // the slot the next copy fills is the oldest one
+      copy();
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = to[i * 32];  // the slot the next copy fills is the oldest one
-    copy();
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      O.x = __fmaf_rn(v[i].x, b[i], __fmul_rn(O.x, a[i]));
-      O.y = __fmaf_rn(v[i].y, b[i], __fmul_rn(O.y, a[i]));
-      O.z = __fmaf_rn(v[i].z, b[i], __fmul_rn(O.z, a[i]));
-      O.w = __fmaf_rn(v[i].w, b[i], __fmul_rn(O.w, a[i]));
-      l = __fmaf_rn(lb[i], b[i], __fmul_rn(l, a[i]));
+      for (int i = 0; i < C; ++i) {
+        const float a = __shfl_sync(0xffffffffu, fa, s - s0 + i), b = __shfl_sync(0xffffffffu, fb, s - s0 + i);
+        const float lb = __shfl_sync(0xffffffffu, ml.y, s - s0 + i);
+        O.x = __fmaf_rn(v[i].x, b, __fmul_rn(O.x, a));
+        O.y = __fmaf_rn(v[i].y, b, __fmul_rn(O.y, a));
+        O.z = __fmaf_rn(v[i].z, b, __fmul_rn(O.z, a));
+        O.w = __fmaf_rn(v[i].w, b, __fmul_rn(O.w, a));
+        l = __fmaf_rn(lb, b, __fmul_rn(l, a));
+      }
     }
-    if (((s + C) & 31) == 0) {
-      ml = ml_next;
-      ml_next = load_ml(s + C + 32);
-    }
+    ml = ml_next;
   }
   cp_async_wait<0>();
   const float r = __frcp_rn(l);
@@ -985,14 +990,14 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         }
         if (warp == 0 && lane < MG && p.lse)
           p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
-        if (n_cut > 0 && !flush(false)) break;
+        if (n_cut > 0 && !flush(walk.left <= 0)) break;
         continue;
       }
       // a part of a pair: counted once the next piece is done too (waiting
       // here for the stores and the count would hold up the blocks behind)
       cut1 = cut0;
       cut0 = {pc.seq, pc.g, pc.s1 - pc.s0, pc.ns};
-      if (++n_cut == 2 && !flush(false)) break;
+      if (++n_cut == 2 && !flush(walk.left <= 0)) break;
     }
     if (!fail && n_cut > 0) flush(true);
   }
