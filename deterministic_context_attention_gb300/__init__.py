@@ -329,44 +329,51 @@ def rlk_attn_decode_paged_splitk_rope(params, q, k_pool, v_pool, n_pages, page_s
            "rlk_attn_decode_paged_splitk_rope")
 
 
-_dtypes = {}  # what the 8-bit cache's arguments may be, by name (filled once torch is there)
+class _Torch:
+    """What the 8-bit cache's calls ask torch for, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.device = torch.cuda.current_device
+        # the stream's address without building a Stream object (3 us of a call's 15), where torch offers it
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        self.kinds = {"codes": (torch.float8_e4m3fn, torch.uint8), "bf16": (torch.bfloat16,),
+                      "f32": (torch.float32,), "i32": (torch.int32,), None: None}
 
 
-def _kinds():
-    import torch
-    _dtypes.update(codes=(torch.float8_e4m3fn, torch.uint8), bf16=(torch.bfloat16,), f32=(torch.float32,),
-                   i32=(torch.int32,))
-    _dtypes["cuda"] = torch.cuda
-    # the stream's address without building a Stream object (3 us of a call's 15), where torch offers it
-    _dtypes["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    return _dtypes
+_torch = None
 
 
 def _dev_args(stream, *args):
-    """Addresses of the tensors an 8-bit cache call reads or writes and its
-    stream, as ``(kind, tensor), ...`` of the kinds above: refuses a tensor that
-    is not contiguous, not on the current CUDA device or of another type (a
-    pointer value or None passes as it is)."""
-    kinds = _dtypes or _kinds()
-    out, dev = [], None
+    """Addresses of the tensors an 8-bit cache call reads or writes, given as
+    (kind, tensor), and of its stream: refuses a tensor that is not contiguous,
+    not on the current CUDA device or of another type (a pointer value or None
+    passes as it is)."""
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    dev = None
+    out = []
     for kind, x in args:
-        if x is not None and not isinstance(x, int):
-            if not hasattr(x, "data_ptr") or not x.is_cuda:
-                raise ValueError("expected a tensor on the current CUDA device")
+        if x is not None and x.__class__ is not int:
             if dev is None:
-                dev = kinds["cuda"].current_device()
-            if x.get_device() != dev:
-                raise ValueError("expected a tensor on the current CUDA device")
+                dev = _torch.device() if getattr(x, "is_cuda", False) else -2
+            try:
+                if x.get_device() != dev:
+                    raise ValueError("expected a tensor on the current CUDA device")
+            except AttributeError:
+                raise ValueError("expected a tensor on the current CUDA device") from None
             if not x.is_contiguous():
                 raise ValueError("expected a contiguous tensor")
-            if kind is not None and x.dtype not in kinds[kind]:
-                raise ValueError(f"expected {' or '.join(str(t) for t in kinds[kind])}, got {x.dtype}")
+            types = _torch.kinds[kind]
+            if types is not None and x.dtype not in types:
+                raise ValueError(f"expected {' or '.join(map(str, types))}, got {x.dtype}")
             x = x.data_ptr()
         out.append(x)
     if stream is None:
-        stream = kinds["stream"](kinds["cuda"].current_device() if dev is None else dev)
-    elif not isinstance(stream, int):
+        stream = _torch.stream(_torch.device() if dev is None else dev)
+    elif stream.__class__ is not int:
         stream = stream.cuda_stream
     out.append(stream)
     return out

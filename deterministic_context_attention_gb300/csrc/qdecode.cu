@@ -102,14 +102,15 @@ struct QDecLayout {
                        kSEmpty = kSFull + kSS, kPFull = kSEmpty + kSS, kPEmpty = kPFull + kPS,
                        kOFull = kPEmpty + kPS, kOEmpty = kOFull + kOS, kStatsFull = kOEmpty + kOS,
                        kSyncMax = kStatsFull + kSR, kStored = kSyncMax + 4, kCounted = kStored + 1,
-                       kScales = kCounted + 1, kNumBars = kScales + kScRing;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort, last [2] (i32)
-  static constexpr int kScOff = (kMiscOff + 16 + 15) / 16 * 16;  // float [K, V][kScRing][16 pages]
+                       kEndCounted = kCounted + 1, kScales = kEndCounted + 1, kNumBars = kScales + kScRing;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort (i32)
+  static constexpr int kCutOff = (kMiscOff + 16 + 15) / 16 * 16;  // the pairs to fold: int4 {seq, g, segments, 1} [2]
+  static constexpr int kScOff = kCutOff + 2 * 16;  // float [K, V][kScRing][16 pages]
   static constexpr int kRowOff = kScOff + 2 * kScRing * 16 * 4;  // staged query rows and RoPE table row
   static constexpr int kRowBytes = MG * 256 + 512;
   static constexpr int kFoldGroups = N == 16 ? 4 : 3;  // per correction warp: segment states being folded
-  static constexpr int kEndGroups = 20;
-  static_assert(4 * kEndGroups * 4 * 512 <= (kSK + kSV) * kKVBytes, "the rings hold them");
+  static constexpr int kEndGroups = 7;  // per correction and softmax warp, in the K and V rings
+  static_assert(12 * kEndGroups * 4 * 512 <= (kSK + kSV) * kKVBytes, "the rings hold them");
   static constexpr int kFoldOff = kRowOff + kQS * kRowBytes;
   static constexpr int kTotal = kFoldOff + 4 * kFoldGroups * 4 * 512;
   static constexpr int kAlloc = kTotal + 1024;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);
+  int4* to_fold = reinterpret_cast<int4*>(smem + L::kCutOff);
   uint32_t* stats = reinterpret_cast<uint32_t*>(smem + L::kStatsOff);
   float* qscale = reinterpret_cast<float*>(smem + L::kQsOff);
   const int tid = threadIdx.x;
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     for (int s = 0; s < L::kScRing; ++s) mbar_init(&bars[L::kScales + s], 32);
     mbar_init(&bars[L::kStored], 4);
     mbar_init(&bars[L::kCounted], 1);
+    mbar_init(&bars[L::kEndCounted], 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -503,6 +505,25 @@ __global__ void __launch_bounds__(kQDThreads, 1)
   uint8_t* p_base = smem + L::kPOff;
   uint8_t* k_base = smem + L::kKOff;
   uint8_t* v_base = smem + L::kVOff;
+
+  // The pairs whose last segment this CTA has counted, by `warps` warps.  Once
+  // all blocks are done (end), the softmax warps help the correction ones and
+  // the K and V rings are free for the copies.
+  auto fold_pairs = [&](bool end) {
+    __threadfence();
+    const int4 c0 = to_fold[0], c1 = to_fold[1];
+    const int n0 = c0.w ? MG : 0, n = n0 + (c1.w ? MG : 0);
+    for (int i = warp; i < n; i += end ? 12 : 4) {
+      const int4 c = i < n0 ? c0 : c1;
+      const int h = c.y * MG + (i < n0 ? i : i - n0);
+      if (end)
+        fold_pair<L::kEndGroups>(p, c.x, c.z, h, lane,
+                                 reinterpret_cast<float4*>(k_base) + warp * L::kEndGroups * 4 * 32);
+      else
+        fold_pair<L::kFoldGroups>(p, c.x, c.z, h, lane,
+                                  reinterpret_cast<float4*>(smem + L::kFoldOff) + warp * L::kFoldGroups * 4 * 32);
+    }
+  };
 
   if (warp == 12 || warp == 13) {
     // ------------------------------------------------------------ producers
@@ -750,6 +771,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const float sl = p.scale_log2;
     const int lps = 31 - __clz(p.page_size);
     uint32_t s_base = 0, sy_it = 0, q_it = 0;
+    bool after_cut = false, end_fold = false;
     const float* k_scales = reinterpret_cast<const float*>(smem + L::kScOff) + (t >> lps);
     const float* v_scales = k_scales + L::kScRing * 16;
     QWalk walk(p);
@@ -757,6 +779,11 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     while (walk.next(p, &pc)) {
       const int kv_len = pc.kv_len, b0 = pc.block0(), nb = pc.block1() - b0;
       const int j0 = static_cast<int>(s_base & 1) == grp ? 0 : 1;
+      // whether the correction warps will count, and fold, after their last
+      // piece: when that is cut, or follows a cut piece
+      const bool cut = !pc.whole();
+      end_fold = walk.left <= 0 && (cut || after_cut);
+      after_cut = cut && !after_cut;
       const uint32_t qslot = q_it & 1;
       bool ok = wait_warp(&bars[L::kQFull + qslot], (q_it >> 1) & 1, abort, p.err, 0xb41);
       if (!ok) break;
@@ -852,6 +879,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       if (fail) break;
       s_base += nb;
     }
+    if (end_fold && wait_warp(&bars[L::kEndCounted], 0, abort, p.err, 0xb47)) fold_pairs(true);
   } else {
     // ------------------------------------------------------------ correction / epilogue
     const int d = tid;  // head dimension lane
@@ -862,41 +890,31 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     } cut0 = {}, cut1 = {};
     int n_cut = 0;
     bool fail = false;
-    // Counts the cut pieces and folds the pairs they complete: every
-    // thread's states are in device memory before the count, and the CTA that
-    // counts a pair's last segment reads them after it.
+    // Counts the cut pieces and folds the pairs they complete: every thread's
+    // states are in device memory before the count, and the CTA that counts a
+    // pair's last segment reads them after it.
     auto flush = [&](bool end) -> bool {
       __threadfence();
       warp_arrive(&bars[L::kStored], lane);
       if (warp == 0) {
         const bool ok = wait_warp(&bars[L::kStored], cut_it & 1, abort, p.err, 0xb54);
         if (!ok) return false;
-        if (lane < n_cut) {
+        if (lane < 2) {
           const Cut q = lane == 0 ? cut0 : cut1;
-          last_flag[lane] = count_segments(p.counts + static_cast<int64_t>(q.seq) * p.hkv + q.g, q.n, q.ns);
-          __threadfence();
+          int last = 0;
+          if (lane < n_cut) {
+            last = count_segments(p.counts + static_cast<int64_t>(q.seq) * p.hkv + q.g, q.n, q.ns);
+            __threadfence();
+          }
+          to_fold[lane] = make_int4(q.seq, q.g, q.ns, last);
         }
-        warp_arrive(&bars[L::kCounted], lane);
+        warp_arrive(&bars[end ? L::kEndCounted : L::kCounted], lane);
       }
-      const bool ok = wait_warp(&bars[L::kCounted], cut_it & 1, abort, p.err, 0xb55);
+      const bool ok = end ? wait_warp(&bars[L::kEndCounted], 0, abort, p.err, 0xb56)
+                          : wait_warp(&bars[L::kCounted], cut_it & 1, abort, p.err, 0xb55);
       if (!ok) return false;
       ++cut_it;
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        if (i >= n_cut || !last_flag[i]) continue;
-        __threadfence();
-        const Cut c = i == 0 ? cut0 : cut1;
-        // once all blocks are done the K and V rings are free: 80 rows a warp
-        // in flight instead of 12 or 16
-        for (int q = warp; q < MG; q += 4) {
-          if (end)
-            fold_pair<L::kEndGroups>(p, c.seq, c.ns, c.g * MG + q, lane,
-                                     reinterpret_cast<float4*>(k_base) + warp * L::kEndGroups * 4 * 32);
-          else
-            fold_pair<L::kFoldGroups>(p, c.seq, c.ns, c.g * MG + q, lane,
-                                      reinterpret_cast<float4*>(smem + L::kFoldOff) + warp * L::kFoldGroups * 4 * 32);
-        }
-      }
+      fold_pairs(end);
       n_cut = 0;
       return true;
     };
