@@ -1388,7 +1388,7 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   int64_t blocks = 0, segments = 0;
   for (int s = 0; s < params->num_seqs; ++s) {
     if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(cache.max_pages) * cache.page_size ||
-        seqlens[s] > INT32_MAX - 1024)
+        seqlens[s] > INT32_MAX - 65536)
       return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: context length %d not in 1..max_pages*page_size", s,
                   seqlens[s]);
     if (rope_table && seqlens[s] > rope_max_pos)

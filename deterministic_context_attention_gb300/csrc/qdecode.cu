@@ -30,15 +30,20 @@
 // Work split.  The blocks of all (sequence, KV head) pairs in order form one
 // line; CTA c of g takes its c-th g-th part by cost (a pair counts 1.5 blocks
 // more than it has), cut at segment boundaries, so the SMs' loads differ by a
-// segment at the most.
-// A CTA that holds a whole pair writes its output; otherwise each segment's
-// state goes to the workspace and the CTA that adds the last segment of a pair
-// (an atomic count; which one it is changes nothing in the result) folds them.
+// segment at the most.  A CTA that holds a whole pair writes its output;
+// otherwise each segment's state goes to the workspace, and the CTA that counts
+// the last segment of a pair (which one changes nothing in the result) folds
+// them.
 //
-// What bounds it: HBM, 32 KB of codes per (KV head, 128-key block) and 4 heads
-// of 4 x 128 x 128 flops against them.  Per block the tensor core issues 4 + 4
-// MMAs (K = 32 codes each; the BF16 decode needs 8 + 16), and the 8 warps of
-// the softmax run two blocks at a time.
+// What bounds it: HBM, 32 KB of codes per (KV head, 128-key block), 0.73 us a
+// block and SM at the measured copy rate; long sequences in 16-token pages and
+// larger run at that (0.69 .. 0.73 us), 8-token pages at 0.87 (32 TMA copies a
+// block: their issue).  Fed from L2 the pipeline takes 0.50 us a block with 4
+// query heads (0.69 while the warp that issues the O products also fetched the
+// scales).  Per block the tensor core issues 4 + 4 MMAs of K = 32 codes (the
+// BF16 decode needs 8 + 16), and the softmax's 8 warps run two blocks at a
+// time.  A call costs about 5 us before its first block is folded and, where
+// pairs are cut, 3 to 6 us for counting and folding.
 //
 // Warp roles (512 threads):
 //   warps 0-3   correction / epilogue: thread d owns head dimension d
@@ -506,9 +511,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
   uint8_t* k_base = smem + L::kKOff;
   uint8_t* v_base = smem + L::kVOff;
 
-  // The pairs whose last segment this CTA has counted, by `warps` warps.  Once
-  // all blocks are done (end), the softmax warps help the correction ones and
-  // the K and V rings are free for the copies.
+  // Folds the pairs whose last segment this CTA has counted.  Once all blocks
+  // are done (end), the softmax warps help the correction ones and the K and V
+  // rings are free for the copies.
   auto fold_pairs = [&](bool end) {
     __threadfence();
     const int4 c0 = to_fold[0], c1 = to_fold[1];
@@ -547,9 +552,10 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     bool fail = false;
     // The query rows, by the V warp (whose ring is the slower one to free): of
     // the first piece before its first page, of each later one once the first
-    // pages of the piece before it are on their way.  Rows and RoPE table row land in shared memory a piece
-    // earlier still.  Rolled loops: a piece runs this code once, and unrolled
-    // it took 3 us, most of it fetching instructions.
+    // pages of the piece before it are on their way; the rows and the RoPE
+    // table's row land in shared memory a piece earlier still.  Rolled loops: a
+    // piece runs this code once, and unrolled it took 3 us, most of it fetching
+    // instructions.
     uint8_t* row_stage = smem + L::kRowOff;
     QWalk qwalk(p);
     uint32_t q_it = 0;
@@ -990,8 +996,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         } else {
           const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + seg) * p.hq + pc.g * MG;
 #pragma unroll
-          for (int q = 0; q < MG; ++q)
-            p.state_o[(r + q) * kHeadDim + d] = O[q];
+          for (int q = 0; q < MG; ++q) p.state_o[(r + q) * kHeadDim + d] = O[q];
           if (warp == 0 && lane < MG) reinterpret_cast<float2*>(p.state_ml)[r + lane] = make_float2(m, l);
         }
       }

@@ -273,6 +273,75 @@ def test_split_on_chip_group_shapes(hq, hkv, k):
     assert_bitwise(qh.decode(rlk, torch, c, q, ctx, hq, k), qh.decode(rlk, torch, c, q, ctx, hq), f"{hq}/{hkv} k {k}")
 
 
+@pytest.fixture(scope="module")
+def long_case():
+    # 79 and 40 segments of 512 keys: cut over many CTAs, folded past 32
+    ctx = [40001, 129, 20000]
+    return qh.filled(ctx, 1, 128, seed=45, spread=False), ctx, synth.normal_bf16(46, synth.T_Q, (3, 4, 128))
+
+
+@pytest.mark.parametrize("split_k", [0, 2, 7, 64])
+def test_split_long_sequences(long_case, split_k):
+    torch, rlk = torch_cuda(), lib()
+    c, ctx, q = long_case
+    one = qh.decode(rlk, torch, c, q, ctx, 4, 1, scale=0.1)
+    assert_bitwise(qh.decode(rlk, torch, c, q, ctx, 4, split_k, scale=0.1), one, f"k {split_k}")
+    if split_k == 0:
+        assert_decode(one, q, c, np.array(ctx, np.int32), 4, 0.1, "long")
+
+
+def test_workspace_contents_do_not_matter(split_case):
+    # zeros, all ones, and what other calls (of other batches) left
+    torch, rlk = torch_cuda(), lib()
+    c, ctx, q = split_case
+    ref = qh.decode(rlk, torch, c, q, ctx, 32)
+    dev, qd = c.device(), qh.to_bf16(torch, q)
+    p, p1 = rlk.make_params(len(ctx), 32, 8), rlk.make_params(2, 32, 8)
+    size = rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx)
+    assert size >= rlk.rlk_attn_workspace_size(p1, rlk.RLK_OP_DECODE_QCACHE, None, ctx[-2:])
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty((len(ctx), 32, 128), device="cuda"), torch.empty((len(ctx), 32), device="cuda")
+    pool = (*dev[:4], c.n_pages, c.page)
+    for fill in (0, 0xFF, None, None):
+        if fill is not None:
+            ws.fill_(fill)
+        out.fill_(float("nan"))
+        rlk.rlk_attn_decode_qcache(p, qd, *pool, dev[4], dev[4].shape[1], ctx, 0, None, 0, out, None, lse, ws)
+        assert np.array_equal(out.cpu().numpy().view(np.uint32), ref[0].view(np.uint32)), fill
+        assert np.array_equal(lse.cpu().numpy().view(np.uint32), ref[2].view(np.uint32)), fill
+        rlk.rlk_attn_decode_qcache(p1, qd[-2:].contiguous(), *pool, dev[4][-2:].contiguous(), dev[4].shape[1], ctx[-2:],
+                                   0, None, 0, out[:2], None, lse[:2], ws)
+        assert np.array_equal(out[:2].cpu().numpy().view(np.uint32), ref[0][-2:].view(np.uint32))
+    rlk.rlk_attn_check_device_error()
+
+
+def test_two_graphs_share_a_workspace(split_case):
+    torch, rlk = torch_cuda(), lib()
+    c, ctx, q = split_case
+    ref = qh.decode(rlk, torch, c, q, ctx, 32)
+    dev = c.device()
+    runs = [[5, 6], [3, 4, 6]]
+    size = max(rlk.rlk_attn_workspace_size(rlk.make_params(len(s), 32, 8), rlk.RLK_OP_DECODE_QCACHE, None,
+                                           [ctx[i] for i in s]) for s in runs)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for s in runs:
+        qd, td = qh.to_bf16(torch, q[s]), dev[4][s].contiguous()
+        out, lse = torch.empty((len(s), 32, 128), device="cuda"), torch.empty((len(s), 32), device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rlk.rlk_attn_decode_qcache(rlk.make_params(len(s), 32, 8), qd, *dev[:4], c.n_pages, c.page, td, td.shape[1],
+                                       [ctx[i] for i in s], 0, None, 0, out, None, lse, ws)
+        graphs.append((graph, s, out, lse, qd, td))
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        graph, s, out, lse = graphs[i][:4]
+        out.fill_(float("nan"))
+        graph.replay()
+        assert np.array_equal(out.cpu().numpy().view(np.uint32), ref[0][s].view(np.uint32)), s
+        assert np.array_equal(lse.cpu().numpy().view(np.uint32), ref[2][s].view(np.uint32)), s
+    rlk.rlk_attn_check_device_error()
+
+
 def test_decode_does_not_depend_on_batch_or_page_order(split_case):
     torch, rlk = torch_cuda(), lib()
     c, ctx, q = split_case
