@@ -663,7 +663,8 @@ def run_reference(args):
 
 def run_profile(args):
     """Run one entry point a few times without timing, for ncu captures:
-    --profile prefill|states|merge|decode|decode-small|decode-long|rope|backward."""
+    --profile prefill|states|merge|decode|decode-small|decode-long|rope|backward|
+    qcache-write|qcache-read|qcache-decode."""
     import torch
     import deterministic_context_attention_gb300 as rlk
     from deterministic_context_attention_gb300 import build as rbuild
@@ -704,6 +705,35 @@ def run_profile(args):
         for _ in range(n):
             rlk.rlk_attn_decode_paged_splitk(pd, qd, kp, vp, n_pages, 16, ptd, pt.shape[1], ctx, 4, o, ob, l, ws,
                                              stream=stream)
+    elif args.profile.startswith("qcache-"):
+        # the 8-bit cache with 64 sequences of 512 to 4096 tokens in 16-token
+        # pages (about 0.3 GB of codes): written whole, read back, attended to
+        g = torch.Generator(device="cuda")
+        g.manual_seed(6)
+        ctx = synth.rng(3, synth.T_LENS).integers(512, 4097, size=64).astype(np.int32)
+        per = (ctx + 15) // 16
+        n_pages, t = int(per.sum()), int(ctx.sum())
+        pt = np.full((64, int(per.max())), -1, np.int32)
+        pt[np.arange(pt.shape[1])[None, :] < per[:, None]] = synth.rng(3, synth.T_PAGES).permutation(n_pages)
+        kp, vp = (torch.empty((n_pages, 8, 16, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.empty((n_pages, 8), device="cuda") for _ in range(2))
+        k, v = (torch.randn((t, 8, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        qd = torch.randn((64, 32, 128), generator=g, device="cuda").to(torch.bfloat16)
+        pd = rlk.make_params(64, 32, 8, 128)
+        pool = (kp, vp, ks, vs, n_pages, 16, dv.i32_to_device(pt), pt.shape[1])
+        cu = synth.cu_seqlens(ctx)
+        o = torch.empty((64, 32, 128), dtype=torch.float32, device="cuda")
+        ob = torch.empty((64, 32, 128), dtype=torch.bfloat16, device="cuda")
+        l = torch.empty((64, 32), dtype=torch.float32, device="cuda")
+        ws = torch.empty(rlk.rlk_attn_workspace_size(pd, rlk.RLK_OP_DECODE_QCACHE, None, ctx), dtype=torch.uint8,
+                         device="cuda")
+        for i in range(n):
+            if i == 0 or args.profile == "qcache-write":
+                rlk.rlk_attn_qcache_write(pd, k, v, cu, None, None, 0, *pool, stream=stream)
+            if args.profile == "qcache-read":
+                rlk.rlk_attn_qcache_read(pd, *pool, cu, None, k, v, stream=stream)
+            elif args.profile == "qcache-decode":
+                rlk.rlk_attn_decode_qcache(pd, qd, *pool, ctx, 0, None, 0, o, ob, l, ws, stream=stream)
     elif args.profile == "backward":
         prob, p, (q, k, v, out, do, lse, dq, dk, dvv, ws), _ = backward_workload(torch, rlk, dv)
         for _ in range(n):
@@ -772,8 +802,8 @@ def main():
     ap.add_argument("--cpu-seconds", type=float, default=15.0)
     ap.add_argument("--reference-rows", type=int, default=512)
     ap.add_argument("--profile", default=None,
-                    choices=["prefill", "states", "merge", "decode", "decode-small", "decode-long", "rope",
-                             "backward"])
+                    choices=["prefill", "states", "merge", "decode", "decode-small", "decode-long", "rope", "qcache-write",
+                             "qcache-read", "qcache-decode", "backward"])
     ap.add_argument("--profile-iters", type=int, default=3)
     args = ap.parse_args()
     if args.profile:
