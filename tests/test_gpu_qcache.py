@@ -290,6 +290,56 @@ def test_split_long_sequences(long_case, split_k):
         assert_decode(one, q, c, np.array(ctx, np.int32), 4, 0.1, "long")
 
 
+@pytest.mark.parametrize("ctx,hq,hkv,page", [
+    ([20000, 30000, 9000, 500, 20001], 8, 8, 16),            # most pairs cut
+    ([100000, 77, 131072, 1, 65000, 40000], 16, 8, 64),      # cut into many pieces
+    ([700] * 230 + [3000] * 20, 40, 8, 128),                 # several pairs a CTA
+    ([300000, 400000], 8, 1, 32),                            # two pairs on all the CTAs
+], ids=["8 heads", "ragged", "short", "long"])
+def test_even_load_equals_whole_pairs(ctx, hq, hkv, page):
+    # thousands of blocks on all the CTAs, cut where the load is even: the same
+    # bits as with every pair on one CTA, on every repetition and replay
+    torch, rlk = torch_cuda(), lib()
+    g = torch.Generator(device="cuda").manual_seed(len(ctx))
+    per = [-(-c // page) for c in ctx]
+    n, n_pages = len(ctx), sum(per)
+    table = np.full((n, max(per)), -1, np.int32)
+    table[np.arange(max(per))[None, :] < np.array(per)[:, None]] = np.random.default_rng(n).permutation(n_pages)
+    pools, scales = [], []
+    for _ in range(2):
+        x = torch.empty((n_pages, hkv, page, 128), dtype=torch.uint8, device="cuda")
+        x.random_(0x30, 0x70, generator=g)  # 0.5 .. 120
+        x |= torch.randint(0, 2, x.shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+        pools.append(x)
+        scales.append(torch.exp2(torch.randint(-8, -4, (n_pages, hkv), generator=g, device="cuda").float()))
+    q = torch.randn((n, hq, 128), generator=g, device="cuda").to(torch.bfloat16)
+    p = rlk.make_params(n, hq, hkv)
+    pool = (*pools, *scales, n_pages, page, torch.from_numpy(table).cuda(), table.shape[1])
+    size = rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def run(k, out, lse):
+        rlk.rlk_attn_decode_qcache(p, q, *pool, ctx, k, None, 0, out, None, lse, ws)
+
+    ref = torch.empty((n, hq, 128), device="cuda"), torch.empty((n, hq), device="cuda")
+    run(1, *ref)
+    rlk.rlk_attn_check_device_error()
+    assert bool(torch.isfinite(ref[0]).all())
+    got = torch.empty_like(ref[0]), torch.empty_like(ref[1])
+    for k in (0, 0, 3, 0, 64, 0):
+        got[0].fill_(float("nan"))
+        run(k, *got)
+        assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(got, ref)), k
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(0, *got)
+    for _ in range(3):
+        got[0].fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(got, ref)), "replay"
+    rlk.rlk_attn_check_device_error()
+
+
 def test_workspace_contents_do_not_matter(split_case):
     # zeros, all ones, and what other calls (of other batches) left
     torch, rlk = torch_cuda(), lib()
@@ -547,7 +597,8 @@ def test_other_stream_and_graph_replay():
     qd, kd, vd = (qh.to_bf16(torch, x) for x in (q, k, v))
     out, outb = torch.empty((4, hq, 128), device="cuda"), torch.empty((4, hq, 128), dtype=torch.bfloat16, device="cuda")
     lse = torch.empty((4, hq), device="cuda")
-    ws = torch.empty(rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx), dtype=torch.uint8, device="cuda")
+    size = rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DECODE_QCACHE, None, ctx)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
 
     def step():
         rlk.rlk_attn_qcache_write(p, kd, vd, [0, 1, 2, 3, 4], pos, None, 0, *pool)
