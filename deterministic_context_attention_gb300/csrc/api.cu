@@ -1362,7 +1362,8 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   if (st) return st;
   if (!q || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
   if (!out_f32 && !out_bf16) return fail(RLK_ERR_INVALID_ARGUMENT, "out_f32 and out_bf16 are both NULL");
-  if (split_k < 0 || split_k > rlk::kMaxSplitK) return fail(RLK_ERR_INVALID_ARGUMENT, "split_k %d not in 0..64", split_k);
+  if (split_k < 0 || split_k > rlk::kMaxSplitK)
+    return fail(RLK_ERR_INVALID_ARGUMENT, "split_k %d not in 0..64", split_k);
   if (!aligned16(q) || !aligned16(out_f32) || !aligned16(out_bf16) || !aligned16(rope_table) ||
       (split_k != 1 && !aligned16(workspace)))
     return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
@@ -1399,7 +1400,8 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
     segments += qdecode_segments(seqlens + s, 1);
     if (4 * blocks + static_cast<int64_t>(rlk::kPairCost) * hkv * params->num_seqs > INT32_MAX - 1024 ||
         segments * hq > INT32_MAX)
-      return fail(RLK_ERR_UNSUPPORTED, "more than 2^29 (block, KV head) or 2^31 (segment, query head) pairs in one launch");
+      return fail(RLK_ERR_UNSUPPORTED,
+                  "more than 2^29 (block, KV head) or 2^31 (segment, query head) pairs in one launch");
     dp.seg0[s + 1] = static_cast<int32_t>(segments);
   }
   const size_t state_bytes = qdecode_state_bytes(segments, hq);

@@ -822,7 +822,10 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         for (int q = 0; q < MG; ++q) {
           const float a = __fmaf_rn(__uint_as_float(raw[2 * MG + q]), 0x1p-10f,
                                     __fmaf_rn(__uint_as_float(raw[MG + q]), 0x1p-5f, __uint_as_float(raw[q])));
-          sc[q] = vis ? __fmul_rn(__fmul_rn(a, qs[q]), sk) : -INFINITY;
+          // (the two scales first: a row near the type's largest over small keys
+          // would leave FP32's range on the way; both are powers of two, so the
+          // order rounds nothing)
+          sc[q] = vis ? __fmul_rn(a, __fmul_rn(qs[q], sk)) : -INFINITY;
           const float m = warp_max_nan(sc[q]);
           if (lane == 0) red[(rb * (MG + 1) + q) * 4 + w] = m;
         }

@@ -165,7 +165,8 @@ def test_read_gives_code_times_scale(page):
             want = vals[c.table[s][at // page], :, at % page]
             # 448 * 2^118 stays below the FP32 maximum, and a product of 4 and
             # 24 bits is exact in FP64: FP32 rounding, then BF16 rounding
-            want = synth.bf16_round(np.nan_to_num(want, nan=0.0).astype(np.float32)) + np.where(np.isnan(want), np.nan, 0)
+            nan = np.isnan(want)
+            want = synth.bf16_round(np.where(nan, 0.0, want).astype(np.float32)) + np.where(nan, np.nan, 0)
             assert np.array_equal(got[cu[s]:cu[s + 1]], want.astype(np.float32), equal_nan=True), f"sequence {s}"
 
 
@@ -196,8 +197,8 @@ def assert_decode(got, q, c, ctx, hq, scale, what):
             tol = vmax * (2.0 ** -16 + 2.0 ** -19 + 2 * serr) + 1e-30
             e = np.abs(out[s, h] - ref[s, h]).max()
             assert e <= tol, f"{what}: sequence {s} head {h}: off by {e:.3g}, at most {tol:.3g}"
-            el = abs(lse[s, h] - ref_lse[s, h])
-            assert el <= 2e-6 + 2.0 ** -21 * abs(ref_lse[s, h]) + serr, f"{what}: lse of sequence {s} head {h}: {el:.3g}"
+            el, tol = abs(lse[s, h] - ref_lse[s, h]), 2e-6 + 2.0 ** -21 * abs(ref_lse[s, h]) + serr
+            assert el <= tol, f"{what}: lse of sequence {s} head {h}: {el:.3g}"
     assert np.array_equal(outb.view(np.uint32), synth.bf16_round(out).view(np.uint32)), f"{what}: BF16 output"
     return float(np.abs(out - ref).max()), float(np.abs(lse - ref_lse).max())
 
@@ -249,6 +250,24 @@ def test_decode_tiny_and_huge_query_rows():
     for e in (-100, 100):
         got = qh.decode(rlk, torch, c, np.ldexp(q, e).astype(np.float32), ctx, 4, scale=2.0 ** (-4 - e))
         assert_bitwise(got, ref, f"2^{e}")
+
+
+def test_decode_huge_query_rows_over_tiny_keys():
+    # a query's size moved to the keys and back (powers of two) is the same
+    # scores, to the ends of the ranges: query elements up to 2^125, keys down
+    # to scales of 2^-119
+    torch, rlk = torch_cuda(), lib()
+    ctx = [200]
+    kv = qh.tokens(ctx, 1, 34, spread=False)
+    q = synth.normal_bf16(35, synth.T_Q, (1, 4, 128))
+    out = []
+    for qe, ke in ((0, 0), (60, -60), (108, -108), (-108, 108), (124, -110)):
+        c = qh.empty_cache(ctx, 1, 16, seed=36)
+        oq.write_tokens(c.k, c.ks, c.table[0], np.ldexp(kv[0][0], ke).astype(np.float32))
+        oq.write_tokens(c.v, c.vs, c.table[0], kv[0][1])
+        out.append(qh.decode(rlk, torch, c, np.ldexp(q, qe).astype(np.float32), ctx, 4, scale=2.0 ** (-4 - qe - ke)))
+    for got in out[1:]:
+        assert_bitwise(got, out[0], "moved")
 
 
 @pytest.fixture(scope="module")
@@ -408,6 +427,23 @@ def test_decode_does_not_depend_on_batch_or_page_order(split_case):
         setattr(moved, name, b)
     moved.table = np.where(c.table >= 0, perm[np.maximum(c.table, 0)], -1).astype(np.int32)
     assert_bitwise(qh.decode(rlk, torch, moved, q, ctx, 32), full, "pages moved")
+
+
+@pytest.mark.parametrize("split_k", [0, 1, 3])
+def test_sequences_that_share_pages(split_case, split_k):
+    # sequences with a common prefix hold the same page ids: each gets what it
+    # gets alone, from the pages as they are
+    torch, rlk = torch_cuda(), lib()
+    c, _, _ = split_case
+    ctx = [4096, 4095, 3000, 3000, 17, 1]
+    table = np.repeat(c.table[6:7], len(ctx), 0)
+    q = synth.normal_bf16(37, synth.T_Q, (len(ctx), 32, 128))
+    got = qh.decode(rlk, torch, c, q, ctx, 32, split_k, table=table)
+    for s in range(len(ctx)):
+        one = qh.decode(rlk, torch, c, q, ctx, 32, split_k, seqs=[s], table=table)
+        assert_bitwise([x[s:s + 1] for x in got], one, f"sequence {s}")
+    assert_decode(got, q, qh.Cache(c.k, c.v, c.ks, c.vs, table, c.page), np.array(ctx, np.int32), 32, 128 ** -0.5,
+                  "shared")
 
 
 def test_decode_300_sequences():
