@@ -802,8 +802,8 @@ def main():
     ap.add_argument("--cpu-seconds", type=float, default=15.0)
     ap.add_argument("--reference-rows", type=int, default=512)
     ap.add_argument("--profile", default=None,
-                    choices=["prefill", "states", "merge", "decode", "decode-small", "decode-long", "rope", "qcache-write",
-                             "qcache-read", "qcache-decode", "backward"])
+                    choices=["prefill", "states", "merge", "decode", "decode-small", "decode-long", "rope",
+                             "qcache-write", "qcache-read", "qcache-decode", "backward"])
     ap.add_argument("--profile-iters", type=int, default=3)
     args = ap.parse_args()
     if args.profile:

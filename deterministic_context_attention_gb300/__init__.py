@@ -379,23 +379,29 @@ def _dev_args(stream, *args):
     return out
 
 
-def _i32_addr(a):
-    """A host int32 array and its address (keep the array until the call returns)."""
+def _i32_addr(a, need):
+    """A host int32 array of at least `need` values and its address (keep the
+    array until the call returns)."""
     if a is None:
         return None, None
     if isinstance(a, (list, tuple)):  # a fraction of what a numpy array of them costs
         a = array.array("i", a)
-        return a, a.buffer_info()[0]
-    a = a if isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous else _i32_host(a)
-    return a, a.ctypes.data
+        n, at = len(a), a.buffer_info()[0]
+    else:
+        a = a if isinstance(a, np.ndarray) and a.dtype == np.int32 and a.flags.c_contiguous else _i32_host(a)
+        n, at = a.size, a.ctypes.data
+    if n < need:
+        raise ValueError(f"expected {need} host integers, got {n}")
+    return a, at
 
 
 def rlk_attn_qcache_write(params, k, v, cu_seqlens, pos_offset, rope_table, rope_max_pos, k_pool, v_pool, k_scale,
                           v_scale, n_pages, page_size, page_table, max_pages, stream=None):
     """Quantise new BF16 K/V rows into the 8-bit pages (rope_table: rotate K
     at its positions first, or None)."""
-    cu, cu_p = _i32_addr(cu_seqlens)
-    po, po_p = _i32_addr(pos_offset)
+    n = params.num_seqs
+    cu, cu_p = _i32_addr(cu_seqlens, n + 1)
+    po, po_p = _i32_addr(pos_offset, n)
     k, v, rt, kp, vp, ks, vs, pt, st = _dev_args(
         stream, ("bf16", k), ("bf16", v), ("f32", rope_table), ("codes", k_pool), ("codes", v_pool), ("f32", k_scale),
         ("f32", v_scale), ("i32", page_table))
@@ -406,8 +412,9 @@ def rlk_attn_qcache_write(params, k, v, cu_seqlens, pos_offset, rope_table, rope
 def rlk_attn_qcache_read(params, k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages,
                          cu_seqlens, pos_offset, k, v, stream=None):
     """Read token ranges of the 8-bit pages back as packed BF16 K/V rows."""
-    cu, cu_p = _i32_addr(cu_seqlens)
-    po, po_p = _i32_addr(pos_offset)
+    n = params.num_seqs
+    cu, cu_p = _i32_addr(cu_seqlens, n + 1)
+    po, po_p = _i32_addr(pos_offset, n)
     kp, vp, ks, vs, pt, k, v, st = _dev_args(
         stream, ("codes", k_pool), ("codes", v_pool), ("f32", k_scale), ("f32", v_scale), ("i32", page_table),
         ("bf16", k), ("bf16", v))
@@ -421,7 +428,7 @@ def rlk_attn_decode_qcache(params, q, k_pool, v_pool, k_scale, v_scale, n_pages,
     """Decode over the 8-bit pages (split_k: 0 spreads the work evenly, k cuts
     a (sequence, KV head) into at most k parts; rope_table: rotate the query
     rows, or None)."""
-    sl, sl_p = _i32_addr(seqlens)
+    sl, sl_p = _i32_addr(seqlens, params.num_seqs)
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     q, kp, vp, ks, vs, pt, rt, of, ob, ls, ws, st = _dev_args(

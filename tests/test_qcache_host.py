@@ -164,3 +164,15 @@ def test_binding_refuses_host_tensors():
     k = torch.zeros((5, 8, 128), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         _write(rlk.make_params(1), k=k, v=k)
+
+
+@pytest.mark.parametrize("call", [
+    lambda p: _write(p, cu=(0, 1), pos=(0, 0)), lambda p: _write(p, cu=(0, 1, 2), pos=(0,)),
+    lambda p: _read(p, cu=(0, 1), pos=None), lambda p: _read(p, cu=(0, 1, 2), pos=(0,)),
+    lambda p: _decode(p, seqlens=(50,)),
+    lambda p: rlk.rlk_attn_decode_qcache(p, 16, 16, 16, 16, 16, 8, 16, 16, 4, np.array([50], np.int32), 1, None, 0, 16,
+                                         None, 16, stream=0)])
+def test_binding_refuses_short_lists(call):
+    # two sequences, lists for one: the library would read past their ends
+    with pytest.raises(ValueError, match="host integers"):
+        call(rlk.make_params(2))
