@@ -1307,10 +1307,11 @@ size_t qdecode_state_bytes(int64_t segments, int hq) {
 
 // Where each of `grid` CTAs starts.  The blocks of all (sequence, KV head)
 // pairs in order form a line on which a pair costs its blocks and kPairCost
-// quarters of a block more; CTA c starts where the c-th of `grid` equal parts
-// does, moved up to the next segment of its pair, or (split_k) to the next of
-// the at most split_k equal runs of segments.  A pair of up to 2 segments is not
-// cut: counting and folding its parts (3 us) costs more than it evens out.
+// quarters of a block more.  CTA c takes the (grid - c)-th part of what is left,
+// to the nearest end of a segment of its pair (so that no more than half a
+// segment is off), or (split_k) of one of the at most split_k equal runs of
+// segments.  A pair of up to 2 segments is not cut: counting and folding its
+// parts (3 us) costs more than it evens out.
 void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int grid, rlk::QStart* start) {
   constexpr int kSeg = rlk::kQSegKeys / 128;
   auto blocks_of = [&](int s) { return (ctx[s] + 127) / 128; };
@@ -1318,9 +1319,9 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
   for (int s = 0; s < num_seqs; ++s) total += static_cast<int64_t>(hkv) * (4 * blocks_of(s) + rlk::kPairCost);
   int s = 0;
   int64_t cost0 = 0, blk0 = 0;  // where sequence s begins on the line, in cost and in blocks
-  int64_t before = 0;
+  int64_t from = 0, before = 0;  // where the last CTA starts, in cost and in blocks
   for (int c = 0; c <= grid; ++c) {
-    const int64_t x = total / grid * c + std::min<int64_t>(c, total % grid);
+    const int64_t x = c == 0 ? 0 : c == grid ? total : from + (total - from) / (grid - c + 1);
     int64_t at;
     rlk::QStart st{0, 0, 0, 0};
     for (; s < num_seqs; ++s) {
@@ -1335,13 +1336,20 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
       const int nb = blocks_of(s), per = 4 * nb + rlk::kPairCost;
       const int64_t pair = (x - cost0) / per;
       const int rest = static_cast<int>(x - cost0 - pair * per);
-      const int b = std::max(rest - rlk::kPairCost + 3, 0) / 4;
       int step = nb > 2 * kSeg ? kSeg : nb;
       if (split_k) step = ((nb + kSeg - 1) / kSeg + split_k - 1) / split_k * kSeg;
-      const int up = std::min((b + step - 1) / step * step, nb);
-      at = blk0 + pair * nb + up;
-      st = {s, static_cast<int32_t>(pair), up, 0};
-      if (up == nb) {  // the next pair, of this sequence or the next
+      // the ends beside x, as blocks of the pair and costs from its start
+      const int b = std::max(rest - rlk::kPairCost, 0) / 4 / step * step;
+      const int up = rest == 0 ? 0 : std::min(b + step, nb);
+      const int lo_cost = b > 0 ? rlk::kPairCost + 4 * b : 0;
+      const int up_cost = rest == 0 ? 0 : up == nb ? per : rlk::kPairCost + 4 * up;
+      const int64_t pair_cost = cost0 + pair * per;
+      const bool low = rest - lo_cost < up_cost - rest && pair_cost + lo_cost > from;
+      const int cut = low ? b : up;
+      from = pair_cost + (low ? lo_cost : up_cost);
+      at = blk0 + pair * nb + cut;
+      st = {s, static_cast<int32_t>(pair), cut, 0};
+      if (cut == nb) {  // the next pair, of this sequence or the next
         st.b = 0;
         if (++st.g == hkv) {
           st.g = 0;
