@@ -160,13 +160,14 @@ rlk_status make_map(CUtensorMap* m, const void* base, uint64_t d1, uint64_t d2, 
 }
 
 // 8-bit pages of one of K, V: codes [n_pages * hkv][page_size][128], 128-byte
-// swizzle, one (page, head) a box; rows past the last page read as zeros.
+// swizzle, up to kQBoxRows tokens of one (page, head) a box; rows past the last
+// page read as zeros.
 rlk_status make_code_map(CUtensorMap* m, const void* base, uint64_t n_pages, uint64_t hkv, uint32_t page_size) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   cuuint64_t dims[3] = {128, page_size, n_pages * hkv};
   cuuint64_t strides[2] = {128, 128ull * page_size};
-  cuuint32_t box[3] = {128, page_size, 1};
+  cuuint32_t box[3] = {128, std::min<cuuint32_t>(page_size, rlk::kQBoxRows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -39,6 +39,7 @@ cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
 // Decode over the 8-bit pages.  The keys of a sequence are cut into segments
 // of kQSegKeys, whatever CTAs take them (qdecode.cu).
 constexpr int kQSegKeys = 512;
+constexpr int kQBoxRows = 32;  // tokens of a page that one copy takes at the most
 constexpr int kQMaxSeqs = 256;  // sequences per launch
 constexpr int kQMaxParts = 160;  // CTAs per launch
 constexpr int kPairCost = 6;  // a (sequence, KV head)'s fixed cost in quarters of a 128-key block (1.2 us of 0.73)

@@ -541,6 +541,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     uint64_t* empty_b = &bars[is_v ? L::kVEmpty : L::kKEmpty];
     uint8_t* ring = is_v ? v_base : k_base;
     const int lps = 31 - __clz(p.page_size), lg = 7 - lps;  // log2 of a page's tokens, of a block's pages
+    const int lbox = min(lps, 31 - __clz(kQBoxRows));       // and of a copy's tokens
     // page ids: two groups of blocks ahead, across pieces
     QGroups cur(p, lg), ahead(p, lg);
     int id = ahead.page_id(p, lg, lane);
@@ -657,16 +658,18 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           n += cur.n;
         }
         uint8_t* dst = ring + stage * L::kKVBytes;
-        const int n_pg = (min(B, cur.pc.kv_len - (cur.b + i) * B) + (1 << lps) - 1) >> lps;
-        if (lane == 0) mbar_arrive_expect_tx(full_b + stage, (n_pg << lps) * 128);
+        const int n_box = (min(B, cur.pc.kv_len - (cur.b + i) * B) + (1 << lbox) - 1) >> lbox;
+        if (lane == 0) mbar_arrive_expect_tx(full_b + stage, (n_box << lbox) * 128);
         __syncwarp();
-        // one copy a page, issued by one lane in a loop the whole warp walks
-        // (issued by the lanes that hold the page ids, one lane after another,
-        // they took more than a block's time at HBM rate)
+        // copies of a page's boxes of up to kQBoxRows tokens (a context's last
+        // page is not read past the box it ends in), issued by one lane in a
+        // loop the whole warp walks (issued by the lanes that hold the page ids,
+        // one lane after another, they took more than a block's time at HBM rate)
 #pragma unroll 4
-        for (int k = 0; k < n_pg; ++k) {
-          const int r = __shfl_sync(0xffffffffu, row, (i << lg) + k);
-          if (leader) tma_load_3d(dst + ((k << lps) * 128), map, full_b + stage, 0, 0, r);
+        for (int k = 0; k < n_box; ++k) {
+          const int r = __shfl_sync(0xffffffffu, row, (i << lg) + (k << lbox >> lps));
+          if (leader)
+            tma_load_3d(dst + ((k << lbox) * 128), map, full_b + stage, 0, (k << lbox) & (p.page_size - 1), r);
         }
         if (++stage == static_cast<uint32_t>(S)) {
           stage = 0;
