@@ -1324,7 +1324,7 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
   for (int c = 0; c <= grid; ++c) {
     const int64_t x = c == 0 ? 0 : c == grid ? total : from + (total - from) / (grid - c + 1);
     int64_t at;
-    rlk::QStart st{0, 0, 0, 0};
+    rlk::QStart st{0, 0, 0, 0, 0};
     for (; s < num_seqs; ++s) {
       const int64_t cost = static_cast<int64_t>(hkv) * (4 * blocks_of(s) + rlk::kPairCost);
       if (x < cost0 + cost) break;
@@ -1349,7 +1349,7 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
       const int cut = low ? b : up;
       from = pair_cost + (low ? lo_cost : up_cost);
       at = blk0 + pair * nb + cut;
-      st = {s, static_cast<int32_t>(pair), cut, 0};
+      st = {s, static_cast<int32_t>(pair), cut, 0, cut};
       if (cut == nb) {  // the next pair, of this sequence or the next
         st.b = 0;
         if (++st.g == hkv) {
@@ -1358,7 +1358,12 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
         }
       }
     }
-    if (c > 0) start[c - 1].left = static_cast<int32_t>(at - before);
+    if (c > 0) {
+      start[c - 1].left = static_cast<int32_t>(at - before);
+      // CTAs that start inside one pair: cut first where the first of them starts
+      const rlk::QStart& b4 = start[c - 1];
+      if (st.b > 0 && b4.b > 0 && b4.seq == st.seq && b4.g == st.g) st.cut = b4.cut;
+    }
     if (c < grid) start[c] = st;
     before = at;
   }

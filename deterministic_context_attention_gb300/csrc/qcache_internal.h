@@ -43,8 +43,9 @@ constexpr int kQBoxRows = 32;  // tokens of a page that one copy takes at the mo
 constexpr int kQMaxSeqs = 256;  // sequences per launch
 constexpr int kQMaxParts = 160;  // CTAs per launch
 constexpr int kPairCost = 6;  // a (sequence, KV head)'s fixed cost in quarters of a 128-key block (1.2 us of 0.73)
-struct alignas(16) QStart {  // where a CTA's work starts, and how many blocks it has
+struct QStart {  // where a CTA's work starts, and how many blocks it has
   int32_t seq, g, b, left;
+  int32_t cut;  // b > 0: the block at which that pair is first cut
 };
 struct QDecodeParams {
   ErrWord* err;
@@ -59,9 +60,10 @@ struct QDecodeParams {
   float* out_f32;
   uint16_t* out_bf16;
   float* lse;
-  // segment states of the pairs several CTAs share: row (seg0[s] + segment) *
-  // hq + head of state_o [.., 128] and state_ml [.., 2] (m in log2, l), and
-  // one count of finished segments per (sequence, KV head)
+  // states of the pairs several CTAs share: row (seg0[s] + segment) * hq + head
+  // of state_o [.., 128] and state_ml [.., 2] (m in log2, l), the first piece's
+  // at its last segment; and one count of finished segments per (sequence, KV
+  // head)
   float* state_o;
   float* state_ml;
   unsigned long long* counts;

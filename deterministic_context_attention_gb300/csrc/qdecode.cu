@@ -31,9 +31,11 @@
 // line; CTA c of g takes its c-th g-th part by cost (a pair counts 1.5 blocks
 // more than it has), cut at segment boundaries, so the SMs' loads differ by a
 // segment at the most.  A CTA that holds a whole pair writes its output;
-// otherwise each segment's state goes to the workspace, and the CTA that counts
+// otherwise a pair's first piece leaves what it has folded as one state, the
+// others the state of each segment, in the workspace, and the CTA that counts
 // the last segment of a pair (which one changes nothing in the result) folds
-// them.
+// them.  (With a state per segment from the first piece too, 64 sequences of
+// 512 .. 32768 tokens took 348 us instead of 342.)
 //
 // What bounds it: HBM, 32 KB of codes per (KV head, 128-key block), 0.73 us a
 // block and SM at the measured copy rate; long sequences in 16-token pages and
@@ -109,7 +111,8 @@ struct QDecLayout {
                        kSyncMax = kStatsFull + kSR, kStored = kSyncMax + 4, kCounted = kStored + 1,
                        kEndCounted = kCounted + 1, kScales = kEndCounted + 1, kNumBars = kScales + kScRing;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base (u32), abort (i32)
-  static constexpr int kCutOff = (kMiscOff + 16 + 15) / 16 * 16;  // the pairs to fold: int4 {seq, g, segments, 1} [2]
+  // pairs to fold: int4 {seq, g, first state, states} [2]
+  static constexpr int kCutOff = (kMiscOff + 16 + 15) / 16 * 16;
   static constexpr int kScOff = kCutOff + 2 * 16;  // float [K, V][kScRing][16 pages]
   static constexpr int kRowOff = kScOff + 2 * kScRing * 16 * 4;  // staged query rows and RoPE table row
   static constexpr int kRowBytes = MG * 256 + 512;
@@ -254,6 +257,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // A piece of work: segments [s0, s1) of the ns of (sequence, KV head g).
 struct QPiece {
   int seq, g, kv_len, nb, s0, s1, ns;
+  int first;  // the segments that the pair's first piece has
   __device__ int block0() const { return s0 * kSegBlocks; }
   __device__ int block1() const { return min(s1 * kSegBlocks, nb); }
   __device__ bool whole() const { return s0 == 0 && s1 == ns; }
@@ -266,12 +270,14 @@ struct QPiece {
 struct QWalk {
   int seq, g, b;  // where the next piece starts
   int left;       // blocks still to take
+  int cut;        // b > 0: where that pair is first cut
   __device__ explicit QWalk(const QDecodeParams& p) {
     const QStart s = p.start[blockIdx.x];
     seq = s.seq;
     g = s.g;
     b = s.b;
     left = s.left;
+    cut = s.cut;
   }
   __device__ bool next(const QDecodeParams& p, QPiece* q) {
     if (left <= 0) return false;
@@ -283,6 +289,7 @@ struct QWalk {
     const int stop = min(left, q->nb - b);
     q->s0 = b / kSegBlocks;
     q->s1 = (b + stop + kSegBlocks - 1) / kSegBlocks;
+    q->first = b > 0 ? cut / kSegBlocks : q->s1;
     left -= stop;
     b = 0;
     if (++g == p.hkv) {
@@ -357,17 +364,19 @@ __device__ __forceinline__ bool count_segments(unsigned long long* word, int n, 
   return last;
 }
 
-// The fold of a cut pair's segment states, one warp a query head: lane l
-// takes head dimensions 4 l .. 4 l + 3.  Groups of 4 segments are copied ahead
+// The fold of a cut pair's ns states (the first piece's, then its other
+// segments', from segment `seg` of the workspace on), one warp a query head: lane
+// l takes head dimensions 4 l .. 4 l + 3.  Groups of 4 segments are copied ahead
 // into the warp's ring (a lane reads what it copied itself).  One warp a
 // scheduler, so what costs is the chain of dependent steps: for 32 segments at
 // a time the running maxima are a scan over the lanes and the factors come out
 // side by side (the same values as one after another: a maximum rounds
 // nothing), which leaves a multiply and an fma a segment on the chain.
 template <int GROUPS>
-__device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, int h, int lane, float4* ring) {
+__device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int seg, int ns, int h, int lane,
+                                       float4* ring) {
   constexpr int C = 4;
-  const int64_t base = static_cast<int64_t>(p.seg0[seq]) * p.hq + h;
+  const int64_t base = static_cast<int64_t>(seg) * p.hq + h;
   const int64_t pitch = static_cast<int64_t>(p.hq) * kHeadDim;
   const float* src = p.state_o + base * kHeadDim + 4 * lane;
   const float2* sml = reinterpret_cast<const float2*>(p.state_ml) + base;
@@ -393,7 +402,7 @@ __device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int ns, 
   float2 ml = load_ml(0);
 #pragma unroll 1
   for (int c = 0; c < GROUPS; ++c) copy();
-  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 O = make_float4(-0.f, -0.f, -0.f, -0.f);  // the first state as it is, its sign of zero too
   float m = -INFINITY, l = 0.f;
 #pragma unroll 1
   for (int s0 = 0; s0 < ns; s0 += 32) {
@@ -522,10 +531,10 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       const int4 c = i < n0 ? c0 : c1;
       const int h = c.y * MG + (i < n0 ? i : i - n0);
       if (end)
-        fold_pair<L::kEndGroups>(p, c.x, c.z, h, lane,
+        fold_pair<L::kEndGroups>(p, c.x, c.z, c.w, h, lane,
                                  reinterpret_cast<float4*>(k_base) + warp * L::kEndGroups * 4 * 32);
       else
-        fold_pair<L::kFoldGroups>(p, c.x, c.z, h, lane,
+        fold_pair<L::kFoldGroups>(p, c.x, c.z, c.w, h, lane,
                                   reinterpret_cast<float4*>(smem + L::kFoldOff) + warp * L::kFoldGroups * 4 * 32);
     }
   };
@@ -898,7 +907,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     uint32_t o_it = 0, cut_it = 0;
     struct Cut {
-      int seq, g, n, ns;
+      int seq, g, n, ns, first;
     } cut0 = {}, cut1 = {};
     int n_cut = 0;
     bool fail = false;
@@ -918,7 +927,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
             last = count_segments(p.counts + static_cast<int64_t>(q.seq) * p.hkv + q.g, q.n, q.ns);
             __threadfence();
           }
-          to_fold[lane] = make_int4(q.seq, q.g, q.ns, last);
+          to_fold[lane] = make_int4(q.seq, q.g, p.seg0[q.seq] + q.first - 1, last ? q.ns - q.first + 1 : 0);
         }
         warp_arrive(&bars[end ? L::kEndCounted : L::kCounted], lane);
       }
@@ -935,8 +944,8 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     while (walk.next(p, &pc)) {
       const bool whole = pc.whole();
       if (!whole && tid == 0) begin_count(p.counts + static_cast<int64_t>(pc.seq) * p.hkv + pc.g, p.nonce);
-      // O: the segment's, T: the sequence's (whole pairs); lane q holds m and
-      // l of query head q
+      // O: the segment's, T: the sequence's (of a pair's first or only piece);
+      // lane q holds m and l of query head q
       float O[MG], T[MG];
 #pragma unroll
       for (int q = 0; q < MG; ++q) O[q] = T[q] = 0.0f;
@@ -987,8 +996,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         ++o_it;
         if ((b + 1) % kSegBlocks != 0 && b + 1 != pc.nb) continue;
         // the segment is complete
-        const int seg = b / kSegBlocks;
-        if (whole) {
+        if (pc.s0 == 0) {
           float mn, ta, tb;
           fold_factors(mt, m, mn, ta, tb);
           lt = __fmaf_rn(l, tb, __fmul_rn(lt, ta));
@@ -999,12 +1007,14 @@ __global__ void __launch_bounds__(kQDThreads, 1)
             const float bq = __shfl_sync(0xffffffffu, tb, q);
             T[q] = __fmaf_rn(O[q], bq, __fmul_rn(T[q], aq));
           }
-        } else {
-          const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + seg) * p.hq + pc.g * MG;
-#pragma unroll
-          for (int q = 0; q < MG; ++q) p.state_o[(r + q) * kHeadDim + d] = O[q];
-          if (warp == 0 && lane < MG) reinterpret_cast<float2*>(p.state_ml)[r + lane] = make_float2(m, l);
+          if (whole || b + 1 < b1) continue;
+          m = mt;  // the pair's first piece leaves as one state, its last segment's
+          l = lt;
         }
+        const int64_t r = static_cast<int64_t>(p.seg0[pc.seq] + b / kSegBlocks) * p.hq + pc.g * MG;
+#pragma unroll
+        for (int q = 0; q < MG; ++q) p.state_o[(r + q) * kHeadDim + d] = pc.s0 == 0 ? T[q] : O[q];
+        if (warp == 0 && lane < MG) reinterpret_cast<float2*>(p.state_ml)[r + lane] = make_float2(m, l);
       }
       if (fail) break;
       if (whole) {
@@ -1025,7 +1035,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       // a part of a pair: counted once the next piece is done too (waiting
       // here for the stores and the count would hold up the blocks behind)
       cut1 = cut0;
-      cut0 = {pc.seq, pc.g, pc.s1 - pc.s0, pc.ns};
+      cut0 = {pc.seq, pc.g, pc.s1 - pc.s0, pc.ns, pc.first};
       if (++n_cut == 2 && !flush(walk.left <= 0)) break;
     }
     if (!fail && n_cut > 0) flush(true);
