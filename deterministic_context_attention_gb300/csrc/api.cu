@@ -1306,18 +1306,18 @@ size_t qdecode_state_bytes(int64_t segments, int hq) {
   return static_cast<size_t>(segments) * hq * (rlk::kHeadDim + 2) * sizeof(float);
 }
 
-// Where each of `grid` CTAs starts.  The blocks of all (sequence, KV head)
-// pairs in order form a line on which a pair costs its blocks and kPairCost
-// quarters of a block more.  CTA c takes the (grid - c)-th part of what is left,
-// to the nearest end of a segment of its pair (so that no more than half a
-// segment is off), or (split_k) of one of the at most split_k equal runs of
-// segments.  A pair of up to 2 segments is not cut: counting and folding its
-// parts (3 us) costs more than it evens out.
-void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int grid, rlk::QStart* start) {
+// Where each of `grid` groups of CTAs starts.  The blocks of all (sequence,
+// head group) pairs in order form a line on which a pair costs its blocks and
+// kPairCost quarters of a block more.  Group c takes the (grid - c)-th part of
+// what is left, to the nearest end of a segment of its pair (so that no more
+// than half a segment is off), or (split_k) of one of the at most split_k equal
+// runs of segments.  A pair of up to 2 segments is not cut: counting and folding
+// its parts (3 us) costs more than it evens out.
+void plan_qdecode(const int32_t* ctx, int num_seqs, int groups, int split_k, int grid, rlk::QStart* start) {
   constexpr int kSeg = rlk::kQSegKeys / 128;
   auto blocks_of = [&](int s) { return (ctx[s] + 127) / 128; };
   int64_t total = 0;
-  for (int s = 0; s < num_seqs; ++s) total += static_cast<int64_t>(hkv) * (4 * blocks_of(s) + rlk::kPairCost);
+  for (int s = 0; s < num_seqs; ++s) total += static_cast<int64_t>(groups) * (4 * blocks_of(s) + rlk::kPairCost);
   int s = 0;
   int64_t cost0 = 0, blk0 = 0;  // where sequence s begins on the line, in cost and in blocks
   int64_t from = 0, before = 0;  // where the last CTA starts, in cost and in blocks
@@ -1326,10 +1326,10 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
     int64_t at;
     rlk::QStart st{0, 0, 0, 0, 0};
     for (; s < num_seqs; ++s) {
-      const int64_t cost = static_cast<int64_t>(hkv) * (4 * blocks_of(s) + rlk::kPairCost);
+      const int64_t cost = static_cast<int64_t>(groups) * (4 * blocks_of(s) + rlk::kPairCost);
       if (x < cost0 + cost) break;
       cost0 += cost;
-      blk0 += static_cast<int64_t>(hkv) * blocks_of(s);
+      blk0 += static_cast<int64_t>(groups) * blocks_of(s);
     }
     if (s == num_seqs) {
       at = blk0;
@@ -1352,7 +1352,7 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
       st = {s, static_cast<int32_t>(pair), cut, 0, cut};
       if (cut == nb) {  // the next pair, of this sequence or the next
         st.b = 0;
-        if (++st.g == hkv) {
+        if (++st.g == groups) {
           st.g = 0;
           ++st.seq;
         }
@@ -1360,7 +1360,7 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int hkv, int split_k, int gr
     }
     if (c > 0) {
       start[c - 1].left = static_cast<int32_t>(at - before);
-      // CTAs that start inside one pair: cut first where the first of them starts
+      // several that start inside one pair: it is cut first where the first of them starts
       const rlk::QStart& b4 = start[c - 1];
       if (st.b > 0 && b4.b > 0 && b4.seq == st.seq && b4.g == st.g) st.cut = b4.cut;
     }
@@ -1429,8 +1429,16 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   CUtensorMap mk, mv;
   if ((st = make_code_map(&mk, cache.k_pool, cache.n_pages, hkv, cache.page_size))) return st;
   if ((st = make_code_map(&mv, cache.v_pool, cache.n_pages, hkv, cache.page_size))) return st;
-  const int grid = static_cast<int>(std::min<int64_t>({dev->num_sms, rlk::kQMaxParts, segments * hkv}));
-  plan_qdecode(dp.ctx, params->num_seqs, hkv, split_k, grid, dp.start);
+  const int sms = std::min(dev->num_sms, rlk::kQMaxParts);
+  // the most KV heads that can be taken side by side (qdecode.cu) with no more
+  // than 1 SM in 64 left over
+  int group = 1;
+  for (int d = 2; d <= hkv && d <= sms; ++d)
+    if (hkv % d == 0 && sms % d <= sms / 64) group = d;
+  const int parts = static_cast<int>(std::min<int64_t>(sms / group, segments * (hkv / group)));
+  const int grid = parts * group;
+  plan_qdecode(dp.ctx, params->num_seqs, hkv / group, split_k, parts, dp.start);
+  dp.group = group;
   dp.err = dev->err;
   dp.num_seqs = params->num_seqs;
   dp.hq = hq;

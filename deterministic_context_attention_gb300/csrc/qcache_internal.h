@@ -43,13 +43,14 @@ constexpr int kQBoxRows = 32;  // tokens of a page that one copy takes at the mo
 constexpr int kQMaxSeqs = 256;  // sequences per launch
 constexpr int kQMaxParts = 160;  // CTAs per launch
 constexpr int kPairCost = 6;  // a (sequence, KV head)'s fixed cost in quarters of a 128-key block (1.2 us of 0.73)
-struct QStart {  // where a CTA's work starts, and how many blocks it has
+struct QStart {  // where a group of CTAs starts (g: a group of KV heads), and how many blocks each has
   int32_t seq, g, b, left;
   int32_t cut;  // b > 0: the block at which that pair is first cut
 };
 struct QDecodeParams {
   ErrWord* err;
   int32_t num_seqs, hq, hkv;
+  int32_t group;  // KV heads that consecutive CTAs take side by side
   float scale_log2;
   const uint16_t* q;  // [num_seqs, hq, 128] BF16
   const float* k_scale;

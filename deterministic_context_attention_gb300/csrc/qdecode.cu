@@ -27,9 +27,13 @@
 // chain: one over every block of a 32768-token sequence, on states written
 // out per block, took 125 us for 4 sequences where the pages take 40.)
 //
-// Work split.  The blocks of all (sequence, KV head) pairs in order form one
-// line; CTA c of g takes its c-th g-th part by cost (a pair counts 1.5 blocks
-// more than it has), cut at segment boundaries, so the SMs' loads differ by a
+// Work split.  Neighbouring CTAs take neighbouring KV heads of the same keys
+// side by side (a group: all 8 heads of 8, as many as divide the SMs), because
+// the heads' pages lie next to each other: 64 sequences of 512 .. 32768 tokens
+// in 16-token pages took 341 us with one head's line of pages a CTA, 333 with
+// the groups.  The blocks of all (sequence, head group) pairs in order form one
+// line; each group takes an equal part of it by cost (a pair counts 1.5 blocks
+// more than it has), cut at segment ends, so the SMs' loads differ by a
 // segment at the most.  A CTA that holds a whole pair writes its output;
 // otherwise a pair's first piece leaves what it has folded as one state, the
 // others the state of each segment, in the workspace, and the CTA that counts
@@ -268,13 +272,13 @@ struct QPiece {
 // in the parameters, it was the first 4 us of every CTA: each probe of a table
 // missed the constant cache).
 struct QWalk {
-  int seq, g, b;  // where the next piece starts
+  int seq, g, b;  // where the next piece starts (g: the first KV head of the group's)
   int left;       // blocks still to take
   int cut;        // b > 0: where that pair is first cut
   __device__ explicit QWalk(const QDecodeParams& p) {
-    const QStart s = p.start[blockIdx.x];
+    const QStart s = p.start[blockIdx.x / p.group];
     seq = s.seq;
-    g = s.g;
+    g = s.g * p.group + blockIdx.x % p.group;
     b = s.b;
     left = s.left;
     cut = s.cut;
@@ -292,8 +296,9 @@ struct QWalk {
     q->first = b > 0 ? cut / kSegBlocks : q->s1;
     left -= stop;
     b = 0;
-    if (++g == p.hkv) {
-      g = 0;
+    g += p.group;
+    if (g >= p.hkv) {
+      g -= p.hkv;
       ++seq;
     }
     return true;

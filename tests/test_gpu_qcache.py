@@ -292,6 +292,19 @@ def test_split_on_chip_group_shapes(hq, hkv, k):
     assert_bitwise(qh.decode(rlk, torch, c, q, ctx, hq, k), qh.decode(rlk, torch, c, q, ctx, hq), f"{hq}/{hkv} k {k}")
 
 
+@pytest.mark.parametrize("hq,hkv", [(3, 3), (10, 5), (14, 7), (12, 12), (20, 20), (32, 32), (160, 160)])
+def test_kv_head_counts(hq, hkv):
+    # heads that divide the SMs, that do not, and more of them than there are SMs
+    torch, rlk = torch_cuda(), lib()
+    ctx = [1, 700, 1500]
+    c = qh.filled(ctx, hkv, 16, seed=38, spread=False)
+    q = synth.normal_bf16(39, synth.T_Q, (3, hq, 128))
+    one = qh.decode(rlk, torch, c, q, ctx, hq, 1, scale=0.1)
+    for k in (0, 2):
+        assert_bitwise(qh.decode(rlk, torch, c, q, ctx, hq, k, scale=0.1), one, f"{hq}/{hkv} k {k}")
+    assert_decode(one, q, c, np.array(ctx, np.int32), hq, 0.1, f"{hq}/{hkv}")
+
+
 @pytest.fixture(scope="module")
 def long_case():
     # 79 and 40 segments of 512 keys: cut over many CTAs, folded past 32
