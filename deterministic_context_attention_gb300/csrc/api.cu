@@ -1266,7 +1266,7 @@ rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const vo
     qp->page0[s + 1] = static_cast<int32_t>(qp->page0[s] + pages);
   }
   const int64_t pages = qp->page0[params->num_seqs];
-  // one block of 8 warps takes 8 (page, K or V, head) units at the most
+  // a CTA takes one (page, K or V, head) unit at the least
   if (pages * 2 * hkv > (static_cast<int64_t>(INT32_MAX) / 8) * 8)
     return fail(RLK_ERR_UNSUPPORTED, "more than 2^31 (page, head) units in one call");
   if (pages == 0) return ok();

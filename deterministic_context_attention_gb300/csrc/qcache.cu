@@ -38,8 +38,12 @@
 namespace rlk {
 namespace {
 
+// A CTA: 8 warps for 128-token pages, whose (page, head)s take them all, else 4
+// (writing 64-token pages: 63.4 us with 8, of which a unit waits for the unit
+// beside it too, 61.7 with 4).
 constexpr int kQThreads = 256;
 constexpr int kQWarps = kQThreads / 32;
+int q_warps(int page_size) { return page_size > 64 ? 8 : 4; }
 constexpr int kQEsMin = 14;  // the biased exponent of the smallest block maximum that sets a scale (e = -120)
 
 // One unit: head `head` of a page (of K or V) and its slots [slot0, slot1),
@@ -58,7 +62,7 @@ __device__ __forceinline__ QUnit q_unit(const QCacheParams& p, int warp) {
   QUnit r;
   const int hkv = p.c.hkv, ps = p.c.page_size;
   const int lw = __clz(R) - __clz(ps);  // log2 of the warps of a unit (1 .. 8)
-  const unsigned u = blockIdx.x * static_cast<unsigned>(kQWarps >> lw) + (warp >> lw);
+  const unsigned u = blockIdx.x * (blockDim.x >> 5 >> lw) + (warp >> lw);
   r.part = warp & ((1 << lw) - 1);
   const unsigned pk = u / hkv;
   r.head = static_cast<int>(u - pk * hkv);
@@ -348,32 +352,33 @@ __global__ void __launch_bounds__(kQThreads) rlk_qcache_read_kernel(const __grid
   }
 }
 
-// blocks of kQWarps warps over every (page, K or V, head, part) of the call
-int64_t q_blocks(const QCacheParams& p, int rows) {
+// CTAs over every (page, K or V, head, part) of the call
+unsigned q_blocks(const QCacheParams& p, int rows) {
   const int64_t warps = static_cast<int64_t>(p.page0[p.num_seqs]) * 2 * p.c.hkv * (p.c.page_size / rows);
-  return (warps + kQWarps - 1) / kQWarps;
+  const int per = q_warps(p.c.page_size);
+  return static_cast<unsigned>((warps + per - 1) / per);
 }
 
 }  // namespace
 
 cudaError_t launch_qcache_write(const QCacheParams& p, cudaStream_t stream) {
   const int rows = std::min(p.c.page_size, 16);
-  const unsigned blocks = static_cast<unsigned>(q_blocks(p, rows));
+  const unsigned blocks = q_blocks(p, rows), threads = 32 * q_warps(p.c.page_size);
   if (p.rope_table) {
-    if (rows == 8) rlk_qcache_write_kernel<8, true><<<blocks, kQThreads, 0, stream>>>(p);
-    else rlk_qcache_write_kernel<16, true><<<blocks, kQThreads, 0, stream>>>(p);
+    if (rows == 8) rlk_qcache_write_kernel<8, true><<<blocks, threads, 0, stream>>>(p);
+    else rlk_qcache_write_kernel<16, true><<<blocks, threads, 0, stream>>>(p);
   } else {
-    if (rows == 8) rlk_qcache_write_kernel<8, false><<<blocks, kQThreads, 0, stream>>>(p);
-    else rlk_qcache_write_kernel<16, false><<<blocks, kQThreads, 0, stream>>>(p);
+    if (rows == 8) rlk_qcache_write_kernel<8, false><<<blocks, threads, 0, stream>>>(p);
+    else rlk_qcache_write_kernel<16, false><<<blocks, threads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream) {
   const int rows = std::min(p.c.page_size, 16);
-  const unsigned blocks = static_cast<unsigned>(q_blocks(p, rows));
-  if (rows == 8) rlk_qcache_read_kernel<8><<<blocks, kQThreads, 0, stream>>>(p);
-  else rlk_qcache_read_kernel<16><<<blocks, kQThreads, 0, stream>>>(p);
+  const unsigned blocks = q_blocks(p, rows), threads = 32 * q_warps(p.c.page_size);
+  if (rows == 8) rlk_qcache_read_kernel<8><<<blocks, threads, 0, stream>>>(p);
+  else rlk_qcache_read_kernel<16><<<blocks, threads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
