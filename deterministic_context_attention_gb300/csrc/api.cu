@@ -1237,14 +1237,14 @@ rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const vo
   if (!cu_seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL");
   if (cu_seqlens[0] != 0) return fail(RLK_ERR_INVALID_ARGUMENT, "cu_seqlens must start at 0");
   const int hkv = params->num_kv_heads, ps = cache.page_size;
-  if (params->num_seqs > rlk::kMaxSeqs)
+  if (params->num_seqs > rlk::kQMaxSeqs)
     return over_ranges(params->num_seqs, [&](int s0, int s1) {
       const rlk_attn_params rp = range_params(params, s0, s1);
       const auto cu = rebase(cu_seqlens, s0, s1);
       const int64_t o = static_cast<int64_t>(cu_seqlens[s0]) * hkv * rlk::kHeadDim;
       return qcache_impl(&rp, adv(k_in, o, 2), adv(v_in, o, 2), adv(k_out, o, 2), adv(v_out, o, 2), cu.data(),
                          pos_offset ? pos_offset + s0 : nullptr, rope_table, rope_max_pos, cache.from(s0), stream);
-    });
+    }, rlk::kQMaxSeqs);
   auto qp = std::make_unique<rlk::QCacheParams>();
   std::memset(qp.get(), 0, sizeof(*qp));
   for (int s = 0; s < params->num_seqs; ++s) {

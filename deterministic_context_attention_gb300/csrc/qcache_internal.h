@@ -7,6 +7,8 @@
 
 namespace rlk {
 
+constexpr int kQMaxSeqs = 256;  // sequences per launch
+
 // The pages: E4M3 codes [n_pages][hkv][page_size][128] and FP32 scales
 // [n_pages][hkv], for K and for V, under one page table.
 struct QCachePools {
@@ -29,9 +31,9 @@ struct QCacheParams {
   uint16_t* v_out;
   const float* rope_table;  // write: rotates K at its positions, or null
   int32_t num_seqs;
-  int32_t cu[kMaxSeqs + 1];
-  int32_t pos0[kMaxSeqs];
-  int32_t page0[kMaxSeqs + 1];  // prefix sum of the pages the sequences touch
+  int32_t cu[kQMaxSeqs + 1];
+  int32_t pos0[kQMaxSeqs];
+  int32_t page0[kQMaxSeqs + 1];  // prefix sum of the pages the sequences touch
 };
 cudaError_t launch_qcache_write(const QCacheParams& p, cudaStream_t stream);
 cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
@@ -40,7 +42,6 @@ cudaError_t launch_qcache_read(const QCacheParams& p, cudaStream_t stream);
 // of kQSegKeys, whatever CTAs take them (qdecode.cu).
 constexpr int kQSegKeys = 512;
 constexpr int kQBoxRows = 32;  // tokens of a page that one copy takes at the most
-constexpr int kQMaxSeqs = 256;  // sequences per launch
 constexpr int kQMaxParts = 160;  // CTAs per launch
 constexpr int kPairCost = 6;  // a (sequence, KV head)'s fixed cost in quarters of a 128-key block (1.2 us of 0.73)
 struct QStart {  // where a group of CTAs starts (g: a group of KV heads), and how many blocks each has
