@@ -49,7 +49,9 @@
 // scales).  Per block the tensor core issues 4 + 4 MMAs of K = 32 codes (the
 // BF16 decode needs 8 + 16), and the softmax's 8 warps run two blocks at a
 // time.  A call costs about 5 us before its first block is folded and, where
-// pairs are cut, 3 to 6 us for counting and folding.
+// pairs are cut, 3 to 6 us for counting and folding: 64 sequences of 512 ..
+// 32768 tokens take 328 .. 336 us (0.96 .. 0.98 of the copy rate), 4 of 32768
+// tokens 56 (0.71).
 //
 // Warp roles (512 threads):
 //   warps 0-3   correction / epilogue: thread d owns head dimension d
