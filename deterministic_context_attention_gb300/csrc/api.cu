@@ -1381,6 +1381,7 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   if (!aligned16(q) || !aligned16(out_f32) || !aligned16(out_bf16) || !aligned16(rope_table) ||
       (split_k != 1 && !aligned16(workspace)))
     return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(RLK_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
   if ((st = check_qcache(params, cache))) return st;
   const int hq = params->num_q_heads, hkv = params->num_kv_heads, B = params->kv_block_size;
   if (B != 128 || hq / hkv > rlk::kDecodeMaxGroup)

@@ -89,9 +89,9 @@ def _read(p, k=16, v=16, cu=(0, 5), pos=(3,), table=16, kp=16, vp=16, ks=16, vs=
 
 
 def _decode(p, q=16, seqlens=(50,), split=1, table=16, rope=None, max_pos=0, kp=16, vp=16, ks=16, vs=16, n_pages=8,
-            page=16, max_pages=4, out=16, outb=None, ws=16, ws_bytes=1 << 20):
+            page=16, max_pages=4, out=16, outb=None, lse=16, ws=16, ws_bytes=1 << 20):
     rlk.rlk_attn_decode_qcache(p, q, kp, vp, ks, vs, n_pages, page, table, max_pages, list(seqlens), split, rope,
-                               max_pos, out, outb, 16, ws, ws_bytes, stream=0)
+                               max_pos, out, outb, lse, ws, ws_bytes, stream=0)
 
 
 BAD_CACHE = [(dict(kp=None), 1), (dict(vp=None), 1), (dict(ks=None), 1), (dict(vs=None), 1), (dict(table=None), 1),
@@ -125,7 +125,7 @@ def test_read_refuses(lib, kw, status):
 @pytest.mark.parametrize("split", [0, 1, 3])
 @pytest.mark.parametrize("kw,status", BAD_CACHE + [
     (dict(q=None), 1), (dict(q=24), 1), (dict(seqlens=(0,)), 1), (dict(seqlens=(65,)), 1), (dict(out=None), 1),
-    (dict(out=None, outb=24), 1), (dict(rope=16, max_pos=49), 1), (dict(rope=18, max_pos=100), 1)])
+    (dict(out=None, outb=24), 1), (dict(lse=18), 1), (dict(rope=16, max_pos=49), 1), (dict(rope=18, max_pos=100), 1)])
 def test_decode_refuses(lib, kw, status, split):
     _refused(lambda: _decode(rlk.make_params(1), split=split, **kw), status)
 
