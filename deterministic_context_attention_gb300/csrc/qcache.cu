@@ -166,8 +166,12 @@ __device__ __forceinline__ uint32_t rescale_byte(uint32_t c, int d) {
 // R: rows a warp takes (8 for 8-token pages, else 16).  Lane l holds elements
 // 8 j .. 8 j + 7 and 64 + 8 j .. (j = l mod 8; the RoPE pairs of one another) of
 // rows 4 i + l / 8.
+// Registers are held to 64 (R = 16), 48 and 40 (R = 8 with and without RoPE):
+// the fewer, the more loads in flight, until they spill.  104,000 tokens of 8
+// heads: with RoPE 113.9 us (120.0 with 80 registers, 127 with 89), 8-token pages
+// 106.5 (114.7 with 60, 146.7 with 32) and with RoPE 124.6 (137 with 71).
 template <int R, bool ROPE>
-__global__ void __launch_bounds__(kQThreads, ROPE ? 3 : 4)
+__global__ void __launch_bounds__(kQThreads, R == 16 ? 4 : (ROPE ? 5 : 6))
     rlk_qcache_write_kernel(const __grid_constant__ QCacheParams p) {
   __shared__ uint32_t s_max[kQWarps];
   constexpr int I = R / 4;
