@@ -66,7 +66,7 @@ struct QDecodeParams {
   uint16_t* out_bf16;
   float* lse;
   // states of the pairs several CTAs share: row (seg0[s] + segment) * hq + head
-  // of state_o [.., 128] and state_ml [.., 2] (m in log2, l), the first piece's
+  // of state_o [.., 128] and state_ml [.., 2] (m unscaled, l), the first piece's
   // at its last segment; and one count of finished segments per (sequence, KV
   // head)
   float* state_o;

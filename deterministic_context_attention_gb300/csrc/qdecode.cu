@@ -14,14 +14,18 @@
 // maximum.  w_c = p_c sv_c / A, with sv_c the V scale of key c's page and A
 // the block's largest of them (as a power of two): four pieces leave at most
 // 2^-19 of w_c.  The K scale multiplies the FP32 score of its key,
-//   x_c = (q . code_c) sk_c scale log2(e).
+//   s_c = (q . code_c) sk_c.
 //
-// Softmax, all in FP32.  A block b of 128 keys gives m_b = max x, p = 2^(x -
-// m_b), l_b = sum p and O_b = sum p v.  Blocks are folded left to right into
-// the segment (kSegBlocks blocks, a fixed cut of the sequence) they lie in,
-// and segments left to right into the sequence, both by
-//   M = max(m, m'),  O = O' 2^(m' - M) + O 2^(m - M),  l likewise,
-// so the arithmetic is the same whichever CTAs take which segments: a result
+// Softmax, all in FP32.  A block b of 128 keys gives m_b = max s, p = 2^((s -
+// m_b) c), l_b = sum p and O_b = sum p v, with c = scale log2(e).  Blocks are
+// folded left to right into the segment (kSegBlocks blocks, a fixed cut of the
+// sequence) they lie in, and segments left to right into the sequence, both by
+//   M = max(m, m'),  O = O' 2^((m' - M) c) + O 2^((m - M) c),  l likewise.
+// Maxima stay unscaled and scores are subtracted before they are scaled: the
+// largest key's p is exactly 1 and no p is above it, however large the scores
+// (p = 2^(s c - rn(m c)) is off by half a last place of m c, a factor of 2 and
+// more from 2^24 on, which the sums below do not hold);
+// the arithmetic is the same whichever CTAs take which segments: a result
 // depends on the cached codes, scales and the query alone, not on the batch,
 // the order of the pages or the split.  (Two levels, because the fold is a
 // chain: one over every block of a 32768-token sequence, on states written
@@ -348,11 +352,19 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// 2^((s - m) c), exactly 1 for s = m.
+__device__ __forceinline__ float weight(float s, float m, float c) { return ex2_hw(__fmul_rn(__fsub_rn(s, m), c)); }
+
 // (O, m, l) folded with a later state: the factors of the two, and m.
-__device__ __forceinline__ void fold_factors(float m, float mb, float& mn, float& a, float& b) {
+__device__ __forceinline__ void fold_factors(float m, float mb, float c, float& mn, float& a, float& b) {
   mn = fmaxf(m, mb);
-  a = ex2_hw(__fsub_rn(m, mn));
-  b = ex2_hw(__fsub_rn(mb, mn));
+  a = weight(m, mn, c);
+  b = weight(mb, mn, c);
+}
+
+// ln of the sum of e^(s scale): m the maximum of s, l the sum relative to it.
+__device__ __forceinline__ float log_sum(float m, float l, float c) {
+  return __fmaf_rn(__fmul_rn(m, c), kLn2f, logf(l));
 }
 
 // The count of a cut pair's finished segments: a word that holds the call's
@@ -422,7 +434,7 @@ __device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int seg,
     }
     float before = __shfl_up_sync(0xffffffffu, run, 1);
     if (lane == 0) before = m;
-    const float fa = ex2_hw(__fsub_rn(before, run)), fb = ex2_hw(__fsub_rn(ml.x, run));
+    const float fa = weight(before, run, p.scale_log2), fb = weight(ml.x, run, p.scale_log2);
     m = __shfl_sync(0xffffffffu, run, 31);
 #pragma unroll 1
     for (int s = s0; s < min(s0 + 32, ns); s += C) {
@@ -452,7 +464,7 @@ __device__ __noinline__ void fold_pair(const QDecodeParams& p, int seq, int seg,
   if (p.out_bf16)
     *(reinterpret_cast<uint2*>(p.out_bf16 + row * kHeadDim) + lane) =
         make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
-  if (p.lse && lane == 0) p.lse[row] = __fmaf_rn(m, kLn2f, logf(l));
+  if (p.lse && lane == 0) p.lse[row] = log_sum(m, l, p.scale_log2);
 }
 
 template <int MG>
@@ -863,8 +875,8 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         float mc[MG], pr[MG];
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
-          mc[q] = __fmul_rn(max4(q), sl);
-          pr[q] = vis ? prob(sc[q], sl, -mc[q]) : 0.0f;
+          mc[q] = max4(q);
+          pr[q] = vis ? weight(sc[q], mc[q], sl) : 0.0f;
         }
         // the block's V anchor A = 2^(ae - 127); w = p (sv 2^7 / A)
         const int ae = max(static_cast<int>(__float_as_uint(max4(MG)) >> 23), 8);
@@ -886,8 +898,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(&bars[L::kPFull + grp], lane);
         // the warp's part of the block sums: p <= 1 (and a block's largest is
-        // 1), so 26 fraction bits of fixed point lose less than FP32 sums
-        // would, in one instruction and in no order
+        // 1), so a warp's sum fits 32 bits with 26 fraction bits.  Each p is
+        // off by at most 2^-27, a block's sum by 128 * 2^-27 of at least 1 (128
+        // FP32 numbers in a tree: 7 * 2^-24), in one instruction and in no order
         uint32_t* st = stats + (s_it % SR) * L::kStatWords;
         uint32_t l_mine = 0;  // lane q: query head q's
         float m_mine = 0.0f;
@@ -982,7 +995,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
             l = lb;
           } else {
             float mn;
-            fold_factors(m, mb, mn, fa, fb);
+            fold_factors(m, mb, p.scale_log2, mn, fa, fb);
             l = __fmaf_rn(lb, fb, __fmul_rn(l, fa));
             m = mn;
           }
@@ -1005,7 +1018,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // the segment is complete
         if (pc.s0 == 0) {
           float mn, ta, tb;
-          fold_factors(mt, m, mn, ta, tb);
+          fold_factors(mt, m, p.scale_log2, mn, ta, tb);
           lt = __fmaf_rn(l, tb, __fmul_rn(lt, ta));
           mt = mn;
 #pragma unroll
@@ -1035,7 +1048,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(o);
         }
         if (warp == 0 && lane < MG && p.lse)
-          p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + lane] = __fmaf_rn(mt, kLn2f, logf(lt));
+          p.lse[static_cast<int64_t>(pc.seq) * p.hq + pc.g * MG + lane] = log_sum(mt, lt, p.scale_log2);
         if (n_cut > 0 && !flush(walk.left <= 0)) break;
         continue;
       }

@@ -1,0 +1,114 @@
+"""Decode over the 8-bit pages at the ends of its ranges: scores far past what
+FP32 holds to a unit, values whose scales differ by many powers of two inside
+a block, products of large query rows and large scales.  Every row against
+FP64 attention over the cached values, with a bound relative to the row's own
+sum of |weight * value|."""
+import numpy as np
+import pytest
+
+import oracle.qcache as oq
+from deterministic_context_attention_gb300 import synth
+from tests import qcache_helpers as qh
+from tests.gpu_helpers import assert_bitwise, lib, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def write_all(c, kv):
+    for s, (k, v) in enumerate(kv):
+        oq.write_tokens(c.k, c.ks, c.table[s], synth.bf16_round(k.astype(np.float32)))
+        oq.write_tokens(c.v, c.vs, c.table[s], synth.bf16_round(v.astype(np.float32)))
+    return c
+
+
+def rows_of(c, s, g, ctx):
+    """(k, v, V scale) of a sequence's cached tokens, float64."""
+    at = np.arange(ctx)
+    page, slot = c.table[s][at // c.page], at % c.page
+    e = oq.e4m3_values()
+    return (e[c.k[page, g, slot]] * c.ks[page, g].astype(np.float64)[:, None],
+            e[c.v[page, g, slot]] * c.vs[page, g].astype(np.float64)[:, None], c.vs[page, g].astype(np.float64))
+
+
+def check(got, c, q, ctx, scale, exact_scores, what):
+    """A weight w = p sv of a block whose largest is A keeps 2^-19 of itself or
+    2^-31 of A (four pieces of 4 bits, each 32 times finer, the last one's
+    place fixed); 128 products are summed in FP32 (128 * 2^-23); the block sum
+    of p is off by at most 128 * 2^-27 of a sum of at least 1, the reciprocal,
+    the exponential and the folds by a few 2^-23 (together under 2^-18 here);
+    an exponent x (base 2) carries three roundings, |x| 2^-22 of the weight.
+    Scores of 128 FP32 products are off by at most 2^-22 sum |q k| * scale,
+    unless they are equal or whole gaps apart (exact_scores)."""
+    out, outb, lse = got
+    hq, hkv = q.shape[1], c.k.shape[1]
+    for s in range(len(ctx)):
+        for h in range(hq):
+            k, v, sv = rows_of(c, s, h // (hq // hkv), ctx[s])
+            qr = q[s, h].astype(np.float64)
+            x = (k @ qr) * scale
+            mag = (np.abs(k) @ np.abs(qr)).max() * scale
+            serr = 2.0 ** -22 * mag
+            x2 = (x - x.max()) * np.log2(np.e)
+            w = np.exp2(x2)
+            l = w.sum()
+            ref, ref_lse = (w @ v) / l, x.max() + np.log(l)
+            big = np.array([(w * sv)[b - b % 128:b - b % 128 + 128].max() for b in range(ctx[s])])
+            floor = np.minimum(w, 2.0 ** -31 * big / sv)
+            each = w * (2.0 ** -16 + 2.0 ** -18 + np.abs(x2) * 2.0 ** -22 + (0.0 if exact_scores else 2 * serr)) + floor
+            tol = (each @ np.abs(v)) / l + 1e-37
+            e = np.abs(out[s, h] - ref)
+            assert np.all(e <= tol), (f"{what}: sequence {s} head {h}: {np.sum(~(e <= tol))} elements, "
+                                      f"{np.max(np.nan_to_num(e / tol, nan=np.inf)):.3g} times what they may be off")
+            el = abs(lse[s, h] - ref_lse)
+            assert el <= 4e-6 + 2.0 ** -21 * abs(ref_lse) + serr, f"{what}: lse of sequence {s} head {h}: {el:.3g}"
+    assert np.array_equal(outb.view(np.uint32), synth.bf16_round(out).view(np.uint32)), f"{what}: BF16 output"
+
+
+def both(c, q, ctx, scale):
+    torch, rlk = torch_cuda(), lib()
+    one = qh.decode(rlk, torch, c, q, ctx, q.shape[1], 1, scale=scale)
+    assert_bitwise(qh.decode(rlk, torch, c, q, ctx, q.shape[1], 0, scale=scale), one, "even load")
+    return one
+
+
+# ---------------------------------------------------------------- large scores
+
+@pytest.mark.parametrize("qe,ke", [(10, 10), (12, 13), (14, 14), (15, 15), (16, 17), (20, 20), (50, 50)])
+def test_equal_keys_with_large_scores(qe, ke):
+    # every key the same: the mean of V, however large the score
+    g = np.random.default_rng([101, qe, ke])
+    ctx, scale = [1, 32, 128, 300, 3001], 128 ** -0.5
+    kv = []
+    for n in ctx:
+        row = synth.bf16_round(np.ldexp(g.standard_normal((1, 2, 128)), ke).astype(np.float32))
+        kv.append((np.repeat(row, n, 0), g.standard_normal((n, 2, 128))))
+    c = write_all(qh.empty_cache(ctx, 2, 16, seed=102), kv)
+    q = synth.bf16_round(np.ldexp(g.standard_normal((len(ctx), 16, 128)), qe).astype(np.float32))
+    check(both(c, q, ctx, scale), c, q, ctx, scale, True, f"2^{qe} 2^{ke}")
+
+
+@pytest.mark.parametrize("qe,ke", [(12, 12), (14, 14), (15, 15), (18, 18), (40, 30)])
+def test_largest_keys_with_large_scores(qe, ke):
+    # gaps between the scores that leave one key, and its copies in other
+    # blocks and segments, all the weight
+    g = np.random.default_rng([103, qe])
+    ctx, scale, hq = [40, 700, 3000], 128 ** -0.5, 4
+    q = synth.bf16_round(np.ldexp(g.standard_normal((len(ctx), hq, 128)), qe).astype(np.float32))
+    kv = []
+    for s, n in enumerate(ctx):
+        k = synth.bf16_round(np.ldexp(g.standard_normal((n, 1, 128)), ke).astype(np.float32))
+        # elements below 2^-13 of a page's largest would be 0 in some pages
+        k[np.abs(k) < 2.0 ** (ke - 9)] = 0.0
+        for h in range(hq):
+            top = int(np.argmax(k[:, 0].astype(np.float64) @ q[s, h]))
+            for at in (n // 3 + h, n - 1 - h):
+                k[at] = k[top]
+        kv.append((k, g.standard_normal((n, 1, 128))))
+    c = write_all(qh.empty_cache(ctx, 1, 16, seed=104), kv)
+    for s, n in enumerate(ctx):  # what the inputs must be for exact_scores
+        k, _, _ = rows_of(c, s, 0, n)
+        for h in range(hq):
+            x = (k @ q[s, h].astype(np.float64)) * scale
+            serr = 2.0 ** -22 * scale * (np.abs(k) @ np.abs(q[s, h].astype(np.float64))).max()
+            assert np.all((x == x.max()) | (x < x.max() - 150 - 2 * serr))
+    check(both(c, q, ctx, scale), c, q, ctx, scale, True, f"2^{qe} 2^{ke}")
