@@ -8,12 +8,16 @@
 // which times 32 fills the same range again), which ride in the N columns the
 // few query heads leave free:
 //   S^T = K_b [q0 | q1 | q2]^T        q 2^x = q0 + q1 / 32 + q2 / 1024
-//   O^T = V_b^T [p0 | p1 | p2 | p3]^T  w 2^7 = p0 + p1 / 32 + p2 / 1024 + p3 / 32768
+//   O^T = V_b^T [p0 | p1 | p2 | p3]^T  w 2^8 = p0 + p1 / 32 + p2 / 1024 + p3 / 32768
 // q 2^x has its row maximum in [128, 256): a BF16 query's 8 significant bits
 // are q0 + q1 / 32 exactly, q2 serves elements 2^13 and more below the row's
 // maximum.  w_c = p_c sv_c / A, with sv_c the V scale of key c's page and A
-// the block's largest of them (as a power of two): four pieces leave at most
-// 2^-19 of w_c.  The K scale multiplies the FP32 score of its key,
+// (a power of two) the largest p sv of the block and query head, so that w <= 1
+// and a page that a head does not attend to takes no bits from the others.
+// What the pieces leave: 2^-19 of w_c down to w = 2^-14, from there (the last
+// piece's smallest step) at most 2^-33 of A, 2^-32 of the largest p sv (2^-31
+// where scales are no powers of two).  The K scale multiplies the FP32 score of
+// its key,
 //   s_c = (q . code_c) sk_c.
 //
 // Softmax, all in FP32.  A block b of 128 keys gives m_b = max s, p = 2^((s -
@@ -94,7 +98,11 @@ struct QDecLayout {
   static constexpr int kPS = 2;           // P^T operand slots
   static constexpr int kQS = 2;           // query slots (the next item's rows are prepared ahead)
   static constexpr int kSS = 4, kOS = 4;  // TMEM rings of S^T and O^T
-  static constexpr int kSR = 8;           // statistics ring
+  // statistics ring: block s is written once P slot s - 2 is free, so O slot
+  // s - 6 and the statistics beside it have been read; 8 where memory allows
+  // (a power of two)
+  static constexpr int kSR = MG < 8 ? 8 : 6;
+  static_assert(kSR >= kPS + kOS, "statistics ring");
   // scales ring: fetched with the K codes, in groups of up to 4 blocks; the
   // softmax reads a block's scales before it frees the block's S slot
   static constexpr int kScRing = 16;
@@ -105,12 +113,12 @@ struct QDecLayout {
   static constexpr int kPOff = kQOff + kQS * kTBytes;
   static constexpr int kKOff = (kPOff + kPS * kTBytes + 1023) / 1024 * 1024;
   static constexpr int kVOff = kKOff + kSK * kKVBytes;
-  // per softmax group, double-buffered by block: float [MG heads, V scale][4
-  // warps] maxima
-  static constexpr int kRedBytes = 2 * (MG + 1) * 16;
+  // per softmax group, double-buffered by block: float [s, log2 of p sv][MG
+  // heads][4 warps] maxima
+  static constexpr int kRedBytes = 2 * 2 * MG * 16;
   static constexpr int kRedOff = kVOff + kSV * kKVBytes;
-  // per block: uint32 l[MG][4 warps], then float m[MG] and the V factor
-  static constexpr int kStatWords = (5 * MG + 1 + 3) / 4 * 4;
+  // per block: uint32 l[MG][4 warps], then float m[MG] and the V factors [MG]
+  static constexpr int kStatWords = (6 * MG + 3) / 4 * 4;
   static constexpr int kStatsOff = kRedOff + 2 * kRedBytes;
   static constexpr int kQsOff = kStatsOff + kSR * kStatWords * 4;  // float [kQS][MG]
   static constexpr int kBarOff = (kQsOff + kQS * MG * 4 + 7) / 8 * 8;
@@ -846,8 +854,11 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         tc_fence_before();
         warp_arrive(&bars[L::kSEmpty + slot], lane);
         const bool vis = (b0 + j) * B + t < kv_len;
-        const int rb = static_cast<int>(sy_it & 1);
-        // scores, and the block maxima over the visible keys (exact)
+        float* rd = red + static_cast<int>(sy_it & 1) * (2 * MG * 4);
+        // the V scale is at most 2^up
+        const float up = static_cast<float>(static_cast<int>((__float_as_uint(sv) + 0x7FFFFFu) >> 23) - 127);
+        // scores, and the warp's maxima over its visible keys: of s (exact), and
+        // of the exponent of p sv, p relative to the warp's own maximum
         float sc[MG];
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
@@ -858,29 +869,39 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           // order rounds nothing)
           sc[q] = vis ? __fmul_rn(a, __fmul_rn(qs[q], sk)) : -INFINITY;
           const float m = warp_max_nan(sc[q]);
-          if (lane == 0) red[(rb * (MG + 1) + q) * 4 + w] = m;
+          const float x = warp_max(vis ? __fmaf_rn(__fsub_rn(sc[q], m), sl, up) : -INFINITY);
+          if (lane == 0) {
+            rd[q * 4 + w] = m;
+            rd[(MG + q) * 4 + w] = x;
+          }
         }
-        {
-          const float m = warp_max(vis ? sv : 0.0f);
-          if (lane == 0) red[(rb * (MG + 1) + MG) * 4 + w] = m;
-        }
-        warp_arrive(&bars[L::kSyncMax + grp * 2 + rb], lane);
-        ok = wait_warp(&bars[L::kSyncMax + grp * 2 + rb], (sy_it >> 1) & 1, abort, p.err, 0xb43);
+        uint64_t* sync = &bars[L::kSyncMax + grp * 2 + (sy_it & 1)];
+        warp_arrive(sync, lane);
+        ok = wait_warp(sync, (sy_it >> 1) & 1, abort, p.err, 0xb43);
         ++sy_it;
         if (!ok) { fail = true; break; }
-        auto max4 = [&](int q) {
-          const float4 r = *reinterpret_cast<const float4*>(red + (rb * (MG + 1) + q) * 4);
-          return max_nan(max_nan(r.x, r.y), max_nan(r.z, r.w));
-        };
-        float mc[MG], pr[MG];
+        // lane q: the block's maximum of query head q, and the exponent ae of
+        // its A = 2^ae (rounded up, so that w <= 1 but for the exponent's last
+        // places: 2^8 w stays far below E4M3's 448)
+        float m_mine;
+        int ae;
+        {
+          const int q = min(lane, MG - 1);
+          const float4 r = *reinterpret_cast<const float4*>(rd + q * 4);
+          const float4 a = *reinterpret_cast<const float4*>(rd + (MG + q) * 4);
+          m_mine = max_nan(max_nan(r.x, r.y), max_nan(r.z, r.w));
+          auto rel = [&](float m, float x) { return __fmaf_rn(__fsub_rn(m, m_mine), sl, x); };
+          ae = __float2int_ru(fmaxf(fmaxf(rel(r.x, a.x), rel(r.y, a.y)), fmaxf(rel(r.z, a.z), rel(r.w, a.w))));
+          ae = min(max(ae, -118), 128);
+        }
+        const float wf_mine = pow2_bits(127 + 8 - ae);
+        const float sv_vis = vis ? sv : 0.0f;  // stale behind the context
+        float pr[MG];
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
-          mc[q] = max4(q);
-          pr[q] = vis ? weight(sc[q], mc[q], sl) : 0.0f;
+          const float m = __shfl_sync(0xffffffffu, m_mine, q);  // (every lane: vis differs between them)
+          pr[q] = vis ? weight(sc[q], m, sl) : 0.0f;
         }
-        // the block's V anchor A = 2^(ae - 127); w = p (sv 2^7 / A)
-        const int ae = max(static_cast<int>(__float_as_uint(max4(MG)) >> 23), 8);
-        const float wf = vis ? __fmul_rn(sv, pow2_bits(261 - ae)) : 0.0f;
         ok = wait_warp(&bars[L::kPEmpty + grp], ((s_it / PS) & 1) ^ 1, abort, p.err, 0xb44);
         if (!ok) { fail = true; break; }
         uint32_t pw[N / 4];
@@ -888,7 +909,11 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         for (int i = 0; i < N / 4; ++i) pw[i] = 0u;
 #pragma unroll
         for (int q = 0; q < MG; q += 2) {
-          float a = __fmul_rn(pr[q], wf), b = q + 1 < MG ? __fmul_rn(pr[q + 1 < MG ? q + 1 : q], wf) : 0.0f;
+          // w 2^8 = (p sv) 2^(8 - ae): p sv stays in range, sv / A need not
+          auto w8 = [&](int h) {
+            return __fmul_rn(__fmul_rn(pr[h], sv_vis), __shfl_sync(0xffffffffu, wf_mine, h));
+          };
+          float a = w8(q), b = q + 1 < MG ? w8(q + 1 < MG ? q + 1 : q) : 0.0f;
           static_assert(kPPieces == 4 && p_col(2, 0) == 8 && p_col(1, 3) == 7, "a pair's pieces are two words");
           const uint32_t c0 = next_piece(a, b), c1 = next_piece(a, b), c2 = next_piece(a, b);
           pw[q] = __byte_perm(c0, c1, 0x5410);
@@ -903,17 +928,17 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // FP32 numbers in a tree: 7 * 2^-24), in one instruction and in no order
         uint32_t* st = stats + (s_it % SR) * L::kStatWords;
         uint32_t l_mine = 0;  // lane q: query head q's
-        float m_mine = 0.0f;
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
           const uint32_t l = __reduce_add_sync(0xffffffffu, __float2uint_rn(__fmul_rn(pr[q], kLUnit)));
           l_mine = lane == q ? l : l_mine;
-          m_mine = lane == q ? mc[q] : m_mine;
         }
-        if (lane < MG) st[lane * 4 + w] = l_mine;
-        if (w == 0) {
-          if (lane == MG) m_mine = pow2_bits(ae - 7);  // PV carries 2^7 / A
-          if (lane <= MG) st[4 * MG + lane] = __float_as_uint(m_mine);
+        if (lane < MG) {
+          st[lane * 4 + w] = l_mine;
+          if (w == 0) {
+            st[4 * MG + lane] = __float_as_uint(m_mine);
+            st[5 * MG + lane] = __float_as_uint(pow2_bits(127 - 8 + ae));  // PV carries 2^8 / A
+          }
         }
         warp_arrive(&bars[L::kStatsFull + (s_it % SR)], lane);
       }
@@ -982,7 +1007,9 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         // fold factors of query head `lane` (overlap the TMEM load)
         const uint32_t* st = stats + sslot * L::kStatWords;
         const bool first = b % kSegBlocks == 0;
-        const float vf = __uint_as_float(st[5 * MG]);
+        float vf[MG];
+#pragma unroll
+        for (int q = 0; q < MG; ++q) vf[q] = __uint_as_float(st[5 * MG + q]);
         float fa = 0.0f, fb = 1.0f;
         if (lane < MG) {
           const float mb = __uint_as_float(st[4 * MG + lane]);
@@ -1010,7 +1037,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
           float pv = __uint_as_float(raw[p_col(q, kPPieces - 1)]);
 #pragma unroll
           for (int k = kPPieces - 2; k >= 0; --k) pv = __fmaf_rn(pv, 0x1p-5f, __uint_as_float(raw[p_col(q, k)]));
-          pv = __fmul_rn(pv, vf);
+          pv = __fmul_rn(pv, vf[q]);
           O[q] = first ? pv : __fmaf_rn(pv, bq, __fmul_rn(O[q], aq));
         }
         ++o_it;

@@ -466,10 +466,15 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
  *     shared by calls that overlap; its contents need no initialisation.
  *     Unused for split_k == 1.
  * The pages' codes go to the tensor core as they are; the query and the
- * probabilities are split into 3 and 4 E4M3 pieces, so neither loses
- * precision to 8 bits (a probability 2^-19 of itself).  Scores, softmax and
- * sums are FP32: blocks of 128 keys are folded left to right into segments of
- * 512 keys, those left to right into the row, with a running maximum.
+ * weights (a probability times its page's V scale) are split into 3 and 4
+ * E4M3 pieces.  That leaves a query element off by at most 2^-27 of its row's
+ * largest, and a weight by at most 2^-19 of itself or 2^-31 of the largest
+ * weight of its 128-key block and query head, whichever is more: a page whose
+ * values are large but get no weight takes nothing from the others.  Scores,
+ * softmax and sums are held in 32 bits (a block's sum of p with 26 fraction
+ * bits, its largest p being 1): blocks of 128 keys are folded left to right
+ * into segments of 512 keys, those left to right into the row, with a running
+ * maximum.
  * Scales must be positive, finite and >= 2^-120.  A query row that holds Inf
  * or NaN gives a NaN row.  The result does not depend on the batch, the page
  * order, split_k or repetition (bit for bit).  Needs kv_block_size 128 and at

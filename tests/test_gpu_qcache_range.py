@@ -112,3 +112,44 @@ def test_largest_keys_with_large_scores(qe, ke):
             serr = 2.0 ** -22 * scale * (np.abs(k) @ np.abs(q[s, h].astype(np.float64))).max()
             assert np.all((x == x.max()) | (x < x.max() - 150 - 2 * serr))
     check(both(c, q, ctx, scale), c, q, ctx, scale, True, f"2^{qe} 2^{ke}")
+
+
+# ---------------------------------------------------------------- V scales
+
+@pytest.mark.parametrize("page,heads", [(16, (4, 1)), (8, (8, 1)), (32, (7, 1)), (16, (3, 3))])
+@pytest.mark.parametrize("gap,e", [(192, 20), (192, 24), (192, 60), (192, 100), (30, 40), (10, 30), (60, 100),
+                                   (60, -100), (192, -110)])
+def test_value_scales_of_unattended_pages(page, heads, gap, e):
+    # pages whose values are 2^e times the others', `gap` below in score: the
+    # rows that attend to the others keep their bits, the rows that attend to
+    # these, or to all, are right as well
+    g = np.random.default_rng([105, gap, e + 200])
+    hq, hkv = heads
+    ctx = [127, 300, 1100]
+    kv = []
+    for n in ctx:
+        level = np.broadcast_to(g.choice([0.0, -0.5, -1.0, -1.75], (n, 1, 1)), (n, hkv, 1)).copy()
+        v = g.standard_normal((n, hkv, 128))
+        apart = np.isin(np.arange(n) // page % 5, (2, 3))
+        level[apart] -= gap
+        v[apart] = np.ldexp(v[apart], e)
+        kv.append((np.broadcast_to(level, (n, hkv, 128)), v))
+    c = write_all(qh.empty_cache(ctx, hkv, page, seed=106), kv)
+    sign = np.array([1.0, -1.0, 0.0, 0.5, 1.0, -0.25, 2.0, 0.125])[np.arange(hq) % 8]
+    q = np.broadcast_to(sign[None, :, None], (len(ctx), hq, 128)).astype(np.float32).copy()
+    check(both(c, q, ctx, 2.0 ** -7), c, q, ctx, 2.0 ** -7, False, f"gap {gap} 2^{e}")
+
+
+def test_values_at_the_smallest_scale():
+    # V scales of 2^-120 (values under 2^-112), beside pages of zeros
+    g = np.random.default_rng(107)
+    ctx = [50, 400]
+    kv = []
+    for n in ctx:
+        v = np.ldexp(g.standard_normal((n, 2, 128)), -116)
+        v[32:48] = 0.0
+        kv.append((g.standard_normal((n, 2, 128)), v))
+    c = write_all(qh.empty_cache(ctx, 2, 16, seed=108), kv)
+    assert c.vs[c.table[0, 0]].max() <= 2.0 ** -119
+    q = synth.bf16_round(g.standard_normal((2, 8, 128)).astype(np.float32))
+    check(both(c, q, ctx, 128 ** -0.5), c, q, ctx, 128 ** -0.5, False, "smallest scale")
