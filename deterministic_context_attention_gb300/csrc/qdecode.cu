@@ -864,10 +864,14 @@ __global__ void __launch_bounds__(kQDThreads, 1)
         for (int q = 0; q < MG; ++q) {
           const float a = __fmaf_rn(__uint_as_float(raw[2 * MG + q]), 0x1p-10f,
                                     __fmaf_rn(__uint_as_float(raw[MG + q]), 0x1p-5f, __uint_as_float(raw[q])));
-          // (the two scales first: a row near the type's largest over small keys
-          // would leave FP32's range on the way; both are powers of two, so the
-          // order rounds nothing)
-          sc[q] = vis ? __fmul_rn(a, __fmul_rn(qs[q], sk)) : -INFINITY;
+          // the two scales first: a row near the type's largest over small keys
+          // would leave FP32's range on the way.  Where they leave it together, a
+          // may still be small, or 0: then one after the other (neither below 1,
+          // so what overflows here is past FP32 anyway).  With the scales that
+          // writing sets, powers of two as the query's are, neither order rounds
+          const float f = __fmul_rn(qs[q], sk);
+          const float s = f <= 3.4028234e38f ? __fmul_rn(a, f) : __fmul_rn(__fmul_rn(a, sk), qs[q]);
+          sc[q] = vis ? s : -INFINITY;
           const float m = warp_max_nan(sc[q]);
           const float x = warp_max(vis ? __fmaf_rn(__fsub_rn(sc[q], m), sl, up) : -INFINITY);
           if (lane == 0) {

@@ -153,3 +153,29 @@ def test_values_at_the_smallest_scale():
     assert c.vs[c.table[0, 0]].max() <= 2.0 ** -119
     q = synth.bf16_round(g.standard_normal((2, 8, 128)).astype(np.float32))
     check(both(c, q, ctx, 128 ** -0.5), c, q, ctx, 128 ** -0.5, False, "smallest scale")
+
+
+# ---------------------------------------------------------------- large scales
+
+@pytest.mark.parametrize("e", [0, 16, 30, 100])
+def test_zero_products_of_large_rows_and_large_scales(e):
+    # query rows up to 2^(20 + e) over K pages up to 2^(120 - e) in other
+    # dimensions: what is left is scores of up to 3 * 2^120, or 0, and a
+    # softmax scale that brings them to 3
+    g = np.random.default_rng([109, e])
+    ctx, scale = [60, 260], 2.0 ** -120
+    kv = []
+    for n in ctx:
+        k = np.zeros((n, 1, 128))
+        k[:, 0, 1] = np.ldexp(g.integers(-3, 4, n).astype(np.float64), 110 - e)
+        k[::3, 0, 2] = 2.0 ** (123 - e)
+        k[:, 0, 3] = np.ldexp(g.standard_normal(n), 115 - e)
+        kv.append((k, g.standard_normal((n, 1, 128))))
+    c = write_all(qh.empty_cache(ctx, 1, 16, seed=110), kv)
+    assert c.ks[c.table[0, 0], 0] == 2.0 ** (116 - e)
+    q = np.zeros((2, 4, 128), np.float32)
+    q[:, :, 0] = 2.0 ** (20 + e)
+    q[:, 1:, 1] = 2.0 ** (10 + e)
+    q[:, 2, 0] *= -1
+    q[:, 3] *= 2.0 ** -20
+    check(both(c, q, ctx, scale), c, q, ctx, scale, False, f"e {e}")
