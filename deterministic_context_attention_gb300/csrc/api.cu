@@ -1222,15 +1222,13 @@ rlk_status check_qcache(const rlk_attn_params* params, const QCache& c) {
   return RLK_OK;
 }
 
-// Write (k_in, v_in set) or read back (k_out, v_out set) of the tokens
+// Write (from k_in, v_in) or read back (to k_out, v_out) of the tokens
 // pos_offset[s] + 0 .. len - 1 of every sequence.
-rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const void* v_in, void* k_out, void* v_out,
-                       const int32_t* cu_seqlens, const int32_t* pos_offset, const float* rope_table,
+rlk_status qcache_impl(const rlk_attn_params* params, bool write, const void* k_in, const void* v_in, void* k_out,
+                       void* v_out, const int32_t* cu_seqlens, const int32_t* pos_offset, const float* rope_table,
                        int32_t rope_max_pos, const QCache& cache, cudaStream_t stream) {
   rlk_status st = check_params(params);
   if (st) return st;
-  const bool write = k_in != nullptr;
-  if (write ? !v_in : (!k_out || !v_out)) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
   if (!aligned16(k_in) || !aligned16(v_in) || !aligned16(k_out) || !aligned16(v_out) || !aligned16(rope_table))
     return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
   if ((st = check_qcache(params, cache))) return st;
@@ -1242,7 +1240,7 @@ rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const vo
       const rlk_attn_params rp = range_params(params, s0, s1);
       const auto cu = rebase(cu_seqlens, s0, s1);
       const int64_t o = static_cast<int64_t>(cu_seqlens[s0]) * hkv * rlk::kHeadDim;
-      return qcache_impl(&rp, adv(k_in, o, 2), adv(v_in, o, 2), adv(k_out, o, 2), adv(v_out, o, 2), cu.data(),
+      return qcache_impl(&rp, write, adv(k_in, o, 2), adv(v_in, o, 2), adv(k_out, o, 2), adv(v_out, o, 2), cu.data(),
                          pos_offset ? pos_offset + s0 : nullptr, rope_table, rope_max_pos, cache.from(s0), stream);
     }, rlk::kQMaxSeqs);
   auto qp = std::make_unique<rlk::QCacheParams>();
@@ -1269,7 +1267,8 @@ rlk_status qcache_impl(const rlk_attn_params* params, const void* k_in, const vo
   // a CTA takes one (page, K or V, head) unit at the least
   if (pages * 2 * hkv > (static_cast<int64_t>(INT32_MAX) / 8) * 8)
     return fail(RLK_ERR_UNSUPPORTED, "more than 2^31 (page, head) units in one call");
-  if (pages == 0) return ok();
+  if (pages == 0) return ok();  // no token in the call: tensors of no rows may be NULL
+  if (write ? (!k_in || !v_in) : (!k_out || !v_out)) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
@@ -1490,9 +1489,8 @@ rlk_status rlk_attn_qcache_write(const rlk_attn_params* params, const void* k, c
                                  int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                                  rlk_stream_t stream) {
   return guarded([&]() -> rlk_status {
-    if (!k || !v) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
     const QCache cache{k_pool, v_pool, k_scale, v_scale, n_pages, page_size, page_table, max_pages};
-    return qcache_impl(params, k, v, nullptr, nullptr, cu_seqlens, pos_offset, rope_table, rope_max_pos, cache,
+    return qcache_impl(params, true, k, v, nullptr, nullptr, cu_seqlens, pos_offset, rope_table, rope_max_pos, cache,
                        stream);
   });
 }
@@ -1502,10 +1500,9 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
                                 const int32_t* page_table, int32_t max_pages, const int32_t* cu_seqlens,
                                 const int32_t* pos_offset, void* k, void* v, rlk_stream_t stream) {
   return guarded([&]() -> rlk_status {
-    if (!k || !v) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
     const QCache cache{const_cast<void*>(k_pool), const_cast<void*>(v_pool), const_cast<float*>(k_scale),
                        const_cast<float*>(v_scale), n_pages, page_size, page_table, max_pages};
-    return qcache_impl(params, nullptr, nullptr, k, v, cu_seqlens, pos_offset, nullptr, 0, cache, stream);
+    return qcache_impl(params, false, nullptr, nullptr, k, v, cu_seqlens, pos_offset, nullptr, 0, cache, stream);
   });
 }
 

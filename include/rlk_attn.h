@@ -418,7 +418,8 @@ int32_t rlk_attn_decode_auto_split(const rlk_attn_params* params, const int32_t*
  * the latest tokens again is a no-op only if they are the same ones: a page's
  * scale never shrinks while it holds tokens.)
  *   k, v: device BF16 [T, Hkv, 128], T = cu_seqlens[num_seqs];
- *   cu_seqlens: HOST [num_seqs + 1] (a sequence may have no new token);
+ *   cu_seqlens: HOST [num_seqs + 1] (a sequence may have no new token, and
+ *     where none has any, k and v may be NULL and nothing is launched);
  *   pos_offset: HOST [num_seqs] tokens already cached, or NULL (0);
  *   rope_table: NULL (k is stored as given), or device, from
  *     rlk_attn_rope_table: k is pre-RoPE and each row is rotated at its
@@ -438,8 +439,8 @@ rlk_status rlk_attn_qcache_write(const rlk_attn_params* params, const void* k, c
  * Reads tokens pos_offset[s] .. pos_offset[s] + len_s - 1 of every sequence
  * back as packed BF16 rows (what rlk_attn_prefill takes as k and v: chunked
  * prefill over the 8-bit cache reads each sequence's tokens 0 .. kv_len - 1).
- *   cu_seqlens: HOST [num_seqs + 1], prefix sums of len_s; pos_offset: HOST
- *     [num_seqs] or NULL (0); k, v: device BF16 [T, Hkv, 128] outputs,
+ *   cu_seqlens: HOST [num_seqs + 1], prefix sums of len_s (0 is fine, as
+ *     above); pos_offset: HOST [num_seqs] or NULL (0); k, v: device BF16 [T, Hkv, 128] outputs,
  *     T = cu_seqlens[num_seqs], bf16_rn(code * scale) (exact for the scales
  *     rlk_attn_qcache_write sets; any finite FP32 scale is taken).
  */

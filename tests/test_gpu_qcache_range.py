@@ -179,3 +179,20 @@ def test_zero_products_of_large_rows_and_large_scales(e):
     q[:, 2, 0] *= -1
     q[:, 3] *= 2.0 ** -20
     check(both(c, q, ctx, scale), c, q, ctx, scale, False, f"e {e}")
+
+
+# ---------------------------------------------------------------- nothing to do
+
+def test_calls_without_a_token_change_nothing():
+    # a step in which no sequence has a new token: tensors of no rows
+    torch, rlk = torch_cuda(), lib()
+    c = qh.filled([20, 33], 2, 16, seed=111, spread=False)
+    dev = c.device()
+    p = rlk.make_params(2, 2, 2)
+    pool = (*dev[:4], c.n_pages, 16, dev[4], dev[4].shape[1])
+    k, v = (torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rlk.rlk_attn_qcache_write(p, k, v, [0, 0, 0], [20, 33], None, 0, *pool)
+    rlk.rlk_attn_qcache_read(p, *pool, [0, 0, 0], None, k, v)
+    rlk.rlk_attn_check_device_error()
+    for d, a in zip(dev[:4], (c.k, c.v, c.ks, c.vs)):
+        assert np.array_equal(d.cpu().numpy().view(np.uint8), a.view(np.uint8))

@@ -159,6 +159,18 @@ def test_every_range_of_a_large_batch_is_checked_first(lib):
     _read(rlk.make_params(2), cu=(0, 0, 0), pos=None)
 
 
+def test_calls_without_a_token_take_empty_tensors(lib):
+    # an empty tensor's address is NULL; one with rows is still refused
+    for n, pos in ((2, (5, 64)), (300, None)):
+        p, cu = rlk.make_params(n), (0,) * (n + 1)
+        _write(p, k=0, v=0, cu=cu, pos=pos)
+        _read(p, k=0, v=0, cu=cu, pos=pos)
+    cu = [0] * 290 + [1] * 11  # the second range of sequences has it
+    for call in (_write, _read):
+        _refused(lambda: call(rlk.make_params(300), k=0, v=0, cu=cu, pos=None), 1)
+        _refused(lambda: call(rlk.make_params(2), k=0, cu=(0, 0, 1), pos=None), 1)
+
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     k = torch.zeros((5, 8, 128), dtype=torch.bfloat16)
