@@ -16,8 +16,8 @@
 //     have given: a page's bytes are a function of its tokens, whatever calls
 //     wrote them, with no BF16 copy of the page being filled;
 //   - code * 2^e is a BF16 number, so reading back is exact.
-// What it costs: values below max * 2^-13 become 0, against a rounding error
-// of up to max * 2^-5 of the largest ones.
+// What it costs: values below max * 2^-13 become 0, where the largest ones are
+// off by up to 2^-4 of themselves.
 //
 // Both passes move 3 bytes per element (2 BF16, 1 code) and are bound by
 // HBM; what could bind the write instead is the integer pipe (half the rate of
@@ -167,9 +167,13 @@ __device__ __forceinline__ uint32_t rescale_byte(uint32_t c, int d) {
 // 8 j .. 8 j + 7 and 64 + 8 j .. (j = l mod 8; the RoPE pairs of one another) of
 // rows 4 i + l / 8.
 // Registers are held to 64 (R = 16), 48 and 40 (R = 8 with and without RoPE):
-// the fewer, the more loads in flight, until they spill.  104,000 tokens of 8
-// heads: with RoPE 113.9 us (120.0 with 80 registers, 127 with 89), 8-token pages
-// 106.5 (114.7 with 60, 146.7 with 32) and with RoPE 124.6 (137 with 71).
+// the fewer, the more loads in flight, and the 16 to 32 bytes a thread that spill
+// at these counts cost less than that gives.  104,000 tokens of 8 heads: with
+// RoPE 113.9 us (120.0 with 80 registers, 127 with 89), 8-token pages 106.5 (114.7
+// with 60, 146.7 with 32) and with RoPE 124.6 (137 with 71).
+// With RoPE a warp waits for its rows and then, row group by row group, for its
+// rows of the table: chunks of 333 to 2048 tokens of 5 sequences take 11 to 12 us
+// for 39 MB, with 48 % of the issue slots used, 28 % of DRAM and 1.24 waves.
 template <int R, bool ROPE>
 __global__ void __launch_bounds__(kQThreads, R == 16 ? 4 : (ROPE ? 5 : 6))
     rlk_qcache_write_kernel(const __grid_constant__ QCacheParams p) {

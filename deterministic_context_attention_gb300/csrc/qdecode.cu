@@ -41,8 +41,10 @@
 // in 16-token pages took 341 us with one head's line of pages a CTA, 333 with
 // the groups.  The blocks of all (sequence, head group) pairs in order form one
 // line; each group takes an equal part of it by cost (a pair counts 1.5 blocks
-// more than it has), cut at segment ends, so the SMs' loads differ by a
-// segment at the most.  A CTA that holds a whole pair writes its output;
+// more than it has), cut at segment ends, so that with split_k = 0 the SMs'
+// loads differ by about a segment, or by up to a pair where pairs are of one or
+// two segments (which are not cut: counting and folding the parts costs more
+// than it evens out).  A CTA that holds a whole pair writes its output;
 // otherwise a pair's first piece leaves what it has folded as one state, the
 // others the state of each segment, in the workspace, and the CTA that counts
 // the last segment of a pair (which one changes nothing in the result) folds
@@ -51,14 +53,15 @@
 //
 // What bounds it: HBM, 32 KB of codes per (KV head, 128-key block), 0.73 us a
 // block and SM at the measured copy rate; long sequences in 16-token pages and
-// larger run at that (0.69 .. 0.73 us), 8-token pages at 0.87 (32 TMA copies a
-// block: their issue).  Fed from L2 the pipeline takes 0.50 us a block with 4
-// query heads (0.69 while the warp that issues the O products also fetched the
-// scales).  Per block the tensor core issues 4 + 4 MMAs of K = 32 codes (the
+// larger run at that (0.69 .. 0.73 us), 8-token pages at 0.9 (32 TMA copies a
+// block: their issue).  Fed from L2 the pipeline takes 0.57 us a block with 4
+// query heads in 64-token pages, 0.66 in 16-token ones, 0.75 with 8 heads (0.19
+// more while the warp that issues the O products also fetched the scales).  Per
+// block the tensor core issues 4 + 4 MMAs of K = 32 codes (the
 // BF16 decode needs 8 + 16), and the softmax's 8 warps run two blocks at a
 // time.  A call costs about 5 us before its first block is folded and, where
 // pairs are cut, 3 to 6 us for counting and folding: 64 sequences of 512 ..
-// 32768 tokens take 328 .. 336 us (0.96 .. 0.98 of the copy rate), 4 of 32768
+// 32768 tokens take 331 .. 336 us (0.96 .. 0.98 of the copy rate), 4 of 32768
 // tokens 56 (0.71).
 //
 // Warp roles (512 threads):

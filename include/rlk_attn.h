@@ -43,11 +43,12 @@
  *     duplicate or missing block in a state table) set the device error word;
  *     read it with rlk_attn_check_device_error().
  *   - A batch may hold up to 2^20 sequences.  One launch's sequence tables
- *     ride in kernel parameters and take 128 sequences, so a larger batch
- *     runs as consecutive ranges of 128 sequences on `stream`, each range a
- *     complete call on its own rows (every range is validated before the
- *     first launch).  A sequence's arithmetic does not depend on the other
- *     sequences of its batch, so the results are those of one launch.
+ *     ride in kernel parameters and take 128 sequences (256 in the 8-bit
+ *     cache's calls), so a larger batch runs as consecutive ranges of that
+ *     many sequences on `stream`, each range a complete call on its own rows
+ *     (every range is validated before the first launch).  A sequence's
+ *     arithmetic does not depend on the other sequences of its batch, so the
+ *     results are those of one launch.
  *   - Causal masking is bottom-right aligned: query row i of a sequence with
  *     q_len queries and kv_len keys sits at key position kv_len - q_len + i
  *     (q_len <= kv_len), so chunked-prefill replay passes the chunk's queries
@@ -441,8 +442,9 @@ rlk_status rlk_attn_qcache_write(const rlk_attn_params* params, const void* k, c
  * prefill over the 8-bit cache reads each sequence's tokens 0 .. kv_len - 1).
  *   cu_seqlens: HOST [num_seqs + 1], prefix sums of len_s (0 is fine, as
  *     above); pos_offset: HOST [num_seqs] or NULL (0); k, v: device BF16 [T, Hkv, 128] outputs,
- *     T = cu_seqlens[num_seqs], bf16_rn(code * scale) (exact for the scales
- *     rlk_attn_qcache_write sets; any finite FP32 scale is taken).
+ *     T = cu_seqlens[num_seqs], code * scale rounded to FP32 and then to BF16
+ *     (exact for the scales rlk_attn_qcache_write sets; any finite FP32 scale
+ *     is taken).
  */
 rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_pool, const void* v_pool,
                                 const float* k_scale, const float* v_scale, int32_t n_pages, int32_t page_size,
@@ -477,9 +479,13 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
  * into segments of 512 keys, those left to right into the row, with a running
  * maximum.
  * Scales must be positive, finite and >= 2^-120.  A query row that holds Inf
- * or NaN gives a NaN row.  The result does not depend on the batch, the page
- * order, split_k or repetition (bit for bit).  Needs kv_block_size 128 and at
- * most 8 query heads per KV head (RLK_ERR_UNSUPPORTED otherwise).
+ * or NaN gives a NaN row, and so may one whose products q . k leave FP32's
+ * range.  The result does not depend on the batch, the page order, split_k or
+ * repetition (bit for bit).  It is not bit for bit the last row of
+ * rlk_attn_prefill over the values rlk_attn_qcache_read gives, as
+ * rlk_attn_decode_paged is over its pool: the fold is another one (within FP32
+ * rounding of it).  Needs kv_block_size 128 and at most 8 query heads per KV
+ * head (RLK_ERR_UNSUPPORTED otherwise).
  */
 rlk_status rlk_attn_decode_qcache(const rlk_attn_params* params, const void* q, const void* k_pool,
                                   const void* v_pool, const float* k_scale, const float* v_scale, int32_t n_pages,
