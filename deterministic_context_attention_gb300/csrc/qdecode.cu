@@ -28,10 +28,10 @@
 // Maxima stay unscaled and scores are subtracted before they are scaled: the
 // largest key's p is exactly 1 and no p is above it, however large the scores
 // (p = 2^(s c - rn(m c)) is off by half a last place of m c, a factor of 2 and
-// more from 2^24 on, which the sums below do not hold);
-// the arithmetic is the same whichever CTAs take which segments: a result
-// depends on the cached codes, scales and the query alone, not on the batch,
-// the order of the pages or the split.  (Two levels, because the fold is a
+// more from 2^24 on, which the sums below do not hold).  The arithmetic is the
+// same whichever CTAs take which segments: a result depends on the cached codes,
+// scales and the query alone, not on the batch, the order of the pages or the
+// split.  (Two levels, because the fold is a
 // chain: one over every block of a 32768-token sequence, on states written
 // out per block, took 125 us for 4 sequences where the pages take 40.)
 //
@@ -57,12 +57,11 @@
 // block: their issue).  Fed from L2 the pipeline takes 0.57 us a block with 4
 // query heads in 64-token pages, 0.66 in 16-token ones, 0.75 with 8 heads (0.19
 // more while the warp that issues the O products also fetched the scales).  Per
-// block the tensor core issues 4 + 4 MMAs of K = 32 codes (the
-// BF16 decode needs 8 + 16), and the softmax's 8 warps run two blocks at a
-// time.  A call costs about 5 us before its first block is folded and, where
-// pairs are cut, 3 to 6 us for counting and folding: 64 sequences of 512 ..
-// 32768 tokens take 331 .. 336 us (0.96 .. 0.98 of the copy rate), 4 of 32768
-// tokens 56 (0.71).
+// block the tensor core issues 4 + 4 MMAs of K = 32 codes (the BF16 decode needs
+// 8 + 16), and the softmax's 8 warps run two blocks at a time.  A call costs
+// about 5 us before its first block is folded and, where pairs are cut, 3 to 6 us
+// for counting and folding: 64 sequences of 512 .. 32768 tokens take 331 .. 336 us
+// (0.96 .. 0.98 of the copy rate), 4 of 32768 tokens 56 (0.71).
 //
 // Warp roles (512 threads):
 //   warps 0-3   correction / epilogue: thread d owns head dimension d

@@ -475,10 +475,10 @@ rlk_status rlk_attn_qcache_read(const rlk_attn_params* params, const void* k_poo
  * weight of its 128-key block and query head, whichever is more: a page whose
  * values are large but get no weight takes nothing from the others.  Scores,
  * softmax and sums are held in 32 bits (a block's sum of p with 26 fraction
- * bits, its largest p being 1; p below 2^-126 is 0, so the V scales of a
- * block's pages must lie within 2^126 of each other): blocks of 128 keys are folded left to right
- * into segments of 512 keys, those left to right into the row, with a running
- * maximum.
+ * bits, its largest p being 1; p below 2^-126 is 0, so a key that far below
+ * the largest must not outweigh it by its V scale): blocks of 128 keys are
+ * folded left to right into segments of 512 keys, those left to right into the
+ * row, with a running maximum.
  * Scales must be positive, finite and >= 2^-120.  A query row that holds Inf
  * or NaN gives a NaN row, and so may one whose products q . k leave FP32's
  * range.  The result does not depend on the batch, the page order, split_k or
