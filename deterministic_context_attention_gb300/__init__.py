@@ -11,6 +11,7 @@ Entry points (same names as the C ABI):
     rlk_attn_prefill_states, rlk_attn_merge_states, rlk_attn_merge_states_noalloc,
     rlk_attn_prefill, rlk_attn_prefill_rope,
     rlk_attn_decode_paged, rlk_attn_backward, rlk_attn_workspace_size,
+    rlk_attn_cache_append,
     rlk_attn_qcache_write, rlk_attn_qcache_read, rlk_attn_decode_qcache,
     rlk_attn_check_device_error, rlk_attn_last_error, rlk_attn_core_id
 """
@@ -103,6 +104,7 @@ def load():
             "rlk_attn_qcache_write": [PP, P, P, P, P, P, i32, P, P, P, P, i32, i32, P, i32, P],
             "rlk_attn_qcache_read": [PP, P, P, P, P, i32, i32, P, i32, P, P, P, P, P],
             "rlk_attn_decode_qcache": [PP, P, P, P, P, P, i32, i32, P, i32, P, i32, P, i32, P, P, P, P, sz, P],
+            "rlk_attn_cache_append": [PP, P, P, P, P, P, P, P, P, i32, i32, P, P, i32, i32, P, i32, P],
             "rlk_attn_backward": [PP, P, P, P, P, P, P, P, i32, P, P, P, P, sz, P],
             "rlk_attn_workspace_size": [PP, i32, P, P],
             "rlk_attn_check_device_error": [P],
@@ -330,7 +332,7 @@ def rlk_attn_decode_paged_splitk_rope(params, q, k_pool, v_pool, n_pages, page_s
 
 
 class _Torch:
-    """What the 8-bit cache's calls ask torch for, looked up once."""
+    """What the caches' calls ask torch for, looked up once."""
 
     def __init__(self):
         import torch
@@ -346,7 +348,7 @@ _torch = None
 
 
 def _dev_args(stream, *args):
-    """Addresses of the tensors an 8-bit cache call reads or writes, given as
+    """Addresses of the tensors a call reads or writes, given as
     (kind, tensor), and of its stream: refuses a tensor that is not contiguous,
     not on the current CUDA device or of another type (a pointer value or None
     passes as it is)."""
@@ -438,6 +440,21 @@ def rlk_attn_decode_qcache(params, q, k_pool, v_pool, k_scale, v_scale, n_pages,
     _check(load().rlk_attn_decode_qcache(params, q, kp, vp, ks, vs, n_pages, page_size, pt, max_pages, sl_p, split_k,
                                          rt, rope_max_pos, of, ob, ls, ws, workspace_bytes, st),
            "rlk_attn_decode_qcache")
+
+
+def rlk_attn_cache_append(params, q, q_out, k, k_out, v, cu_seqlens, pos_offset, rope_table, rope_max_pos, rope_width,
+                          k_pool, v_pool, n_pages, page_size, page_table, max_pages, stream=None):
+    """Append BF16 K/V rows to the paged cache, K rotated on the way (rope_table
+    None: stored as given); q into q_out and the rotated keys packed into
+    k_out where given."""
+    n = params.num_seqs
+    cu, cu_p = _i32_addr(cu_seqlens, n + 1)
+    po, po_p = _i32_addr(pos_offset, n)
+    q, qo, k, ko, v, rt, kp, vp, pt, st = _dev_args(
+        stream, ("bf16", q), ("bf16", q_out), ("bf16", k), ("bf16", k_out), ("bf16", v), ("f32", rope_table),
+        ("bf16", k_pool), ("bf16", v_pool), ("i32", page_table))
+    _check(load().rlk_attn_cache_append(params, q, qo, k, ko, v, cu_p, po_p, rt, rope_max_pos, rope_width, kp, vp,
+                                        n_pages, page_size, pt, max_pages, st), "rlk_attn_cache_append")
 
 
 def rlk_attn_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,

@@ -32,6 +32,7 @@ cudaError_t launch_merge(const MergeParams& p, int num_sms, cudaStream_t stream)
 bool decode_transposed_supported(const FwdParams& p);
 cudaError_t launch_decode_merge(const FwdParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_decode(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           int grid, cudaStream_t stream);
 cudaError_t launch_decode_cooperative(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -49,6 +50,7 @@ static_assert(sizeof(rlk::FwdParams) + 3 * sizeof(CUtensorMap) + 256 <= 32764,
 static_assert(sizeof(rlk::MergeParams) <= 4096, "merge parameters");
 static_assert(sizeof(rlk::QCacheParams) <= 4096 && sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) <= 8192,
               "8-bit cache parameters");
+static_assert(sizeof(rlk::AppendParams) <= 4096, "append parameters");
 static_assert(sizeof(rlk_attn_slab) == sizeof(rlk::Slab), "slab layout");
 
 // The device error word.  Host code reaches it through its device address,
@@ -1177,7 +1179,7 @@ rlk_status rlk_attn_decode_paged_splitk_rope(const rlk_attn_params* params, cons
 
 namespace {
 
-// The 8-bit cache's entry points allocate on the host (plans, launch
+// The entry points from here on allocate on the host (plans, launch
 // parameters): an exception there ends the call with a status.
 template <class Fn>
 rlk_status guarded(Fn&& call) {
@@ -1519,6 +1521,112 @@ rlk_status rlk_attn_decode_qcache(const rlk_attn_params* params, const void* q, 
                         workspace, workspace_bytes, stream);
   });
 }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- paged BF16 cache
+
+namespace {
+
+rlk_status append_impl(const rlk_attn_params* params, const void* q, void* q_out, const void* k, void* k_out,
+                       const void* v, const int32_t* cu_seqlens, const int32_t* pos_offset, const float* rope_table,
+                       int32_t rope_max_pos, int32_t rope_width, void* k_pool, void* v_pool, int32_t n_pages,
+                       int32_t page_size, const int32_t* page_table, int32_t max_pages, cudaStream_t stream) {
+  rlk_status st = check_params(params);
+  if (st) return st;
+  if (!k_pool || !v_pool || !page_table) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL cache argument");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out) || !aligned16(v) ||
+      !aligned16(rope_table) || !aligned16(k_pool) || !aligned16(v_pool))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(page_table) & 3u)
+    return fail(RLK_ERR_INVALID_ARGUMENT, "page table must be 4-byte aligned");
+  if ((q == nullptr) != (q_out == nullptr)) return fail(RLK_ERR_INVALID_ARGUMENT, "q without q_out, or q_out without q");
+  if ((q || k_out) && !rope_table) return fail(RLK_ERR_INVALID_ARGUMENT, "q and k_out need a RoPE table");
+  if (rope_table && rope_width != 64 && rope_width != 128)
+    return fail(RLK_ERR_UNSUPPORTED, "rope_width %d: must be 64 or 128", rope_width);
+  const int B = params->kv_block_size;
+  if (page_size < 8 || page_size > B || B % page_size)
+    return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
+  if (n_pages < 1 || max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
+  if (!cu_seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL");
+  if (cu_seqlens[0] != 0) return fail(RLK_ERR_INVALID_ARGUMENT, "cu_seqlens must start at 0");
+  const int hq = params->num_q_heads, hkv = params->num_kv_heads;
+  if (params->num_seqs > rlk::kAppendMaxSeqs)
+    return over_ranges(params->num_seqs, [&](int s0, int s1) {
+      const rlk_attn_params rp = range_params(params, s0, s1);
+      const auto cu = rebase(cu_seqlens, s0, s1);
+      const int64_t oq = static_cast<int64_t>(cu_seqlens[s0]) * hq * rlk::kHeadDim;
+      const int64_t ok_ = static_cast<int64_t>(cu_seqlens[s0]) * hkv * rlk::kHeadDim;
+      return append_impl(&rp, adv(q, oq, 2), adv(q_out, oq, 2), adv(k, ok_, 2), adv(k_out, ok_, 2), adv(v, ok_, 2),
+                         cu.data(), pos_offset ? pos_offset + s0 : nullptr, rope_table, rope_max_pos, rope_width,
+                         k_pool, v_pool, n_pages, page_size, page_table + static_cast<int64_t>(s0) * max_pages,
+                         max_pages, stream);
+    }, rlk::kAppendMaxSeqs);
+  rlk::AppendParams ap;
+  std::memset(&ap, 0, sizeof(ap));
+  for (int s = 0; s < params->num_seqs; ++s) {
+    const int64_t len = static_cast<int64_t>(cu_seqlens[s + 1]) - cu_seqlens[s];
+    if (len < 0) return fail(RLK_ERR_INVALID_ARGUMENT, "cu_seqlens not monotone at sequence %d", s);
+    const int64_t p0 = pos_offset ? pos_offset[s] : 0;
+    if (p0 < 0) return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: negative position offset", s);
+    const int64_t end = p0 + len;
+    if (len > 0 && (end > static_cast<int64_t>(max_pages) * page_size || end > INT32_MAX))
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: positions up to %lld are past its %d pages", s,
+                  static_cast<long long>(end - 1), max_pages);
+    if (len > 0 && rope_table && end > rope_max_pos)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: position %lld is past the RoPE table (%d positions)", s,
+                  static_cast<long long>(end - 1), rope_max_pos);
+    ap.cu[s + 1] = cu_seqlens[s + 1];
+    ap.pos0[s] = static_cast<int32_t>(p0);
+  }
+  const int64_t tokens = cu_seqlens[params->num_seqs];
+  if (tokens == 0) return ok();  // no token in the call: tensors of no rows may be NULL
+  if (!k || !v) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
+  if (tokens * (hq + 2 * static_cast<int64_t>(hkv)) > static_cast<int64_t>(INT32_MAX) * 16)
+    return fail(RLK_ERR_UNSUPPORTED, "more than 2^35 rows in one call");
+  if (g_dry_run) return ok();
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev))) return st;
+  ap.err = dev->err;
+  ap.q = static_cast<const uint16_t*>(q);
+  ap.q_out = static_cast<uint16_t*>(q_out);
+  ap.k = static_cast<const uint16_t*>(k);
+  ap.k_out = static_cast<uint16_t*>(k_out);
+  ap.v = static_cast<const uint16_t*>(v);
+  ap.rope_table = rope_table;
+  ap.rope_width = rope_width;
+  ap.hq = hq;
+  ap.hkv = hkv;
+  ap.num_seqs = params->num_seqs;
+  ap.k_pool = static_cast<uint16_t*>(k_pool);
+  ap.v_pool = static_cast<uint16_t*>(v_pool);
+  ap.page_table = page_table;
+  ap.n_pages = n_pages;
+  while ((1 << ap.page_shift) < page_size) ++ap.page_shift;
+  ap.max_pages = max_pages;
+  cudaError_t e = rlk::launch_append(ap, stream);
+  if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "cache append launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, void* q_out, const void* k,
+                                 void* k_out, const void* v, const int32_t* cu_seqlens, const int32_t* pos_offset,
+                                 const float* rope_table, int32_t rope_max_pos, int32_t rope_width, void* k_pool,
+                                 void* v_pool, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                                 int32_t max_pages, rlk_stream_t stream) {
+  return guarded([&]() -> rlk_status {
+    return append_impl(params, q, q_out, k, k_out, v, cu_seqlens, pos_offset, rope_table, rope_max_pos, rope_width,
+                       k_pool, v_pool, n_pages, page_size, page_table, max_pages, stream);
+  });
+}
+
+}  // extern "C"
+
+extern "C" {
 
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op, const int32_t* cu_seqlens_q,
                                const int32_t* cu_seqlens_k) {

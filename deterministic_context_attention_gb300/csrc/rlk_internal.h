@@ -130,6 +130,27 @@ struct RopeParams {
   int32_t pos0[kMaxSeqs];
 };
 
+// Append to the paged BF16 cache: row i of sequence s is the token at position
+// pos0[s] + i; its K and V rows go into the pools [n_pages, page, hkv, 128].
+constexpr int kAppendMaxSeqs = 256;  // sequences per launch
+struct AppendParams {
+  ErrWord* err;
+  const uint16_t* q;  // [T, hq, 128] or null
+  uint16_t* q_out;
+  const uint16_t* k;  // [T, hkv, 128]
+  uint16_t* k_out;    // or null
+  const uint16_t* v;
+  const float* rope_table;  // [positions][cos 64, sin 64], or null
+  int32_t rope_width;       // 64 or 128
+  int32_t hq, hkv, num_seqs;
+  uint16_t* k_pool;
+  uint16_t* v_pool;
+  const int32_t* page_table;
+  int32_t n_pages, page_shift, max_pages;  // page size 2^page_shift
+  int32_t cu[kAppendMaxSeqs + 1];
+  int32_t pos0[kAppendMaxSeqs];
+};
+
 // Per-device set-up, run once per device (with it current) before the first
 // launch there: the kernels' dynamic shared memory limits and launch checks.
 // Function attributes are per device, so every device a process uses needs

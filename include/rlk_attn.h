@@ -43,8 +43,8 @@
  *     duplicate or missing block in a state table) set the device error word;
  *     read it with rlk_attn_check_device_error().
  *   - A batch may hold up to 2^20 sequences.  One launch's sequence tables
- *     ride in kernel parameters and take 128 sequences (256 in the 8-bit
- *     cache's calls), so a larger batch runs as consecutive ranges of that
+ *     ride in kernel parameters and take 128 sequences (256 in the calls of
+ *     the 8-bit cache and in rlk_attn_cache_append), so a larger batch runs as consecutive ranges of that
  *     many sequences on `stream`, each range a complete call on its own rows
  *     (every range is validated before the first launch).  A sequence's
  *     arithmetic does not depend on the other sequences of its batch, so the
@@ -378,6 +378,41 @@ rlk_status rlk_attn_decode_paged_splitk_rope(const rlk_attn_params* params, cons
  * [P4] split-KV policy as an explicit, fixed knob.
  */
 int32_t rlk_attn_decode_auto_split(const rlk_attn_params* params, const int32_t* seqlens, int32_t num_sms);
+
+/*
+ * Appends K and V rows to the paged BF16 cache that the rlk_attn_decode_paged*
+ * calls read, with RoPE on the way: row i of sequence s is the token at
+ * position p = pos_offset[s] + i, and its rows go into slot p % page_size of
+ * page page_table[s * max_pages + p / page_size].
+ *   k, v: device BF16 [T, Hkv, 128], T = cu_seqlens[num_seqs];
+ *   k_pool, v_pool: device BF16 [n_pages, page_size, Hkv, 128]; slots of no
+ *     token of the call are left as they are;
+ *   cu_seqlens: HOST [num_seqs + 1] (a sequence may have no new token, and
+ *     where none has any, the tensors may be NULL and nothing is launched);
+ *   pos_offset: HOST [num_seqs] tokens already cached, or NULL (0);
+ *   rope_table: NULL (k is stored as given), or device, from
+ *     rlk_attn_rope_table, every position < rope_max_pos: k is pre-RoPE and
+ *     rotated at its position.  rope_width 128: the form of rlk_attn_rope,
+ *     with its bits.  rope_width 64: each half of a row is rotated by itself,
+ *     pairs (i, i + 32) of a half with the angle p * theta^(-2i/64), which is
+ *     entry 2i of the same table: the maps of rlk_attn_diff_prefill;
+ *   q, q_out: device BF16 [T, Hq, 128], or both NULL: the queries of the same
+ *     tokens are rotated into q_out (which may be q) in the same launch;
+ *   k_out: device BF16 [T, Hkv, 128] (may be k), or NULL: the rotated keys
+ *     packed as well, as the prefill of the same tokens reads them.
+ *     q and k_out need a table.
+ * A page id outside the pool sets RLK_ERR_BAD_PAGE on the device error word;
+ * its rows are not stored in the pools.  Two tokens of a call must not share a
+ * slot, and other calls in flight must not read or write the slots written.
+ * params: num_seqs, num_q_heads, num_kv_heads, kv_block_size (page_size >= 8
+ * divides it) and head_dim are read.
+ */
+rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, void* q_out, const void* k,
+                                 void* k_out, const void* v, const int32_t* cu_seqlens,
+                                 const int32_t* pos_offset, const float* rope_table, int32_t rope_max_pos,
+                                 int32_t rope_width, void* k_pool, void* v_pool, int32_t n_pages,
+                                 int32_t page_size, const int32_t* page_table, int32_t max_pages,
+                                 rlk_stream_t stream);
 
 /*
  * 8-bit paged KV cache: K and V as E4M3 codes (1 byte each) with one FP32
