@@ -11,7 +11,7 @@ Entry points (same names as the C ABI):
     rlk_attn_prefill_states, rlk_attn_merge_states, rlk_attn_merge_states_noalloc,
     rlk_attn_prefill, rlk_attn_prefill_rope,
     rlk_attn_decode_paged, rlk_attn_backward, rlk_attn_workspace_size,
-    rlk_attn_cache_append,
+    rlk_attn_cache_append, rlk_attn_diff_prefill, rlk_attn_diff_decode,
     rlk_attn_qcache_write, rlk_attn_qcache_read, rlk_attn_decode_qcache,
     rlk_attn_check_device_error, rlk_attn_last_error, rlk_attn_core_id
 """
@@ -34,7 +34,7 @@ STATUS_NAMES = {
     3: "RLK_ERR_WORKSPACE_TOO_SMALL", 4: "RLK_ERR_DUPLICATE_BLOCK", 5: "RLK_ERR_MISSING_BLOCK",
     6: "RLK_ERR_DEVICE_TIMEOUT", 7: "RLK_ERR_CUDA", 8: "RLK_ERR_BAD_PAGE", 9: "RLK_ERR_BAD_STATE_TABLE",
 }
-RLK_OP_MERGE, RLK_OP_BACKWARD, RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE = 1, 2, 3, 4
+RLK_OP_MERGE, RLK_OP_BACKWARD, RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE, RLK_OP_DIFF_DECODE = 1, 2, 3, 4, 5
 CONTIGUOUS, ZIGZAG = 0, 1
 
 
@@ -105,6 +105,8 @@ def load():
             "rlk_attn_qcache_read": [PP, P, P, P, P, i32, i32, P, i32, P, P, P, P, P],
             "rlk_attn_decode_qcache": [PP, P, P, P, P, P, i32, i32, P, i32, P, i32, P, i32, P, P, P, P, sz, P],
             "rlk_attn_cache_append": [PP, P, P, P, P, P, P, P, P, i32, i32, P, P, i32, i32, P, i32, P],
+            "rlk_attn_diff_prefill": [PP, P, P, P, P, P, P, i32, P, P, P, P, P],
+            "rlk_attn_diff_decode": [PP, P, P, P, P, i32, i32, P, i32, P, i32, P, P, P, P, sz, P],
             "rlk_attn_backward": [PP, P, P, P, P, P, P, P, i32, P, P, P, P, sz, P],
             "rlk_attn_workspace_size": [PP, i32, P, P],
             "rlk_attn_check_device_error": [P],
@@ -186,7 +188,7 @@ def rlk_attn_block_manifest_hash(params, cu_seqlens_q, cu_seqlens_k) -> int:
 
 
 def rlk_attn_workspace_size(params, op, cu_seqlens_q, cu_seqlens_k=None) -> int:
-    """RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE: pass the decode context
+    """RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE, RLK_OP_DIFF_DECODE: pass the decode context
     lengths as cu_seqlens_k (cu_seqlens_q may be None)."""
     cq = None if cu_seqlens_q is None else _i32_host(cu_seqlens_q)
     ck = _i32_host(cu_seqlens_k if cu_seqlens_k is not None else cu_seqlens_q)
@@ -455,6 +457,34 @@ def rlk_attn_cache_append(params, q, q_out, k, k_out, v, cu_seqlens, pos_offset,
         ("bf16", k_pool), ("bf16", v_pool), ("i32", page_table))
     _check(load().rlk_attn_cache_append(params, q, qo, k, ko, v, cu_p, po_p, rt, rope_max_pos, rope_width, kp, vp,
                                         n_pages, page_size, pt, max_pages, st), "rlk_attn_cache_append")
+
+
+def rlk_attn_diff_prefill(params, q, k, v, lam, cu_seqlens_q, cu_seqlens_k, cp_rank, out_f32, out_bf16, out2, lse,
+                          stream=None):
+    """Differential attention over packed rows: out = O_1 - lam[h] O_2 (out2:
+    O_2, lse [Tq, Hq, 2]; each may be None)."""
+    n = params.num_seqs
+    cq, cq_p = _i32_addr(cu_seqlens_q, n + 1)
+    ck, ck_p = _i32_addr(cu_seqlens_k, n + 1)
+    q, k, v, lm, of, ob, o2, ls, st = _dev_args(
+        stream, ("bf16", q), ("bf16", k), ("bf16", v), ("f32", lam), ("f32", out_f32), ("bf16", out_bf16),
+        ("f32", out2), ("f32", lse))
+    _check(load().rlk_attn_diff_prefill(params, q, k, v, lm, cq_p, ck_p, cp_rank, of, ob, o2, ls, st),
+           "rlk_attn_diff_prefill")
+
+
+def rlk_attn_diff_decode(params, q, lam, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, split_k,
+                         out_f32, out_bf16, lse, workspace=None, workspace_bytes=None, stream=None):
+    """Differential attention of one token a sequence over the paged cache
+    (split_k: 1 in one pass without a workspace, 0 lets the library pick)."""
+    sl, sl_p = _i32_addr(seqlens, params.num_seqs)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    q, lm, kp, vp, pt, of, ob, ls, ws, st = _dev_args(
+        stream, ("bf16", q), ("f32", lam), ("bf16", k_pool), ("bf16", v_pool), ("i32", page_table), ("f32", out_f32),
+        ("bf16", out_bf16), ("f32", lse), (None, workspace))
+    _check(load().rlk_attn_diff_decode(params, q, lm, kp, vp, n_pages, page_size, pt, max_pages, sl_p, split_k, of, ob,
+                                       ls, ws, workspace_bytes, st), "rlk_attn_diff_decode")
 
 
 def rlk_attn_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,

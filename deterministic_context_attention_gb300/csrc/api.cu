@@ -505,6 +505,43 @@ rlk_status rlk_attn_prefill_states(const rlk_attn_params* params, const void* q,
 
 namespace {
 
+// The query tiles of a prefill (cp_rank >= 0: of that rank's rows), longest first.
+std::vector<rlk::FwdTile> prefill_tiles(const rlk_attn_params* params, const int32_t* cu_seqlens_q,
+                                        const int32_t* cu_seqlens_k, int32_t cp_rank) {
+  const int B = params->kv_block_size;
+  std::vector<std::pair<int, rlk::FwdTile>> costed;
+  for (int s = 0; s < params->num_seqs; ++s) {
+    const int ql = cu_seqlens_q[s + 1] - cu_seqlens_q[s];
+    const int kl = cu_seqlens_k[s + 1] - cu_seqlens_k[s];
+    if (ql == 0) continue;
+    std::vector<Chunk> parts;
+    if (cp_rank < 0) parts.push_back({-1, 0, ql});
+    else
+      for (const Chunk& c : partition(ql, params->cp_size, params->cp_layout))
+        if (c.rank == cp_rank && c.end > c.begin) parts.push_back(c);
+    for (const Chunk& c : parts) {
+      for (int r = c.begin; r < c.end; r += rlk::kTileRows) {
+        rlk::FwdTile t;
+        std::memset(&t, 0, sizeof(t));
+        t.seq = s;
+        t.row_begin = r;
+        t.row_count = std::min(rlk::kTileRows, c.end - r);
+        t.block = -1;
+        const int pmax = kl - ql + r + t.row_count - 1;
+        costed.push_back({pmax / B + 1, t});
+      }
+    }
+  }
+  // longest first; ties by (sequence, row) so the schedule is a pure function of the inputs
+  std::stable_sort(costed.begin(), costed.end(),
+                   [](const std::pair<int, rlk::FwdTile>& a, const std::pair<int, rlk::FwdTile>& b) {
+                     return a.first > b.first;
+                   });
+  std::vector<rlk::FwdTile> tiles;
+  for (auto& c : costed) tiles.push_back(c.second);
+  return tiles;
+}
+
 // The fused prefill, with the query rows rotated by RoPE when rope_table is
 // given (at their absolute positions kv_len - q_len + i): by a pass into the
 // output buffer for whole sequences, inside the kernel for one CP rank's
@@ -542,38 +579,9 @@ rlk_status prefill_impl(const rlk_attn_params* params, const void* q, const void
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
+  const std::vector<rlk::FwdTile> tiles = prefill_tiles(params, cu_seqlens_q, cu_seqlens_k, cp_rank);
+  if (tiles.empty()) return ok();
   const int B = params->kv_block_size;
-  std::vector<std::pair<int, rlk::FwdTile>> costed;
-  for (int s = 0; s < params->num_seqs; ++s) {
-    const int ql = cu_seqlens_q[s + 1] - cu_seqlens_q[s];
-    const int kl = cu_seqlens_k[s + 1] - cu_seqlens_k[s];
-    if (ql == 0) continue;
-    std::vector<Chunk> parts;
-    if (cp_rank < 0) parts.push_back({-1, 0, ql});
-    else
-      for (const Chunk& c : partition(ql, params->cp_size, params->cp_layout))
-        if (c.rank == cp_rank && c.end > c.begin) parts.push_back(c);
-    for (const Chunk& c : parts) {
-      for (int r = c.begin; r < c.end; r += rlk::kTileRows) {
-        rlk::FwdTile t;
-        std::memset(&t, 0, sizeof(t));
-        t.seq = s;
-        t.row_begin = r;
-        t.row_count = std::min(rlk::kTileRows, c.end - r);
-        t.block = -1;
-        const int pmax = kl - ql + r + t.row_count - 1;
-        costed.push_back({pmax / B + 1, t});
-      }
-    }
-  }
-  if (costed.empty()) return ok();
-  // longest first; ties by (sequence, row) so the schedule is a pure function of the inputs
-  std::stable_sort(costed.begin(), costed.end(),
-                   [](const std::pair<int, rlk::FwdTile>& a, const std::pair<int, rlk::FwdTile>& b) {
-                     return a.first > b.first;
-                   });
-  std::vector<rlk::FwdTile> tiles;
-  for (auto& c : costed) tiles.push_back(c.second);
   const int tq = cu_seqlens_q[params->num_seqs], tk = cu_seqlens_k[params->num_seqs];
   CUtensorMap mq, mk, mv;
   if (rope_table && cp_rank < 0) {
@@ -643,7 +651,8 @@ namespace {
 rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const void* k_pool, const void* v_pool,
                              int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                              const int32_t* seqlens, const float* rope_table, int32_t rope_max_pos,
-                             float* out_f32, void* out_bf16, float* lse, cudaStream_t stream) {
+                             float* out_f32, void* out_bf16, float* lse, cudaStream_t stream,
+                             const float* lambda = nullptr) {
   rlk_status st = check_params(params);
   if (st) return st;
   if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
@@ -657,8 +666,8 @@ rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const
       const int64_t o = static_cast<int64_t>(s0) * params->num_q_heads;
       return decode_paged_impl(&rp, adv(q, o * 128, 2), k_pool, v_pool, n_pages, page_size,
                                page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, rope_table,
-                               rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4),
-                               stream);
+                               rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2),
+                               adv(lse, lambda ? 2 * o : o, 4), stream, lambda);
     });
   const int B = params->kv_block_size;
   if (page_size < 8 || page_size > B || B % page_size)
@@ -719,6 +728,7 @@ rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const
   fp->page_size = page_size;
   fp->n_pages = n_pages;
   fp->rope_table = rope_table;
+  fp->lambda = lambda;
   if (!rlk::decode_transposed_supported(*fp)) {
     if ((st = launch_fwd_tiles(fp.get(), tiles, 1, mq, mk, mv, dev, stream))) return st;
     return ok();
@@ -965,7 +975,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
                               int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                               const int32_t* seqlens, int32_t split_k, const float* rope_table,
                               int32_t rope_max_pos, float* out_f32, void* out_bf16, float* lse, void* workspace,
-                              size_t workspace_bytes, cudaStream_t stream) {
+                              size_t workspace_bytes, cudaStream_t stream, const float* lambda = nullptr) {
   rlk_status st = check_params(params);
   if (st) return st;
   if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
@@ -981,7 +991,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
       return decode_splitk_impl(&rp, adv(q, o * 128, 2), k_pool, v_pool, n_pages, page_size,
                                 page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, split_k,
                                 rope_table, rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2),
-                                adv(lse, o, 4), workspace, workspace_bytes, stream);
+                                adv(lse, lambda ? 2 * o : o, 4), workspace, workspace_bytes, stream, lambda);
     });
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || (out_f32 && !aligned16(out_f32)) ||
       (out_bf16 && !aligned16(out_bf16)) || !aligned16(workspace))
@@ -1007,24 +1017,27 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
         return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: position %d is past the RoPE table (%d positions)", s,
                     seqlens[s] - 1, rope_max_pos);
   }
-  const size_t need = rlk_attn_workspace_size(params, RLK_OP_DECODE_SPLIT, nullptr, seqlens);
+  // rows of the state table per block: a query head's, or those of its two maps
+  const int table_rows = lambda ? 2 * params->num_q_heads : params->num_q_heads;
+  const size_t need =
+      rlk_attn_workspace_size(params, lambda ? RLK_OP_DIFF_DECODE : RLK_OP_DECODE_SPLIT, nullptr, seqlens);
   if (!workspace || workspace_bytes < need)
     return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes, need);
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
   if (split_k == 0) {
-    split_k = choose_split(seqlens, params->num_seqs, params->num_kv_heads, params->num_q_heads, B, dev->num_sms);
+    split_k = choose_split(seqlens, params->num_seqs, params->num_kv_heads, table_rows, B, dev->num_sms);
     // one range per sequence is the single-pass decode, which needs no state table
     if (split_k == 1)
       return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens,
-                               rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
+                               rope_table, rope_max_pos, out_f32, out_bf16, lse, stream, lambda);
   }
-  // state table: pair (block_base[s] + b) * Hq + head; o_b FP32 [pair][128], then lse_b [pair]
+  // state table: pair (block_base[s] + b) * rows + row; o_b FP32 [pair][128], then lse_b [pair]
   std::vector<int32_t> block_base(params->num_seqs + 1, 0);
   for (int s = 0; s < params->num_seqs; ++s) block_base[s + 1] = block_base[s] + (seqlens[s] + B - 1) / B;
-  const int64_t pairs = static_cast<int64_t>(block_base[params->num_seqs]) * params->num_q_heads;
-  bool on_chip = fold_on_chip(params->num_seqs, params->num_kv_heads, params->num_q_heads, split_k, dev->num_sms);
+  const int64_t pairs = static_cast<int64_t>(block_base[params->num_seqs]) * table_rows;
+  bool on_chip = fold_on_chip(params->num_seqs, params->num_kv_heads, table_rows, split_k, dev->num_sms);
   std::vector<std::pair<int, rlk::FwdTile>> costed;
   if (on_chip) {
     // item r of a pair takes its blocks r, r + k, r + 2k, ...: the pair's
@@ -1084,6 +1097,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     fp->cu_k[s] = seqlens[s];
     fp->cu_q[s] = block_base[s];
   }
+  fp->lambda = lambda;
   fp->state_o = static_cast<float*>(workspace);
   fp->state_lse = static_cast<float*>(workspace) + pairs * rlk::kHeadDim;
   fp->rope_table = rope_table;
@@ -1116,7 +1130,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     fp->num_items = fp->num_tiles;
     static_assert(rlk::kUnwritten == 0xFFFFFFFFu, "the table fill is all-ones bytes");
     cudaError_t e = self_fill ? cudaSuccess : cudaMemsetAsync(workspace, 0xFF, state_bytes, stream);
-    const int grid = fp->num_items + fold_ctas(params->num_seqs, params->num_q_heads);
+    const int grid = fp->num_items + fold_ctas(params->num_seqs, table_rows);
     if (e == cudaSuccess) e = rlk::launch_decode_cooperative(*fp, mq, mk, mv, grid, stream);
     if (e == cudaSuccess) return ok();
     if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported)
@@ -1626,19 +1640,116 @@ rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, v
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- differential attention
+
+namespace {
+
+rlk_status check_diff(const rlk_attn_params* params, const float* lambda) {
+  rlk_status st = check_params(params);
+  if (st) return st;
+  if (params->kv_block_size != 128) return fail(RLK_ERR_UNSUPPORTED, "differential attention takes KV block 128");
+  if (!lambda) return fail(RLK_ERR_INVALID_ARGUMENT, "lambda is NULL");
+  if (reinterpret_cast<uintptr_t>(lambda) & 3u) return fail(RLK_ERR_INVALID_ARGUMENT, "lambda must be 4-byte aligned");
+  return RLK_OK;
+}
+
+rlk_status diff_prefill_impl(const rlk_attn_params* params, const void* q, const void* k, const void* v,
+                             const float* lambda, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                             int32_t cp_rank, float* out_f32, void* out_bf16, float* out2, float* lse,
+                             cudaStream_t stream) {
+  rlk_status st = check_diff(params, lambda);
+  if (st) return st;
+  if ((st = check_cu(params, cu_seqlens_q, cu_seqlens_k))) return st;
+  if (cp_rank < -1 || cp_rank >= params->cp_size) return fail(RLK_ERR_INVALID_ARGUMENT, "cp_rank %d", cp_rank);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out_f32) || !aligned16(out_bf16) ||
+      !aligned16(out2))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(RLK_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
+  const int tq = cu_seqlens_q[params->num_seqs], tk = cu_seqlens_k[params->num_seqs];
+  if (tq == 0) return ok();  // no query in the call: tensors of no rows may be NULL
+  if (!q || !k || !v) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
+  if (!out_f32 && !out_bf16) return fail(RLK_ERR_INVALID_ARGUMENT, "out_f32 and out_bf16 are both NULL");
+  if (params->num_seqs > rlk::kMaxSeqs)
+    return over_ranges(params->num_seqs, [&](int s0, int s1) {
+      const rlk_attn_params rp = range_params(params, s0, s1);
+      const auto cq = rebase(cu_seqlens_q, s0, s1), ck = rebase(cu_seqlens_k, s0, s1);
+      const int64_t oq = static_cast<int64_t>(cu_seqlens_q[s0]) * params->num_q_heads;
+      const int64_t ok_ = static_cast<int64_t>(cu_seqlens_k[s0]) * params->num_kv_heads;
+      return diff_prefill_impl(&rp, adv(q, oq * 128, 2), adv(k, ok_ * 128, 2), adv(v, ok_ * 128, 2), lambda, cq.data(),
+                               ck.data(), cp_rank, adv(out_f32, oq * 128, 4), adv(out_bf16, oq * 128, 2),
+                               adv(out2, oq * 128, 4), adv(lse, oq * 2, 4), stream);
+    });
+  if (g_dry_run) return ok();
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev))) return st;
+  const std::vector<rlk::FwdTile> tiles = prefill_tiles(params, cu_seqlens_q, cu_seqlens_k, cp_rank);
+  if (tiles.empty()) return ok();
+  CUtensorMap mq, mk, mv;
+  if ((st = make_map(&mq, q, params->num_q_heads, tq, 1, rlk::kTileRows))) return st;
+  if ((st = make_map(&mk, k, params->num_kv_heads, tk, 1, 128))) return st;
+  if ((st = make_map(&mv, v, params->num_kv_heads, tk, 1, 128))) return st;
+  auto fp = std::make_unique<rlk::FwdParams>();
+  base_fwd(fp.get(), params, dev, rlk::kModeDiff);
+  fill_seqs(fp.get(), params, cu_seqlens_q, cu_seqlens_k);
+  fp->out_f32 = out_f32;
+  fp->out_bf16 = static_cast<uint16_t*>(out_bf16);
+  fp->lse = lse;
+  fp->lambda = lambda;
+  fp->out2 = out2;
+  if ((st = launch_fwd_tiles(fp.get(), tiles, params->num_q_heads, mq, mk, mv, dev, stream))) return st;
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+rlk_status rlk_attn_diff_prefill(const rlk_attn_params* params, const void* q, const void* k, const void* v,
+                                 const float* lambda, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                 int32_t cp_rank, float* out_f32, void* out_bf16, float* out2, float* lse,
+                                 rlk_stream_t stream) {
+  return guarded([&]() -> rlk_status {
+    return diff_prefill_impl(params, q, k, v, lambda, cu_seqlens_q, cu_seqlens_k, cp_rank, out_f32, out_bf16, out2,
+                             lse, stream);
+  });
+}
+
+rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, const float* lambda, const void* k_pool,
+                                const void* v_pool, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                                int32_t max_pages, const int32_t* seqlens, int32_t split_k, float* out_f32,
+                                void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
+                                rlk_stream_t stream) {
+  return guarded([&]() -> rlk_status {
+    rlk_status st = check_diff(params, lambda);
+    if (st) return st;
+    if (params->num_q_heads / params->num_kv_heads > rlk::kDecodeMaxGroup)
+      return fail(RLK_ERR_UNSUPPORTED, "differential decode takes at most %d query heads per KV head",
+                  rlk::kDecodeMaxGroup);
+    if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(page_table)) & 3u)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "lse and page table must be 4-byte aligned");
+    if (split_k == 1)  // no state table, no workspace
+      return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, nullptr,
+                               0, out_f32, out_bf16, lse, stream, lambda);
+    return decode_splitk_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, split_k,
+                              nullptr, 0, out_f32, out_bf16, lse, workspace, workspace_bytes, stream, lambda);
+  });
+}
+
+}  // extern "C"
+
 extern "C" {
 
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op, const int32_t* cu_seqlens_q,
                                const int32_t* cu_seqlens_k) {
   if (check_params(params) != RLK_OK) return 0;
-  if (op == RLK_OP_DECODE_SPLIT) {
+  if (op == RLK_OP_DECODE_SPLIT || op == RLK_OP_DIFF_DECODE) {
     if (!cu_seqlens_k) return 0;
     int64_t blocks = 0;
     for (int s = 0; s < params->num_seqs; ++s) {
       if (cu_seqlens_k[s] < 1) return 0;
       blocks += (cu_seqlens_k[s] + params->kv_block_size - 1) / params->kv_block_size;
     }
-    const int64_t pairs = blocks * params->num_q_heads;
+    const int64_t pairs = blocks * params->num_q_heads * (op == RLK_OP_DIFF_DECODE ? 2 : 1);
     return split_table_bytes(pairs) + split_flag_bytes(params->num_seqs, params->num_kv_heads);
   }
   if (op == RLK_OP_DECODE_QCACHE) {

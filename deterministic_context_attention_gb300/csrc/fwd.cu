@@ -57,18 +57,22 @@ constexpr int kRegsSoftmax = 128;
 constexpr int kRegsProducer = 48;
 static_assert(kRegsCorrection + 2 * kRegsSoftmax + kRegsProducer <= 4 * kRegsLaunch, "register split");
 
-template <int B>
+// DIFF: differential attention, whose items hold one map at a time: 64 of the
+// 128 columns of Q and K.  The freed shared memory keeps the second map's
+// output until the first one's is final.
+template <int B, bool DIFF = false>
 struct FwdLayout {
   static constexpr int kSK = (B == 128) ? 3 : 4;         // K ring
   static constexpr int kSV = (B == 128) ? 2 : 4;         // V ring
   static constexpr int kStatsRing = 8;
-  static constexpr int kQBytes = kTileRows * kHeadDim * 2;  // 32 KB, two 64-column halves
-  static constexpr int kQHalf = kTileRows * 128;            // bytes of one half
+  static constexpr int kQHalf = kTileRows * 128;            // bytes of one 64-column half
+  static constexpr int kQBytes = (DIFF ? 1 : 2) * kQHalf;   // 32 KB, two halves (one map: 16 KB)
   static constexpr int kKVHalf = B * 128;                   // bytes of one 64-column half
-  static constexpr int kKVBytes = 2 * kKVHalf;              // K (or V) of one block
+  static constexpr int kKVBytes = 2 * kKVHalf;              // V of one block
+  static constexpr int kKBytes = (DIFF ? 1 : 2) * kKVHalf;  // K of one block
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQBytes;
-  static constexpr int kVOff = kKOff + kSK * kKVBytes;
+  static constexpr int kVOff = kKOff + kSK * kKBytes;
   static constexpr int kBarOff = kVOff + kSV * kKVBytes;
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + kSK, kVFull = kKEmpty + kSK,
                        kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV, kPFull = kSFull + 2, kPVFull = kPFull + 2,
@@ -83,7 +87,9 @@ struct FwdLayout {
   // epilogue staging: per correction warp 32 rows x 128 B (one column chunk)
   static constexpr int kEpiOff = kPageOff + 2 * kPageWin * 4;
   static constexpr int kEpiBytes = 4 * 32 * 128;
-  static constexpr int kTotal = kEpiOff + kEpiBytes;
+  // the second map's rows: float4 [32][128 rows]
+  static constexpr int kParkOff = kEpiOff + kEpiBytes;
+  static constexpr int kTotal = kParkOff + (DIFF ? kTileRows * kHeadDim * 4 : 0);
   static constexpr int kAlloc = kTotal + 1024;
   static_assert(kAlloc <= 232448, "forward shared memory");
   static_assert(kEpiOff % 16 == 0, "staging alignment");
@@ -134,11 +140,25 @@ __device__ __forceinline__ ItemInfo item_info(const FwdParams& p, int item) {
   return it;
 }
 
+// Differential attention walks every item twice, round 2k with the second
+// map and round 2k + 1 with the first, so that the first one's epilogue can
+// subtract; the rounds of the other modes are the items'.
+template <int MODE>
+__device__ __forceinline__ int sched_round(int round) {
+  return MODE == kModeDiff ? round >> 1 : round;
+}
+template <int MODE>
+__device__ __forceinline__ int map_of(int round) {
+  return MODE == kModeDiff ? 1 - (round & 1) : 0;
+}
+
 // Item of this CTA in round k of the static schedule: CTAs take one item per
 // round from the longest-first list, in ascending CTA order on even rounds
 // and descending on odd ones, which evens out the per-CTA work.  A CTA's item
 // index grows with the round, so its loop ends at the first round without one.
-__device__ __forceinline__ int snake_item(int round) {
+template <int MODE>
+__device__ __forceinline__ int snake_item(int r) {
+  const int round = sched_round<MODE>(r);
   const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
   return round * g + ((round & 1) ? g - 1 - c : c);
 }
@@ -273,7 +293,8 @@ template <int B, int MODE, bool ROPE>
 __global__ void __launch_bounds__(512, 1)
     rlk_fwd_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-  using L = FwdLayout<B>;
+  constexpr bool DIFF = MODE == kModeDiff;
+  using L = FwdLayout<B, DIFF>;
   constexpr int SK = L::kSK, SV = L::kSV, SR = L::kStatsRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -339,7 +360,7 @@ __global__ void __launch_bounds__(512, 1)
       int32_t* page_cache = reinterpret_cast<int32_t*>(smem + L::kPageOff);
       int cached_win0 = -1, cached_win1 = -1;
       // load K (IS_V false) or V of block b into its ring slot; false on abort
-      auto load_kv = [&](const ItemInfo& it, int g, int b, bool is_v) -> bool {
+      auto load_kv = [&](const ItemInfo& it, int map_i, int g, int b, bool is_v) -> bool {
         const uint32_t idx = is_v ? v_it : k_it;
         const int S = is_v ? SV : SK;
         const uint32_t stage = idx % S;
@@ -347,14 +368,14 @@ __global__ void __launch_bounds__(512, 1)
         uint64_t* full = &bars[(is_v ? L::kVFull : L::kKFull) + stage];
         bool ok = mbar_wait(empty, ((idx / S) & 1) ^ 1, abort, p.err, is_v ? 0x103 : 0x102);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        uint8_t* dst = (is_v ? v_base : k_base) + stage * L::kKVBytes;
+        uint8_t* dst = is_v ? v_base + stage * L::kKVBytes : k_base + stage * L::kKBytes;
         const CUtensorMap* map = is_v ? &tm_v : &tm_k;
         if (MODE != kModeDecode) {
           if (lane == 0) {
-            mbar_arrive_expect_tx(full, L::kKVBytes);
+            mbar_arrive_expect_tx(full, is_v ? L::kKVBytes : L::kKBytes);
             const int r = it.k_tok0 + b * B;
-            tma_load_3d(dst, map, full, 0, g, r);
-            tma_load_3d(dst + L::kKVHalf, map, full, 64, g, r);
+            tma_load_3d(dst, map, full, DIFF && !is_v ? 64 * map_i : 0, g, r);
+            if (!DIFF || is_v) tma_load_3d(dst + L::kKVHalf, map, full, 64, g, r);
           }
         } else {
           const int ps = p.page_size;
@@ -399,8 +420,8 @@ __global__ void __launch_bounds__(512, 1)
         if (is_v) ++v_it; else ++k_it;
         return true;
       };
-      for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-        const int item = snake_item(round);
+      for (int round = 0; sched_round<MODE>(round) * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+        const int item = snake_item<MODE>(round);
         if (item >= p.num_items) continue;
         const ItemInfo it = item_info<MODE>(p, item);
         bool ok = mbar_wait(&bars[L::kQEmpty], (q_it & 1) ^ 1, abort, p.err, 0x101);
@@ -417,8 +438,8 @@ __global__ void __launch_bounds__(512, 1)
           } else {
             mbar_arrive_expect_tx(&bars[L::kQFull], L::kQBytes);
             const int row0 = it.q_tok0 + it.row_begin;
-            tma_load_3d(smem + L::kQOff, &tm_q, &bars[L::kQFull], 0, it.head, row0);
-            tma_load_3d(smem + L::kQOff + L::kQHalf, &tm_q, &bars[L::kQFull], 64, it.head, row0);
+            tma_load_3d(smem + L::kQOff, &tm_q, &bars[L::kQFull], DIFF ? 64 * map_of<MODE>(round) : 0, it.head, row0);
+            if (!DIFF) tma_load_3d(smem + L::kQOff + L::kQHalf, &tm_q, &bars[L::kQFull], 64, it.head, row0);
           }
         }
         ++q_it;
@@ -427,8 +448,8 @@ __global__ void __launch_bounds__(512, 1)
         // consumption order: K_0, K_1, V_0, K_2, V_1, ...
         bool fail = false;
         for (int j = 0; j <= it.nb && !fail; ++j) {
-          if (j < it.nb && !load_kv(it, g, it.blk0 + j, false)) fail = true;
-          if (!fail && j >= 1 && !load_kv(it, g, it.blk0 + j - 1, true)) fail = true;
+          if (j < it.nb && !load_kv(it, map_of<MODE>(round), g, it.blk0 + j, false)) fail = true;
+          if (!fail && j >= 1 && !load_kv(it, map_of<MODE>(round), g, it.blk0 + j - 1, true)) fail = true;
         }
         if (fail || *abort) break;
       }
@@ -443,8 +464,8 @@ __global__ void __launch_bounds__(512, 1)
       // ~700 cycles) is read while the current item runs, not between the
       // last PV and the next item's first S
       ItemInfo nxt;
-      if (snake_item(0) < p.num_items) nxt = item_info<MODE>(p, snake_item(0));
-      for (int round = 0; snake_item(round) < p.num_items; ++round) {
+      if (snake_item<MODE>(0) < p.num_items) nxt = item_info<MODE>(p, snake_item<MODE>(0));
+      for (int round = 0; snake_item<MODE>(round) < p.num_items; ++round) {
         const ItemInfo it = nxt;
         // with RoPE in the prefill the softmax warps hand over the rotated tile
         bool ok = mbar_wait(&bars[ROPE ? L::kQRot : L::kQFull], q_it & 1, abort, p.err, 0x201);
@@ -459,12 +480,13 @@ __global__ void __launch_bounds__(512, 1)
           tc_fence_after();
           // the whole warp walks the K-steps (warp-uniform descriptors); the
           // elected lane issues
-          const Desc kd0 = make_desc(smem_u32(k_base + stage * L::kKVBytes), 16, 1024);
+          const Desc kd0 = make_desc(smem_u32(k_base + stage * L::kKBytes), 16, 1024);
           const uint32_t d = tm_s + ((sb + j) & 1) * 128;
-          // S = Q K^T: K-steps 0-3 in the first 64-column half, 4-7 in the second
+          // S = Q K^T: K-steps 0-3 in the first 64-column half, 4-7 in the
+          // second (one map of differential attention: its half alone)
           if (leader) mma_ss<0>(d, qd0, 0, kd0, 0, kIdescS);
 #pragma unroll
-          for (int k = 1; k < kHeadDim / 16; ++k)
+          for (int k = 1; k < (DIFF ? 4 : kHeadDim / 16); ++k)
             if (leader)
               mma_ss<1>(d, qd0, (k >> 2) * (L::kQHalf >> 4) + (k & 3) * 2, kd0, (k >> 2) * (L::kKVHalf >> 4) + (k & 3) * 2,
                         kIdescS);
@@ -476,7 +498,7 @@ __global__ void __launch_bounds__(512, 1)
           return true;
         };
         if (!issue_s(0)) break;
-        if (snake_item(round + 1) < p.num_items) nxt = item_info<MODE>(p, snake_item(round + 1));
+        if (snake_item<MODE>(round + 1) < p.num_items) nxt = item_info<MODE>(p, snake_item<MODE>(round + 1));
         bool fail = false;
         for (int j = 0; j < it.nb; ++j) {
           if (j + 1 < it.nb) {
@@ -551,8 +573,8 @@ __global__ void __launch_bounds__(512, 1)
     float* xmax = reinterpret_cast<float*>(smem + L::kXchOff);  // [2][128]
     float* xsum = xmax + 2 * kTileRows;                          // [2][128]
     uint32_t s_it = 0, st_it = 0;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = snake_item(round);
+    for (int round = 0; sched_round<MODE>(round) * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+      const int item = snake_item<MODE>(round);
       if (item >= p.num_items) continue;
       const ItemInfo it = item_info<MODE>(p, item);
       const bool valid = row_of_lane<MODE>(r) < it.row_count;
@@ -636,14 +658,15 @@ __global__ void __launch_bounds__(512, 1)
     // start.  The states mode reads it in place: its epilogue stores the
     // states block by block, and there the read-ahead measured ~6 % slower.
     ItemInfo nxt;
-    if (MODE == kModeFused && snake_item(0) < p.num_items) nxt = item_info<MODE>(p, snake_item(0));
-    for (int round = 0; snake_item(round) < p.num_items; ++round) {
+    if (MODE != kModeStates && MODE != kModeDecode && snake_item<MODE>(0) < p.num_items)
+      nxt = item_info<MODE>(p, snake_item<MODE>(0));
+    for (int round = 0; snake_item<MODE>(round) < p.num_items; ++round) {
       ItemInfo it;
-      if (MODE == kModeFused) {
+      if (MODE == kModeFused || DIFF) {
         it = nxt;
-        if (snake_item(round + 1) < p.num_items) nxt = item_info<MODE>(p, snake_item(round + 1));
+        if (snake_item<MODE>(round + 1) < p.num_items) nxt = item_info<MODE>(p, snake_item<MODE>(round + 1));
       } else {
-        it = item_info<MODE>(p, snake_item(round));
+        it = item_info<MODE>(p, snake_item<MODE>(round));
       }
       const bool valid = row_of_lane<MODE>(r) < it.row_count;
       const bool warp_rows = __any_sync(0xffffffffu, valid);
@@ -751,7 +774,7 @@ __global__ void __launch_bounds__(512, 1)
         ++st_it;
       }
       if (fail) break;
-      if (MODE == kModeFused) {
+      if (MODE == kModeFused || DIFF) {
         // epilogue: O and L are final.  Each warp stages its 32 rows through
         // shared memory one 128-byte column chunk at a time (chunk j of a
         // row in slot j ^ (row & 7), so neither side conflicts on banks) and
@@ -768,7 +791,29 @@ __global__ void __launch_bounds__(512, 1)
             if (tr < it.row_count) store(row_base + static_cast<int64_t>(tr) * p.hq, jj, v);
           }
         };
-        if (p.out_f32) {
+        // differential attention: out = O1 - lambda O2, one fma an element;
+        // O2, final a round earlier, waits in shared memory (thread r's own
+        // 16-byte pieces, 128 rows apart)
+        const bool second = DIFF && map_of<MODE>(round) == 1;
+        if (DIFF) {
+          float4* park = reinterpret_cast<float4*>(smem + L::kParkOff) + r;
+          if (second) {
+#pragma unroll
+            for (int e = 0; e < kHeadDim; e += 4) park[e / 4 * kTileRows] = make_float4(O[e], O[e + 1], O[e + 2], O[e + 3]);
+          } else {
+            const float nl = -__ldg(p.lambda + it.head);
+#pragma unroll
+            for (int e = 0; e < kHeadDim; e += 4) {
+              const float4 x = park[e / 4 * kTileRows];
+              O[e] = __fmaf_rn(nl, x.x, O[e]);
+              O[e + 1] = __fmaf_rn(nl, x.y, O[e + 1]);
+              O[e + 2] = __fmaf_rn(nl, x.z, O[e + 2]);
+              O[e + 3] = __fmaf_rn(nl, x.w, O[e + 3]);
+            }
+          }
+        }
+        float* const out_f32 = second ? p.out2 : p.out_f32;
+        if (out_f32) {
 #pragma unroll
           for (int c = 0; c < kHeadDim / 32; ++c) {
 #pragma unroll
@@ -777,12 +822,12 @@ __global__ void __launch_bounds__(512, 1)
                   make_float4(O[32 * c + 4 * j], O[32 * c + 4 * j + 1], O[32 * c + 4 * j + 2], O[32 * c + 4 * j + 3]);
             __syncwarp();
             write_chunks([&](int64_t row_idx, int jj, const float4& v) {
-              reinterpret_cast<float4*>(p.out_f32 + row_idx * kHeadDim + 32 * c)[jj] = v;
+              reinterpret_cast<float4*>(out_f32 + row_idx * kHeadDim + 32 * c)[jj] = v;
             });
             __syncwarp();
           }
         }
-        if (p.out_bf16) {
+        if (p.out_bf16 && !second) {
 #pragma unroll
           for (int c = 0; c < kHeadDim / 64; ++c) {
 #pragma unroll
@@ -799,7 +844,10 @@ __global__ void __launch_bounds__(512, 1)
             __syncwarp();
           }
         }
-        if (p.lse && valid) p.lse[row_base + static_cast<int64_t>(r) * p.hq] = Lrun;
+        if (p.lse && valid) {
+          const int64_t row_idx = row_base + static_cast<int64_t>(r) * p.hq;
+          p.lse[DIFF ? 2 * row_idx + map_of<MODE>(round) : row_idx] = Lrun;
+        }
       } else if (MODE == kModeDecode && valid) {
         // epilogue (decode): the group's rows are spread over the lane
         // quadrants; few rows, written directly
@@ -839,7 +887,7 @@ __global__ void __launch_bounds__(512, 1)
 // ---------------------------------------------------------------- launchers
 template <int B, int MODE, bool ROPE>
 static cudaError_t configure_fwd_t() {
-  using L = FwdLayout<B>;
+  using L = FwdLayout<B, MODE == kModeDiff>;
   auto kern = rlk_fwd_kernel<B, MODE, ROPE>;
   // The warpgroup register split (208 / 128 / 128 / 48) needs the launch to
   // grant 128 registers per thread; with fewer, setmaxnreg.inc would wait
@@ -861,6 +909,7 @@ cudaError_t configure_fwd_kernels() {
   if ((e = configure_fwd_t<128, kModeFused, true>()) != cudaSuccess) return e;
   if ((e = configure_fwd_t<128, kModeStates, false>()) != cudaSuccess) return e;
   if ((e = configure_fwd_t<128, kModeDecode, false>()) != cudaSuccess) return e;
+  if ((e = configure_fwd_t<128, kModeDiff, false>()) != cudaSuccess) return e;
   if ((e = configure_fwd_t<64, kModeFused, false>()) != cudaSuccess) return e;
   if ((e = configure_fwd_t<64, kModeFused, true>()) != cudaSuccess) return e;
   if ((e = configure_fwd_t<64, kModeStates, false>()) != cudaSuccess) return e;
@@ -870,7 +919,7 @@ cudaError_t configure_fwd_kernels() {
 template <int B, int MODE, bool ROPE>
 static cudaError_t launch_fwd_t(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                 const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  rlk_fwd_kernel<B, MODE, ROPE><<<grid, kThreads, FwdLayout<B>::kAlloc, stream>>>(p, tq, tk, tv);
+  rlk_fwd_kernel<B, MODE, ROPE><<<grid, kThreads, FwdLayout<B, MODE == kModeDiff>::kAlloc, stream>>>(p, tq, tk, tv);
   return cudaGetLastError();
 }
 
@@ -884,6 +933,7 @@ cudaError_t launch_fwd(const FwdParams& p, const CUtensorMap& tq, const CUtensor
                     : launch_fwd_t<128, kModeFused, false>(p, tq, tk, tv, grid, stream);
       case kModeStates: return launch_fwd_t<128, kModeStates, false>(p, tq, tk, tv, grid, stream);
       case kModeDecode: return launch_fwd_t<128, kModeDecode, false>(p, tq, tk, tv, grid, stream);
+      case kModeDiff: return launch_fwd_t<128, kModeDiff, false>(p, tq, tk, tv, grid, stream);
     }
   } else if (p.block == 64) {
     switch (p.mode) {

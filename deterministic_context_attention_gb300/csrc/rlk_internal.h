@@ -30,7 +30,7 @@ struct ErrWord {
   unsigned int site;
 };
 
-enum FwdMode : int { kModeFused = 0, kModeStates = 1, kModeDecode = 2 };
+enum FwdMode : int { kModeFused = 0, kModeStates = 1, kModeDecode = 2, kModeDiff = 3 };
 
 // One unit of forward work: up to 128 query rows of one sequence (all query
 // heads are looped inside the grid), or, for decode, one (sequence, KV head)
@@ -80,6 +80,10 @@ struct FwdParams {
   // transposed decode: RoPE table [positions][cos 64, sin 64] (FP32); when
   // set, the query rows are rotated at position kv_len - 1 after they land
   const float* rope_table;
+  // differential attention: the weight of each query head's second map, and
+  // that map's output [rows, hq, 128] (or null)
+  const float* lambda;
+  float* out2;
   // sequences: fused/states use cu_q / cu_k (packed offsets); decode uses
   // cu_k[s] as the context length of sequence s.
   int32_t cu_q[kMaxSeqs + 1];

@@ -415,6 +415,54 @@ rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, v
                                  rlk_stream_t stream);
 
 /*
+ * Differential attention: the difference of two softmax maps with a learned
+ * weight.  A 128-wide head of q and k holds two 64-wide maps, elements 0..63
+ * (map 1) and 64..127 (map 2); both weigh the same 128-wide v:
+ *     O_m = softmax(softmax_scale * q_m k_m^T) v       (causal, per map)
+ *     out = O_1 - lambda[h] * O_2                      (query head h)
+ * Each O_m is a canonical fold of block states, as in rlk_attn_prefill; out is
+ * fma(-lambda, O_2, O_1) in FP32, rounded to BF16 only at the final write.
+ * So out has the same bits for every chunking, batch, CP rank, page order and
+ * split, and a decode row those of the prefill's last row.
+ *   lambda: device FP32 [Hq];
+ *   params: as for rlk_attn_prefill, kv_block_size 128 (RLK_ERR_UNSUPPORTED
+ *     otherwise); softmax_scale is usually 1/sqrt(64).
+ */
+
+/*
+ * Differential attention over packed rows (full prefill or chunked replay;
+ * arguments as in rlk_attn_prefill).  Outputs: out_f32 [Tq, Hq, 128] FP32 and
+ * out_bf16 (either may be NULL, not both), out2 [Tq, Hq, 128] FP32 (O_2, which
+ * the backward reads; may be NULL), lse [Tq, Hq, 2] FP32 (natural log, of maps
+ * 1 and 2; may be NULL).  Where no sequence has a query, the tensors may be
+ * NULL and nothing is launched.
+ */
+rlk_status rlk_attn_diff_prefill(const rlk_attn_params* params, const void* q, const void* k,
+                                 const void* v, const float* lambda, const int32_t* cu_seqlens_q,
+                                 const int32_t* cu_seqlens_k, int32_t cp_rank, float* out_f32,
+                                 void* out_bf16, float* out2, float* lse, rlk_stream_t stream);
+
+/*
+ * Differential attention of one new token a sequence over the paged BF16
+ * cache: q [num_seqs, Hq, 128], cache and seqlens as in rlk_attn_decode_paged,
+ * out_f32 / out_bf16 [num_seqs, Hq, 128] (not both NULL), lse [num_seqs, Hq, 2]
+ * (may be NULL).  q and the cached keys are rotated already where RoPE is used
+ * (rlk_attn_cache_append does both, with rope_width 64).
+ *   split_k: 1 takes each (sequence, KV head) in one pass and needs no
+ *     workspace; 2..64 splits its KV blocks as rlk_attn_decode_paged_splitk
+ *     does; 0 lets the library pick.  The same bits for all.
+ *   workspace: device, 16-byte aligned, >= rlk_attn_workspace_size(params,
+ *     RLK_OP_DIFF_DECODE, NULL, seqlens) bytes; its contents do not matter.
+ * At most 8 query heads per KV head (RLK_ERR_UNSUPPORTED otherwise).
+ */
+rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, const float* lambda,
+                                const void* k_pool, const void* v_pool, int32_t n_pages,
+                                int32_t page_size, const int32_t* page_table, int32_t max_pages,
+                                const int32_t* seqlens, int32_t split_k, float* out_f32, void* out_bf16,
+                                float* lse, void* workspace, size_t workspace_bytes,
+                                rlk_stream_t stream);
+
+/*
  * 8-bit paged KV cache: K and V as E4M3 codes (1 byte each) with one FP32
  * scale per (page, KV head), half the bytes of the BF16 pools a decode step
  * reads.  All three calls below share
@@ -577,10 +625,11 @@ rlk_status rlk_attn_merge_states_noalloc(const rlk_attn_params* params, const in
                                          int64_t n_state_pairs, float* out_f32, void* out_bf16, float* lse,
                                          rlk_stream_t stream);
 
-enum { RLK_OP_MERGE = 1, RLK_OP_BACKWARD = 2, RLK_OP_DECODE_SPLIT = 3, RLK_OP_DECODE_QCACHE = 4 };
+enum { RLK_OP_MERGE = 1, RLK_OP_BACKWARD = 2, RLK_OP_DECODE_SPLIT = 3, RLK_OP_DECODE_QCACHE = 4,
+       RLK_OP_DIFF_DECODE = 5 };
 
 /* Workspace bytes an entry point needs (HOST cu_seqlens; 0 on bad input).
- * RLK_OP_DECODE_SPLIT and RLK_OP_DECODE_QCACHE take the decode context
+ * RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE and RLK_OP_DIFF_DECODE take the decode context
  * lengths (seqlens) as cu_seqlens_k and ignore cu_seqlens_q. */
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op,
                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k);
