@@ -11,7 +11,7 @@ Entry points (same names as the C ABI):
     rlk_attn_prefill_states, rlk_attn_merge_states, rlk_attn_merge_states_noalloc,
     rlk_attn_prefill, rlk_attn_prefill_rope,
     rlk_attn_decode_paged, rlk_attn_backward, rlk_attn_workspace_size,
-    rlk_attn_cache_append, rlk_attn_diff_prefill, rlk_attn_diff_decode,
+    rlk_attn_cache_append, rlk_attn_diff_prefill, rlk_attn_diff_decode, rlk_attn_diff_backward,
     rlk_attn_qcache_write, rlk_attn_qcache_read, rlk_attn_decode_qcache,
     rlk_attn_check_device_error, rlk_attn_last_error, rlk_attn_core_id
 """
@@ -34,7 +34,8 @@ STATUS_NAMES = {
     3: "RLK_ERR_WORKSPACE_TOO_SMALL", 4: "RLK_ERR_DUPLICATE_BLOCK", 5: "RLK_ERR_MISSING_BLOCK",
     6: "RLK_ERR_DEVICE_TIMEOUT", 7: "RLK_ERR_CUDA", 8: "RLK_ERR_BAD_PAGE", 9: "RLK_ERR_BAD_STATE_TABLE",
 }
-RLK_OP_MERGE, RLK_OP_BACKWARD, RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE, RLK_OP_DIFF_DECODE = 1, 2, 3, 4, 5
+RLK_OP_MERGE, RLK_OP_BACKWARD, RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE = 1, 2, 3, 4
+RLK_OP_DIFF_DECODE, RLK_OP_DIFF_BACKWARD = 5, 6
 CONTIGUOUS, ZIGZAG = 0, 1
 
 
@@ -107,6 +108,7 @@ def load():
             "rlk_attn_cache_append": [PP, P, P, P, P, P, P, P, P, i32, i32, P, P, i32, i32, P, i32, P],
             "rlk_attn_diff_prefill": [PP, P, P, P, P, P, P, i32, P, P, P, P, P],
             "rlk_attn_diff_decode": [PP, P, P, P, P, i32, i32, P, i32, P, i32, P, P, P, P, sz, P],
+            "rlk_attn_diff_backward": [PP, P, P, P, P, P, P, P, P, P, i32, P, P, P, P, P, sz, P],
             "rlk_attn_backward": [PP, P, P, P, P, P, P, P, i32, P, P, P, P, sz, P],
             "rlk_attn_workspace_size": [PP, i32, P, P],
             "rlk_attn_check_device_error": [P],
@@ -485,6 +487,19 @@ def rlk_attn_diff_decode(params, q, lam, k_pool, v_pool, n_pages, page_size, pag
         ("bf16", out_bf16), ("f32", lse), (None, workspace))
     _check(load().rlk_attn_diff_decode(params, q, lm, kp, vp, n_pages, page_size, pt, max_pages, sl_p, split_k, of, ob,
                                        ls, ws, workspace_bytes, st), "rlk_attn_diff_decode")
+
+
+def rlk_attn_diff_backward(params, q, k, v, lam, out_f32, out2, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, dlam,
+                           workspace, workspace_bytes=None, stream=None):
+    """Gradients of differential attention: dq, dk, dv and dlam [Hq], FP32."""
+    cu, cu_p = _i32_addr(cu_seqlens, params.num_seqs + 1)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    q, k, v, lm, of, o2, do, ls, dq, dk, dv, dl, ws, st = _dev_args(
+        stream, ("bf16", q), ("bf16", k), ("bf16", v), ("f32", lam), ("f32", out_f32), ("f32", out2), ("bf16", dout),
+        ("f32", lse), ("f32", dq), ("f32", dk), ("f32", dv), ("f32", dlam), (None, workspace))
+    _check(load().rlk_attn_diff_backward(params, q, k, v, lm, of, o2, do, ls, cu_p, cp_rank, dq, dk, dv, dl, ws,
+                                         workspace_bytes, st), "rlk_attn_diff_backward")
 
 
 def rlk_attn_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,

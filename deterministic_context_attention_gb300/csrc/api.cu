@@ -41,8 +41,8 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
                         const float* out_f32, const void* dout, const float* lse,
                         const int32_t* cu, int32_t cp_rank, float* dq, float* dk, float* dv,
                         void* workspace, size_t workspace_bytes, ErrWord* err, int num_sms,
-                        cudaStream_t stream);
-size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu);
+                        cudaStream_t stream, const DiffBackward* diff);
+size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu, int maps);
 }  // namespace rlk
 
 static_assert(sizeof(rlk::FwdParams) + 3 * sizeof(CUtensorMap) + 256 <= 32764,
@@ -673,7 +673,7 @@ rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const
   if (page_size < 8 || page_size > B || B % page_size)
     return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
   if (n_pages < 1 || max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
-  if (static_cast<int64_t>(n_pages + 1) * page_size >= (int64_t(1) << 31))
+  if ((static_cast<int64_t>(n_pages) + 1) * page_size >= (int64_t(1) << 31))
     return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit token coordinates");
   for (int s = 0; s < params->num_seqs; ++s)
     if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(max_pages) * page_size)
@@ -1004,7 +1004,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
   if (page_size < 8 || page_size > B || B % page_size)
     return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
   if (n_pages < 1 || max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
-  if (static_cast<int64_t>(n_pages + 1) * page_size >= (int64_t(1) << 31))
+  if ((static_cast<int64_t>(n_pages) + 1) * page_size >= (int64_t(1) << 31))
     return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit token coordinates");
   for (int s = 0; s < params->num_seqs; ++s)
     if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(max_pages) * page_size)
@@ -1737,6 +1737,71 @@ rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, co
 
 }  // extern "C"
 
+namespace {
+
+rlk_status diff_backward_impl(const rlk_attn_params* params, const void* q, const void* k, const void* v,
+                              const float* out_f32, const void* dout, const float* lse, const int32_t* cu_seqlens,
+                              int32_t cp_rank, float* dq, float* dk, float* dv, void* workspace,
+                              size_t workspace_bytes, const rlk::DiffBackward& diff, cudaStream_t stream) {
+  rlk_status st = check_diff(params, diff.lambda);
+  if (st) return st;
+  if ((st = check_cu(params, cu_seqlens, cu_seqlens))) return st;
+  if (cp_rank < -1 || cp_rank >= params->cp_size) return fail(RLK_ERR_INVALID_ARGUMENT, "cp_rank %d", cp_rank);
+  if (!diff.dlambda) return fail(RLK_ERR_INVALID_ARGUMENT, "dlambda is NULL");
+  if ((reinterpret_cast<uintptr_t>(diff.dlambda) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 7u))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "dlambda must be 4-byte aligned, lse 8-byte aligned");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out_f32) || !aligned16(diff.out2) ||
+      !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+  const int T = cu_seqlens[params->num_seqs], hq = params->num_q_heads, hkv = params->num_kv_heads;
+  if (T > 0 && (!q || !k || !v || !out_f32 || !diff.out2 || !dout || !lse || !dq || !dk || !dv))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "NULL tensor");
+  if (params->num_seqs > rlk::kMaxSeqs)
+    // each range reuses the workspace from its start; dlambda sums over the ranges in order
+    return over_ranges(params->num_seqs, [&](int s0, int s1) {
+      const rlk_attn_params rp = range_params(params, s0, s1);
+      const auto cu = rebase(cu_seqlens, s0, s1);
+      const int64_t oq = static_cast<int64_t>(cu_seqlens[s0]) * hq, ok_ = static_cast<int64_t>(cu_seqlens[s0]) * hkv;
+      const rlk::DiffBackward part{diff.lambda, adv(diff.out2, oq * 128, 4), diff.dlambda, s0 > 0};
+      return diff_backward_impl(&rp, adv(q, oq * 128, 2), adv(k, ok_ * 128, 2), adv(v, ok_ * 128, 2),
+                                adv(out_f32, oq * 128, 4), adv(dout, oq * 128, 2), adv(lse, oq * 2, 4), cu.data(),
+                                cp_rank, adv(dq, oq * 128, 4), adv(dk, ok_ * 128, 4), adv(dv, ok_ * 128, 4), workspace,
+                                workspace_bytes, part, stream);
+    });
+  const size_t need = rlk::backward_workspace_bytes(params, cu_seqlens, 2);
+  if (T > 0 && (!workspace || workspace_bytes < need))
+    return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (g_dry_run) return ok();
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev))) return st;
+  if (T == 0) {  // no row: a gradient of zeros (or nothing to add)
+    cudaError_t e = diff.add ? cudaSuccess : cudaMemsetAsync(diff.dlambda, 0, hq * sizeof(float), stream);
+    if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "dlambda fill: %s", cudaGetErrorString(e));
+    return ok();
+  }
+  st = rlk::run_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,
+                         workspace_bytes, dev->err, dev->num_sms, stream, &diff);
+  if (st) return fail(st, "differential backward launch: %s", cudaGetErrorString(cudaPeekAtLastError()));
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+rlk_status rlk_attn_diff_backward(const rlk_attn_params* params, const void* q, const void* k, const void* v,
+                                  const float* lambda, const float* out_f32, const float* out2, const void* dout,
+                                  const float* lse, const int32_t* cu_seqlens, int32_t cp_rank, float* dq, float* dk,
+                                  float* dv, float* dlambda, void* workspace, size_t workspace_bytes,
+                                  rlk_stream_t stream) {
+  return guarded([&]() -> rlk_status {
+    return diff_backward_impl(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,
+                              workspace_bytes, rlk::DiffBackward{lambda, out2, dlambda, false}, stream);
+  });
+}
+
+}  // extern "C"
+
 extern "C" {
 
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op, const int32_t* cu_seqlens_q,
@@ -1768,9 +1833,9 @@ size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op, const 
     const size_t bytes = static_cast<size_t>(params->num_seqs) * max_blocks * sizeof(int32_t);
     return (bytes + 255) / 256 * 256;
   }
-  if (op == RLK_OP_BACKWARD) {
+  if (op == RLK_OP_BACKWARD || op == RLK_OP_DIFF_BACKWARD) {
     if (check_cu(params, cu_seqlens_q, cu_seqlens_q) != RLK_OK) return 0;
-    return rlk::backward_workspace_bytes(params, cu_seqlens_q);
+    return rlk::backward_workspace_bytes(params, cu_seqlens_q, op == RLK_OP_DIFF_BACKWARD ? 2 : 1);
   }
   return 0;
 }
@@ -1925,14 +1990,14 @@ rlk_status rlk_attn_backward(const rlk_attn_params* params, const void* q, const
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out_f32) || !aligned16(dout) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
-  const size_t need = rlk::backward_workspace_bytes(params, cu_seqlens);
+  const size_t need = rlk::backward_workspace_bytes(params, cu_seqlens, 1);
   if (!workspace || workspace_bytes < need)
     return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
   st = rlk::run_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,
-                         workspace_bytes, dev->err, dev->num_sms, stream);
+                         workspace_bytes, dev->err, dev->num_sms, stream, nullptr);
   if (st) return st;
   return ok();
 }

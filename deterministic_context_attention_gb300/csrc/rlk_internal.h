@@ -155,6 +155,15 @@ struct AppendParams {
   int32_t pos0[kAppendMaxSeqs];
 };
 
+// What the differential backward takes beside the plain one's tensors; add:
+// dlambda is added to (a later range of the batch's sequences).
+struct DiffBackward {
+  const float* lambda;  // [hq]
+  const float* out2;    // [T, hq, 128]: the second map's output
+  float* dlambda;       // [hq]
+  bool add;
+};
+
 // Per-device set-up, run once per device (with it current) before the first
 // launch there: the kernels' dynamic shared memory limits and launch checks.
 // Function attributes are per device, so every device a process uses needs

@@ -463,6 +463,31 @@ rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, co
                                 rlk_stream_t stream);
 
 /*
+ * Gradients of differential attention over whole sequences (q_len = kv_len),
+ * for dout [T, Hq, 128] BF16:
+ *     P_m = exp(softmax_scale q_m k_m^T - lse_m),  dP = dout v^T,
+ *     Delta_2 = dout . O_2,  Delta_1 = dout . out + lambda Delta_2,
+ *     dS_1 = P_1 (dP - Delta_1),  dS_2 = -lambda P_2 (dP - Delta_2),
+ *     dv = (P_1 - lambda P_2)^T dout,
+ *     dq_m = softmax_scale dS_m k_m,  dk_m = softmax_scale dS_m^T q_m,
+ *     dlambda[h] = -(sum of Delta_2 over the rows of head h)
+ * with dk and dv summed over a KV head's query heads.
+ *   out_f32, out2, lse: the outputs of rlk_attn_diff_prefill;
+ *   dq [T, Hq, 128], dk, dv [T, Hkv, 128], dlambda [Hq]: device FP32;
+ *   cp_rank: as in rlk_attn_backward (-1: everything; else the rank's dq rows
+ *     and dk/dv blocks); dlambda is the whole batch's for every rank;
+ *   workspace: device, >= rlk_attn_workspace_size(..., RLK_OP_DIFF_BACKWARD, ...).
+ * Fixed reduction orders, no atomics.  A batch without a row sets dlambda to
+ * zero, and its tensors may be NULL.
+ */
+rlk_status rlk_attn_diff_backward(const rlk_attn_params* params, const void* q, const void* k,
+                                  const void* v, const float* lambda, const float* out_f32,
+                                  const float* out2, const void* dout, const float* lse,
+                                  const int32_t* cu_seqlens, int32_t cp_rank, float* dq, float* dk,
+                                  float* dv, float* dlambda, void* workspace, size_t workspace_bytes,
+                                  rlk_stream_t stream);
+
+/*
  * 8-bit paged KV cache: K and V as E4M3 codes (1 byte each) with one FP32
  * scale per (page, KV head), half the bytes of the BF16 pools a decode step
  * reads.  All three calls below share
@@ -626,7 +651,7 @@ rlk_status rlk_attn_merge_states_noalloc(const rlk_attn_params* params, const in
                                          rlk_stream_t stream);
 
 enum { RLK_OP_MERGE = 1, RLK_OP_BACKWARD = 2, RLK_OP_DECODE_SPLIT = 3, RLK_OP_DECODE_QCACHE = 4,
-       RLK_OP_DIFF_DECODE = 5 };
+       RLK_OP_DIFF_DECODE = 5, RLK_OP_DIFF_BACKWARD = 6 };
 
 /* Workspace bytes an entry point needs (HOST cu_seqlens; 0 on bad input).
  * RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE and RLK_OP_DIFF_DECODE take the decode context
