@@ -48,8 +48,9 @@ size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu, i
 static_assert(sizeof(rlk::FwdParams) + 3 * sizeof(CUtensorMap) + 256 <= 32764,
               "forward kernel parameters exceed the 32 KB launch limit");
 static_assert(sizeof(rlk::MergeParams) <= 4096, "merge parameters");
-static_assert(sizeof(rlk::QCacheParams) <= 4096 && sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) <= 8192,
-              "8-bit cache parameters");
+static_assert(sizeof(rlk::QCacheParams) <= 4096 && sizeof(rlk::QDecodeParams) + 2 * sizeof(CUtensorMap) <= 8192 &&
+                  sizeof(rlk::DDecodeParams) + 3 * sizeof(CUtensorMap) <= 8192,
+              "8-bit cache and differential decode parameters");
 static_assert(sizeof(rlk::AppendParams) <= 4096, "append parameters");
 static_assert(sizeof(rlk_attn_slab) == sizeof(rlk::Slab), "slab layout");
 
@@ -118,7 +119,7 @@ rlk_status device_info(DeviceInfo** out) {
     if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "cudaGetSymbolAddress(merge scratch): %s", cudaGetErrorString(e));
     if ((e = rlk::configure_fwd_kernels()) != cudaSuccess || (e = rlk::configure_decode_kernels()) != cudaSuccess ||
         (e = rlk::configure_merge_kernels()) != cudaSuccess || (e = rlk::configure_bwd_kernels()) != cudaSuccess ||
-        (e = rlk::configure_qdecode_kernels()) != cudaSuccess)
+        (e = rlk::configure_qdecode_kernels()) != cudaSuccess || (e = rlk::configure_ddecode_kernels()) != cudaSuccess)
       return fail(RLK_ERR_CUDA, "kernel set-up on device %d: %s", dev, cudaGetErrorString(e));
     d.ready = true;
   }
@@ -651,8 +652,7 @@ namespace {
 rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const void* k_pool, const void* v_pool,
                              int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                              const int32_t* seqlens, const float* rope_table, int32_t rope_max_pos,
-                             float* out_f32, void* out_bf16, float* lse, cudaStream_t stream,
-                             const float* lambda = nullptr) {
+                             float* out_f32, void* out_bf16, float* lse, cudaStream_t stream) {
   rlk_status st = check_params(params);
   if (st) return st;
   if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
@@ -666,8 +666,8 @@ rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const
       const int64_t o = static_cast<int64_t>(s0) * params->num_q_heads;
       return decode_paged_impl(&rp, adv(q, o * 128, 2), k_pool, v_pool, n_pages, page_size,
                                page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, rope_table,
-                               rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2),
-                               adv(lse, lambda ? 2 * o : o, 4), stream, lambda);
+                               rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, o, 4),
+                               stream);
     });
   const int B = params->kv_block_size;
   if (page_size < 8 || page_size > B || B % page_size)
@@ -728,7 +728,6 @@ rlk_status decode_paged_impl(const rlk_attn_params* params, const void* q, const
   fp->page_size = page_size;
   fp->n_pages = n_pages;
   fp->rope_table = rope_table;
-  fp->lambda = lambda;
   if (!rlk::decode_transposed_supported(*fp)) {
     if ((st = launch_fwd_tiles(fp.get(), tiles, 1, mq, mk, mv, dev, stream))) return st;
     return ok();
@@ -975,7 +974,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
                               int32_t n_pages, int32_t page_size, const int32_t* page_table, int32_t max_pages,
                               const int32_t* seqlens, int32_t split_k, const float* rope_table,
                               int32_t rope_max_pos, float* out_f32, void* out_bf16, float* lse, void* workspace,
-                              size_t workspace_bytes, cudaStream_t stream, const float* lambda = nullptr) {
+                              size_t workspace_bytes, cudaStream_t stream) {
   rlk_status st = check_params(params);
   if (st) return st;
   if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
@@ -991,7 +990,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
       return decode_splitk_impl(&rp, adv(q, o * 128, 2), k_pool, v_pool, n_pages, page_size,
                                 page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, split_k,
                                 rope_table, rope_max_pos, adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2),
-                                adv(lse, lambda ? 2 * o : o, 4), workspace, workspace_bytes, stream, lambda);
+                                adv(lse, o, 4), workspace, workspace_bytes, stream);
     });
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || (out_f32 && !aligned16(out_f32)) ||
       (out_bf16 && !aligned16(out_bf16)) || !aligned16(workspace))
@@ -1017,27 +1016,24 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
         return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: position %d is past the RoPE table (%d positions)", s,
                     seqlens[s] - 1, rope_max_pos);
   }
-  // rows of the state table per block: a query head's, or those of its two maps
-  const int table_rows = lambda ? 2 * params->num_q_heads : params->num_q_heads;
-  const size_t need =
-      rlk_attn_workspace_size(params, lambda ? RLK_OP_DIFF_DECODE : RLK_OP_DECODE_SPLIT, nullptr, seqlens);
+  const size_t need = rlk_attn_workspace_size(params, RLK_OP_DECODE_SPLIT, nullptr, seqlens);
   if (!workspace || workspace_bytes < need)
     return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes, need);
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
   if (split_k == 0) {
-    split_k = choose_split(seqlens, params->num_seqs, params->num_kv_heads, table_rows, B, dev->num_sms);
+    split_k = choose_split(seqlens, params->num_seqs, params->num_kv_heads, params->num_q_heads, B, dev->num_sms);
     // one range per sequence is the single-pass decode, which needs no state table
     if (split_k == 1)
       return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens,
-                               rope_table, rope_max_pos, out_f32, out_bf16, lse, stream, lambda);
+                               rope_table, rope_max_pos, out_f32, out_bf16, lse, stream);
   }
-  // state table: pair (block_base[s] + b) * rows + row; o_b FP32 [pair][128], then lse_b [pair]
+  // state table: pair (block_base[s] + b) * Hq + head; o_b FP32 [pair][128], then lse_b [pair]
   std::vector<int32_t> block_base(params->num_seqs + 1, 0);
   for (int s = 0; s < params->num_seqs; ++s) block_base[s + 1] = block_base[s] + (seqlens[s] + B - 1) / B;
-  const int64_t pairs = static_cast<int64_t>(block_base[params->num_seqs]) * table_rows;
-  bool on_chip = fold_on_chip(params->num_seqs, params->num_kv_heads, table_rows, split_k, dev->num_sms);
+  const int64_t pairs = static_cast<int64_t>(block_base[params->num_seqs]) * params->num_q_heads;
+  bool on_chip = fold_on_chip(params->num_seqs, params->num_kv_heads, params->num_q_heads, split_k, dev->num_sms);
   std::vector<std::pair<int, rlk::FwdTile>> costed;
   if (on_chip) {
     // item r of a pair takes its blocks r, r + k, r + 2k, ...: the pair's
@@ -1097,7 +1093,6 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     fp->cu_k[s] = seqlens[s];
     fp->cu_q[s] = block_base[s];
   }
-  fp->lambda = lambda;
   fp->state_o = static_cast<float*>(workspace);
   fp->state_lse = static_cast<float*>(workspace) + pairs * rlk::kHeadDim;
   fp->rope_table = rope_table;
@@ -1130,7 +1125,7 @@ rlk_status decode_splitk_impl(const rlk_attn_params* params, const void* q, cons
     fp->num_items = fp->num_tiles;
     static_assert(rlk::kUnwritten == 0xFFFFFFFFu, "the table fill is all-ones bytes");
     cudaError_t e = self_fill ? cudaSuccess : cudaMemsetAsync(workspace, 0xFF, state_bytes, stream);
-    const int grid = fp->num_items + fold_ctas(params->num_seqs, table_rows);
+    const int grid = fp->num_items + fold_ctas(params->num_seqs, params->num_q_heads);
     if (e == cudaSuccess) e = rlk::launch_decode_cooperative(*fp, mq, mk, mv, grid, stream);
     if (e == cudaSuccess) return ok();
     if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported)
@@ -1384,6 +1379,37 @@ void plan_qdecode(const int32_t* ctx, int num_seqs, int groups, int split_k, int
   }
 }
 
+// The launch: groups of KV heads taken side by side (qdecode.cu), the most with
+// no more than 1 SM in 64 left over, and CTAs per head of a group.
+struct DecodeGrid {
+  int group, parts;
+};
+DecodeGrid decode_grid(int hkv, int64_t segments, int num_sms) {
+  const int sms = std::min(num_sms, rlk::kQMaxParts);
+  int group = 1;
+  for (int d = 2; d <= hkv && d <= sms; ++d)
+    if (hkv % d == 0 && sms % d <= sms / 64) group = d;
+  return {group, static_cast<int>(std::min<int64_t>(sms / group, segments * (hkv / group)))};
+}
+
+// The counts' nonce, new to every call, stands for their being zero; inside a
+// graph capture, where replays repeat it (and other graphs may use the
+// workspace in between), a fill precedes the launch.
+rlk_status begin_counts(unsigned long long* counts, size_t bytes, uint64_t* nonce, cudaStream_t stream) {
+  *nonce = next_fill_nonce() >> 24;
+  if (*nonce == 0) *nonce = 1;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+    (void)cudaGetLastError();
+    cap = cudaStreamCaptureStatusActive;  // unknown: take the form that is safe in both
+  }
+  if (cap != cudaStreamCaptureStatusNone) {
+    cudaError_t e = cudaMemsetAsync(counts, 0, bytes, stream);
+    if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "decode count fill: %s", cudaGetErrorString(e));
+  }
+  return RLK_OK;
+}
+
 rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCache& cache, const int32_t* seqlens,
                         int32_t split_k, const float* rope_table, int32_t rope_max_pos, float* out_f32,
                         void* out_bf16, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -1445,16 +1471,9 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
   CUtensorMap mk, mv;
   if ((st = make_code_map(&mk, cache.k_pool, cache.n_pages, hkv, cache.page_size))) return st;
   if ((st = make_code_map(&mv, cache.v_pool, cache.n_pages, hkv, cache.page_size))) return st;
-  const int sms = std::min(dev->num_sms, rlk::kQMaxParts);
-  // the most KV heads that can be taken side by side (qdecode.cu) with no more
-  // than 1 SM in 64 left over
-  int group = 1;
-  for (int d = 2; d <= hkv && d <= sms; ++d)
-    if (hkv % d == 0 && sms % d <= sms / 64) group = d;
-  const int parts = static_cast<int>(std::min<int64_t>(sms / group, segments * (hkv / group)));
-  const int grid = parts * group;
-  plan_qdecode(dp.ctx, params->num_seqs, hkv / group, split_k, parts, dp.start);
-  dp.group = group;
+  const DecodeGrid g = decode_grid(hkv, segments, dev->num_sms);
+  plan_qdecode(dp.ctx, params->num_seqs, hkv / g.group, split_k, g.parts, dp.start);
+  dp.group = g.group;
   dp.err = dev->err;
   dp.num_seqs = params->num_seqs;
   dp.hq = hq;
@@ -1475,22 +1494,9 @@ rlk_status qdecode_impl(const rlk_attn_params* params, const void* q, const QCac
     dp.state_o = static_cast<float*>(workspace);
     dp.state_ml = dp.state_o + segments * hq * rlk::kHeadDim;
     dp.counts = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + state_bytes);
-    // the counts' nonce, new to every call, stands for their being zero;
-    // inside a graph capture, where replays repeat it (and other graphs may
-    // use the workspace in between), a fill precedes the launch
-    dp.nonce = next_fill_nonce() >> 24;
-    if (dp.nonce == 0) dp.nonce = 1;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
-      (void)cudaGetLastError();
-      cap = cudaStreamCaptureStatusActive;  // unknown: take the form that is safe in both
-    }
-    if (cap != cudaStreamCaptureStatusNone) {
-      cudaError_t e = cudaMemsetAsync(dp.counts, 0, count_bytes, stream);
-      if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "8-bit decode count fill: %s", cudaGetErrorString(e));
-    }
+    if ((st = begin_counts(dp.counts, count_bytes, &dp.nonce, stream))) return st;
   }
-  cudaError_t e = rlk::launch_qdecode(dp, mk, mv, grid, stream);
+  cudaError_t e = rlk::launch_qdecode(dp, mk, mv, g.parts * g.group, stream);
   if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "8-bit decode launch: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -1700,6 +1706,99 @@ rlk_status diff_prefill_impl(const rlk_attn_params* params, const void* q, const
   return ok();
 }
 
+rlk_status diff_decode_impl(const rlk_attn_params* params, const void* q, const float* lambda, const void* k_pool,
+                            const void* v_pool, int32_t n_pages, int32_t page_size, const int32_t* page_table,
+                            int32_t max_pages, const int32_t* seqlens, int32_t split_k, float* out_f32, void* out_bf16,
+                            float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  rlk_status st = check_diff(params, lambda);
+  if (st) return st;
+  if (!q || !k_pool || !v_pool || !page_table || !seqlens) return fail(RLK_ERR_INVALID_ARGUMENT, "NULL argument");
+  if (!out_f32 && !out_bf16) return fail(RLK_ERR_INVALID_ARGUMENT, "out_f32 and out_bf16 are both NULL");
+  if (split_k < 0 || split_k > rlk::kMaxSplitK)
+    return fail(RLK_ERR_INVALID_ARGUMENT, "split_k %d not in 0..64", split_k);
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out_f32) || !aligned16(out_bf16) ||
+      (split_k != 1 && !aligned16(workspace)))
+    return fail(RLK_ERR_INVALID_ARGUMENT, "tensors must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(page_table)) & 3u)
+    return fail(RLK_ERR_INVALID_ARGUMENT, "lse and page table must be 4-byte aligned");
+  const int hq = params->num_q_heads, hkv = params->num_kv_heads, B = 128;
+  if (hq / hkv > rlk::kDecodeMaxGroup)
+    return fail(RLK_ERR_UNSUPPORTED, "differential decode takes at most %d query heads per KV head",
+                rlk::kDecodeMaxGroup);
+  if (page_size < 8 || page_size > B || B % page_size)
+    return fail(RLK_ERR_UNSUPPORTED, "page_size %d must be >= 8 and divide kv_block_size %d", page_size, B);
+  if (n_pages < 1 || max_pages < 1) return fail(RLK_ERR_INVALID_ARGUMENT, "n_pages / max_pages < 1");
+  if ((static_cast<int64_t>(n_pages) + 1) * page_size > INT32_MAX)
+    return fail(RLK_ERR_UNSUPPORTED, "page pool too large for 32-bit token coordinates");
+  if (params->num_seqs > rlk::kQMaxSeqs)
+    // each range reuses the workspace from its start (the ranges run in order
+    // on the stream, and a range needs no more than the whole call)
+    return over_ranges(params->num_seqs, [&](int s0, int s1) {
+      const rlk_attn_params rp = range_params(params, s0, s1);
+      const int64_t o = static_cast<int64_t>(s0) * hq;
+      return diff_decode_impl(&rp, adv(q, o * 128, 2), lambda, k_pool, v_pool, n_pages, page_size,
+                              page_table + static_cast<int64_t>(s0) * max_pages, max_pages, seqlens + s0, split_k,
+                              adv(out_f32, o * 128, 4), adv(out_bf16, o * 128, 2), adv(lse, 2 * o, 4), workspace,
+                              workspace_bytes, stream);
+    }, rlk::kQMaxSeqs);
+  rlk::DDecodeParams dp;
+  std::memset(&dp, 0, sizeof(dp));
+  int64_t blocks = 0, segments = 0;
+  for (int s = 0; s < params->num_seqs; ++s) {
+    if (seqlens[s] < 1 || static_cast<int64_t>(seqlens[s]) > static_cast<int64_t>(max_pages) * page_size ||
+        seqlens[s] > INT32_MAX - 65536)
+      return fail(RLK_ERR_INVALID_ARGUMENT, "sequence %d: context length %d not in 1..max_pages*page_size", s,
+                  seqlens[s]);
+    dp.ctx[s] = seqlens[s];
+    blocks += (static_cast<int64_t>(seqlens[s]) + B - 1) / B * hkv;
+    segments += qdecode_segments(seqlens + s, 1);
+    if (4 * blocks + static_cast<int64_t>(rlk::kPairCost) * hkv * params->num_seqs > INT32_MAX - 1024 ||
+        segments * 2 * hq > INT32_MAX)
+      return fail(RLK_ERR_UNSUPPORTED,
+                  "more than 2^29 (block, KV head) or 2^30 (segment, query head) pairs in one launch");
+    dp.seg0[s + 1] = static_cast<int32_t>(segments);
+  }
+  const size_t state_bytes = qdecode_state_bytes(segments, 2 * hq);
+  const size_t count_bytes = static_cast<size_t>(params->num_seqs) * hkv * sizeof(uint64_t);
+  if (split_k != 1 && (!workspace || workspace_bytes < state_bytes + count_bytes))
+    return fail(RLK_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", workspace_bytes,
+                state_bytes + count_bytes);
+  if (g_dry_run) return ok();
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev))) return st;
+  const uint64_t tokens = static_cast<uint64_t>(n_pages) * page_size;
+  const uint32_t box = std::min<uint32_t>(page_size, rlk::kQBoxRows);
+  CUtensorMap mq, mk, mv;
+  if ((st = make_map(&mq, q, hq, params->num_seqs, 1, 1))) return st;
+  if ((st = make_map(&mk, k_pool, hkv, tokens, 1, box))) return st;
+  if ((st = make_map(&mv, v_pool, hkv, tokens, 1, box))) return st;
+  const DecodeGrid g = decode_grid(hkv, segments, dev->num_sms);
+  plan_qdecode(dp.ctx, params->num_seqs, hkv / g.group, split_k, g.parts, dp.start);
+  dp.group = g.group;
+  dp.err = dev->err;
+  dp.num_seqs = params->num_seqs;
+  dp.hq = hq;
+  dp.hkv = hkv;
+  dp.scale_log2 = scale_log2(params);
+  dp.lambda = lambda;
+  dp.page_table = page_table;
+  dp.n_pages = n_pages;
+  dp.page_size = page_size;
+  dp.max_pages = max_pages;
+  dp.out_f32 = out_f32;
+  dp.out_bf16 = static_cast<uint16_t*>(out_bf16);
+  dp.lse = lse;
+  if (split_k != 1) {
+    dp.state_o = static_cast<float*>(workspace);
+    dp.state_ml = dp.state_o + segments * 2 * hq * rlk::kHeadDim;
+    dp.counts = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + state_bytes);
+    if ((st = begin_counts(dp.counts, count_bytes, &dp.nonce, stream))) return st;
+  }
+  cudaError_t e = rlk::launch_ddecode(dp, mq, mk, mv, g.parts * g.group, stream);
+  if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "differential decode launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -1720,18 +1819,8 @@ rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, co
                                 void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
                                 rlk_stream_t stream) {
   return guarded([&]() -> rlk_status {
-    rlk_status st = check_diff(params, lambda);
-    if (st) return st;
-    if (params->num_q_heads / params->num_kv_heads > rlk::kDecodeMaxGroup)
-      return fail(RLK_ERR_UNSUPPORTED, "differential decode takes at most %d query heads per KV head",
-                  rlk::kDecodeMaxGroup);
-    if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(page_table)) & 3u)
-      return fail(RLK_ERR_INVALID_ARGUMENT, "lse and page table must be 4-byte aligned");
-    if (split_k == 1)  // no state table, no workspace
-      return decode_paged_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, nullptr,
-                               0, out_f32, out_bf16, lse, stream, lambda);
-    return decode_splitk_impl(params, q, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens, split_k,
-                              nullptr, 0, out_f32, out_bf16, lse, workspace, workspace_bytes, stream, lambda);
+    return diff_decode_impl(params, q, lambda, k_pool, v_pool, n_pages, page_size, page_table, max_pages, seqlens,
+                            split_k, out_f32, out_bf16, lse, workspace, workspace_bytes, stream);
   });
 }
 
@@ -1807,21 +1896,22 @@ extern "C" {
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op, const int32_t* cu_seqlens_q,
                                const int32_t* cu_seqlens_k) {
   if (check_params(params) != RLK_OK) return 0;
-  if (op == RLK_OP_DECODE_SPLIT || op == RLK_OP_DIFF_DECODE) {
+  if (op == RLK_OP_DECODE_SPLIT) {
     if (!cu_seqlens_k) return 0;
     int64_t blocks = 0;
     for (int s = 0; s < params->num_seqs; ++s) {
       if (cu_seqlens_k[s] < 1) return 0;
       blocks += (cu_seqlens_k[s] + params->kv_block_size - 1) / params->kv_block_size;
     }
-    const int64_t pairs = blocks * params->num_q_heads * (op == RLK_OP_DIFF_DECODE ? 2 : 1);
+    const int64_t pairs = blocks * params->num_q_heads;
     return split_table_bytes(pairs) + split_flag_bytes(params->num_seqs, params->num_kv_heads);
   }
-  if (op == RLK_OP_DECODE_QCACHE) {
+  if (op == RLK_OP_DECODE_QCACHE || op == RLK_OP_DIFF_DECODE) {
     if (!cu_seqlens_k) return 0;
     for (int s = 0; s < params->num_seqs; ++s)
       if (cu_seqlens_k[s] < 1) return 0;
-    return qdecode_state_bytes(qdecode_segments(cu_seqlens_k, params->num_seqs), params->num_q_heads) +
+    const int rows = params->num_q_heads * (op == RLK_OP_DIFF_DECODE ? 2 : 1);
+    return qdecode_state_bytes(qdecode_segments(cu_seqlens_k, params->num_seqs), rows) +
            static_cast<size_t>(params->num_seqs) * params->num_kv_heads * sizeof(uint64_t);
   }
   if (op == RLK_OP_MERGE) {

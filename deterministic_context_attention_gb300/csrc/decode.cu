@@ -48,10 +48,7 @@ namespace {
 constexpr int kDThreads = 512;
 constexpr int kDN = 16;  // MMA N: the group's query heads, padded with zero rows
 
-// MR: the operand rows the softmax scratch holds (16 for differential
-// attention over more than 4 query heads per KV head).
-template <int MR>
-struct DecLayoutT {
+struct DecLayout {
   static constexpr int B = 128;
   static constexpr int kSK = 3, kSV = 2;  // K and V rings
   static constexpr int kPS = 2;           // P^T operand slots
@@ -65,14 +62,14 @@ struct DecLayoutT {
   static constexpr int kKOff = kQOff + kTBytes;
   static constexpr int kVOff = kKOff + kSK * kKVBytes;
   static constexpr int kPOff = kVOff + kSV * kKVBytes;    // [slot][hi, lo] tiles
-  // per softmax group: block maxima float [2][4][MR] and partial sums float
-  // [2][4][MR][32], double-buffered by block
-  static constexpr int kRedBytes = 2 * 4 * MR * 4;
-  static constexpr int kPartBytes = 2 * 4 * MR * 32 * 4;
+  // per softmax group: block maxima float [2][4][kDecodeMaxGroup] and
+  // partial sums float [2][4][kDecodeMaxGroup][32], double-buffered by block
+  static constexpr int kRedBytes = 2 * 4 * kDecodeMaxGroup * 4;
+  static constexpr int kPartBytes = 2 * 4 * kDecodeMaxGroup * 32 * 4;
   static constexpr int kRedOff = kPOff + kPS * 2 * kTBytes;
   static constexpr int kPartOff = kRedOff + 2 * kRedBytes;
-  static constexpr int kStatsOff = kPartOff + 2 * kPartBytes;  // float2 [kSR][MR]
-  static constexpr int kBarOff = kStatsOff + kSR * MR * 8;
+  static constexpr int kStatsOff = kPartOff + 2 * kPartBytes;  // float2 [kSR][kDecodeMaxGroup]
+  static constexpr int kBarOff = kStatsOff + kSR * kDecodeMaxGroup * 8;
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + kSK, kVFull = kKEmpty + kSK,
                        kVEmpty = kVFull + kSV, kSFull = kVEmpty + kSV, kSEmpty = kSFull + kSS,
                        kPFull = kSEmpty + kSS, kPEmpty = kPFull + kPS, kOFull = kPEmpty + kPS,
@@ -86,8 +83,7 @@ struct DecLayoutT {
   static constexpr int kTotal = kPageOff + 2 * kPageWin * 4;
   static constexpr int kAlloc = kTotal + 1024;
 };
-using DecLayout = DecLayoutT<kDecodeMaxGroup>;
-static_assert(DecLayoutT<16>::kAlloc <= 232448, "decode shared memory");
+static_assert(DecLayout::kAlloc <= 232448, "decode shared memory");
 static_assert(DecLayout::kPageWin == 1 << 9, "the producers index the page window with shifts by 9");
 static_assert(DecLayout::kKOff % 1024 == 0 && DecLayout::kVOff % 1024 == 0 && DecLayout::kPOff % 1024 == 0,
               "128-byte-swizzled tiles start on 1024-byte boundaries");
@@ -146,17 +142,16 @@ constexpr int kFillThreads = 384;
 __device__ __forceinline__ void fill_item_slots(const FwdParams& p, const DecItem& di, int G, int t) {
   const int64_t blk0 = p.cu_q[di.seq] + di.b0;
   const int per = G * (kHeadDim / 4);  // 16-byte pieces of one block's states
-  const int all = p.hkv * G;           // rows of one block over all KV heads
   const float u = __uint_as_float(kUnwritten);
   const float4 u4 = make_float4(u, u, u, u);
   for (int i = t; i < di.nb * per; i += kFillThreads) {
     const int j = i / per;
-    reinterpret_cast<float4*>(p.state_o + ((blk0 + static_cast<int64_t>(j) * di.stride) * all + di.g * G) *
+    reinterpret_cast<float4*>(p.state_o + ((blk0 + static_cast<int64_t>(j) * di.stride) * p.hq + di.g * G) *
                                               kHeadDim)[i - j * per] = u4;
   }
   for (int i = t; i < di.nb * G; i += kFillThreads) {
     const int j = i / G;
-    p.state_lse[(blk0 + static_cast<int64_t>(j) * di.stride) * all + di.g * G + (i - j * G)] = u;
+    p.state_lse[(blk0 + static_cast<int64_t>(j) * di.stride) * p.hq + di.g * G + (i - j * G)] = u;
   }
 }
 
@@ -185,19 +180,18 @@ __device__ __forceinline__ float warp_max(float v) {
 // another).  When the producers fill the table themselves (fill_flag set),
 // the chain first waits until every item of the pair has published its
 // flag: before that, an item's slots may still hold an earlier call's
-// states.  Returns false on a timeout (reported) or an abort; the folded O
-// (of the lane's dimensions) and lse otherwise.
-__device__ __forceinline__ bool fold_row_on_chip(const FwdParams& p, int G, int seq, int g, int q, int lane,
-                                                 volatile int* abort, float4& O, float& Lrun) {
+// states.  Returns false on a timeout (reported) or an abort.
+__device__ __noinline__ bool fold_chain_on_chip(const FwdParams& p, int seq, int g, int q, int lane,
+                                                volatile int* abort) {
   constexpr int C = 8;
-  const int all = p.hkv * G;
+  const int G = p.group;
   const int nbp = (p.cu_k[seq] + DecLayout::B - 1) / DecLayout::B;
   const int64_t base = p.cu_q[seq];
   // lane i: the lse of block c0 + i; every lane: dimensions 4 lane .. of the
   // chunk's blocks (past the chunk: its last block, a valid value)
-  auto lse_src = [&](int c0, int nc) { return p.state_lse + (base + c0 + min(lane, nc - 1)) * all + g * G + q; };
+  auto lse_src = [&](int c0, int nc) { return p.state_lse + (base + c0 + min(lane, nc - 1)) * p.hq + g * G + q; };
   auto o_src = [&](int c0, int nc, int i) {
-    return p.state_o + ((base + c0 + min(i, nc - 1)) * all + g * G + q) * kHeadDim + 4 * lane;
+    return p.state_o + ((base + c0 + min(i, nc - 1)) * p.hq + g * G + q) * kHeadDim + 4 * lane;
   };
   auto issue = [&](int c0, float& lsl, float4 (&v)[C]) {
     const int nc = min(C, nbp - c0);
@@ -253,8 +247,8 @@ __device__ __forceinline__ bool fold_row_on_chip(const FwdParams& p, int G, int 
     }
     __syncwarp();
   }
-  O = make_float4(0.f, 0.f, 0.f, 0.f);
-  Lrun = -INFINITY;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  float Lrun = -INFINITY;
   float lsl, lsn = 0.f;
   float4 v[C], vn[C];
   issue(0, lsl, v);
@@ -284,69 +278,27 @@ __device__ __forceinline__ bool fold_row_on_chip(const FwdParams& p, int G, int 
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = vn[i];
   }
-  return true;
-}
-
-// Query head q's row of the output, dimensions 4 lane .. 4 lane + 3.
-__device__ __forceinline__ void fold_write(const FwdParams& p, int64_t row, int lane, const float4& O) {
+  const int64_t row = static_cast<int64_t>(seq) * p.hq + g * G + q;
   if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + row * kHeadDim + 4 * lane) = O;
   if (p.out_bf16) {
     const uint32_t w0 = pack_bf16x2(O.x, O.y), w1 = pack_bf16x2(O.z, O.w);
     *reinterpret_cast<uint2*>(p.out_bf16 + row * kHeadDim + 4 * lane) = make_uint2(w0, w1);
   }
-}
-
-__device__ __noinline__ bool fold_chain_on_chip(const FwdParams& p, int seq, int g, int q, int lane,
-                                                volatile int* abort) {
-  float4 O;
-  float Lrun;
-  if (!fold_row_on_chip(p, p.group, seq, g, q, lane, abort, O, Lrun)) return false;
-  const int64_t row = static_cast<int64_t>(seq) * p.hq + g * p.group + q;
-  fold_write(p, row, lane, O);
   if (lane == 0 && p.lse) p.lse[row] = Lrun;
   return true;
 }
 
-// Differential attention: row q = 2 i + m is map m of the group's query head
-// i, and the two warps of a head (neighbours in a CTA) meet at a barrier, the
-// second map's O in shared memory.  Both arrive whatever became of their
-// folds, so neither waits for long.
-__device__ __noinline__ void fold_pair_on_chip(const FwdParams& p, int seq, int g, int q, int lane, int warp,
-                                               float4 (*xch)[33], volatile int* abort) {
-  float4 O;
-  float Lrun;
-  const bool done = fold_row_on_chip(p, 2 * p.group, seq, g, q, lane, abort, O, Lrun);
-  if (q & 1) {
-    xch[warp >> 1][lane] = O;
-    if (lane == 0) xch[warp >> 1][32].x = done ? 1.0f : 0.0f;
-  }
-  named_bar_sync(1 + (warp >> 1), 64);
-  if (!done) return;
-  const int64_t row = static_cast<int64_t>(seq) * p.hq + g * p.group + (q >> 1);
-  if (lane == 0 && p.lse) p.lse[2 * row + (q & 1)] = Lrun;
-  if ((q & 1) || xch[warp >> 1][32].x == 0.0f) return;
-  const float nl = -__ldg(p.lambda + g * p.group + (q >> 1));
-  const float4 x = xch[warp >> 1][lane];
-  O = make_float4(__fmaf_rn(nl, x.x, O.x), __fmaf_rn(nl, x.y, O.y), __fmaf_rn(nl, x.z, O.z), __fmaf_rn(nl, x.w, O.w));
-  fold_write(p, row, lane, O);
-}
-
-// MG: the operand rows -- the group's query heads -- rounded up to 1, 2, 4 or 8
-// (rows at or past their number are skipped at run time).
-// DIFF: differential attention.  Operand row 2 i + m holds map m of query head
-// i: its 64 columns, and zeros in the other map's, so that the products, the
-// softmax and the fold run as for 2 G plain heads (adding exact zeros changes
-// no bit of S) and the cache is read once for both maps; up to 16 rows.
+// MG: the group's query heads rounded up to 1, 2, 4 or 8 (heads at or past
+// the group size are skipped at run time).
 // FOLD: the instance the split decode with the fold on chip launches (its
 // CTAs past the items fold); the others never carry the fold code.
-template <int MG, bool FOLD, bool DIFF>
+template <int MG, bool FOLD>
 __global__ void __launch_bounds__(kDThreads, 1)
     rlk_decode_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-  using L = DecLayoutT<(MG > kDecodeMaxGroup ? 16 : kDecodeMaxGroup)>;
-  constexpr int MR = MG > kDecodeMaxGroup ? 16 : kDecodeMaxGroup;
+  using L = DecLayout;
   constexpr int B = L::B, SK = L::kSK, SV = L::kSV, PS = L::kPS, SS = L::kSS, OS = L::kOS, SR = L::kSR;
-  static_assert(MG <= (DIFF ? 16 : kDecodeMaxGroup) && PS == 2, "decode layout");
+  static_assert(MG <= kDecodeMaxGroup && PS == 2, "decode layout");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -356,7 +308,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int G = DIFF ? 2 * p.group : p.group;  // operand rows
+  const int G = p.group;
 
   // operand rows at or past G are never written: they must read as zero
   for (int i = tid; i < L::kTBytes / 16; i += kDThreads)
@@ -421,10 +373,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     const int per_seq = p.hkv * G;
     if (p.split_stride > 0 && chain < p.fold_seqs * per_seq) {
       const int seq = chain / per_seq, g = (chain % per_seq) / G, q = chain % G;
-      if (DIFF)
-        fold_pair_on_chip(p, seq, g, q, lane, warp, reinterpret_cast<float4(*)[33]>(smem + L::kKOff), abort);
-      else
-        fold_chain_on_chip(p, seq, g, q, lane, abort);
+      fold_chain_on_chip(p, seq, g, q, lane, abort);
     }
   } else if (warp == 12 || warp == 13) {
     // ------------------------------------------------------------ producers
@@ -453,12 +402,8 @@ __global__ void __launch_bounds__(kDThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         if (lane == 0) {
           // the group's query rows 0..G-1 of the 16-row operand tile
-          mbar_arrive_expect_tx(&bars[L::kQFull], p.group * kHeadDim * 2);
-          for (int i = 0; DIFF && i < p.group; ++i) {  // map 1 in row 2 i, map 2 in row 2 i + 1
-            tma_load_3d(q_tile + 2 * i * 128, &tm_q, &bars[L::kQFull], 0, g * p.group + i, seq);
-            tma_load_3d(q_tile + L::kTHalf + (2 * i + 1) * 128, &tm_q, &bars[L::kQFull], 64, g * p.group + i, seq);
-          }
-          for (int i = 0; !DIFF && i < G; ++i) {
+          mbar_arrive_expect_tx(&bars[L::kQFull], G * kHeadDim * 2);
+          for (int i = 0; i < G; ++i) {
             tma_load_3d(q_tile + i * 128, &tm_q, &bars[L::kQFull], 0, g * G + i, seq);
             tma_load_3d(q_tile + L::kTHalf + i * 128, &tm_q, &bars[L::kQFull], 64, g * G + i, seq);
           }
@@ -527,7 +472,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
       const DecItem di = dec_item(p, item);
       const int kv_len = di.kv_len, nb = di.nb;
       // with RoPE the correction warps hand over the rotated rows
-      bool ok = mbar_wait(&bars[!DIFF && p.rope_table ? L::kQRope : L::kQFull], q_it & 1, abort, p.err, 0x601);
+      bool ok = mbar_wait(&bars[p.rope_table ? L::kQRope : L::kQFull], q_it & 1, abort, p.err, 0x601);
       if (!__all_sync(0xffffffffu, ok)) break;
       ++q_it;
       const uint32_t kb = k_it, sb = s_it;
@@ -732,7 +677,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
           if (lane == 0) {
             float lse_b, rcp;
             block_stats(mc[q], a, lse_b, rcp);
-            stats[sslot * MR + q] = make_float2(lse_b, rcp);
+            stats[sslot * kDecodeMaxGroup + q] = make_float2(lse_b, rcp);
           }
         }
         mbar_arrive(&bars[L::kStatsFull + sslot]);
@@ -751,7 +696,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
       const DecItem di = dec_item(p, item);
       const int seq = di.seq, g = di.g, nb = di.nb;
       const bool split = p.state_o != nullptr;
-      if (!DIFF && p.rope_table) {
+      if (p.rope_table) {
         // RoPE of the query rows at position kv_len - 1, in place: thread t
         // takes pairs 4u .. 4u+3 (u = t mod 16) of row t / 16; the pair's
         // second element sits at the same offset of the second half
@@ -821,7 +766,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
         // fold coefficients of query head `lane` (overlap the TMEM load)
         float lb = -INFINITY, rc = 0.0f, al = 0.0f, be = 0.0f, Lp = 0.0f;
         if (lane < G) {
-          const float2 st = stats[sslot * MR + lane];
+          const float2 st = stats[sslot * kDecodeMaxGroup + lane];
           lb = st.x;
           rc = st.y;
           if (j > 0 && !split) fold_coeffs(Lrun, lb, Lp, al, be);
@@ -832,7 +777,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
         // o_b = PV * (1/l); O = fma(o_b, beta, O * alpha), or (split) the
         // block state written out
         const int64_t blk = p.cu_q[seq] + di.b0 + j * di.stride;  // state-table block
-        const int64_t pair_b = blk * (p.hkv * G) + g * G;
+        const int64_t pair_b = blk * p.hq + g * G;
 #pragma unroll
         for (int q = 0; q < MG; ++q) {
           const float rq = __shfl_sync(0xffffffffu, rc, q);
@@ -862,23 +807,14 @@ __global__ void __launch_bounds__(kDThreads, 1)
       if (split) continue;
       // epilogue: O and L are final
 #pragma unroll
-      for (int q = 0; DIFF && q < MG; q += 2) {
-        if (q < G) {
-          const int64_t row = static_cast<int64_t>(seq) * p.hq + g * p.group + (q >> 1);
-          const float o = __fmaf_rn(-__ldg(p.lambda + g * p.group + (q >> 1)), O[q + 1], O[q]);
-          if (p.out_f32) p.out_f32[row * kHeadDim + d] = o;
-          if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(o);
-        }
-      }
-#pragma unroll
-      for (int q = 0; !DIFF && q < MG; ++q) {
+      for (int q = 0; q < MG; ++q) {
         if (q < G) {
           const int64_t row = static_cast<int64_t>(seq) * p.hq + g * G + q;
           if (p.out_f32) p.out_f32[row * kHeadDim + d] = O[q];
           if (p.out_bf16) p.out_bf16[row * kHeadDim + d] = f32_to_bf16_rn(O[q]);
         }
       }
-      if (warp == 0 && lane < G && p.lse) p.lse[(static_cast<int64_t>(seq) * p.hkv + g) * G + lane] = Lrun;
+      if (warp == 0 && lane < G && p.lse) p.lse[static_cast<int64_t>(seq) * p.hq + g * G + lane] = Lrun;
     }
   }
 
@@ -897,23 +833,23 @@ __global__ void __launch_bounds__(kDThreads, 1)
   }
 }
 
-template <int MG, bool DIFF>
+template <int MG>
 cudaError_t launch_decode_t(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             int grid, cudaStream_t stream) {
-  rlk_decode_kernel<MG, false, DIFF><<<grid, kDThreads, DecLayoutT<(MG > 8 ? 16 : 8)>::kAlloc, stream>>>(p, tq, tk, tv);
+  rlk_decode_kernel<MG, false><<<grid, kDThreads, DecLayout::kAlloc, stream>>>(p, tq, tk, tv);
   return cudaGetLastError();
 }
 
 // The split decode with the fold on chip: its fold warps wait for states
 // that other CTAs of the launch publish, so every CTA must be resident at
 // once -- a cooperative launch guarantees it (or fails).
-template <int MG, bool DIFF>
+template <int MG>
 cudaError_t launch_decode_coop_t(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
   void* args[] = {const_cast<FwdParams*>(&p), const_cast<CUtensorMap*>(&tq), const_cast<CUtensorMap*>(&tk),
                   const_cast<CUtensorMap*>(&tv)};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(&rlk_decode_kernel<MG, true, DIFF>), dim3(grid),
-                                     dim3(kDThreads), args, DecLayoutT<(MG > 8 ? 16 : 8)>::kAlloc, stream);
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(&rlk_decode_kernel<MG, true>), dim3(grid),
+                                     dim3(kDThreads), args, DecLayout::kAlloc, stream);
 }
 
 // Split decode, second step: the canonical fold of one (sequence, query head)
@@ -939,16 +875,11 @@ struct DecFoldParams {
   float* out_f32;
   uint16_t* out_bf16;
   float* lse;
-  const float* lambda;
   int32_t num_seqs, hq;
   int32_t block_base[kMaxSeqs + 1];  // first state-table block of each sequence
   int32_t ctx[kMaxSeqs + 1];         // context length of each sequence
 };
 
-// DIFF: the states of query head h's maps are rows 2 h and 2 h + 1 of a block;
-// the second map's chunks go through the ring first, then the first one's, and
-// out = O1 - lambda O2.
-template <bool DIFF>
 __global__ void __launch_bounds__(kDmThreads) rlk_decode_merge_kernel(const __grid_constant__ DecFoldParams p) {
   extern __shared__ __align__(16) uint8_t dsm[];
   const int t = threadIdx.x;
@@ -958,14 +889,11 @@ __global__ void __launch_bounds__(kDmThreads) rlk_decode_merge_kernel(const __gr
     const int h = static_cast<int>(w - static_cast<int64_t>(seq) * p.hq);
     const int nb = (p.ctx[seq] + DecLayout::B - 1) / DecLayout::B;
     const int nchunks = (nb + kDmChunk - 1) / kDmChunk;
-    const int rows = DIFF ? 2 * p.hq : p.hq;  // of one block
-    const int nring = DIFF ? 2 * nchunks : nchunks;
-    // chunk ci of the ring -> stage ci % kDmStages; a warp copies one block's 512 B of o
-    auto issue = [&](int ci) {
-      if (ci < nring) {
-        const int c = DIFF && ci >= nchunks ? ci - nchunks : ci;
-        const int64_t pair0 = static_cast<int64_t>(p.block_base[seq]) * rows + (DIFF ? 2 * h + (ci < nchunks) : h);
-        uint8_t* st = dsm + (ci % kDmStages) * kDmStageBytes;
+    const int64_t pair0 = static_cast<int64_t>(p.block_base[seq]) * p.hq + h;
+    // chunk c -> stage c % kDmStages; a warp copies one block's 512 B of o
+    auto issue = [&](int c) {
+      if (c < nchunks) {
+        uint8_t* st = dsm + (c % kDmStages) * kDmStageBytes;
         float* so = reinterpret_cast<float*>(st);
         float* sl = reinterpret_cast<float*>(st + kDmChunk * kHeadDim * 4);
 #pragma unroll
@@ -974,12 +902,12 @@ __global__ void __launch_bounds__(kDmThreads) rlk_decode_merge_kernel(const __gr
           const int j = i >> 5, seg = i & 31;
           const int b = c * kDmChunk + j;
           if (b < nb) {
-            const int64_t pr = pair0 + static_cast<int64_t>(b) * rows;
+            const int64_t pr = pair0 + static_cast<int64_t>(b) * p.hq;
             cp_async16(so + j * kHeadDim + seg * 4, p.state_o + pr * kHeadDim + seg * 4);
           }
         }
         if (t < kDmChunk && c * kDmChunk + t < nb) {
-          const int64_t pr = pair0 + static_cast<int64_t>(c * kDmChunk + t) * rows;
+          const int64_t pr = pair0 + static_cast<int64_t>(c * kDmChunk + t) * p.hq;
           cp_async4(sl + t, p.state_lse + pr);
         }
       }
@@ -988,17 +916,11 @@ __global__ void __launch_bounds__(kDmThreads) rlk_decode_merge_kernel(const __gr
 #pragma unroll
     for (int c = 0; c < kDmStages - 1; ++c) issue(c);
     float O = 0.f, L = -INFINITY;
-    float O2 = 0.f, L2 = 0.f;  // DIFF: the second map's
-    for (int ci = 0; ci < nring; ++ci) {
-      issue(ci + kDmStages - 1);
+    for (int c = 0; c < nchunks; ++c) {
+      issue(c + kDmStages - 1);
       cp_async_wait<kDmStages - 1>();
       __syncthreads();
-      const int c = DIFF && ci >= nchunks ? ci - nchunks : ci;
-      if (DIFF && ci == nchunks) {
-        O2 = O;
-        L2 = L;
-      }
-      const uint8_t* st = dsm + (ci % kDmStages) * kDmStageBytes;
+      const uint8_t* st = dsm + (c % kDmStages) * kDmStageBytes;
       const float* so = reinterpret_cast<const float*>(st);
       const float* sl = reinterpret_cast<const float*>(st + kDmChunk * kHeadDim * 4);
       const int jn = min(kDmChunk, nb - c * kDmChunk);
@@ -1026,13 +948,9 @@ __global__ void __launch_bounds__(kDmThreads) rlk_decode_merge_kernel(const __gr
     }
     cp_async_wait<0>();
     const int64_t row = static_cast<int64_t>(seq) * p.hq + h;
-    if (DIFF) O = __fmaf_rn(-__ldg(p.lambda + h), O2, O);
     if (p.out_f32) p.out_f32[row * kHeadDim + t] = O;
     if (p.out_bf16) p.out_bf16[row * kHeadDim + t] = f32_to_bf16_rn(O);
-    if (p.lse && t == 0) {
-      p.lse[DIFF ? 2 * row : row] = L;
-      if (DIFF) p.lse[2 * row + 1] = L2;
-    }
+    if (p.lse && t == 0) p.lse[row] = L;
   }
 }
 
@@ -1043,28 +961,22 @@ bool decode_transposed_supported(const FwdParams& p) {
          DecLayout::kPageWin % (DecLayout::B / p.page_size) == 0;
 }
 
-template <int MG, bool DIFF>
+template <int MG>
 cudaError_t configure_decode_mg() {
-  constexpr int kBytes = DecLayoutT<(MG > 8 ? 16 : 8)>::kAlloc;
-  cudaError_t e = cudaFuncSetAttribute(rlk_decode_kernel<MG, false, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kBytes);
+  cudaError_t e = cudaFuncSetAttribute(rlk_decode_kernel<MG, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       DecLayout::kAlloc);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(rlk_decode_kernel<MG, true, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  return cudaFuncSetAttribute(rlk_decode_kernel<MG, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              DecLayout::kAlloc);
 }
 
 cudaError_t configure_decode_kernels() {
   cudaError_t e;
-  if ((e = configure_decode_mg<1, false>())) return e;
-  if ((e = configure_decode_mg<2, false>())) return e;
-  if ((e = configure_decode_mg<4, false>())) return e;
-  if ((e = configure_decode_mg<8, false>())) return e;
-  if ((e = configure_decode_mg<2, true>())) return e;
-  if ((e = configure_decode_mg<4, true>())) return e;
-  if ((e = configure_decode_mg<8, true>())) return e;
-  if ((e = configure_decode_mg<16, true>())) return e;
-  if ((e = cudaFuncSetAttribute(rlk_decode_merge_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDmSmem)))
-    return e;
-  return cudaFuncSetAttribute(rlk_decode_merge_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDmSmem);
+  if ((e = configure_decode_mg<1>())) return e;
+  if ((e = configure_decode_mg<2>())) return e;
+  if ((e = configure_decode_mg<4>())) return e;
+  if ((e = configure_decode_mg<8>())) return e;
+  return cudaFuncSetAttribute(rlk_decode_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDmSmem);
 }
 
 cudaError_t launch_decode_merge(const FwdParams& p, int num_sms, cudaStream_t stream) {
@@ -1074,7 +986,6 @@ cudaError_t launch_decode_merge(const FwdParams& p, int num_sms, cudaStream_t st
   f.out_f32 = p.out_f32;
   f.out_bf16 = p.out_bf16;
   f.lse = p.lse;
-  f.lambda = p.lambda;
   f.num_seqs = p.num_tiles;  // the caller passes the sequence count here
   f.hq = p.hq;
   for (int s = 0; s <= kMaxSeqs; ++s) {
@@ -1083,36 +994,24 @@ cudaError_t launch_decode_merge(const FwdParams& p, int num_sms, cudaStream_t st
   }
   const int64_t pairs = static_cast<int64_t>(f.num_seqs) * f.hq;
   const int64_t blocks = std::min<int64_t>(std::max<int64_t>(pairs, 1), static_cast<int64_t>(num_sms) * 3);
-  (p.lambda ? rlk_decode_merge_kernel<true> : rlk_decode_merge_kernel<false>)<<<static_cast<int>(blocks), kDmThreads, kDmSmem, stream>>>(f);
+  rlk_decode_merge_kernel<<<static_cast<int>(blocks), kDmThreads, kDmSmem, stream>>>(f);
   return cudaGetLastError();
 }
 
 cudaError_t launch_decode_cooperative(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                                       const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  if (p.lambda) {
-    if (p.group <= 1) return launch_decode_coop_t<2, true>(p, tq, tk, tv, grid, stream);
-    if (p.group <= 2) return launch_decode_coop_t<4, true>(p, tq, tk, tv, grid, stream);
-    if (p.group <= 4) return launch_decode_coop_t<8, true>(p, tq, tk, tv, grid, stream);
-    return launch_decode_coop_t<16, true>(p, tq, tk, tv, grid, stream);
-  }
-  if (p.group <= 1) return launch_decode_coop_t<1, false>(p, tq, tk, tv, grid, stream);
-  if (p.group <= 2) return launch_decode_coop_t<2, false>(p, tq, tk, tv, grid, stream);
-  if (p.group <= 4) return launch_decode_coop_t<4, false>(p, tq, tk, tv, grid, stream);
-  return launch_decode_coop_t<8, false>(p, tq, tk, tv, grid, stream);
+  if (p.group <= 1) return launch_decode_coop_t<1>(p, tq, tk, tv, grid, stream);
+  if (p.group <= 2) return launch_decode_coop_t<2>(p, tq, tk, tv, grid, stream);
+  if (p.group <= 4) return launch_decode_coop_t<4>(p, tq, tk, tv, grid, stream);
+  return launch_decode_coop_t<8>(p, tq, tk, tv, grid, stream);
 }
 
 cudaError_t launch_decode(const FwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           int grid, cudaStream_t stream) {
-  if (p.lambda) {
-    if (p.group <= 1) return launch_decode_t<2, true>(p, tq, tk, tv, grid, stream);
-    if (p.group <= 2) return launch_decode_t<4, true>(p, tq, tk, tv, grid, stream);
-    if (p.group <= 4) return launch_decode_t<8, true>(p, tq, tk, tv, grid, stream);
-    return launch_decode_t<16, true>(p, tq, tk, tv, grid, stream);
-  }
-  if (p.group <= 1) return launch_decode_t<1, false>(p, tq, tk, tv, grid, stream);
-  if (p.group <= 2) return launch_decode_t<2, false>(p, tq, tk, tv, grid, stream);
-  if (p.group <= 4) return launch_decode_t<4, false>(p, tq, tk, tv, grid, stream);
-  return launch_decode_t<8, false>(p, tq, tk, tv, grid, stream);
+  if (p.group <= 1) return launch_decode_t<1>(p, tq, tk, tv, grid, stream);
+  if (p.group <= 2) return launch_decode_t<2>(p, tq, tk, tv, grid, stream);
+  if (p.group <= 4) return launch_decode_t<4>(p, tq, tk, tv, grid, stream);
+  return launch_decode_t<8>(p, tq, tk, tv, grid, stream);
 }
 
 }  // namespace rlk

@@ -634,7 +634,11 @@ __global__ void __launch_bounds__(512, 1)
         w = mbar_wait(xbar, x_par, abort, p.err, 0x303);
         x_par ^= 1;
         if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
-        if (h == 0 && warp_rows && has) block_stats(mc, __fadd_rn(xsum[r], xsum[kTileRows + r]), lse_b, rcp);
+        if (DIFF && h == 0 && warp_rows && has) {  // the fold takes mc and the sum as they are
+          lse_b = mc;
+          rcp = __fadd_rn(xsum[r], xsum[kTileRows + r]);
+        }
+        if (!DIFF && h == 0 && warp_rows && has) block_stats(mc, __fadd_rn(xsum[r], xsum[kTileRows + r]), lse_b, rcp);
         if (h == 0) {
           stats[(st_it % SR) * kTileRows + r] = make_float2(lse_b, rcp);
           mbar_arrive(&bars[L::kStatsFull + (st_it % SR)]);
@@ -670,7 +674,8 @@ __global__ void __launch_bounds__(512, 1)
       }
       const bool valid = row_of_lane<MODE>(r) < it.row_count;
       const bool warp_rows = __any_sync(0xffffffffu, valid);
-      float Lrun = -INFINITY;
+      float Lrun = -INFINITY;  // (differential: the running maximum, and the sum in lsum)
+      float lsum = 0.0f;
       int64_t slab_off = it.slab_off;  // states: the slab of block blk0 + j
       bool fail = false;
       for (int j = 0; j < it.nb; ++j) {
@@ -738,13 +743,17 @@ __global__ void __launch_bounds__(512, 1)
         } else {
           tmem_ld32(ta, x0);
           float Lp = 0.f, alpha = 0.f, beta = 0.f;
-          if (j > 0 && has) fold_coeffs(Lrun, lse_b, Lp, alpha, beta);  // overlaps the PV load
+          if (j > 0 && has) {  // overlaps the PV load
+            if (DIFF) fold_max_coeffs(Lrun, lse_b, Lp, alpha, beta);
+            else fold_coeffs(Lrun, lse_b, Lp, alpha, beta);
+          }
           const float2 rc2 = make_float2(rcp, rcp), al2 = make_float2(alpha, alpha), be2 = make_float2(beta, beta);
           // o_b = PV * (1/l); O = fma(o_b, beta, O * alpha)  (packed, two lanes at a time)
           auto fold32 = [&](const uint32_t (&xa)[32], int o0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 oa = fmul2(make_float2(__uint_as_float(xa[e]), __uint_as_float(xa[e + 1])), rc2);
+              const float2 pv = make_float2(__uint_as_float(xa[e]), __uint_as_float(xa[e + 1]));
+              const float2 oa = DIFF ? pv : fmul2(pv, rc2);
               if (j == 0) {
                 O[o0 + e] = oa.x;
                 O[o0 + e + 1] = oa.y;
@@ -769,6 +778,7 @@ __global__ void __launch_bounds__(512, 1)
           mbar_arrive(&bars[L::kPVEmpty + buf]);  // PV read: the buffer is free
           fold32(x1, 96);
           if (has) Lrun = (j == 0) ? lse_b : Lp;
+          if (DIFF && has) lsum = (j == 0) ? rcp : __fmaf_rn(rcp, beta, __fmul_rn(lsum, alpha));
         }
         ++pv_it;
         ++st_it;
@@ -796,6 +806,9 @@ __global__ void __launch_bounds__(512, 1)
         // 16-byte pieces, 128 rows apart)
         const bool second = DIFF && map_of<MODE>(round) == 1;
         if (DIFF) {
+          const float rl = __frcp_rn(lsum);
+#pragma unroll
+          for (int e = 0; e < kHeadDim; ++e) O[e] = __fmul_rn(O[e], rl);
           float4* park = reinterpret_cast<float4*>(smem + L::kParkOff) + r;
           if (second) {
 #pragma unroll
@@ -846,7 +859,8 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (p.lse && valid) {
           const int64_t row_idx = row_base + static_cast<int64_t>(r) * p.hq;
-          p.lse[DIFF ? 2 * row_idx + map_of<MODE>(round) : row_idx] = Lrun;
+          if (DIFF) p.lse[2 * row_idx + map_of<MODE>(round)] = __fmaf_rn(Lrun, kLn2f, logf(lsum));
+          else p.lse[row_idx] = Lrun;
         }
       } else if (MODE == kModeDecode && valid) {
         // epilogue (decode): the group's rows are spread over the lane

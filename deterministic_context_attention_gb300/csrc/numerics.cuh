@@ -158,6 +158,20 @@ __device__ __forceinline__ float fold_elem(float O, float o, float alpha, float 
   return __fmaf_rn(o, beta, __fmul_rn(O, alpha));
 }
 
+// Fold of running (O, m, l) with a block's (PV, mc, l_b), both relative to
+// 2^m (log2 domain; mc as the block's probabilities used it, so that the
+// rounding of mc is in none of the weights):
+//   m' = max(m, mc), alpha = 2^(m - m'), beta = 2^(mc - m')
+//   O  = fma(PV, beta, O * alpha), l = fma(l_b, beta, l * alpha)
+// and at the end O / l and lse = fma(m, ln2, ln l).  It keeps no log sums, whose
+// last place (2^-19 at 40) the canonical fold adds up over the blocks: the
+// difference of two maps' outputs needs what that loses.
+__device__ __forceinline__ void fold_max_coeffs(float m, float mb, float& mn, float& alpha, float& beta) {
+  mn = fmaxf(m, mb);
+  alpha = ex2_hw(__fsub_rn(m, mn));
+  beta = ex2_hw(__fsub_rn(mb, mn));
+}
+
 // RoPE of one rotate-half pair (x0 = element i, x1 = element i + 64) with
 // the table's FP32 cos / sin of its position and frequency, in the one FP32
 // form every RoPE path of the library uses (the products rounded to FP32 on

@@ -81,4 +81,30 @@ cudaError_t configure_qdecode_kernels();
 cudaError_t launch_qdecode(const QDecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                            cudaStream_t stream);
 
+// Differential decode over the BF16 pages, cut and folded like the 8-bit one.
+// States: row (seg0[s] + segment) * 2 hq + 2 head + map of state_o [.., 128] and
+// state_ml [.., 2].
+struct DDecodeParams {
+  ErrWord* err;
+  int32_t num_seqs, hq, hkv;
+  int32_t group;  // KV heads that consecutive CTAs take side by side
+  float scale_log2;
+  const float* lambda;  // [hq]
+  const int32_t* page_table;
+  int32_t n_pages, page_size, max_pages;
+  float* out_f32;
+  uint16_t* out_bf16;
+  float* lse;  // [num_seqs, hq, 2]
+  float* state_o;
+  float* state_ml;
+  unsigned long long* counts;
+  uint64_t nonce;  // 40 bits, new to every call
+  int32_t ctx[kQMaxSeqs];
+  int32_t seg0[kQMaxSeqs + 1];
+  QStart start[kQMaxParts];
+};
+cudaError_t configure_ddecode_kernels();
+cudaError_t launch_ddecode(const DDecodeParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int grid, cudaStream_t stream);
+
 }  // namespace rlk

@@ -80,14 +80,13 @@
 #include "numerics.cuh"
 #include "ptx.cuh"
 #include "qcache_internal.h"
+#include "segments.cuh"
 
 namespace rlk {
 namespace {
 
 constexpr int kQDThreads = 512;
 constexpr int kQPieces = 3, kPPieces = 4;
-constexpr int kSegBlocks = kQSegKeys / 128;
-constexpr float kLUnit = 0x1p26f;  // block sums of p: fixed point, 26 fraction bits
 
 // MG: query heads per KV head.  N: MMA columns, their pieces (of Q at column
 // piece * MG + head, of P at p_col)
@@ -235,162 +234,12 @@ struct TmemRow<32> {
   static __device__ __forceinline__ void ld(uint32_t a, uint32_t (&r)[32]) { tmem_ld32(a, r); }
 };
 
-// A warp's wait on a barrier (bounded, mbar_wait): one test and one vote when
-// the phase is complete already, the rest out of line (the roles' code
-// competes for the instruction cache).
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, ErrWord* err,
-                                       unsigned int site) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
-}
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, ErrWord* err,
-                                          unsigned int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return wait_slow(bar, parity, abort, err, site);
-}
-
-// One arrival for the whole warp, after every lane's earlier writes.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-}
-
-// Row maximum of the 32 lanes of a warp (exact; every lane receives it).
-__device__ __forceinline__ float warp_max(float v) {
-  float m;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
-}
-
-// The same, NaN where any lane holds one, and the maximum of two like it: a NaN
-// score makes its row's maximum, and from there the whole row, NaN.
-__device__ __forceinline__ float warp_max_nan(float v) {
-  float m;
-  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-  return m;
-}
-
-// A piece of work: segments [s0, s1) of the ns of (sequence, KV head g).
-struct QPiece {
-  int seq, g, kv_len, nb, s0, s1, ns;
-  int first;  // the segments that the pair's first piece has
-  __device__ int block0() const { return s0 * kSegBlocks; }
-  __device__ int block1() const { return min(s1 * kSegBlocks, nb); }
-  __device__ bool whole() const { return s0 == 0 && s1 == ns; }
-};
-
-// The pieces of this CTA, in order; every role walks them on its own from the
-// CTA's start, which the host worked out (found here, by searching the tables
-// in the parameters, it was the first 4 us of every CTA: each probe of a table
-// missed the constant cache).
-struct QWalk {
-  int seq, g, b;  // where the next piece starts (g: the first KV head of the group's)
-  int left;       // blocks still to take
-  int cut;        // b > 0: where that pair is first cut
-  __device__ explicit QWalk(const QDecodeParams& p) {
-    const QStart s = p.start[blockIdx.x / p.group];
-    seq = s.seq;
-    g = s.g * p.group + blockIdx.x % p.group;
-    b = s.b;
-    left = s.left;
-    cut = s.cut;
-  }
-  __device__ bool next(const QDecodeParams& p, QPiece* q) {
-    if (left <= 0) return false;
-    q->seq = seq;
-    q->g = g;
-    q->kv_len = p.ctx[seq];
-    q->nb = (q->kv_len + 127) / 128;
-    q->ns = (q->nb + kSegBlocks - 1) / kSegBlocks;
-    const int stop = min(left, q->nb - b);
-    q->s0 = b / kSegBlocks;
-    q->s1 = (b + stop + kSegBlocks - 1) / kSegBlocks;
-    q->first = b > 0 ? cut / kSegBlocks : q->s1;
-    left -= stop;
-    b = 0;
-    g += p.group;
-    if (g >= p.hkv) {
-      g -= p.hkv;
-      ++seq;
-    }
-    return true;
-  }
-};
-
-// The blocks of those pieces in groups of up to 4 consecutive ones of a piece
-// whose page ids fill a warp (32 pages: 2 blocks of 8-token pages, 4 of larger).
-struct QGroups {
-  QWalk walk;
-  QPiece pc;
-  int b, n;  // first block, blocks
-  bool ok;
-  __device__ QGroups(const QDecodeParams& p, int lg) : walk(p) {
-    b = n = 0;
-    ok = walk.next(p, &pc);
-    if (ok) begin(pc.block0(), lg);
-  }
-  __device__ void begin(int first, int lg) {
-    b = first;
-    n = min(1 << min(5 - lg, 2), pc.block1() - b);
-  }
-  __device__ void step(const QDecodeParams& p, int lg) {
-    if (!ok) return;
-    if (b + n >= pc.block1()) {
-      ok = walk.next(p, &pc);
-      if (ok) begin(pc.block0(), lg);
-    } else {
-      begin(b + n, lg);
-    }
-  }
-  // lane l: the id of page l of the group (-1: none)
-  __device__ int page_id(const QDecodeParams& p, int lg, int lane) const {
-    const int gp = (b << lg) + lane;
-    if (!ok || lane >= (n << lg) || gp * (128 >> lg) >= pc.kv_len) return -1;
-    return __ldg(p.page_table + static_cast<int64_t>(pc.seq) * p.max_pages + gp);
-  }
-};
-
 __device__ const float g_unit_scale = 1.0f;  // the scale of a page id out of range
 
 // Arrives on bar once this thread's earlier cp.async copies have landed (the
 // arrival is one of the barrier's count).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// 2^((s - m) c), exactly 1 for s = m.
-__device__ __forceinline__ float weight(float s, float m, float c) { return ex2_hw(__fmul_rn(__fsub_rn(s, m), c)); }
-
-// (O, m, l) folded with a later state: the factors of the two, and m.
-__device__ __forceinline__ void fold_factors(float m, float mb, float c, float& mn, float& a, float& b) {
-  mn = fmaxf(m, mb);
-  a = weight(m, mn, c);
-  b = weight(mb, mn, c);
-}
-
-// ln of the sum of e^(s scale): m the maximum of s, l the sum relative to it.
-__device__ __forceinline__ float log_sum(float m, float l, float c) {
-  return __fmaf_rn(__fmul_rn(m, c), kLn2f, logf(l));
-}
-
-// The count of a cut pair's finished segments: a word that holds the call's
-// nonce (40 bits) over the count (24).  Another nonce means that no segment of
-// this call has been counted yet; every CTA with a part of the pair sees to it
-// early (begin_count) that the word holds its nonce, so that counting is one
-// addition.  The CTA that counts the last segment clears the word.
-__device__ __forceinline__ void begin_count(unsigned long long* word, uint64_t nonce) {
-  const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
-  // where this fails, another CTA of the call has done it
-  if ((old >> 24) != nonce) atomicCAS(word, old, static_cast<unsigned long long>(nonce << 24));
-}
-__device__ __forceinline__ bool count_segments(unsigned long long* word, int n, int ns) {
-  const bool last = (atomicAdd(word, static_cast<unsigned long long>(n)) & 0xFFFFFFu) + n == static_cast<unsigned>(ns);
-  if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
-  return last;
 }
 
 // The fold of a cut pair's ns states (the first piece's, then its other
@@ -581,7 +430,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     const int lps = 31 - __clz(p.page_size), lg = 7 - lps;  // log2 of a page's tokens, of a block's pages
     const int lbox = min(lps, 31 - __clz(kQBoxRows));       // and of a copy's tokens
     // page ids: two groups of blocks ahead, across pieces
-    QGroups cur(p, lg), ahead(p, lg);
+    QGroups<QDecodeParams> cur(p, lg), ahead(p, lg);
     int id = ahead.page_id(p, lg, lane);
     ahead.step(p, lg);
     int id1 = ahead.page_id(p, lg, lane);
@@ -596,7 +445,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     // piece runs this code once, and unrolled it took 3 us, most of it fetching
     // instructions.
     uint8_t* row_stage = smem + L::kRowOff;
-    QWalk qwalk(p);
+    QWalk<QDecodeParams> qwalk(p);
     uint32_t q_it = 0;
     bool q_more = false;
     auto fetch_rows = [&]() {
@@ -725,7 +574,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     constexpr uint32_t kIdS = idesc_e4m3(128, N, false, false);  // A = K (K-major), B = Q pieces (K-major)
     const uint32_t leader = elect_one_sync();
     uint32_t stage = 0, kpar = 0, s_it = 0, q_it = 0;
-    QWalk walk(p);
+    QWalk<QDecodeParams> walk(p);
     QPiece pc;
     while (walk.next(p, &pc)) {
       const uint32_t qslot = q_it & 1;
@@ -764,7 +613,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     constexpr uint32_t kIdO = idesc_e4m3(128, N, true, true);  // A = V^T (dims contiguous), B = P^T (pieces contiguous)
     const uint32_t leader = elect_one_sync();
     uint32_t stage = 0, vpar = 0, o_it = 0;
-    QWalk walk(p);
+    QWalk<QDecodeParams> walk(p);
     QPiece pc;
     while (walk.next(p, &pc)) {
       bool fail = false;
@@ -821,7 +670,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
     bool after_cut = false, end_fold = false;
     const float* k_scales = reinterpret_cast<const float*>(smem + L::kScOff) + (t >> lps);
     const float* v_scales = k_scales + L::kScRing * 16;
-    QWalk walk(p);
+    QWalk<QDecodeParams> walk(p);
     QPiece pc;
     while (walk.next(p, &pc)) {
       const int kv_len = pc.kv_len, b0 = pc.block0(), nb = pc.block1() - b0;
@@ -990,7 +839,7 @@ __global__ void __launch_bounds__(kQDThreads, 1)
       n_cut = 0;
       return true;
     };
-    QWalk walk(p);
+    QWalk<QDecodeParams> walk(p);
     QPiece pc;
     while (walk.next(p, &pc)) {
       const bool whole = pc.whole();

@@ -32,10 +32,11 @@ def _weights(q, k, scale, m):
     return p / p.sum(1)[:, None], lse, err
 
 
-def _fold(lse, nk):
-    """The fold of a row's block states: per block, a log sum rounded at its own
-    size and a few roundings of the coefficients."""
-    return -(-nk // 128) * 2.0 ** -21 * (1 + np.abs(lse))
+def _fold(nk):
+    """The fold of a row's block states, relative: per block, two factors by the
+    hardware's exponential (2^-22 each) and a few roundings, once in the
+    weighted sum and once in the sum of the weights."""
+    return 2 * (-(-nk // 128) + 2) * (2 * 2.0 ** -22 + 4 * 2.0 ** -24)
 
 
 def forward(q, k, v, lam, scale):
@@ -51,11 +52,11 @@ def forward(q, k, v, lam, scale):
             p, l, e = _weights(q[:, h], k[:, h // g], scale, m)
             vv = v[:, h // g]
             # P in two BF16 pieces (2^-18), 256 products summed in FP32 (2^-15)
-            rel = e + _fold(l, nk) + 2.0 ** -15 + 2.0 ** -18
+            rel = e + _fold(nk) + 2.0 ** -15 + 2.0 ** -18
             o.append(p @ vv)
             t.append(rel[:, None] * (p @ np.abs(vv)))
             lse[:, h, m] = l
-            tol_lse[:, h, m] = e + _fold(l, nk) + 2.0 ** -20 + 2.0 ** -23 * np.abs(l)
+            tol_lse[:, h, m] = e + _fold(nk) + 2.0 ** -20 + 2.0 ** -23 * np.abs(l)
         out[:, h] = o[0] - lam[h] * o[1]
         out2[:, h] = o[1]
         tol2[:, h] = t[1]
@@ -79,7 +80,7 @@ def backward(q, k, v, lam, dout, scale):
             cols = slice(m * M, (m + 1) * M)
             p, l, e = _weights(q[:, h], k[:, kv], scale, m)
             # a weight from the saved log sum, which has its own error
-            rel = (2 * e + _fold(l, n) + 2.0 ** -21 * (1 + np.abs(l)))[:, None]
+            rel = (2 * e + _fold(n) + 2.0 ** -21 * (1 + np.abs(l)))[:, None]
             delta = (p * dp).sum(1, keepdims=True)
             o = p @ vv
             # Delta from the saved outputs: their error, and sums of 128 products

@@ -134,8 +134,8 @@ def test_every_range_of_a_large_batch_is_checked_first(lib):
 
 def test_workspace_sizes(lib):
     p = rlk.make_params(2, 32, 8)
-    # 516 bytes a (block, map of a query head), 8 a (sequence, KV head, item)
-    assert rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DIFF_DECODE, None, [129, 1]) == 3 * 64 * 516 + 2 * 8 * 64 * 8
+    # 520 bytes a (512-key segment, map of a query head), 8 a (sequence, KV head)
+    assert rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DIFF_DECODE, None, [513, 1]) == 3 * 64 * 520 + 2 * 8 * 8
     # lse and Delta of two maps, the rows padded by 128
     assert rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DIFF_BACKWARD, [0, 3, 9]) == (9 + 128) * 32 * 4 * 4
     assert rlk.rlk_attn_workspace_size(p, rlk.RLK_OP_DIFF_DECODE, None, [129, 0]) == 0
