@@ -29,49 +29,13 @@
 #include <vector>
 
 #include "../../include/rlk_attn.h"
+#include "bwd_internal.h"
 #include "numerics.cuh"
 #include "ptx.cuh"
 #include "rlk_internal.h"
 
 namespace rlk {
 
-
-constexpr float kLog2e = 1.44269504088896340736f;
-
-struct alignas(16) BwdItem {
-  int32_t seq;
-  int32_t head;   // dK/dV: KV head g; dQ: query head h
-  int32_t block;  // dK/dV: KV block j; dQ: first row of the query tile
-  int32_t rows;   // dQ: rows of the tile written; dK/dV: unused
-};
-
-constexpr int kMaxBwdTiles = 1800;
-
-// The item list holds tiles; item i is head i mod item_heads of tile
-// i / item_heads (the heads of a tile are adjacent in the longest-first
-// order), so a launch takes kMaxBwdTiles * heads items.
-struct BwdParams {
-  ErrWord* err;
-  int32_t hq, hkv, group, num_items;
-  int32_t item_heads, pad0;
-  int64_t t_pad;        // row stride of the transposed lse / Delta
-  float scale, scale_log2;
-  const float* lse_t;   // [hq][t_pad] (differential: [hq][2 maps][t_pad])
-  const float* delta_t; // [hq][t_pad] (the same)
-  const float* lambda;  // differential: [hq]
-  float* dq;
-  float* dk;
-  float* dv;
-  int32_t cu[kMaxSeqs + 1];
-  BwdItem items[kMaxBwdTiles];
-};
-
-__device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int item) {
-  const int t = item / p.item_heads;
-  BwdItem it = p.items[t];
-  it.head = item - t * p.item_heads;
-  return it;
-}
 
 // ------------------------------------------------------------------ preprocess
 struct PrepParams {
@@ -207,17 +171,12 @@ __device__ __forceinline__ uint64_t mndesc(uint32_t tile, int k) {  // MN-major 
 //   ds = p * (dp - Delta)
 // KIND 0: dK/dV (rows = keys of block j, columns = query rows);
 // KIND 1: dQ    (rows = query rows,       columns = keys of block j).
-// DIFF: differential attention.  A step is one map m of a (tile, head) pair
-// (m = 0, then 1, on the same streamed tiles): S from the map's half of the
-// columns, P of map 2 times -lambda, so that dV sums both maps' and dS_m, which
-// goes with the map's half of Q or K, needs nothing else.
-template <int KIND, bool DIFF>
+template <int KIND>
 __global__ void __launch_bounds__(384, 1)
     rlk_bwd_kernel(const __grid_constant__ BwdParams p, const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_do) {
   using L = BwdLayoutT<KIND>;
-  constexpr int NM = DIFF ? 2 : 1;  // steps on one pair of streamed tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -268,7 +227,6 @@ __global__ void __launch_bounds__(384, 1)
     } else {
       nsteps = (it.block + it.rows - 1) / 128 + 1;
     }
-    nsteps *= NM;
   };
 
   if (warp == 8) {
@@ -302,7 +260,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       ++res_it;
-      for (int t = 0; t < nsteps / NM; ++t) {
+      for (int t = 0; t < nsteps; ++t) {
         if (KIND == 1) {
           // K_j into slot t mod 3 (free once the accumulation of the step
           // three back is done), V_j into slot t mod 2 (free once the dP of
@@ -363,7 +321,6 @@ __global__ void __launch_bounds__(384, 1)
     // half only after acc_c(t) has read it.  dQ issues S/dP whole (below).
     constexpr uint32_t kIdK = idesc_bf16(128, 64, false, false);   // both operands K-major, N = 64
     constexpr uint32_t kIdMN = idesc_bf16(128, 128, false, true);  // A in TMEM, B MN-major
-    constexpr uint32_t kIdMap = idesc_bf16(128, DIFF ? 64 : 128, false, true);  // B one map's half (dK, dQ)
     uint32_t res_it = 0, st_it = 0, s_it = 0, acc_it = 0;
     // the whole warp walks the K-steps (warp-uniform descriptors) and the
     // elected lane issues each MMA: a lone lane in a divergent branch issues
@@ -380,12 +337,11 @@ __global__ void __launch_bounds__(384, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       ++res_it;
       // S^T|S and dP^T|dP of half c of step t (stream stage of step t)
-      auto issue_sdp = [&](uint32_t st_addr, int c, int m) {
+      auto issue_sdp = [&](uint32_t st_addr, int c) {
         const uint32_t boff = static_cast<uint32_t>(c) * 64 * 128;  // rows 64c.. of the streamed tiles
-        const uint32_t moff = DIFF ? static_cast<uint32_t>(m) * L::kHalf : 0;  // the map's half of the columns
 #pragma unroll
-        for (int k = 0; k < (DIFF ? 4 : 8); ++k)
-          if (leader) umma_ss(tm_s + 64 * c, kdesc(res_addr + moff, k), kdesc(st_addr + moff + boff, k), kIdK, k > 0);
+        for (int k = 0; k < 8; ++k)
+          if (leader) umma_ss(tm_s + 64 * c, kdesc(res_addr, k), kdesc(st_addr + boff, k), kIdK, k > 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (leader)
@@ -394,11 +350,8 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
       };
       // dK/dV: K-steps 4c..4c+3 of the accumulators (first: the item's first product)
-      // (differential: dK's own first product is that of its map's first step)
-      auto issue_acc = [&](uint32_t st_addr, int c, int m, bool first, bool first_map) {
+      auto issue_acc = [&](uint32_t st_addr, int c, bool first) {
         const int k0 = 4 * c;
-        const uint32_t moff = DIFF ? static_cast<uint32_t>(m) * L::kHalf : 0;
-        const uint32_t tk = tm_acc1 + (DIFF ? 64 * m : 0);
         if (KIND == 0) {
           // dV += P^T dO ; dK += dS^T Q   (B operands MN-major: N = D, K = query rows)
 #pragma unroll
@@ -410,11 +363,10 @@ __global__ void __launch_bounds__(384, 1)
             if (leader) umma_ts(tm_acc0, tm_s + 16 * k + 8, mndesc(st_addr + L::kTile, k), kIdMN, 1u);
 #pragma unroll
           for (int k = k0; k < k0 + 4; ++k)
-            if (leader)
-              umma_ts(tk, tm_dp + 16 * k, mndesc(st_addr + moff, k), kIdMap, (first_map && k == k0) ? 0u : 1u);
+            if (leader) umma_ts(tm_acc1, tm_dp + 16 * k, mndesc(st_addr, k), kIdMN, (first && k == k0) ? 0u : 1u);
 #pragma unroll
           for (int k = k0; k < k0 + 4; ++k)
-            if (leader) umma_ts(tk, tm_dp + 16 * k + 8, mndesc(st_addr + moff, k), kIdMap, 1u);
+            if (leader) umma_ts(tm_acc1, tm_dp + 16 * k + 8, mndesc(st_addr, k), kIdMN, 1u);
         }
         __syncwarp();
       };
@@ -435,48 +387,44 @@ __global__ void __launch_bounds__(384, 1)
         constexpr uint32_t kIdK128 = idesc_bf16(128, 128, false, false);
         auto k_slot = [&](uint32_t si) { return smem_u32(st_base + (si % L::kKSlots) * L::kTile); };
         auto v_slot = [&](uint32_t si) { return smem_u32(smem + L::kVOff + (si % L::kVSlots) * L::kTile); };
-        auto issue_sdp128 = [&](uint32_t si, int m, bool last, uint32_t s) {
+        auto issue_sdp128 = [&](uint32_t si, bool last, uint32_t s) {
           const uint32_t ts = dq_area(s % 3), tdp = dq_area((s + 1) % 3);
           const uint32_t ka = k_slot(si), va = v_slot(si);
-          const uint32_t moff = DIFF ? static_cast<uint32_t>(m) * L::kHalf : 0;  // the map's half of the columns
 #pragma unroll
-          for (int k = 0; k < (DIFF ? 4 : 8); ++k)
-            if (leader) umma_ss(ts, kdesc(res_addr + moff, k), kdesc(ka + moff, k), kIdK128, k > 0);
+          for (int k = 0; k < 8; ++k)
+            if (leader) umma_ss(ts, kdesc(res_addr, k), kdesc(ka, k), kIdK128, k > 0);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (leader) umma_ss(tdp, kdesc(res_addr + L::kTile, k), kdesc(va, k), kIdK128, k > 0);
           if (leader) {
             umma_commit(&bars[L::kSFull]);
             umma_commit(&bars[L::kSFull + 1]);
-            if (m == NM - 1) umma_commit(&bars[L::kVEmpty + si % L::kVSlots]);  // V_j is read by dP only
+            umma_commit(&bars[L::kVEmpty + si % L::kVSlots]);  // V_j is read by dP only
             if (last) umma_commit(&bars[L::kResEmpty]);  // the item's last S/dP: the resident pair is free
           }
           __syncwarp();
         };
         // dQ += dS K_j over K-steps 4c..4c+3, with dS in area tds and K_j at ka
-        auto issue_acc_dq = [&](uint32_t ka, int c, int m, bool first, uint32_t tds) {
+        auto issue_acc_dq = [&](uint32_t ka, int c, bool first, uint32_t tds) {
           const int k0 = 4 * c;
-          const uint32_t td = tm_acc0 + (DIFF ? 64 * m : 0), kb = ka + (DIFF ? static_cast<uint32_t>(m) * L::kHalf : 0);
 #pragma unroll
           for (int k = k0; k < k0 + 4; ++k)
-            if (leader) umma_ts(td, tds + 16 * k, mndesc(kb, k), kIdMap, (first && k == k0) ? 0u : 1u);
+            if (leader) umma_ts(tm_acc0, tds + 16 * k, mndesc(ka, k), kIdMN, (first && k == k0) ? 0u : 1u);
 #pragma unroll
           for (int k = k0; k < k0 + 4; ++k)
-            if (leader) umma_ts(td, tds + 16 * k + 8, mndesc(kb, k), kIdMap, 1u);
+            if (leader) umma_ts(tm_acc0, tds + 16 * k + 8, mndesc(ka, k), kIdMN, 1u);
           __syncwarp();
         };
         {
           bool w = mbar_wait(&bars[L::kStFull + st_it % L::kKSlots], (st_it / L::kKSlots) & 1, abort, p.err, 0x613);
           if (!__all_sync(0xffffffffu, w)) break;
           tc_fence_after();
-          issue_sdp128(st_it, 0, nsteps == 1, s_it);
+          issue_sdp128(st_it, nsteps == 1, s_it);
         }
         ok = mbar_wait(&bars[L::kAccEmpty], (acc_it & 1) ^ 1, abort, p.err, 0x612);
         if (!__all_sync(0xffffffffu, ok)) break;
         for (int t = 0; t < nsteps; ++t) {
-          const int m = t % NM;
-          const bool pair_end = m == NM - 1;  // the streamed tiles' last step
-          const uint32_t cur = st_it, nxt = pair_end ? st_it + 1 : st_it;
+          const uint32_t cur = st_it, nxt = st_it + 1;
           const bool more = t + 1 < nsteps;
           const uint32_t tds = dq_area(s_it % 3);
           const uint32_t pf = L::kPFull + 2 * (s_it & 1), pph = (s_it >> 1) & 1;
@@ -486,26 +434,26 @@ __global__ void __launch_bounds__(384, 1)
           bool w = mbar_wait(&bars[L::kSDPRead], s_it & 1, abort, p.err, 0x616);
           if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
           if (more) {
-            w = !pair_end || mbar_wait(&bars[L::kStFull + nxt % L::kKSlots], (nxt / L::kKSlots) & 1, abort, p.err, 0x615);
+            w = mbar_wait(&bars[L::kStFull + nxt % L::kKSlots], (nxt / L::kKSlots) & 1, abort, p.err, 0x615);
             if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
             tc_fence_after();
-            issue_sdp128(nxt, (t + 1) % NM, t + 2 == nsteps, s_it + 1);
+            issue_sdp128(nxt, t + 2 == nsteps, s_it + 1);
           }
           w = mbar_wait(&bars[pf], pph, abort, p.err, 0x614);
           if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
           tc_fence_after();
-          issue_acc_dq(k_slot(cur), 0, m, t < NM, tds);
+          issue_acc_dq(k_slot(cur), 0, t == 0, tds);
           w = mbar_wait(&bars[pf + 1], pph, abort, p.err, 0x614);
           if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
           tc_fence_after();
-          issue_acc_dq(k_slot(cur), 1, m, false, tds);
+          issue_acc_dq(k_slot(cur), 1, false, tds);
           if (leader) {
-            if (pair_end) umma_commit(&bars[L::kStEmpty + cur % L::kKSlots]);  // K_j no longer read
+            umma_commit(&bars[L::kStEmpty + cur % L::kKSlots]);  // K_j no longer read
             if (!more) umma_commit(&bars[L::kAccFull]);
           }
           __syncwarp();
           ++s_it;
-          if (pair_end) ++st_it;
+          ++st_it;
         }
         if (fail) break;
         ++acc_it;
@@ -515,8 +463,8 @@ __global__ void __launch_bounds__(384, 1)
         bool w = mbar_wait(&bars[L::kStFull + st_it % L::kStages], (st_it / L::kStages) & 1, abort, p.err, 0x613);
         if (!__all_sync(0xffffffffu, w)) break;
         tc_fence_after();
-        issue_sdp(stage_addr(st_it), 0, 0);
-        issue_sdp(stage_addr(st_it), 1, 0);
+        issue_sdp(stage_addr(st_it), 0);
+        issue_sdp(stage_addr(st_it), 1);
         if (nsteps == 1) {
           if (leader) umma_commit(&bars[L::kResEmpty]);  // the item's last S/dP: the resident pair is free
           __syncwarp();
@@ -526,27 +474,25 @@ __global__ void __launch_bounds__(384, 1)
       ok = mbar_wait(&bars[L::kAccEmpty], (acc_it & 1) ^ 1, abort, p.err, 0x612);
       if (!__all_sync(0xffffffffu, ok)) break;
       for (int t = 0; t < nsteps; ++t) {
-        const int m = t % NM;
-        const bool pair_end = m == NM - 1;  // the streamed tiles' last step
-        const uint32_t cur = st_it, nxt = pair_end ? st_it + 1 : st_it;
+        const uint32_t cur = st_it, nxt = st_it + 1;
         const bool more = t + 1 < nsteps;
         for (int c = 0; c < 2; ++c) {
           bool w = mbar_wait(&bars[L::kPFull + c], s_it & 1, abort, p.err, 0x614);
           if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
           tc_fence_after();
-          issue_acc(stage_addr(cur), c, m, t == 0 && c == 0, t < NM && c == 0);
+          issue_acc(stage_addr(cur), c, t == 0 && c == 0);
           if (c == 1 && leader) {
-            if (pair_end) umma_commit(&bars[L::kStEmpty + cur % L::kStages]);  // the stage is no longer read
+            umma_commit(&bars[L::kStEmpty + cur % L::kStages]);  // step t's stage is no longer read
             if (!more) umma_commit(&bars[L::kAccFull]);
           }
           __syncwarp();
           if (more) {
-            if (c == 0 && pair_end) {
+            if (c == 0) {
               w = mbar_wait(&bars[L::kStFull + nxt % L::kStages], (nxt / L::kStages) & 1, abort, p.err, 0x615);
               if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
               tc_fence_after();
             }
-            issue_sdp(stage_addr(nxt), c, (t + 1) % NM);
+            issue_sdp(stage_addr(nxt), c);
             if (c == 1 && t + 2 == nsteps) {
               if (leader) umma_commit(&bars[L::kResEmpty]);  // the item's last S/dP: the resident pair is free
               __syncwarp();
@@ -555,7 +501,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (fail) break;
         ++s_it;
-        if (pair_end) ++st_it;
+        ++st_it;
       }
       if (fail) break;
       ++acc_it;
@@ -581,35 +527,25 @@ __global__ void __launch_bounds__(384, 1)
       item_steps(it, len, nsteps);
       const int tok0 = p.cu[it.seq];
       // dQ: this thread's row statistics are fixed for the item
-      float row_lse2 = 0.f, row_delta = 0.f, row_lse2b = 0.f, row_deltab = 0.f;  // b: the second map's
-      float nlam = 0.f;  // -lambda of the step's query head
+      float row_lse2 = 0.f, row_delta = 0.f;
       int row_pos = 0;
       bool row_ok = false;
       if (KIND == 1) {
         row_pos = it.block + r;
         row_ok = r < it.rows && row_pos < len;
         if (row_ok) {
-          const int64_t idx = NM * static_cast<int64_t>(it.head) * p.t_pad + tok0 + row_pos;
+          const int64_t idx = static_cast<int64_t>(it.head) * p.t_pad + tok0 + row_pos;
           row_lse2 = __fmul_rn(p.lse_t[idx], kLog2e);
           row_delta = p.delta_t[idx];
-          if (DIFF) {
-            row_lse2b = __fmul_rn(p.lse_t[idx + p.t_pad], kLog2e);
-            row_deltab = p.delta_t[idx + p.t_pad];
-          }
         }
-        if (DIFF) nlam = -__ldg(p.lambda + it.head);
       }
       const int key_pos = (KIND == 0) ? it.block * 128 + r : 0;
       // dK/dV: the column statistics (lse, Delta of the step's query rows) of
       // this warp's columns in both halves, loaded one step ahead
       float nl[2] = {0.f, 0.f}, nd[2] = {0.f, 0.f};
-      float nlam_next = 0.f;
       auto load_stats = [&](int t) {
-        const int u = t / NM;
-        const int i = it.block + u / p.group;
-        const int hh = it.head * p.group + u % p.group;
-        const int h = DIFF ? 2 * hh + t % NM : hh;  // row of the statistics
-        if (DIFF) nlam_next = -__ldg(p.lambda + hh);
+        const int i = it.block + t / p.group;
+        const int h = it.head * p.group + t % p.group;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int qp = i * 128 + 64 * c + 32 * wh + lane;
@@ -624,8 +560,7 @@ __global__ void __launch_bounds__(384, 1)
         float* vb = vecs + ((s_it & 1) * 8 + warp) * 128;  // [half][lse2 32, Delta 32] of this warp's columns
         int col0;  // position of column 0 of this step
         if (KIND == 0) {
-          col0 = (it.block + t / NM / p.group) * 128;
-          nlam = nlam_next;
+          col0 = (it.block + t / p.group) * 128;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {  // each warp stages its own copy (warp-local sync only)
             vb[64 * c + lane] = __fmul_rn(nl[c], kLog2e);
@@ -634,11 +569,9 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
           if (t + 1 < nsteps) load_stats(t + 1);
         } else {
-          col0 = t / NM * 128;
+          col0 = t * 128;
         }
-        const bool map2 = DIFF && t % NM == 1;
         const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-        const float2 pcoef = map2 ? make_float2(nlam, nlam) : make_float2(1.0f, 1.0f);
         const uint32_t ts_e = (KIND == 0) ? tm_s : dq_area(s_it % 3);
         const uint32_t tdp_e = (KIND == 0) ? tm_dp : dq_area((s_it + 1) % 3);
         const uint32_t tds_e = (KIND == 0) ? tm_dp : ts_e;  // dQ writes dS over S
@@ -690,9 +623,8 @@ __global__ void __launch_bounds__(384, 1)
           auto arith = [&](auto masked) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float rl = map2 ? row_lse2b : row_lse2, rd = map2 ? row_deltab : row_delta;
-              float4 l4 = make_float4(rl, rl, rl, rl);
-              float4 d4 = make_float4(rd, rd, rd, rd);
+              float4 l4 = make_float4(row_lse2, row_lse2, row_lse2, row_lse2);
+              float4 d4 = make_float4(row_delta, row_delta, row_delta, row_delta);
               if (KIND == 0) {
                 l4 = *reinterpret_cast<const float4*>(vc + e);
                 d4 = *reinterpret_cast<const float4*>(vc + 32 + e);
@@ -719,7 +651,6 @@ __global__ void __launch_bounds__(384, 1)
                   pp.x = okA ? pp.x : 0.0f;
                   pp.y = okB ? pp.y : 0.0f;
                 }
-                if constexpr (DIFF) pp = fmul2(pp, pcoef);  // 1, or -lambda
                 const float2 ds = fmul2(pp, fsub2(make_float2(__uint_as_float(dr[e + u]), __uint_as_float(dr[e + u + 1])),
                                                   make_float2(da[u], da[u + 1])));
                 // a 16-column group of TMEM holds one K-step: its 8 hi words, then its 8 lo words
@@ -870,7 +801,6 @@ template <int KIND, bool DIFF>
 cudaError_t launch_bwd(BwdParams* bp, const std::vector<BwdItem>& tiles, int heads, const CUtensorMap& mq,
                        const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int num_sms,
                        cudaStream_t stream) {
-  auto kern = rlk_bwd_kernel<KIND, DIFF>;
   cudaError_t e = cudaSuccess;
   bp->item_heads = heads;
   for (size_t i0 = 0; i0 < tiles.size(); i0 += kMaxBwdTiles) {
@@ -878,8 +808,12 @@ cudaError_t launch_bwd(BwdParams* bp, const std::vector<BwdItem>& tiles, int hea
     std::copy(tiles.begin() + i0, tiles.begin() + i0 + n, bp->items);
     bp->num_items = static_cast<int32_t>(n) * heads;
     const int grid = std::min(bp->num_items, num_sms);
-    kern<<<grid, 384, BwdLayoutT<KIND>::kAlloc, stream>>>(*bp, mq, mk, mv, mdo);
-    e = cudaGetLastError();
+    if (DIFF) {
+      e = launch_dbwd<KIND>(*bp, grid, mq, mk, mv, mdo, stream);
+    } else {
+      rlk_bwd_kernel<KIND><<<grid, 384, BwdLayoutT<KIND>::kAlloc, stream>>>(*bp, mq, mk, mv, mdo);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -889,18 +823,13 @@ cudaError_t launch_bwd(BwdParams* bp, const std::vector<BwdItem>& tiles, int hea
 
 static_assert(sizeof(BwdParams) + 4 * sizeof(CUtensorMap) + 256 <= 32764, "backward parameters");
 
-template <int KIND, bool DIFF>
-static cudaError_t configure_bwd_t() {
-  return cudaFuncSetAttribute(rlk_bwd_kernel<KIND, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              BwdLayoutT<KIND>::kAlloc);
-}
-
 cudaError_t configure_bwd_kernels() {
-  cudaError_t e;
-  if ((e = configure_bwd_t<0, false>()) != cudaSuccess) return e;
-  if ((e = configure_bwd_t<1, false>()) != cudaSuccess) return e;
-  if ((e = configure_bwd_t<0, true>()) != cudaSuccess) return e;
-  return configure_bwd_t<1, true>();
+  cudaError_t e = cudaFuncSetAttribute(rlk_bwd_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       BwdLayoutT<0>::kAlloc);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(rlk_bwd_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdLayoutT<1>::kAlloc);
+  if (e != cudaSuccess) return e;
+  return configure_dbwd_kernels();
 }
 
 // lse and Delta of every query head (of its `maps` maps), transposed

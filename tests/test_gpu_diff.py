@@ -361,6 +361,24 @@ def test_empty_batches():
     assert not bool(dlam.any())
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_other_sequences_do_not_leak(bad):
+    # a sequence of NaN or Inf beside ones whose last tiles it shares
+    import torch
+    lens = [130, 70, 5, 300]
+    p = Problem(lens, lens, 8, 2, seed=21)
+    fwd, bwd = p.forward(), p.backward()
+    at = slice(int(p.cq[1]), int(p.cq[2]))
+    for x in (p.q, p.k, p.v, p.dout):
+        x[at] = bad
+    keep = torch.ones(int(p.cq[-1]), dtype=torch.bool)
+    keep[at] = False
+    got = p.forward()
+    _same([x[keep] for x in got], [x[keep] for x in fwd], "forward")
+    assert not bool(torch.isfinite(got[0][at]).any())
+    _same([x[keep] for x in p.backward(fwd=got)[:3]], [x[keep] for x in bwd[:3]], "backward")
+
+
 # ---------------------------------------------------------------- decode
 
 class Paged:
