@@ -24,18 +24,19 @@
 //     group, query tiles ascending from the diagonal, heads inside.  TMEM rows
 //     are keys, columns queries; four 64-column areas rotate:
 //       a: S_1 -> P'    b: S_2 -> dS_2    c: dP -> dS_1    d: S_1 of u + 1
-//     in the tensor core's order  dV(u) S_2(u+1)>a | dK_2(u) dP(u+1)>b dK_1(u)
-//     S_1(u+2)>c, each product into an area that the one issued before it has
-//     read, so that P of u + 1 is formed while dK(u) and dP(u + 1) run.
+//     S_2 of u + 1 follows dV(u) into a, dP of u + 1 follows dK_2(u) into b,
+//     S_1 of u + 2 follows dK_1(u) into c, so that P of u + 1 is formed while
+//     dK(u) and dP(u + 1) run.
 //   KIND 1 (dQ): resident Q_i, dO_i; streamed K_j, V_j, ascending.  TMEM rows
 //     are queries, columns keys; two sets of three areas, S_1, S_2 (dS_m over
-//     them) and dP:  S/dP(u+1) | dQ_1(u) dQ_2(u).
+//     them) and dP, one computed while the other is used.
 //
 // Warp roles (512 threads):
 //   warps 0-7    P and dS: warp w takes TMEM lane quadrant w mod 4 and 32 of the
 //                64 columns
-//   warp  8      TMA producer, warp 9 TMEM allocator and MMA issuer, warp 10 the
-//                column statistics of dK/dV
+//   warp  8      TMA producer
+//   warp  9      TMEM allocator, issuer of S and dP; warp 11 of dV, dK, dQ
+//   warp  10     the column statistics of dK/dV
 //   warps 12-15  accumulators to global memory
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -52,8 +53,8 @@ namespace {
 
 constexpr int kDBThreads = 512;
 constexpr int kDBRegsLaunch = 128;
-// P/dS warps 168, producer / MMA 48, accumulators 128
-static_assert(2 * 168 + 48 + 128 <= 4 * kDBRegsLaunch, "register split");
+// P/dS warps 160, producer / MMA 48, accumulators 144
+static_assert(2 * 160 + 48 + 144 <= 4 * kDBRegsLaunch, "register split");
 constexpr int kFlush = 8;  // tiles (of 16 products) between flushes of an accumulator
 
 struct DBwdLayout {
@@ -67,7 +68,8 @@ struct DBwdLayout {
   static constexpr int kVecFloats = 4 * 128 + 4;  // lse_1, lse_2 (log2), Delta_1, Delta_2 of 128 queries; -lambda
   static constexpr int kBarOff = kVecOff + 2 * kVecFloats * 4;
   static constexpr int kResFull = 0, kResEmpty = 1, kStFull = 2, kStEmpty = 4, kSFull = 6, kDPFull = 8, kPFull = 10,
-                       kDSFull = 12, kAccFull = 14, kAccEmpty = 16, kVecFull = 18, kVecEmpty = 20, kNumBars = 22;
+                       kDSFull = 12, kAccFull = 14, kAccEmpty = 16, kVecFull = 18, kVecEmpty = 20, kVDone = 22,
+                       kK2Done = 24, kK1Done = 26, kNumBars = 28;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kTotal = kMiscOff + 16;
   static constexpr int kAlloc = kTotal + 1024;
@@ -76,16 +78,13 @@ static_assert(DBwdLayout::kAlloc <= 232448, "backward shared memory");
 static_assert(DBwdLayout::kBarOff % 16 == 0, "alignment");
 using L = DBwdLayout;
 
-__device__ __forceinline__ uint64_t kdesc(uint32_t tile, int k) {  // K-major operand, K-step k (16 elements)
-  return sdesc_sw128(tile + (k >> 2) * L::kHalf + (k & 3) * 32, 16, 1024);
-}
-__device__ __forceinline__ uint64_t mndesc(uint32_t tile, int k) {  // MN-major operand, K-step k (16 rows)
-  return sdesc_sw128(tile + k * 16 * 128, L::kHalf, 1024);
-}
+// KIND 0: area a of step n; b, c and d follow it mod 4, and d(n) = a(n + 1)
+__device__ __forceinline__ uint32_t area_a(uint32_t n) { return (0u - n) & 3u; }
 
 // A warp's bounded wait, and one arrival for a whole warp.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, ErrWord* err,
                                          unsigned int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
@@ -105,6 +104,13 @@ template <int KIND>
 __device__ __forceinline__ int item_tiles(const BwdParams& p, const BwdItem& it) {
   const int len = p.cu[it.seq + 1] - p.cu[it.seq];
   return KIND == 0 ? ((len + 127) / 128 - it.block) * p.group : (it.block + it.rows - 1) / 128 + 1;
+}
+
+// A load from shared memory that stays where it is written.
+__device__ __forceinline__ float4 lds4(const float* p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(p)) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void red_add4(float* p, const float4& v) {
@@ -139,6 +145,9 @@ __global__ void __launch_bounds__(kDBThreads, 1)
       mbar_init(&bars[L::kAccEmpty + s], 4);
       mbar_init(&bars[L::kVecFull + s], 1);
       mbar_init(&bars[L::kVecEmpty + s], 8);
+      mbar_init(&bars[L::kVDone + s], 1);
+      mbar_init(&bars[L::kK2Done + s], 1);
+      mbar_init(&bars[L::kK1Done + s], 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -183,6 +192,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           tma_load_3d(a + L::kTile, m1, bar, 0, it.head, r);
           tma_load_3d(a + L::kTile + L::kHalf, m1, bar, 64, it.head, r);
         }
+        int row = KIND == 0 ? tok0 + it.block * 128 : tok0, h = KIND == 0 ? it.head * p.group : it.head / p.group;
         for (int t = 0; t < tiles; ++t, ++st_it) {
           const uint32_t stage = st_it & 1;
           if (!wait_all(&bars[L::kStEmpty + stage], ((st_it >> 1) & 1) ^ 1, abort, p.err, 0xd02)) { fail = true; break; }
@@ -192,69 +202,67 @@ __global__ void __launch_bounds__(kDBThreads, 1)
             mbar_arrive_expect_tx(bar, 2 * L::kTile);
             const CUtensorMap* m0 = KIND == 0 ? &tm_q : &tm_k;
             const CUtensorMap* m1 = KIND == 0 ? &tm_do : &tm_v;
-            const int h = KIND == 0 ? it.head * p.group + t % p.group : it.head / p.group;
-            const int r = tok0 + (KIND == 0 ? it.block + t / p.group : t) * 128;
-            tma_load_3d(d, m0, bar, 0, h, r);
-            tma_load_3d(d + L::kHalf, m0, bar, 64, h, r);
-            tma_load_3d(d + L::kTile, m1, bar, 0, h, r);
-            tma_load_3d(d + L::kTile + L::kHalf, m1, bar, 64, h, r);
+            tma_load_3d(d, m0, bar, 0, h, row);
+            tma_load_3d(d + L::kHalf, m0, bar, 64, h, row);
+            tma_load_3d(d + L::kTile, m1, bar, 0, h, row);
+            tma_load_3d(d + L::kTile + L::kHalf, m1, bar, 64, h, row);
+          }
+          if (KIND == 1 || ++h == (it.head + 1) * p.group) {  // (KIND 0: the next query tile after the group's heads)
+            if (KIND == 0) h -= p.group;
+            row += 128;
           }
         }
       }
     } else if (warp == 9) {
-      // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdK = idesc_bf16(128, 64, false, false);    // S, dP: both operands K-major
-      constexpr uint32_t kIdV = idesc_bf16(128, 128, false, true);    // dV: A in TMEM, B MN-major
-      constexpr uint32_t kIdMap = idesc_bf16(128, 64, false, true);   // dK_m, dQ_m
+      // ---------------------------------------------------------- S / dP issuer
+      constexpr uint32_t kIdK = idesc_bf16(128, 64, false, false);  // both operands K-major
       const uint32_t leader = elect_one_sync();
       // S_m of half c of the streamed tile at st: the map's four K-steps
       auto issue_s = [&](uint32_t d, uint32_t st, int c, int m) {
+        const Desc a = make_desc(res_addr + m * L::kHalf, 16, 1024), b = make_desc(st + m * L::kHalf + c * 64 * 128, 16, 1024);
+        if (leader) {
+          mma_ss<0>(d, a, 0, b, 0, kIdK);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (leader)
-            umma_ss(d, kdesc(res_addr + m * L::kHalf, k), kdesc(st + m * L::kHalf + c * 64 * 128, k), kIdK, k > 0);
+          for (int k = 1; k < 4; ++k) mma_ss<1>(d, a, 2 * k, b, 2 * k, kIdK);
+        }
       };
       auto issue_dp = [&](uint32_t d, uint32_t st, int c) {
+        const Desc a = make_desc(res_addr + L::kTile, 16, 1024), b = make_desc(st + L::kTile + c * 64 * 128, 16, 1024);
+        if (leader) {
+          mma_ss<0>(d, a, 0, b, 0, kIdK);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (leader) umma_ss(d, kdesc(res_addr + L::kTile, k), kdesc(st + L::kTile + c * 64 * 128, k), kIdK, k > 0);
-      };
-      // acc (+)= the 64-column area a (hi, then lo, of four K-steps) times rows 64 c .. of the tile at b
-      auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t b, int c, uint32_t id, bool first) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (leader) umma_ts(acc, a + 16 * k, mndesc(b, 4 * c + k), id, (first && k == 0) ? 0u : 1u);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (leader) umma_ts(acc, a + 16 * k + 8, mndesc(b, 4 * c + k), id, 1u);
+          for (int k = 1; k < 8; ++k)
+            mma_ss<1>(d, a, (k >> 2) * (L::kHalf >> 4) + (k & 3) * 2, b, (k >> 2) * (L::kHalf >> 4) + (k & 3) * 2, kIdK);
+        }
       };
       auto commit = [&](int bar) {
         if (leader) umma_commit(&bars[bar]);
       };
-      uint32_t res_it = 0, st_it = 0, u_it = 0, fl_it = 0;
+      auto wait = [&](int bar, uint32_t parity, unsigned int site) {
+        const bool ok = wait_all(&bars[bar], parity, abort, p.err, site);
+        tc_fence_after();
+        return ok;
+      };
+      uint32_t res_it = 0, st_it = 0, n = 0;
       bool fail = false;
       for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
         const int item = item_of_round(p, round);
         if (item < 0) continue;
         const BwdItem it = bwd_item(p, item);
         const int tiles = item_tiles<KIND>(p, it), steps = 2 * tiles;
-        auto wait = [&](int bar, uint32_t parity, unsigned int site) {
-          const bool ok = wait_all(&bars[bar], parity, abort, p.err, site);
-          tc_fence_after();
-          return ok;
-        };
+        // of the streamed tiles only those of the last 128 rows can be short
+        const int len = p.cu[it.seq + 1] - p.cu[it.seq];
+        const int short_from = KIND == 0 ? tiles - p.group : (len & ~127) / 128, short_rows = len & 127;
         // the item's streamed tile t has landed; its rows past the sequence's
         // end (another sequence's, whose Inf or NaN times a weight of 0 would
         // be NaN) become zeros
-        const int len = p.cu[it.seq + 1] - p.cu[it.seq];
         auto landed = [&](int t) {
           const uint32_t si = st_it + t;
           if (!wait(L::kStFull + (si & 1), (si >> 1) & 1, 0xd12)) return false;
-          const int valid = len - (KIND == 0 ? it.block + t / p.group : t) * 128;
-          if (valid < 128) {
+          if (short_rows && t >= short_from) {
             uint8_t* d = st_base + (si & 1) * 2 * L::kTile;
-            for (int i = lane; i < (128 - valid) * 32; i += 32) {
-              const int row = valid + (i >> 5), piece = i & 31;  // 16-byte pieces: 8 per half row, two tiles
+            for (int i = lane; i < (128 - short_rows) * 32; i += 32) {
+              const int row = short_rows + (i >> 5), piece = i & 31;  // 16-byte pieces: 8 per half row, two tiles
               *reinterpret_cast<uint4*>(d + (piece >> 3) * L::kHalf + row * 128 + (piece & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
             }
@@ -265,88 +273,112 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         };
         if (!wait(L::kResFull, res_it & 1, 0xd11) || !landed(0)) break;
         ++res_it;
-        if constexpr (KIND == 0) {
-          uint32_t a = area(0), b = area(1), c3 = area(2), d = area(3);
-          const uint32_t acc_v = tmem + 256, acc_k = tmem + 384;
-          issue_s(a, stage_addr(st_it), 0, 0);
-          issue_s(b, stage_addr(st_it), 0, 1);
-          commit(L::kSFull + (u_it & 1));
-          issue_dp(c3, stage_addr(st_it), 0);
-          commit(L::kDPFull + (u_it & 1));
-          issue_s(d, stage_addr(st_it), 1, 0);
-          __syncwarp();
-          for (int u = 0; u < steps; ++u, ++u_it) {
-            const int t = u >> 1, c = u & 1;
-            const bool first = c == 0 && t % kFlush == 0;  // of an accumulator
-            const bool last = c == 1 && (t % kFlush == kFlush - 1 || t + 1 == tiles);
-            const uint32_t cur = stage_addr(st_it + t), nxt = stage_addr(st_it + ((u + 1) >> 1));
-            const uint32_t par = (u_it >> 1) & 1, npar = (u_it + 1) & 1;
-            if (!wait(L::kPFull + (u_it & 1), par, 0xd13)) { fail = true; break; }
-            if (first && !wait(L::kAccEmpty, (fl_it & 1) ^ 1, 0xd14)) { fail = true; break; }
-            issue_acc(acc_v, a, cur + L::kTile, c, kIdV, first);
-            if (last) commit(L::kAccFull);
-            if (u + 1 < steps) {
-              issue_s(a, nxt, c ^ 1, 1);
-              commit(L::kSFull + npar);
-            }
-            __syncwarp();
-            if (!wait(L::kDSFull + (u_it & 1), par, 0xd15)) { fail = true; break; }
-            if (first && !wait(L::kAccEmpty + 1, (fl_it & 1) ^ 1, 0xd16)) { fail = true; break; }
-            issue_acc(acc_k + 64, b, cur + L::kHalf, c, kIdMap, first);
-            if (u + 1 < steps) {
-              issue_dp(b, nxt, c ^ 1);
-              commit(L::kDPFull + npar);
-              if (u + 2 == steps) commit(L::kResEmpty);  // the item's last S/dP
-            }
-            issue_acc(acc_k, c3, cur, c, kIdMap, first);
-            if (last) {
-              commit(L::kAccFull + 1);
-              ++fl_it;
-            }
-            if (c == 1) commit(L::kStEmpty + ((st_it + t) & 1));
-            if (u + 2 < steps) {
-              if (c == 0 && !landed((u + 2) >> 1)) { fail = true; break; }
-              issue_s(c3, stage_addr(st_it + ((u + 2) >> 1)), c, 0);
-            }
-            __syncwarp();
-            const uint32_t x = d;
-            d = c3;
-            c3 = b;
-            b = a;
-            a = x;
-          }
-        } else {
-          const uint32_t acc = tmem + 384;
-          auto issue_set = [&](uint32_t set, uint32_t st, int c) {
-            issue_s(area(3 * set), st, c, 0);
-            issue_s(area(3 * set + 1), st, c, 1);
-            issue_dp(area(3 * set + 2), st, c);
-            commit(L::kSFull + set);
-          };
-          issue_set(u_it & 1, stage_addr(st_it), 0);
-          __syncwarp();
-          for (int u = 0; u < steps; ++u, ++u_it) {
-            const int t = u >> 1, c = u & 1;
-            const bool first = c == 0 && t % kFlush == 0;
-            const bool last = c == 1 && (t % kFlush == kFlush - 1 || t + 1 == tiles);
-            const uint32_t set = u_it & 1, cur = stage_addr(st_it + t);
+        for (int u = 0; u < steps; ++u, ++n) {
+          const int c = u & 1;
+          const uint32_t st = stage_addr(st_it + (u >> 1)), x = n & 1;
+          if constexpr (KIND == 0) {
+            // an area is free once the product that read it last is done: that
+            // of a(n), dK_1 of n - 2; of b(n), dV of n - 1; of c(n), dK_2 of n - 1
+            auto issue_s1 = [&](uint32_t k, uint32_t at, int cc) {
+              if (!wait(L::kK1Done + (k & 1), ((k >> 1) & 1) ^ 1, 0xd13)) return false;
+              issue_s(area(area_a(k)), at, cc, 0);
+              return true;
+            };
+            if (u == 0 && !issue_s1(n, st, 0)) { fail = true; break; }
+            if (n > 0 && !wait(L::kVDone + (x ^ 1), ((n - 1) >> 1) & 1, 0xd14)) { fail = true; break; }
+            issue_s(area((area_a(n) + 1) & 3), st, c, 1);
+            commit(L::kSFull + x);
+            if (n > 0 && !wait(L::kK2Done + (x ^ 1), ((n - 1) >> 1) & 1, 0xd15)) { fail = true; break; }
+            issue_dp(area((area_a(n) + 2) & 3), st, c);
+            commit(L::kDPFull + x);
+            if (u + 1 == steps) commit(L::kResEmpty);  // the item's last S/dP
             if (u + 1 < steps) {
               if (c == 1 && !landed((u + 1) >> 1)) { fail = true; break; }
-              issue_set(set ^ 1, stage_addr(st_it + ((u + 1) >> 1)), c ^ 1);
-              if (u + 2 == steps) commit(L::kResEmpty);  // the item's last S/dP
+              if (!issue_s1(n + 1, stage_addr(st_it + ((u + 1) >> 1)), c ^ 1)) { fail = true; break; }
             }
-            __syncwarp();
-            if (!wait(L::kDSFull + set, (u_it >> 1) & 1, 0xd15)) { fail = true; break; }
-            if (first && !wait(L::kAccEmpty, (fl_it & 1) ^ 1, 0xd14)) { fail = true; break; }
-            issue_acc(acc, area(3 * set), cur, c, kIdMap, first);
-            issue_acc(acc + 64, area(3 * set + 1), cur + L::kHalf, c, kIdMap, first);
-            if (last) {
-              commit(L::kAccFull);
-              ++fl_it;
-            }
-            if (c == 1) commit(L::kStEmpty + ((st_it + t) & 1));
-            __syncwarp();
+          } else {
+            if (c == 0 && u > 0 && !landed(u >> 1)) { fail = true; break; }
+            if (!wait(L::kVDone + x, ((n >> 1) & 1) ^ 1, 0xd13)) { fail = true; break; }  // the set's last products
+            issue_s(area(3 * x), st, c, 0);
+            issue_s(area(3 * x + 1), st, c, 1);
+            issue_dp(area(3 * x + 2), st, c);
+            commit(L::kSFull + x);
+            if (u + 1 == steps) commit(L::kResEmpty);
           }
+          __syncwarp();
+        }
+        st_it += tiles;
+      }
+    } else if (warp == 11) {
+      // ---------------------------------------------------------- accumulation issuer
+      // (a warp of its own: the tensor core's queue holds a few products, and
+      // one warp's barrier checks between its bursts let it run dry)
+      constexpr uint32_t kIdV = idesc_bf16(128, 128, false, true);   // dV: A in TMEM, B MN-major
+      constexpr uint32_t kIdMap = idesc_bf16(128, 64, false, true);  // dK_m, dQ_m
+      const uint32_t leader = elect_one_sync();
+      // acc (+)= the 64-column area a (hi, then lo, of four K-steps) times rows 64 c .. of the tile at b
+      auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t b, int c, uint32_t id, bool first) {
+        const Desc bd = make_desc(b + c * 64 * 128, L::kHalf, 1024);
+        if (leader) {
+          if (first) mma_ts<0>(acc, a, bd, 0, id);
+          else mma_ts<1>(acc, a, bd, 0, id);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mma_ts<1>(acc, a + 16 * k, bd, 128 * k, id);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ts<1>(acc, a + 16 * k + 8, bd, 128 * k, id);
+        }
+      };
+      auto commit = [&](int bar) {
+        if (leader) umma_commit(&bars[bar]);
+      };
+      auto wait = [&](int bar, uint32_t parity, unsigned int site) {
+        const bool ok = wait_all(&bars[bar], parity, abort, p.err, site);
+        tc_fence_after();
+        return ok;
+      };
+      uint32_t st_it = 0, n = 0, fl_v = 0, fl_k = 0;
+      bool fail = false;
+      for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
+        const int item = item_of_round(p, round);
+        if (item < 0) continue;
+        const BwdItem it = bwd_item(p, item);
+        const int tiles = item_tiles<KIND>(p, it), steps = 2 * tiles;
+        for (int u = 0; u < steps; ++u, ++n) {
+          const int t = u >> 1, c = u & 1;
+          const bool first = c == 0 && t % kFlush == 0;  // of dV (dQ)
+          const bool last = c == 1 && (t % kFlush == kFlush - 1 || t + 1 == tiles);
+          const uint32_t st = stage_addr(st_it + t), x = n & 1, par = (n >> 1) & 1;
+          if constexpr (KIND == 0) {
+            const uint32_t a = area_a(n);
+            const bool first_k = c == 0 && (t == 0 || t % kFlush == kFlush / 2);
+            const bool last_k = c == 1 && (t % kFlush == kFlush / 2 - 1 || t + 1 == tiles);
+            if (first && !wait(L::kAccEmpty, (fl_v & 1) ^ 1, 0xd21)) { fail = true; break; }
+            if (!wait(L::kPFull + x, par, 0xd22)) { fail = true; break; }
+            issue_acc(tmem + 256, area(a), st + L::kTile, c, kIdV, first);
+            commit(L::kVDone + x);
+            if (last) commit(L::kAccFull);
+            __syncwarp();
+            if (first_k && !wait(L::kAccEmpty + 1, (fl_k & 1) ^ 1, 0xd23)) { fail = true; break; }
+            if (!wait(L::kDSFull + x, par, 0xd24)) { fail = true; break; }
+            issue_acc(tmem + 448, area((a + 1) & 3), st + L::kHalf, c, kIdMap, first_k);
+            commit(L::kK2Done + x);
+            issue_acc(tmem + 384, area((a + 2) & 3), st, c, kIdMap, first_k);
+            commit(L::kK1Done + x);
+            if (last_k) {
+              commit(L::kAccFull + 1);
+              ++fl_k;
+            }
+          } else {
+            if (first && !wait(L::kAccEmpty, (fl_v & 1) ^ 1, 0xd21)) { fail = true; break; }
+            if (!wait(L::kDSFull + x, par, 0xd24)) { fail = true; break; }
+            issue_acc(tmem + 384, area(3 * x), st, c, kIdMap, first);
+            issue_acc(tmem + 448, area(3 * x + 1), st + L::kHalf, c, kIdMap, first);
+            commit(L::kVDone + x);
+            if (last) commit(L::kAccFull);
+          }
+          if (last) ++fl_v;
+          if (c == 1) commit(L::kStEmpty + ((st_it + t) & 1));
+          __syncwarp();
         }
         st_it += tiles;
       }
@@ -362,8 +394,12 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         const BwdItem it = bwd_item(p, item);
         const int tiles = item_tiles<KIND>(p, it);
         const int tok0 = p.cu[it.seq], len = p.cu[it.seq + 1] - tok0;
+        int q0 = it.block * 128, h = it.head * p.group - 1;
         for (int t = 0; t < tiles; ++t, ++v_it) {
-          const int q0 = (it.block + t / p.group) * 128, h = it.head * p.group + t % p.group;
+          if (++h == (it.head + 1) * p.group) {
+            h -= p.group;
+            q0 += 128;
+          }
           const int64_t at = 2 * static_cast<int64_t>(h) * p.t_pad + tok0 + q0;
           float x[4][4];
 #pragma unroll
@@ -392,57 +428,71 @@ __global__ void __launch_bounds__(kDBThreads, 1)
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ P / dS
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
-    const int wq = warp & 3, wh = warp >> 2;
-    const int r = wq * 32 + lane;  // tile row = TMEM lane
-    const uint32_t off = (static_cast<uint32_t>(wq * 32) << 16) + 32 * wh;  // the warp's lanes and columns of an area
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;" ::: "memory");
+    const int wh = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // tile row = TMEM lane
+    const uint32_t off = (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * wh;  // the warp's lanes and columns of an area
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-    uint32_t u_it = 0, v_it = 0;
+    uint32_t s_it = 0, v_it = 0;
     bool fail = false;
-    // stores a 32-column group's parts: per 16 columns 8 words hi, then 8 lo
-    auto put = [&](uint32_t ta, const uint32_t (&w)[32]) { tmem_st32(ta + off, w); };
+    auto f2 = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
+    auto bar_wait = [&](int bar, uint32_t parity, unsigned int site) {
+      const bool ok = wait_all(&bars[bar], parity, abort, p.err, site);
+      tc_fence_after();
+      return ok;
+    };
+    auto stored = [&](int bar) {
+      tmem_st_wait();
+      tc_fence_before();
+      arrive_warp(&bars[bar], lane);
+    };
     for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
       const int item = item_of_round(p, round);
       if (item < 0) continue;
       const BwdItem it = bwd_item(p, item);
-      const int tiles = item_tiles<KIND>(p, it), steps = 2 * tiles;
+      const int tiles = item_tiles<KIND>(p, it);
       const int tok0 = p.cu[it.seq], len = p.cu[it.seq + 1] - tok0;
       if constexpr (KIND == 0) {
         const int key_pos = it.block * 128 + r;
-        uint32_t a = 0, b = 1, c3 = 2, d = 3;
-        for (int u = 0; u < steps; ++u, ++u_it) {
-          const int t = u >> 1, c = u & 1;
-          const uint32_t vb = (v_it + t) & 1, par = (u_it >> 1) & 1;
+        int q0 = it.block * 128 + 32 * wh, hh = 0;  // position of the warp's first column
+        for (int u = 0; u < 2 * tiles; ++u, ++s_it) {
+          const int c = u & 1;
+          const uint32_t a = area_a(s_it), vb = v_it & 1, x = s_it & 1, par = (s_it >> 1) & 1;
+          const uint32_t ta = area(a) + off, tb = area((a + 1) & 3) + off, td = area((a + 2) & 3) + off;
           const float* v = vecs + vb * L::kVecFloats + 64 * c + 32 * wh;
-          const int q0 = (it.block + t / p.group) * 128 + 64 * c + 32 * wh;  // position of the warp's first column
-          bool ok = c == 1 || wait_all(&bars[L::kVecFull + vb], ((v_it + t) >> 1) & 1, abort, p.err, 0xd31);
-          ok = ok && wait_all(&bars[L::kSFull + (u_it & 1)], par, abort, p.err, 0xd32);
-          if (!ok) { fail = true; break; }
-          tc_fence_after();
+          if (c == 0 && !bar_wait(L::kVecFull + vb, (v_it >> 1) & 1, 0xd31)) { fail = true; break; }
+          // the columns' statistics go into registers before the waits: S and dP
+          // take the whole of shared memory's bandwidth, and a load beside them
+          // takes hundreds of cycles
+          float4 l1[8], l2[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            l1[i] = lds4(v + 4 * i);
+            l2[i] = lds4(v + 128 + 4 * i);
+          }
+          const float nl = *reinterpret_cast<const volatile float*>(vecs + vb * L::kVecFloats + 512);
+          if (!bar_wait(L::kSFull + x, par, 0xd32)) { fail = true; break; }
           // P_1 and -lambda P_2 of the warp's elements, kept for dS
           uint32_t p1[32], p2[32];
-          tmem_ld32(area(a) + off, p1);
-          tmem_ld32(area(b) + off, p2);
-          tmem_ld_wait(p1);
-          tmem_ld_wait(p2);
-          const float nl = vecs[vb * L::kVecFloats + 512];
+          tmem_ld32(ta, p1);
+          tmem_ld32(tb, p2);
           const float2 nl2 = make_float2(nl, nl);
           const bool full = __all_sync(0xffffffffu, key_pos < len && q0 + 31 < len && q0 >= key_pos);
-          {
-            uint32_t w[32];
-            auto probs = [&](auto masked) {
+          tmem_ld_wait(p1);
+          tmem_ld_wait(p2);
+          auto weights = [&](auto masked) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 l1 = *reinterpret_cast<const float4*>(v + e);
-                const float4 l2 = *reinterpret_cast<const float4*>(v + 128 + e);
-                const float la[4] = {l1.x, l1.y, l1.z, l1.w}, lb[4] = {l2.x, l2.y, l2.z, l2.w};
+            for (int k = 0; k < 32; k += 16) {
+              uint32_t w[16];  // a K-step of the product: 8 words hi, then 8 lo
+#pragma unroll
+              for (int e = k; e < k + 16; e += 4) {
+                const float la[4] = {l1[e / 4].x, l1[e / 4].y, l1[e / 4].z, l1[e / 4].w};
+                const float lb[4] = {l2[e / 4].x, l2[e / 4].y, l2[e / 4].z, l2[e / 4].w};
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
-                  const float2 x = ffma2(make_float2(__uint_as_float(p1[e + i]), __uint_as_float(p1[e + i + 1])), sl2,
-                                         make_float2(-la[i], -la[i + 1]));
-                  const float2 y = ffma2(make_float2(__uint_as_float(p2[e + i]), __uint_as_float(p2[e + i + 1])), sl2,
-                                         make_float2(-lb[i], -lb[i + 1]));
-                  float2 q = make_float2(ex2_hw(x.x), ex2_hw(x.y)), s = make_float2(ex2_hw(y.x), ex2_hw(y.y));
+                  const float2 y = ffma2(f2(p1[e + i], p1[e + i + 1]), sl2, make_float2(-la[i], -la[i + 1]));
+                  const float2 z = ffma2(f2(p2[e + i], p2[e + i + 1]), sl2, make_float2(-lb[i], -lb[i + 1]));
+                  float2 q = make_float2(ex2_hw(y.x), ex2_hw(y.y)), s = make_float2(ex2_hw(z.x), ex2_hw(z.y));
                   if constexpr (decltype(masked)::value) {
                     const int qa = q0 + e + i, qb = qa + 1;
                     const bool oka = key_pos < len && qa < len && qa >= key_pos;
@@ -455,52 +505,61 @@ __global__ void __launch_bounds__(kDBThreads, 1)
                   p1[e + i + 1] = __float_as_uint(q.y);
                   p2[e + i] = __float_as_uint(s.x);
                   p2[e + i + 1] = __float_as_uint(s.y);
-                  const int slot = ((e + i) >> 4) * 16 + (((e + i) & 15) >> 1);
-                  split_pair2(fadd2(q, s), w[slot], w[slot + 8]);
+                  const int slot = (e - k + i) >> 1;
+                  split_pair2(fadd2(q, s), w[slot], w[8 + slot]);
                 }
               }
-            };
-            if (full) probs(std::false_type{});
-            else probs(std::true_type{});
-            put(area(a), w);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          arrive_warp(&bars[L::kPFull + (u_it & 1)], lane);
-          if (!wait_all(&bars[L::kDPFull + (u_it & 1)], par, abort, p.err, 0xd33)) { fail = true; break; }
-          tc_fence_after();
-          uint32_t dp[32], w[32];
-          tmem_ld32(area(c3) + off, dp);
+              tmem_st16(ta + k, w);
+            }
+          };
+          if (full) weights(std::false_type{});
+          else weights(std::true_type{});
+          stored(L::kPFull + x);
+          float4 e1[4], e2[4];
+          auto deltas = [&](int k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e1[i] = lds4(v + 256 + k + 4 * i);
+              e2[i] = lds4(v + 384 + k + 4 * i);
+            }
+          };
+          deltas(0);
+          if (!bar_wait(L::kDPFull + x, par, 0xd33)) { fail = true; break; }
+          uint32_t dp[32];
+          tmem_ld32(td, dp);
           tmem_ld_wait(dp);
 #pragma unroll
-          for (int m = 1; m >= 0; --m) {
+          for (int k = 0; k < 32; k += 16) {
+            uint32_t w1[16], w2[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 dl = *reinterpret_cast<const float4*>(v + 256 + 128 * m + e);
-              const float da[4] = {dl.x, dl.y, dl.z, dl.w};
+            for (int e = k; e < k + 16; e += 4) {
+              const float4 d1 = e1[(e - k) / 4], d2 = e2[(e - k) / 4];
+              const float da[4] = {d1.x, d1.y, d1.z, d1.w}, db[4] = {d2.x, d2.y, d2.z, d2.w};
 #pragma unroll
               for (int i = 0; i < 4; i += 2) {
-                const float2 q = m ? make_float2(__uint_as_float(p2[e + i]), __uint_as_float(p2[e + i + 1]))
-                                   : make_float2(__uint_as_float(p1[e + i]), __uint_as_float(p1[e + i + 1]));
-                const float2 ds = fmul2(q, fsub2(make_float2(__uint_as_float(dp[e + i]), __uint_as_float(dp[e + i + 1])),
-                                                 make_float2(da[i], da[i + 1])));
-                const int slot = ((e + i) >> 4) * 16 + (((e + i) & 15) >> 1);
-                split_pair2(ds, w[slot], w[slot + 8]);
+                const float2 g = f2(dp[e + i], dp[e + i + 1]);
+                const int slot = (e - k + i) >> 1;
+                split_pair2(fmul2(f2(p2[e + i], p2[e + i + 1]), fsub2(g, make_float2(db[i], db[i + 1]))), w2[slot], w2[8 + slot]);
+                split_pair2(fmul2(f2(p1[e + i], p1[e + i + 1]), fsub2(g, make_float2(da[i], da[i + 1]))), w1[slot], w1[8 + slot]);
               }
             }
-            put(area(m ? b : c3), w);
+            if (k == 0) deltas(16);
+            tmem_st16(tb + k, w2);
+            tmem_st16(td + k, w1);
           }
-          tmem_st_wait();
-          tc_fence_before();
-          arrive_warp(&bars[L::kDSFull + (u_it & 1)], lane);
-          if (c == 1) arrive_warp(&bars[L::kVecEmpty + vb], lane);
-          const uint32_t x = d;
-          d = c3;
-          c3 = b;
-          b = a;
-          a = x;
+          stored(L::kDSFull + x);
+          if (c == 0) {
+            q0 += 64;
+          } else {
+            arrive_warp(&bars[L::kVecEmpty + vb], lane);
+            ++v_it;
+            q0 -= 64;
+            if (++hh == p.group) {
+              hh = 0;
+              q0 += 128;
+            }
+          }
         }
-        v_it += tiles;
       } else {
         // the row's statistics are fixed for the item
         const int row_pos = it.block + r;
@@ -514,56 +573,56 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           dl2 = __ldg(p.delta_t + at + p.t_pad);
         }
         const float nl = -__ldg(p.lambda + it.head);
-        for (int u = 0; u < steps; ++u, ++u_it) {
-          const uint32_t set = u_it & 1;
-          const int k0 = (u >> 1) * 128 + 64 * (u & 1) + 32 * wh;  // position of the warp's first column
-          if (!wait_all(&bars[L::kSFull + set], (u_it >> 1) & 1, abort, p.err, 0xd32)) { fail = true; break; }
-          tc_fence_after();
-          uint32_t dp[32], s1[32], s2[32];
-          tmem_ld32(area(3 * set) + off, s1);
-          tmem_ld32(area(3 * set + 2) + off, dp);
-          tmem_ld32(area(3 * set + 1) + off, s2);
+        const float2 nl2 = make_float2(nl, nl), n1 = make_float2(-lse1, -lse1), n2 = make_float2(-lse2, -lse2),
+                     d1 = make_float2(dl1, dl1), d2 = make_float2(dl2, dl2);
+        int k0 = 32 * wh;  // position of the warp's first column
+        for (int u = 0; u < 2 * tiles; ++u, ++s_it, k0 += 64) {
+          const uint32_t x = s_it & 1;
+          const uint32_t t1 = area(3 * x) + off, t2 = t1 + 64, td = t1 + 128;
+          if (!bar_wait(L::kSFull + x, (s_it >> 1) & 1, 0xd32)) { fail = true; break; }
+          uint32_t s1[32], s2[32], dp[32];
+          tmem_ld32(t1, s1);
+          tmem_ld32(td, dp);
+          tmem_ld32(t2, s2);
+          const bool full = __all_sync(0xffffffffu, row_ok && k0 + 31 <= row_pos);
           tmem_ld_wait(s1);
           tmem_ld_wait(dp);
           tmem_ld_wait(s2);
-          const bool full = __all_sync(0xffffffffu, row_ok && k0 + 31 <= row_pos);
-          auto one = [&](uint32_t (&s)[32], uint32_t ta, float lse, float dl, float coef, auto second, auto masked) {
-            const float2 nlse = make_float2(-lse, -lse), d2 = make_float2(dl, dl), c2 = make_float2(coef, coef);
-            uint32_t w[32];
+          auto grads = [&](auto masked) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl2, nlse);
-              float2 q = make_float2(ex2_hw(x.x), ex2_hw(x.y));
-              if constexpr (decltype(masked)::value) {
-                q.x = row_ok && k0 + e <= row_pos ? q.x : 0.0f;
-                q.y = row_ok && k0 + e + 1 <= row_pos ? q.y : 0.0f;
+            for (int k = 0; k < 32; k += 16) {
+              uint32_t w1[16], w2[16];
+#pragma unroll
+              for (int e = k; e < k + 16; e += 2) {
+                const float2 y = ffma2(f2(s1[e], s1[e + 1]), sl2, n1), z = ffma2(f2(s2[e], s2[e + 1]), sl2, n2);
+                float2 q = make_float2(ex2_hw(y.x), ex2_hw(y.y)), s = make_float2(ex2_hw(z.x), ex2_hw(z.y));
+                if constexpr (decltype(masked)::value) {
+                  const bool oka = row_ok && k0 + e <= row_pos, okb = row_ok && k0 + e + 1 <= row_pos;
+                  q = make_float2(oka ? q.x : 0.0f, okb ? q.y : 0.0f);
+                  s = make_float2(oka ? s.x : 0.0f, okb ? s.y : 0.0f);
+                }
+                const float2 g = f2(dp[e], dp[e + 1]);
+                const int slot = (e - k) >> 1;
+                split_pair2(fmul2(q, fsub2(g, d1)), w1[slot], w1[8 + slot]);
+                split_pair2(fmul2(fmul2(s, nl2), fsub2(g, d2)), w2[slot], w2[8 + slot]);
               }
-              if constexpr (decltype(second)::value) q = fmul2(q, c2);
-              const float2 ds = fmul2(q, fsub2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), d2));
-              const int slot = (e >> 4) * 16 + ((e & 15) >> 1);
-              split_pair2(ds, w[slot], w[slot + 8]);
+              tmem_st16(t1 + k, w1);
+              tmem_st16(t2 + k, w2);
             }
-            put(ta, w);
           };
-          if (full) {
-            one(s1, area(3 * set), lse1, dl1, 1.0f, std::false_type{}, std::false_type{});
-            one(s2, area(3 * set + 1), lse2, dl2, nl, std::true_type{}, std::false_type{});
-          } else {
-            one(s1, area(3 * set), lse1, dl1, 1.0f, std::false_type{}, std::true_type{});
-            one(s2, area(3 * set + 1), lse2, dl2, nl, std::true_type{}, std::true_type{});
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          arrive_warp(&bars[L::kDSFull + set], lane);
+          if (full) grads(std::false_type{});
+          else grads(std::true_type{});
+          stored(L::kDSFull + x);
         }
       }
     }
   } else {
     // ------------------------------------------------------------ accumulators to global memory
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;" ::: "memory");
     const int wq = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     float4* stg = reinterpret_cast<float4*>(smem + L::kStageOff + wq * (32 * 128));
-    uint32_t fl_it = 0;
+    uint32_t fl[2] = {0, 0};
     bool fail = false;
     for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
       const int item = item_of_round(p, round);
@@ -576,48 +635,51 @@ __global__ void __launch_bounds__(kDBThreads, 1)
       const int rows = KIND == 0 ? min(32, len - row0) : min(32, min(it.rows - 32 * wq, len - row0));
       const int heads = KIND == 0 ? p.hkv : p.hq;
       const int64_t base = (static_cast<int64_t>(tok0 + row0) * heads + it.head) * kHeadDim;
-      for (int t0 = 0; t0 < tiles && !fail; t0 += kFlush, ++fl_it) {
+      // dV (dQ) and dK half a period apart, so that one leaves while the other is summed
+      for (int t = 0; t < tiles && !fail; t += kFlush / 2) {
+        const bool end = t + kFlush / 2 >= tiles;
+        const int v_now = t % kFlush != 0 || end, k_now = KIND == 0 && (t % kFlush == 0 || end);
 #pragma unroll 1
-        for (int which = 0; which < (KIND == 0 ? 2 : 1); ++which) {
-          if (!wait_all(&bars[L::kAccFull + which], fl_it & 1, abort, p.err, 0xd41)) { fail = true; break; }
+        for (int which = 0; which < 2; ++which) {
+          if (!(which ? k_now : v_now)) continue;
+          if (!wait_all(&bars[L::kAccFull + which], fl[which] & 1, abort, p.err, 0xd41)) { fail = true; break; }
+          ++fl[which];
           tc_fence_after();
+          // the whole accumulator into registers, so that the next products
+          // wait for this alone
           const uint32_t src = tmem + (KIND == 0 && which == 0 ? 256 : 384) + lane_off;
+          uint32_t x[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(src + 32 * i, x[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld_wait(x[i]);
+          tc_fence_before();
+          arrive_warp(&bars[L::kAccEmpty + which], lane);
           float* dst = (KIND == 1 ? p.dq : which == 0 ? p.dv : p.dk) + base;
           const float mul = KIND == 0 && which == 0 ? 1.0f : p.scale;
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t x[2][32];
-            tmem_ld32(src + 32 * c, x[0]);
-            tmem_ld32(src + 32 * c + 32, x[1]);
-            tmem_ld_wait(x[0]);
-            tmem_ld_wait(x[1]);
-            if (c == 2) {  // read: free for the next products
-              tc_fence_before();
-              arrive_warp(&bars[L::kAccEmpty + which], lane);
-            }
-            // each 32-column chunk through shared memory (piece j of a row in
-            // slot j ^ (row & 7)), so that four rows leave as whole 128-byte lines
+          const bool fresh = which ? t == 0 || tiles <= kFlush / 2 : t < kFlush;  // nothing in the output yet
+          // each 32-column chunk through shared memory (piece j of a row in
+          // slot j ^ (row & 7)), so that four rows leave as whole 128-byte lines
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < 4; ++i) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                stg[lane * 8 + (j ^ (lane & 7))] =
-                    make_float4(__fmul_rn(__uint_as_float(x[i][4 * j]), mul), __fmul_rn(__uint_as_float(x[i][4 * j + 1]), mul),
-                                __fmul_rn(__uint_as_float(x[i][4 * j + 2]), mul),
-                                __fmul_rn(__uint_as_float(x[i][4 * j + 3]), mul));
-              __syncwarp();
+            for (int j = 0; j < 8; ++j)
+              stg[lane * 8 + (j ^ (lane & 7))] =
+                  make_float4(__fmul_rn(__uint_as_float(x[i][4 * j]), mul), __fmul_rn(__uint_as_float(x[i][4 * j + 1]), mul),
+                              __fmul_rn(__uint_as_float(x[i][4 * j + 2]), mul),
+                              __fmul_rn(__uint_as_float(x[i][4 * j + 3]), mul));
+            __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int rr = 4 * k + (lane >> 3), jj = lane & 7;
-                if (rr < rows) {
-                  float* to = dst + static_cast<int64_t>(rr) * heads * kHeadDim + 32 * (c + i) + 4 * jj;
-                  const float4 val = stg[rr * 8 + (jj ^ (rr & 7))];
-                  if (t0 == 0) *reinterpret_cast<float4*>(to) = val;
-                  else red_add4(to, val);
-                }
+            for (int k = 0; k < 8; ++k) {
+              const int rr = 4 * k + (lane >> 3), jj = lane & 7;
+              if (rr < rows) {
+                float* to = dst + static_cast<int64_t>(rr) * heads * kHeadDim + 32 * i + 4 * jj;
+                const float4 val = stg[rr * 8 + (jj ^ (rr & 7))];
+                if (fresh) *reinterpret_cast<float4*>(to) = val;
+                else red_add4(to, val);
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
         }
       }

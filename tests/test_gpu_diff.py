@@ -316,7 +316,9 @@ def test_backward_without_the_second_map_is_the_plain_one():
     ref = [torch.empty(x.shape, device="cuda") for x in (q, k, v)]
     rlk.rlk_attn_backward(p.params, one, k, v, fwd[0], dout, fwd[3][..., 0].contiguous(), p.cq, -1, *ref, ws)
     for x, y in ((dq[..., :64], ref[0][..., :64]), (dk[..., :64], ref[1][..., :64]), (dv, ref[2])):
-        assert float((x - y).norm()) <= 1e-6 * float(y.norm())
+        # each side is within GRAD_REL_L2 of the definition (the sums' cuts differ,
+        # and the tensor core truncates: 2^-24 of the sum a product)
+        assert float((x - y).norm()) <= 2 * GRAD_REL_L2 * float(y.norm())
     assert not bool(dq[..., 64:].any()) and not bool(dk[..., 64:].any()) and bool(dlam.any())
 
 
