@@ -3,7 +3,7 @@
 //
 // With P_m = exp(scale q_m k_m^T - lse_m), dP = dO V^T and Delta_m = dO . O_m:
 //   dV   = (P_1 - lambda P_2)^T dO
-//   dS_1 = P_1 (dP - Delta_1),  dS_2 = -lambda P_2 (dP - Delta_2)
+//   dS_1 = P_1 (dP - Delta_1),  dS_2 = P_2 (lambda Delta_2 - lambda dP)
 //   dQ_m = scale dS_m K_m,      dK_m = scale dS_m^T Q_m
 // Both maps share dP, and their P's meet in one product for dV: per 128 x 128
 // tile pair the tensor core takes 48 units of a 128 x 128 x 16 product for
@@ -57,26 +57,29 @@ constexpr int kDBRegsLaunch = 128;
 static_assert(2 * 160 + 48 + 144 <= 4 * kDBRegsLaunch, "register split");
 constexpr int kFlush = 8;  // tiles (of 16 products) between flushes of an accumulator
 
+template <int KIND>
 struct DBwdLayout {
   static constexpr int kTile = 128 * kHeadDim * 2;  // one 128 x 128 BF16 tile, two 64-column halves
   static constexpr int kHalf = 128 * 128;
-  static constexpr int kStages = 2;
+  // streamed tiles: dK/dV (Q_i, dO_i) in two slots each; dQ K_j in three, V_j,
+  // which dP alone reads, in two
+  static constexpr int kSlots = KIND == 0 ? 2 : 3, kSlots2 = 2;
   static constexpr int kResOff = 0;  // (K_j, V_j) or (Q_i, dO_i)
   static constexpr int kStreamOff = 2 * kTile;
-  static constexpr int kStageOff = kStreamOff + kStages * 2 * kTile;  // the flush's staging: 4 warps x 32 rows x 128 B
-  static constexpr int kVecOff = kStageOff + 4 * 32 * 128;
-  static constexpr int kVecFloats = 4 * 128 + 4;  // lse_1, lse_2 (log2), Delta_1, Delta_2 of 128 queries; -lambda
-  static constexpr int kBarOff = kVecOff + 2 * kVecFloats * 4;
-  static constexpr int kResFull = 0, kResEmpty = 1, kStFull = 2, kStEmpty = 4, kSFull = 6, kDPFull = 8, kPFull = 10,
-                       kDSFull = 12, kAccFull = 14, kAccEmpty = 16, kVecFull = 18, kVecEmpty = 20, kVDone = 22,
-                       kK2Done = 24, kK1Done = 26, kNumBars = 28;
+  static constexpr int kStream2Off = kStreamOff + kSlots * kTile;
+  static constexpr int kStageOff = kStream2Off + kSlots2 * kTile;  // dK/dV: the flush's staging, 4 warps x 32 rows x 128 B
+  static constexpr int kVecOff = kStageOff + (KIND == 0 ? 4 * 32 * 128 : 0);
+  static constexpr int kVecFloats = 4 * 128 + 4;  // lse_1, lse_2 (log2), Delta_1, lambda Delta_2 of 128 queries; -lambda
+  static constexpr int kBarOff = kVecOff + (KIND == 0 ? 2 * kVecFloats * 4 : 0);
+  static constexpr int kResFull = 0, kResEmpty = 1, kStFull = 2, kStEmpty = 5, kSt2Empty = 8, kSFull = 10, kDPFull = 12,
+                       kPFull = 14, kDSFull = 16, kAccFull = 18, kAccEmpty = 20, kVecFull = 22, kVecEmpty = 24, kVDone = 26,
+                       kK2Done = 28, kK1Done = 30, kNumBars = 32;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kTotal = kMiscOff + 16;
   static constexpr int kAlloc = kTotal + 1024;
+  static_assert(kAlloc <= 232448, "backward shared memory");
+  static_assert(kBarOff % 16 == 0, "alignment");
 };
-static_assert(DBwdLayout::kAlloc <= 232448, "backward shared memory");
-static_assert(DBwdLayout::kBarOff % 16 == 0, "alignment");
-using L = DBwdLayout;
 
 // KIND 0: area a of step n; b, c and d follow it mod 4, and d(n) = a(n + 1)
 __device__ __forceinline__ uint32_t area_a(uint32_t n) { return (0u - n) & 3u; }
@@ -124,6 +127,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
     rlk_dbwd_kernel(const __grid_constant__ BwdParams p, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_do) {
+  using L = DBwdLayout<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
@@ -134,9 +138,12 @@ __global__ void __launch_bounds__(kDBThreads, 1)
   if (tid == 0) {
     mbar_init(&bars[L::kResFull], 1);
     mbar_init(&bars[L::kResEmpty], 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(&bars[L::kStFull + s], 1);
       mbar_init(&bars[L::kStEmpty + s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[L::kSt2Empty + s], 1);
       mbar_init(&bars[L::kSFull + s], 1);
       mbar_init(&bars[L::kDPFull + s], 1);
       mbar_init(&bars[L::kPFull + s], 8);
@@ -163,8 +170,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
   // KIND 0: areas 0 .. 3, dV in 256 .. 383, dK in 384 .. 511; KIND 1: areas 0 .. 5, dQ in 384 .. 511
   auto area = [&](uint32_t i) { return tmem + 64 * i; };
   const uint32_t res_addr = smem_u32(smem + L::kResOff);
-  uint8_t* st_base = smem + L::kStreamOff;
-  auto stage_addr = [&](uint32_t t) { return smem_u32(st_base + (t & 1) * 2 * L::kTile); };
+  auto slot_addr = [&](uint32_t t) { return smem_u32(smem + L::kStreamOff + (t % L::kSlots) * L::kTile); };
+  auto slot2_addr = [&](uint32_t t) { return smem_u32(smem + L::kStream2Off + (t % L::kSlots2) * L::kTile); };
 
   if (warp >= 8 && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
@@ -194,18 +201,22 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         }
         int row = KIND == 0 ? tok0 + it.block * 128 : tok0, h = KIND == 0 ? it.head * p.group : it.head / p.group;
         for (int t = 0; t < tiles; ++t, ++st_it) {
-          const uint32_t stage = st_it & 1;
-          if (!wait_all(&bars[L::kStEmpty + stage], ((st_it >> 1) & 1) ^ 1, abort, p.err, 0xd02)) { fail = true; break; }
+          // both tiles land on the first one's barrier
+          const uint32_t slot = st_it % L::kSlots, slot2 = st_it % L::kSlots2;
+          bool ok = wait_all(&bars[L::kStEmpty + slot], ((st_it / L::kSlots) & 1) ^ 1, abort, p.err, 0xd02);
+          ok = ok && (KIND == 0 || wait_all(&bars[L::kSt2Empty + slot2], ((st_it / L::kSlots2) & 1) ^ 1, abort, p.err, 0xd03));
+          if (!ok) { fail = true; break; }
           if (lane == 0) {
-            uint8_t* d = st_base + stage * 2 * L::kTile;
-            uint64_t* bar = &bars[L::kStFull + stage];
+            uint8_t* d = smem + L::kStreamOff + slot * L::kTile;
+            uint8_t* d2 = smem + L::kStream2Off + slot2 * L::kTile;
+            uint64_t* bar = &bars[L::kStFull + slot];
             mbar_arrive_expect_tx(bar, 2 * L::kTile);
             const CUtensorMap* m0 = KIND == 0 ? &tm_q : &tm_k;
             const CUtensorMap* m1 = KIND == 0 ? &tm_do : &tm_v;
             tma_load_3d(d, m0, bar, 0, h, row);
             tma_load_3d(d + L::kHalf, m0, bar, 64, h, row);
-            tma_load_3d(d + L::kTile, m1, bar, 0, h, row);
-            tma_load_3d(d + L::kTile + L::kHalf, m1, bar, 64, h, row);
+            tma_load_3d(d2, m1, bar, 0, h, row);
+            tma_load_3d(d2 + L::kHalf, m1, bar, 64, h, row);
           }
           if (KIND == 1 || ++h == (it.head + 1) * p.group) {  // (KIND 0: the next query tile after the group's heads)
             if (KIND == 0) h -= p.group;
@@ -227,7 +238,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         }
       };
       auto issue_dp = [&](uint32_t d, uint32_t st, int c) {
-        const Desc a = make_desc(res_addr + L::kTile, 16, 1024), b = make_desc(st + L::kTile + c * 64 * 128, 16, 1024);
+        const Desc a = make_desc(res_addr + L::kTile, 16, 1024), b = make_desc(st + c * 64 * 128, 16, 1024);
         if (leader) {
           mma_ss<0>(d, a, 0, b, 0, kIdK);
 #pragma unroll
@@ -258,13 +269,15 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         // be NaN) become zeros
         auto landed = [&](int t) {
           const uint32_t si = st_it + t;
-          if (!wait(L::kStFull + (si & 1), (si >> 1) & 1, 0xd12)) return false;
+          if (!wait(L::kStFull + si % L::kSlots, (si / L::kSlots) & 1, 0xd12)) return false;
           if (short_rows && t >= short_from) {
-            uint8_t* d = st_base + (si & 1) * 2 * L::kTile;
-            for (int i = lane; i < (128 - short_rows) * 32; i += 32) {
-              const int row = short_rows + (i >> 5), piece = i & 31;  // 16-byte pieces: 8 per half row, two tiles
-              *reinterpret_cast<uint4*>(d + (piece >> 3) * L::kHalf + row * 128 + (piece & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+            uint8_t* d = smem + L::kStreamOff + (si % L::kSlots) * L::kTile;
+            uint8_t* d2 = smem + L::kStream2Off + (si % L::kSlots2) * L::kTile;
+            for (int i = lane; i < (128 - short_rows) * 16; i += 32) {
+              const int row = short_rows + (i >> 4), piece = i & 15;  // 16-byte pieces: 8 per half row
+              const int at = (piece >> 3) * L::kHalf + row * 128 + (piece & 7) * 16;
+              *reinterpret_cast<uint4*>(d + at) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(d2 + at) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -275,7 +288,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         ++res_it;
         for (int u = 0; u < steps; ++u, ++n) {
           const int c = u & 1;
-          const uint32_t st = stage_addr(st_it + (u >> 1)), x = n & 1;
+          const uint32_t st = slot_addr(st_it + (u >> 1)), st2 = slot2_addr(st_it + (u >> 1)), x = n & 1;
           if constexpr (KIND == 0) {
             // an area is free once the product that read it last is done: that
             // of a(n), dK_1 of n - 2; of b(n), dV of n - 1; of c(n), dK_2 of n - 1
@@ -289,20 +302,21 @@ __global__ void __launch_bounds__(kDBThreads, 1)
             issue_s(area((area_a(n) + 1) & 3), st, c, 1);
             commit(L::kSFull + x);
             if (n > 0 && !wait(L::kK2Done + (x ^ 1), ((n - 1) >> 1) & 1, 0xd15)) { fail = true; break; }
-            issue_dp(area((area_a(n) + 2) & 3), st, c);
+            issue_dp(area((area_a(n) + 2) & 3), st2, c);
             commit(L::kDPFull + x);
             if (u + 1 == steps) commit(L::kResEmpty);  // the item's last S/dP
             if (u + 1 < steps) {
               if (c == 1 && !landed((u + 1) >> 1)) { fail = true; break; }
-              if (!issue_s1(n + 1, stage_addr(st_it + ((u + 1) >> 1)), c ^ 1)) { fail = true; break; }
+              if (!issue_s1(n + 1, slot_addr(st_it + ((u + 1) >> 1)), c ^ 1)) { fail = true; break; }
             }
           } else {
             if (c == 0 && u > 0 && !landed(u >> 1)) { fail = true; break; }
-            if (!wait(L::kVDone + x, ((n >> 1) & 1) ^ 1, 0xd13)) { fail = true; break; }  // the set's last products
+            if (!wait(L::kK2Done + x, ((n >> 1) & 1) ^ 1, 0xd13)) { fail = true; break; }  // the set's last products
             issue_s(area(3 * x), st, c, 0);
             issue_s(area(3 * x + 1), st, c, 1);
-            issue_dp(area(3 * x + 2), st, c);
+            issue_dp(area(3 * x + 2), st2, c);
             commit(L::kSFull + x);
+            if (c == 1) commit(L::kSt2Empty + ((st_it + (u >> 1)) & 1));  // V_j: dP alone reads it
             if (u + 1 == steps) commit(L::kResEmpty);
           }
           __syncwarp();
@@ -347,14 +361,14 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           const int t = u >> 1, c = u & 1;
           const bool first = c == 0 && t % kFlush == 0;  // of dV (dQ)
           const bool last = c == 1 && (t % kFlush == kFlush - 1 || t + 1 == tiles);
-          const uint32_t st = stage_addr(st_it + t), x = n & 1, par = (n >> 1) & 1;
+          const uint32_t st = slot_addr(st_it + t), x = n & 1, par = (n >> 1) & 1;
           if constexpr (KIND == 0) {
             const uint32_t a = area_a(n);
             const bool first_k = c == 0 && (t == 0 || t % kFlush == kFlush / 2);
             const bool last_k = c == 1 && (t % kFlush == kFlush / 2 - 1 || t + 1 == tiles);
             if (first && !wait(L::kAccEmpty, (fl_v & 1) ^ 1, 0xd21)) { fail = true; break; }
             if (!wait(L::kPFull + x, par, 0xd22)) { fail = true; break; }
-            issue_acc(tmem + 256, area(a), st + L::kTile, c, kIdV, first);
+            issue_acc(tmem + 256, area(a), slot2_addr(st_it + t), c, kIdV, first);
             commit(L::kVDone + x);
             if (last) commit(L::kAccFull);
             __syncwarp();
@@ -373,19 +387,19 @@ __global__ void __launch_bounds__(kDBThreads, 1)
             if (!wait(L::kDSFull + x, par, 0xd24)) { fail = true; break; }
             issue_acc(tmem + 384, area(3 * x), st, c, kIdMap, first);
             issue_acc(tmem + 448, area(3 * x + 1), st + L::kHalf, c, kIdMap, first);
-            commit(L::kVDone + x);
+            commit(L::kK2Done + x);
             if (last) commit(L::kAccFull);
           }
           if (last) ++fl_v;
-          if (c == 1) commit(L::kStEmpty + ((st_it + t) & 1));
+          if (c == 1) commit(L::kStEmpty + (st_it + t) % L::kSlots);
           __syncwarp();
         }
         st_it += tiles;
       }
     } else if (warp == 10 && KIND == 0) {
       // ---------------------------------------------------------- column statistics
-      // of each streamed tile's queries: lse_m log2 e and Delta_m, 0 past the
-      // sequence's end, and -lambda of the tile's head
+      // of each streamed tile's queries: lse_m log2 e, Delta_1 and lambda Delta_2, 0
+      // past the sequence's end, and -lambda of the tile's head
       uint32_t v_it = 0;
       bool fail = false;
       for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
@@ -419,7 +433,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
             v[32 * i + lane] = __fmul_rn(x[0][i], kLog2e);
             v[128 + 32 * i + lane] = __fmul_rn(x[1][i], kLog2e);
             v[256 + 32 * i + lane] = x[2][i];
-            v[384 + 32 * i + lane] = x[3][i];
+            v[384 + 32 * i + lane] = __fmul_rn(-nl, x[3][i]);
           }
           if (lane == 0) v[512] = nl;
           arrive_warp(&bars[L::kVecFull + (v_it & 1)], lane);
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           }
           const float nl = *reinterpret_cast<const volatile float*>(vecs + vb * L::kVecFloats + 512);
           if (!bar_wait(L::kSFull + x, par, 0xd32)) { fail = true; break; }
-          // P_1 and -lambda P_2 of the warp's elements, kept for dS
+          // P_1 and P_2 of the warp's elements, kept for dS
           uint32_t p1[32], p2[32];
           tmem_ld32(ta, p1);
           tmem_ld32(tb, p2);
@@ -500,13 +514,12 @@ __global__ void __launch_bounds__(kDBThreads, 1)
                     q = make_float2(oka ? q.x : 0.0f, okb ? q.y : 0.0f);
                     s = make_float2(oka ? s.x : 0.0f, okb ? s.y : 0.0f);
                   }
-                  s = fmul2(s, nl2);
                   p1[e + i] = __float_as_uint(q.x);
                   p1[e + i + 1] = __float_as_uint(q.y);
                   p2[e + i] = __float_as_uint(s.x);
                   p2[e + i + 1] = __float_as_uint(s.y);
                   const int slot = (e - k + i) >> 1;
-                  split_pair2(fadd2(q, s), w[slot], w[8 + slot]);
+                  split_pair2(ffma2(s, nl2, q), w[slot], w[8 + slot]);
                 }
               }
               tmem_st16(ta + k, w);
@@ -539,7 +552,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
               for (int i = 0; i < 4; i += 2) {
                 const float2 g = f2(dp[e + i], dp[e + i + 1]);
                 const int slot = (e - k + i) >> 1;
-                split_pair2(fmul2(f2(p2[e + i], p2[e + i + 1]), fsub2(g, make_float2(db[i], db[i + 1]))), w2[slot], w2[8 + slot]);
+                split_pair2(fmul2(f2(p2[e + i], p2[e + i + 1]), ffma2(g, nl2, make_float2(db[i], db[i + 1]))), w2[slot],
+                            w2[8 + slot]);
                 split_pair2(fmul2(f2(p1[e + i], p1[e + i + 1]), fsub2(g, make_float2(da[i], da[i + 1]))), w1[slot], w1[8 + slot]);
               }
             }
@@ -574,7 +588,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         }
         const float nl = -__ldg(p.lambda + it.head);
         const float2 nl2 = make_float2(nl, nl), n1 = make_float2(-lse1, -lse1), n2 = make_float2(-lse2, -lse2),
-                     d1 = make_float2(dl1, dl1), d2 = make_float2(dl2, dl2);
+                     d1 = make_float2(dl1, dl1), d2 = make_float2(__fmul_rn(-nl, dl2), __fmul_rn(-nl, dl2));
         int k0 = 32 * wh;  // position of the warp's first column
         for (int u = 0; u < 2 * tiles; ++u, ++s_it, k0 += 64) {
           const uint32_t x = s_it & 1;
@@ -604,7 +618,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
                 const float2 g = f2(dp[e], dp[e + 1]);
                 const int slot = (e - k) >> 1;
                 split_pair2(fmul2(q, fsub2(g, d1)), w1[slot], w1[8 + slot]);
-                split_pair2(fmul2(fmul2(s, nl2), fsub2(g, d2)), w2[slot], w2[8 + slot]);
+                split_pair2(fmul2(s, ffma2(g, nl2, d2)), w2[slot], w2[8 + slot]);
               }
               tmem_st16(t1 + k, w1);
               tmem_st16(t2 + k, w2);
@@ -658,6 +672,24 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           float* dst = (KIND == 1 ? p.dq : which == 0 ? p.dv : p.dk) + base;
           const float mul = KIND == 0 && which == 0 ? 1.0f : p.scale;
           const bool fresh = which ? t == 0 || tiles <= kFlush / 2 : t < kFlush;  // nothing in the output yet
+          if (KIND == 1) {
+            // no room for staging beside the third slot: each thread its own row
+            if (lane < rows) {
+              float* to = dst + static_cast<int64_t>(lane) * heads * kHeadDim;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float4 val =
+                      make_float4(__fmul_rn(__uint_as_float(x[i][4 * j]), mul), __fmul_rn(__uint_as_float(x[i][4 * j + 1]), mul),
+                                  __fmul_rn(__uint_as_float(x[i][4 * j + 2]), mul),
+                                  __fmul_rn(__uint_as_float(x[i][4 * j + 3]), mul));
+                  if (fresh) *reinterpret_cast<float4*>(to + 32 * i + 4 * j) = val;
+                  else red_add4(to + 32 * i + 4 * j, val);
+                }
+              }
+            }
+          } else
           // each 32-column chunk through shared memory (piece j of a row in
           // slot j ^ (row & 7)), so that four rows leave as whole 128-byte lines
 #pragma unroll
@@ -711,7 +743,8 @@ cudaError_t configure_t() {
     fprintf(stderr, "rlk_dbwd_kernel<%d>: %d registers at launch, the split needs %d\n", KIND, a.numRegs, kDBRegsLaunch);
     return cudaErrorInvalidConfiguration;
   }
-  return cudaFuncSetAttribute(rlk_dbwd_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  return cudaFuncSetAttribute(rlk_dbwd_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              DBwdLayout<KIND>::kAlloc);
 }
 
 }  // namespace
@@ -724,7 +757,7 @@ cudaError_t configure_dbwd_kernels() {
 template <int KIND>
 cudaError_t launch_dbwd(const BwdParams& p, int grid, const CUtensorMap& mq, const CUtensorMap& mk,
                         const CUtensorMap& mv, const CUtensorMap& mdo, cudaStream_t stream) {
-  rlk_dbwd_kernel<KIND><<<grid, kDBThreads, L::kAlloc, stream>>>(p, mq, mk, mv, mdo);
+  rlk_dbwd_kernel<KIND><<<grid, kDBThreads, DBwdLayout<KIND>::kAlloc, stream>>>(p, mq, mk, mv, mdo);
   return cudaGetLastError();
 }
 template cudaError_t launch_dbwd<0>(const BwdParams&, int, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
