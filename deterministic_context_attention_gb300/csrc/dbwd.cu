@@ -7,35 +7,48 @@
 //   dQ_m = scale dS_m K_m,      dK_m = scale dS_m^T Q_m
 // Both maps share dP, and their P's meet in one product for dV: per 128 x 128
 // tile pair the tensor core takes 48 units of a 128 x 128 x 16 product for
-// dK/dV and 32 for dQ (map by map, with dP and dV of each, it is 72 and 40:
-// 1000 + 700 us for 2 x 4096 tokens of 32 heads where this form takes less than
-// half).  P and dS enter as two BF16 parts, as in the plain backward.
+// dK/dV and 32 for dQ (map by map, with dP and dV of each, it is 72 and 40: that
+// form, the plain kernels run over both maps, took 1000 + 700 us for 2 x 4096
+// tokens of 32 heads over 8, this one 740 + 445).  P and dS enter as two BF16
+// parts, as in the plain backward.
 //
 // Accumulation.  The tensor core truncates its FP32 sums: 5e-8 of the value a
 // product on the average, all to one side, 1.1e-4 of dV after the 4096 products
 // of a long sequence's group.  So an accumulator takes 128 products at most
 // (kFlush tiles); then four warps of their own add it to the output in global
-// memory, rounded to nearest, while the other accumulator's products go on.  A
-// thread adds to addresses that no other thread writes, in order, so the sums
-// are the same in every run.
+// memory, rounded to nearest, while the other accumulator's products go on: the
+// gradients are then 4e-6 off.  A thread adds (red.add, so that nothing waits
+// for the old value) to addresses that no other thread writes, in order, so the
+// sums are the same in every run.
 //
 // Work of a step u: 64 streamed rows (half a tile) against 128 resident ones.
 //   KIND 0 (dK/dV): resident K_j, V_j; streamed Q_i, dO_i of every head of the
 //     group, query tiles ascending from the diagonal, heads inside.  TMEM rows
 //     are keys, columns queries; four 64-column areas rotate:
 //       a: S_1 -> P'    b: S_2 -> dS_2    c: dP -> dS_1    d: S_1 of u + 1
-//     S_2 of u + 1 follows dV(u) into a, dP of u + 1 follows dK_2(u) into b,
-//     S_1 of u + 2 follows dK_1(u) into c, so that P of u + 1 is formed while
-//     dK(u) and dP(u + 1) run.
+//     (P' = P_1 - lambda P_2).  S_2 of u + 1 follows dV(u) into a, dP of u + 1
+//     follows dK_2(u) into b, S_1 of u + 2 follows dK_1(u) into c, so that P of
+//     u + 1 is formed while dK(u) and dP(u + 1) run.  Each waits for the commit
+//     of the product whose operand it overwrites: the tensor core orders the
+//     products of one accumulator only.
 //   KIND 1 (dQ): resident Q_i, dO_i; streamed K_j, V_j, ascending.  TMEM rows
 //     are queries, columns keys; two sets of three areas, S_1, S_2 (dS_m over
 //     them) and dP, one computed while the other is used.
+//
+// What bounds it: P and dS between the products.  A step's products take the
+// tensor core 1792 cycles (dQ 1280), its 64 columns of exponentials, splits and
+// TMEM traffic 1650 on their own and 3000 beside products with both operands in
+// shared memory, whose bandwidth those take whole; 3160 a step are measured
+// (dQ 1900).  So statistics are in registers before each wait, and the warps
+// that form P and dS spill nothing.  At 2 x 4096 tokens (687 GFLOP by the
+// formulas, dK/dV and dQ together) that is 1185 us, 580 TFLOP/s.
 //
 // Warp roles (512 threads):
 //   warps 0-7    P and dS: warp w takes TMEM lane quadrant w mod 4 and 32 of the
 //                64 columns
 //   warp  8      TMA producer
-//   warp  9      TMEM allocator, issuer of S and dP; warp 11 of dV, dK, dQ
+//   warp  9      TMEM allocator, issuer of S and dP; warp 11 of dV, dK, dQ (one
+//                warp for all: dK/dV 813 us, dQ 536)
 //   warp  10     the column statistics of dK/dV
 //   warps 12-15  accumulators to global memory
 #include <cuda.h>
@@ -55,14 +68,16 @@ constexpr int kDBThreads = 512;
 constexpr int kDBRegsLaunch = 128;
 // P/dS warps 160, producer / MMA 48, accumulators 144
 static_assert(2 * 160 + 48 + 144 <= 4 * kDBRegsLaunch, "register split");
-constexpr int kFlush = 8;  // tiles (of 16 products) between flushes of an accumulator
+// tiles (of 16 products) between flushes of an accumulator, dV and dK half a
+// period apart
+constexpr int kFlush = 8;
 
 template <int KIND>
 struct DBwdLayout {
   static constexpr int kTile = 128 * kHeadDim * 2;  // one 128 x 128 BF16 tile, two 64-column halves
   static constexpr int kHalf = 128 * 128;
   // streamed tiles: dK/dV (Q_i, dO_i) in two slots each; dQ K_j in three, V_j,
-  // which dP alone reads, in two
+  // which dP alone reads, in two (two and two with staging for the flush: 475 us)
   static constexpr int kSlots = KIND == 0 ? 2 : 3, kSlots2 = 2;
   static constexpr int kResOff = 0;  // (K_j, V_j) or (Q_i, dO_i)
   static constexpr int kStreamOff = 2 * kTile;
@@ -426,7 +441,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
             x[3][i] = in ? __ldg(p.delta_t + k + p.t_pad) : 0.f;
           }
           const float nl = -__ldg(p.lambda + h);
-          if (!wait_all(&bars[L::kVecEmpty + (v_it & 1)], ((v_it >> 1) & 1) ^ 1, abort, p.err, 0xd21)) { fail = true; break; }
+          if (!wait_all(&bars[L::kVecEmpty + (v_it & 1)], ((v_it >> 1) & 1) ^ 1, abort, p.err, 0xd25)) { fail = true; break; }
           float* v = vecs + (v_it & 1) * L::kVecFloats;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -659,8 +674,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           if (!wait_all(&bars[L::kAccFull + which], fl[which] & 1, abort, p.err, 0xd41)) { fail = true; break; }
           ++fl[which];
           tc_fence_after();
-          // the whole accumulator into registers, so that the next products
-          // wait for this alone
+          // the whole accumulator into registers: the next products wait for
+          // this alone
           const uint32_t src = tmem + (KIND == 0 && which == 0 ? 256 : 384) + lane_off;
           uint32_t x[4][32];
 #pragma unroll
@@ -672,8 +687,9 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           float* dst = (KIND == 1 ? p.dq : which == 0 ? p.dv : p.dk) + base;
           const float mul = KIND == 0 && which == 0 ? 1.0f : p.scale;
           const bool fresh = which ? t == 0 || tiles <= kFlush / 2 : t < kFlush;  // nothing in the output yet
-          if (KIND == 1) {
-            // no room for staging beside the third slot: each thread its own row
+          if constexpr (KIND == 1) {
+            // no room for staging beside the third slot: each thread its own
+            // row (dK/dV: 775 us so, 740 staged)
             if (lane < rows) {
               float* to = dst + static_cast<int64_t>(lane) * heads * kHeadDim;
 #pragma unroll
@@ -689,29 +705,30 @@ __global__ void __launch_bounds__(kDBThreads, 1)
                 }
               }
             }
-          } else
-          // each 32-column chunk through shared memory (piece j of a row in
-          // slot j ^ (row & 7)), so that four rows leave as whole 128-byte lines
+          } else {
+            // each 32-column chunk through shared memory (piece j of a row in
+            // slot j ^ (row & 7)), so that four rows leave as whole 128-byte lines
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              stg[lane * 8 + (j ^ (lane & 7))] =
-                  make_float4(__fmul_rn(__uint_as_float(x[i][4 * j]), mul), __fmul_rn(__uint_as_float(x[i][4 * j + 1]), mul),
-                              __fmul_rn(__uint_as_float(x[i][4 * j + 2]), mul),
-                              __fmul_rn(__uint_as_float(x[i][4 * j + 3]), mul));
-            __syncwarp();
+              for (int j = 0; j < 8; ++j)
+                stg[lane * 8 + (j ^ (lane & 7))] =
+                    make_float4(__fmul_rn(__uint_as_float(x[i][4 * j]), mul), __fmul_rn(__uint_as_float(x[i][4 * j + 1]), mul),
+                                __fmul_rn(__uint_as_float(x[i][4 * j + 2]), mul),
+                                __fmul_rn(__uint_as_float(x[i][4 * j + 3]), mul));
+              __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int rr = 4 * k + (lane >> 3), jj = lane & 7;
-              if (rr < rows) {
-                float* to = dst + static_cast<int64_t>(rr) * heads * kHeadDim + 32 * i + 4 * jj;
-                const float4 val = stg[rr * 8 + (jj ^ (rr & 7))];
-                if (fresh) *reinterpret_cast<float4*>(to) = val;
-                else red_add4(to, val);
+              for (int k = 0; k < 8; ++k) {
+                const int rr = 4 * k + (lane >> 3), jj = lane & 7;
+                if (rr < rows) {
+                  float* to = dst + static_cast<int64_t>(rr) * heads * kHeadDim + 32 * i + 4 * jj;
+                  const float4 val = stg[rr * 8 + (jj ^ (rr & 7))];
+                  if (fresh) *reinterpret_cast<float4*>(to) = val;
+                  else red_add4(to, val);
+                }
               }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
       }

@@ -44,7 +44,8 @@
  *     read it with rlk_attn_check_device_error().
  *   - A batch may hold up to 2^20 sequences.  One launch's sequence tables
  *     ride in kernel parameters and take 128 sequences (256 in the calls of
- *     the 8-bit cache and in rlk_attn_cache_append), so a larger batch runs as consecutive ranges of that
+ *     the 8-bit cache, rlk_attn_cache_append and rlk_attn_diff_decode), so a
+ *     larger batch runs as consecutive ranges of that
  *     many sequences on `stream`, each range a complete call on its own rows
  *     (every range is validated before the first launch).  A sequence's
  *     arithmetic does not depend on the other sequences of its batch, so the
@@ -420,11 +421,17 @@ rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, v
  * (map 1) and 64..127 (map 2); both weigh the same 128-wide v:
  *     O_m = softmax(softmax_scale * q_m k_m^T) v       (causal, per map)
  *     out = O_1 - lambda[h] * O_2                      (query head h)
- * Each O_m is a canonical fold of block states, as in rlk_attn_prefill; out is
- * fma(-lambda, O_2, O_1) in FP32, rounded to BF16 only at the final write.
- * So out has the same bits for every chunking, batch, CP rank, page order and
- * split, and a decode row those of the prefill's last row.
- *   lambda: device FP32 [Hq];
+ * The states of a map's KV blocks are folded left to right with a running
+ * maximum and sum (not by their lse, whose FP32 spacing the difference of two
+ * nearly equal maps would show); out is fma(-lambda, O_2, O_1) in FP32, rounded
+ * to BF16 only at the final write.  So the prefill's out has the same bits for
+ * every chunking, batch and CP rank, and the decode's for every batch, page
+ * order and split_k.  The decode folds its blocks in segments of 512 keys: its
+ * rows are those of the prefill's last row within FP32 rounding, not bit for
+ * bit.
+ * A score softmax_scale * q_m k_m^T has to be finite in FP32.  Outputs must not
+ * overlap inputs or each other.
+ *   lambda: device FP32 [Hq], any finite value;
  *   params: as for rlk_attn_prefill, kv_block_size 128 (RLK_ERR_UNSUPPORTED
  *     otherwise); softmax_scale is usually 1/sqrt(64).
  */
@@ -449,10 +456,13 @@ rlk_status rlk_attn_diff_prefill(const rlk_attn_params* params, const void* q, c
  * (may be NULL).  q and the cached keys are rotated already where RoPE is used
  * (rlk_attn_cache_append does both, with rope_width 64).
  *   split_k: 1 takes each (sequence, KV head) in one pass and needs no
- *     workspace; 2..64 splits its KV blocks as rlk_attn_decode_paged_splitk
- *     does; 0 lets the library pick.  The same bits for all.
- *   workspace: device, 16-byte aligned, >= rlk_attn_workspace_size(params,
- *     RLK_OP_DIFF_DECODE, NULL, seqlens) bytes; its contents do not matter.
+ *     workspace; 2..64 cuts it into at most that many equal parts; 0 cuts the
+ *     blocks of all sequences and KV heads evenly over the SMs (the choice for
+ *     speed).  The same bits for all.
+ *   workspace: for split_k != 1, device, 16-byte aligned,
+ *     >= rlk_attn_workspace_size(params, RLK_OP_DIFF_DECODE, NULL, seqlens)
+ *     bytes, not shared by calls that overlap; its contents need no
+ *     initialisation.  Unused for split_k == 1.
  * At most 8 query heads per KV head (RLK_ERR_UNSUPPORTED otherwise).
  */
 rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, const float* lambda,
@@ -477,8 +487,9 @@ rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, co
  *   cp_rank: as in rlk_attn_backward (-1: everything; else the rank's dq rows
  *     and dk/dv blocks); dlambda is the whole batch's for every rank;
  *   workspace: device, >= rlk_attn_workspace_size(..., RLK_OP_DIFF_BACKWARD, ...).
- * Fixed reduction orders, no atomics.  A batch without a row sets dlambda to
- * zero, and its tensors may be NULL.
+ * Fixed reduction orders: the same bits in every run, for every batch and CP
+ * rank (dlambda: for the batch as a whole).  A batch without a row sets dlambda
+ * to zero, and its other tensors may be NULL.
  */
 rlk_status rlk_attn_diff_backward(const rlk_attn_params* params, const void* q, const void* k,
                                   const void* v, const float* lambda, const float* out_f32,
@@ -654,8 +665,8 @@ enum { RLK_OP_MERGE = 1, RLK_OP_BACKWARD = 2, RLK_OP_DECODE_SPLIT = 3, RLK_OP_DE
        RLK_OP_DIFF_DECODE = 5, RLK_OP_DIFF_BACKWARD = 6 };
 
 /* Workspace bytes an entry point needs (HOST cu_seqlens; 0 on bad input).
- * RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE and RLK_OP_DIFF_DECODE take the decode context
- * lengths (seqlens) as cu_seqlens_k and ignore cu_seqlens_q. */
+ * RLK_OP_DECODE_SPLIT, RLK_OP_DECODE_QCACHE and RLK_OP_DIFF_DECODE take the
+ * decode context lengths (seqlens) as cu_seqlens_k and ignore cu_seqlens_q. */
 size_t rlk_attn_workspace_size(const rlk_attn_params* params, int32_t op,
                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k);
 
