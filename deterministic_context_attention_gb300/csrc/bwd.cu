@@ -48,6 +48,7 @@ struct PrepParams {
   float* delta_t;
   const float* out2;    // differential
   const float* lambda;
+  unsigned int* counter;
 };
 
 // One warp per (row, head): lane l takes elements 4l..4l+3 (fma in order),
@@ -75,8 +76,9 @@ __global__ void __launch_bounds__(256) rlk_bwd_prep_kernel(const __grid_constant
 
 // Differential attention: Delta of both maps from the forward's outputs,
 //   Delta_2 = dO . O_2,   Delta_1 = dO . O_1 = dO . out + lambda Delta_2
-// (the same order of sums), at rows 2 h and 2 h + 1.
+// (the same order of sums), at rows 2 h and 2 h + 1; the count of dQ items to 0.
 __global__ void __launch_bounds__(256) rlk_bwd_prep_diff_kernel(const __grid_constant__ PrepParams p) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0u;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); w < p.rows * p.hq; w += warps) {
@@ -800,7 +802,7 @@ int owner_of(int pos, int n, int cp, int layout) {
 template <int KIND, bool DIFF>
 cudaError_t launch_bwd(BwdParams* bp, const std::vector<BwdItem>& tiles, int heads, const CUtensorMap& mq,
                        const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo, int num_sms,
-                       cudaStream_t stream) {
+                       bool overlap, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   bp->item_heads = heads;
   for (size_t i0 = 0; i0 < tiles.size(); i0 += kMaxBwdTiles) {
@@ -809,7 +811,9 @@ cudaError_t launch_bwd(BwdParams* bp, const std::vector<BwdItem>& tiles, int hea
     bp->num_items = static_cast<int32_t>(n) * heads;
     const int grid = std::min(bp->num_items, num_sms);
     if (DIFF) {
-      e = launch_dbwd<KIND>(*bp, grid, mq, mk, mv, mdo, stream);
+      // a further launch counts from zero again (the first one's zero is the preprocess's)
+      if (KIND == 1 && i0 && (e = cudaMemsetAsync(bp->counter, 0, sizeof(*bp->counter), stream)) != cudaSuccess) return e;
+      e = launch_dbwd<KIND>(*bp, grid, mq, mk, mv, mdo, overlap && i0 == 0, stream);
     } else {
       rlk_bwd_kernel<KIND><<<grid, 384, BwdLayoutT<KIND>::kAlloc, stream>>>(*bp, mq, mk, mv, mdo);
       e = cudaGetLastError();
@@ -832,10 +836,11 @@ cudaError_t configure_bwd_kernels() {
   return configure_dbwd_kernels();
 }
 
-// lse and Delta of every query head (of its `maps` maps), transposed
+// lse and Delta of every query head (of its `maps` maps), transposed; two maps:
+// then the count of items taken
 size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu, int maps) {
   const size_t t_pad = static_cast<size_t>(cu[prm->num_seqs]) + 128;
-  return (2 * maps * t_pad * prm->num_q_heads * sizeof(float) + 255) / 256 * 256;
+  return (2 * maps * t_pad * prm->num_q_heads * sizeof(float) + (maps > 1 ? 16 : 0) + 255) / 256 * 256;
 }
 
 rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k, const void* v,
@@ -855,6 +860,7 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   PrepParams pp;
   pp.out2 = diff ? diff->out2 : nullptr;
   pp.lambda = diff ? diff->lambda : nullptr;
+  pp.counter = diff ? reinterpret_cast<unsigned int*>(delta_t + t_pad * prm->num_q_heads * maps) : nullptr;
   pp.hq = prm->num_q_heads;
   pp.rows = T;
   pp.t_pad = t_pad;
@@ -892,6 +898,7 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   bp->lse_t = lse_t;
   bp->delta_t = delta_t;
   bp->lambda = diff ? diff->lambda : nullptr;
+  bp->counter = pp.counter;
   bp->dq = dq;
   bp->dk = dk;
   bp->dv = dv;
@@ -925,12 +932,13 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   std::vector<BwdItem> tiles;
   for (auto& x : kv) tiles.push_back(x.second);
   auto launch0 = diff ? launch_bwd<0, true> : launch_bwd<0, false>;
-  if (!tiles.empty() && launch0(bp.get(), tiles, prm->num_kv_heads, mq, mk, mv, mdo, num_sms, stream) != cudaSuccess)
+  if (!tiles.empty() && launch0(bp.get(), tiles, prm->num_kv_heads, mq, mk, mv, mdo, num_sms, false, stream) != cudaSuccess)
     return RLK_ERR_CUDA;
+  const bool overlap = !tiles.empty();
   tiles.clear();
   for (auto& x : qi) tiles.push_back(x.second);
   auto launch1 = diff ? launch_bwd<1, true> : launch_bwd<1, false>;
-  if (!tiles.empty() && launch1(bp.get(), tiles, prm->num_q_heads, mq, mk, mv, mdo, num_sms, stream) != cudaSuccess)
+  if (!tiles.empty() && launch1(bp.get(), tiles, prm->num_q_heads, mq, mk, mv, mdo, num_sms, overlap, stream) != cudaSuccess)
     return RLK_ERR_CUDA;
   return RLK_OK;
 }

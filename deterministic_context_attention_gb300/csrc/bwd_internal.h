@@ -30,6 +30,7 @@ struct BwdParams {
   const float* lse_t;   // [hq][t_pad] (differential: [hq][2 maps][t_pad])
   const float* delta_t; // [hq][t_pad] (the same)
   const float* lambda;  // differential: [hq]
+  unsigned int* counter;  // differential dQ: items taken beyond each CTA's first, 0 at the launch
   float* dq;
   float* dk;
   float* dv;
@@ -45,9 +46,10 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int item) {
 }
 
 // One launch of the differential kernels: KIND 0 dK/dV, 1 dQ (dbwd.cu).
+// overlap: dQ may start on SMs that the launch before it, dK/dV's, leaves.
 template <int KIND>
 cudaError_t launch_dbwd(const BwdParams& p, int grid, const CUtensorMap& mq, const CUtensorMap& mk,
-                        const CUtensorMap& mv, const CUtensorMap& mdo, cudaStream_t stream);
+                        const CUtensorMap& mv, const CUtensorMap& mdo, bool overlap, cudaStream_t stream);
 cudaError_t configure_dbwd_kernels();
 
 }  // namespace rlk

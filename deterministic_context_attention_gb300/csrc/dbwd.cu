@@ -43,6 +43,14 @@
 // that form P and dS spill nothing.  At 2 x 4096 tokens (687 GFLOP by the
 // formulas, dK/dV and dQ together) that is 1185 us, 580 TFLOP/s.
 //
+// The two launches overlap: dK/dV's CTAs, all resident, let dQ's be scheduled at
+// once, and one of those starts on each SM that the former leave (the shared
+// memory holds one).  dQ reads nothing of dK/dV's, takes its items longest first
+// from a counter, so that the SMs end together, and waits for dK/dV before its
+// end.  7 sequences of 5 to 1201 tokens, 40 heads over 8: 343 -> 313 us for the
+// whole call, 2 x 4096: 1265 -> 1230 (one kernel with both roles' code: 335 and
+// 1290, its dQ loop 10 % slower).
+//
 // Warp roles (512 threads):
 //   warps 0-7    P and dS: warp w takes TMEM lane quadrant w mod 4 and 32 of the
 //                64 columns
@@ -88,8 +96,10 @@ struct DBwdLayout {
   static constexpr int kBarOff = kVecOff + (KIND == 0 ? 2 * kVecFloats * 4 : 0);
   static constexpr int kResFull = 0, kResEmpty = 1, kStFull = 2, kStEmpty = 5, kSt2Empty = 8, kSFull = 10, kDPFull = 12,
                        kPFull = 14, kDSFull = 16, kAccFull = 18, kAccEmpty = 20, kVecFull = 22, kVecEmpty = 24, kVDone = 26,
-                       kK2Done = 28, kK1Done = 30, kNumBars = 32;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+                       kK2Done = 28, kK1Done = 30, kItemFull = 32, kItemEmpty = 36, kNumBars = 40;
+  static constexpr int kItems = 4;  // dQ: items published, not yet taken by every warp
+  static constexpr int kItemOff = kBarOff + kNumBars * 8;
+  static constexpr int kMiscOff = kItemOff + kItems * 4;
   static constexpr int kTotal = kMiscOff + 16;
   static constexpr int kAlloc = kTotal + 1024;
   static_assert(kAlloc <= 232448, "backward shared memory");
@@ -108,12 +118,6 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-
-__device__ __forceinline__ int item_of_round(const BwdParams& p, int round) {  // snake order, -1: none
-  const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-  const int item = round * g + ((round & 1) ? g - 1 - c : c);
-  return item < p.num_items ? item : -1;
 }
 
 // Streamed tiles of an item.  KIND 0: (query tile from j to the last) x (heads
@@ -148,6 +152,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  volatile int* items = reinterpret_cast<volatile int*>(smem + L::kItemOff);
   float* vecs = reinterpret_cast<float*>(smem + L::kVecOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -171,9 +176,14 @@ __global__ void __launch_bounds__(kDBThreads, 1)
       mbar_init(&bars[L::kK2Done + s], 1);
       mbar_init(&bars[L::kK1Done + s], 1);
     }
+    for (int s = 0; s < L::kItems; ++s) {
+      mbar_init(&bars[L::kItemFull + s], 1);
+      mbar_init(&bars[L::kItemEmpty + s], kDBThreads / 32 - 2);
+    }
     *abort = 0;
     fence_mbar_init();
   }
+  if (KIND == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // dQ may start on SMs left over
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -188,19 +198,36 @@ __global__ void __launch_bounds__(kDBThreads, 1)
   auto slot_addr = [&](uint32_t t) { return smem_u32(smem + L::kStreamOff + (t % L::kSlots) * L::kTile); };
   auto slot2_addr = [&](uint32_t t) { return smem_u32(smem + L::kStream2Off + (t % L::kSlots2) * L::kTile); };
 
+  // The CTA's items, in step for all its warps: the first is the CTA's number.
+  // dK/dV: snake order over the longest-first list.  dQ: whatever the producer
+  // took from the counter.
+  const int first_item = blockIdx.x;
+  bool fail = false;
+  auto next_item = [&](uint32_t& n) -> int {
+    if constexpr (KIND == 0) {
+      const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x), k = static_cast<int>(++n);
+      return k * g + ((k & 1) ? g - 1 - c : c);
+    } else {
+      const uint32_t s = n % L::kItems;
+      fail = fail || !wait_all(&bars[L::kItemFull + s], (n / L::kItems) & 1, abort, p.err, 0xd51);
+      const int item = items[s];
+      arrive_warp(&bars[L::kItemEmpty + s], lane);
+      ++n;
+      return item;
+    }
+  };
+
   if (warp >= 8 && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
     if (warp == 8) {
       // ---------------------------------------------------------- producer
       uint32_t res_it = 0, st_it = 0;
-      bool fail = false;
-      for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-        const int item = item_of_round(p, round);
-        if (item < 0) continue;
+      uint32_t taken = 0;
+      for (int item = first_item, next = 0; !fail && item < p.num_items; item = next) {
         const BwdItem it = bwd_item(p, item);
         const int tiles = item_tiles<KIND>(p, it);
         const int tok0 = p.cu[it.seq];
-        if (!wait_all(&bars[L::kResEmpty], (res_it & 1) ^ 1, abort, p.err, 0xd01)) break;
+        if (!wait_all(&bars[L::kResEmpty], (res_it & 1) ^ 1, abort, p.err, 0xd01)) { fail = true; break; }
         ++res_it;
         if (lane == 0) {
           uint8_t* a = smem + L::kResOff;
@@ -221,6 +248,9 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           bool ok = wait_all(&bars[L::kStEmpty + slot], ((st_it / L::kSlots) & 1) ^ 1, abort, p.err, 0xd02);
           ok = ok && (KIND == 0 || wait_all(&bars[L::kSt2Empty + slot2], ((st_it / L::kSlots2) & 1) ^ 1, abort, p.err, 0xd03));
           if (!ok) { fail = true; break; }
+          // the next item is taken as late as hides the trip: the CTA that is
+          // done first gets it
+          if (KIND == 1 && lane == 0 && t + 1 == tiles) next = static_cast<int>(gridDim.x + atomicAdd(p.counter, 1u));
           if (lane == 0) {
             uint8_t* d = smem + L::kStreamOff + slot * L::kTile;
             uint8_t* d2 = smem + L::kStream2Off + slot2 * L::kTile;
@@ -237,6 +267,18 @@ __global__ void __launch_bounds__(kDBThreads, 1)
             if (KIND == 0) h -= p.group;
             row += 128;
           }
+        }
+        if constexpr (KIND == 0) {
+          next = next_item(taken);
+        } else {
+          const uint32_t s = taken % L::kItems;
+          fail = fail || !wait_all(&bars[L::kItemEmpty + s], ((taken / L::kItems) & 1) ^ 1, abort, p.err, 0xd04);
+          ++taken;
+          if (lane == 0) {
+            items[s] = next;
+            mbar_arrive(&bars[L::kItemFull + s]);
+          }
+          next = __shfl_sync(0xffffffffu, next, 0);
         }
       }
     } else if (warp == 9) {
@@ -270,10 +312,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         return ok;
       };
       uint32_t res_it = 0, st_it = 0, n = 0;
-      bool fail = false;
-      for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-        const int item = item_of_round(p, round);
-        if (item < 0) continue;
+      uint32_t taken = 0;
+      for (int item = first_item; !fail && item < p.num_items; item = next_item(taken)) {
         const BwdItem it = bwd_item(p, item);
         const int tiles = item_tiles<KIND>(p, it), steps = 2 * tiles;
         // of the streamed tiles only those of the last 128 rows can be short
@@ -299,7 +339,7 @@ __global__ void __launch_bounds__(kDBThreads, 1)
           }
           return true;
         };
-        if (!wait(L::kResFull, res_it & 1, 0xd11) || !landed(0)) break;
+        if (!wait(L::kResFull, res_it & 1, 0xd11) || !landed(0)) { fail = true; break; }
         ++res_it;
         for (int u = 0; u < steps; ++u, ++n) {
           const int c = u & 1;
@@ -366,10 +406,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         return ok;
       };
       uint32_t st_it = 0, n = 0, fl_v = 0, fl_k = 0;
-      bool fail = false;
-      for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-        const int item = item_of_round(p, round);
-        if (item < 0) continue;
+      uint32_t taken = 0;
+      for (int item = first_item; !fail && item < p.num_items; item = next_item(taken)) {
         const BwdItem it = bwd_item(p, item);
         const int tiles = item_tiles<KIND>(p, it), steps = 2 * tiles;
         for (int u = 0; u < steps; ++u, ++n) {
@@ -416,10 +454,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
       // of each streamed tile's queries: lse_m log2 e, Delta_1 and lambda Delta_2, 0
       // past the sequence's end, and -lambda of the tile's head
       uint32_t v_it = 0;
-      bool fail = false;
-      for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-        const int item = item_of_round(p, round);
-        if (item < 0) continue;
+      uint32_t taken = 0;
+      for (int item = first_item; !fail && item < p.num_items; item = next_item(taken)) {
         const BwdItem it = bwd_item(p, item);
         const int tiles = item_tiles<KIND>(p, it);
         const int tok0 = p.cu[it.seq], len = p.cu[it.seq + 1] - tok0;
@@ -463,7 +499,6 @@ __global__ void __launch_bounds__(kDBThreads, 1)
     const uint32_t off = (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * wh;  // the warp's lanes and columns of an area
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t s_it = 0, v_it = 0;
-    bool fail = false;
     auto f2 = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
     auto bar_wait = [&](int bar, uint32_t parity, unsigned int site) {
       const bool ok = wait_all(&bars[bar], parity, abort, p.err, site);
@@ -475,9 +510,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
       tc_fence_before();
       arrive_warp(&bars[bar], lane);
     };
-    for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = item_of_round(p, round);
-      if (item < 0) continue;
+    uint32_t taken = 0;
+    for (int item = first_item; !fail && item < p.num_items; item = next_item(taken)) {
       const BwdItem it = bwd_item(p, item);
       const int tiles = item_tiles<KIND>(p, it);
       const int tok0 = p.cu[it.seq], len = p.cu[it.seq + 1] - tok0;
@@ -652,10 +686,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     float4* stg = reinterpret_cast<float4*>(smem + L::kStageOff + wq * (32 * 128));
     uint32_t fl[2] = {0, 0};
-    bool fail = false;
-    for (int round = 0; !fail && round * static_cast<int>(gridDim.x) < p.num_items; ++round) {
-      const int item = item_of_round(p, round);
-      if (item < 0) continue;
+    uint32_t taken = 0;
+    for (int item = first_item; !fail && item < p.num_items; item = next_item(taken)) {
       const BwdItem it = bwd_item(p, item);
       const int tiles = item_tiles<KIND>(p, it);
       const int tok0 = p.cu[it.seq], len = p.cu[it.seq + 1] - tok0;
@@ -736,6 +768,8 @@ __global__ void __launch_bounds__(kDBThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  // (dQ, launched while dK/dV may still run, ends after it)
+  if (KIND == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -773,13 +807,22 @@ cudaError_t configure_dbwd_kernels() {
 
 template <int KIND>
 cudaError_t launch_dbwd(const BwdParams& p, int grid, const CUtensorMap& mq, const CUtensorMap& mk,
-                        const CUtensorMap& mv, const CUtensorMap& mdo, cudaStream_t stream) {
-  rlk_dbwd_kernel<KIND><<<grid, kDBThreads, DBwdLayout<KIND>::kAlloc, stream>>>(p, mq, mk, mv, mdo);
-  return cudaGetLastError();
+                        const CUtensorMap& mv, const CUtensorMap& mdo, bool overlap, cudaStream_t stream) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(kDBThreads);
+  c.dynamicSmemBytes = DBwdLayout<KIND>::kAlloc;
+  c.stream = stream;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&c, rlk_dbwd_kernel<KIND>, p, mq, mk, mv, mdo);
 }
 template cudaError_t launch_dbwd<0>(const BwdParams&, int, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                    const CUtensorMap&, cudaStream_t);
+                                    const CUtensorMap&, bool, cudaStream_t);
 template cudaError_t launch_dbwd<1>(const BwdParams&, int, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                    const CUtensorMap&, cudaStream_t);
+                                    const CUtensorMap&, bool, cudaStream_t);
 
 }  // namespace rlk
