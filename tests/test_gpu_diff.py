@@ -349,6 +349,55 @@ def test_more_sequences_than_one_launch_takes():
     _within(_np(grads[3]), want, tol + 3 * 2.0 ** -23 * np.abs(want), "dlam")
 
 
+def test_more_tiles_than_one_launch_takes():
+    # 118 sequences of 16 tiles: both directions need a second launch, whose
+    # results are those of each sequence alone
+    import torch
+    n, each, hq = 118, 2001, 2
+    p = Problem([1], [1], hq, 1)
+    p.q_lens = p.k_lens = [each] * n
+    p.cq = p.ck = _cu(p.q_lens)
+    g = torch.Generator(device="cuda").manual_seed(23)
+    rows = lambda h: torch.randn((n * each, h, 128), device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    dev = (rows(hq), rows(1), rows(1), torch.tensor([0.3, 0.7], device="cuda"))
+    p.dout = rows(hq).float().cpu().numpy()
+    fwd = p.forward(dev)
+    grads = p.backward(dev, fwd)
+    for s in (0, 57, 117):
+        a = slice(s * each, (s + 1) * each)
+        one = Problem([1], [1], hq, 1)
+        one.q_lens = one.k_lens = [each]
+        one.cq = one.ck = _cu([each])
+        one.dout = p.dout[a]
+        sub = (*(x[a].contiguous() for x in dev[:3]), dev[3])
+        alone = one.forward(sub)
+        _same(alone, [x[a] for x in fwd], s)
+        _same(one.backward(sub, alone)[:3], [x[a] for x in grads[:3]], s)
+
+
+def test_two_backward_calls_at_once():
+    # on two streams, each with its own workspace and outputs
+    import torch
+    p = Problem([700, 33], [700, 33], 8, 2, seed=24)
+    dev = p.device()
+    fwd = p.forward(dev)
+    want = p.backward(dev, fwd)
+    out, _, out2, lse = fwd
+    dout = torch.from_numpy(p.dout).cuda().to(torch.bfloat16)
+    need = rlk.rlk_attn_workspace_size(p.params, rlk.RLK_OP_DIFF_BACKWARD, p.cq)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.full_like(x, float("nan")) for x in want] for _ in streams]
+    ws = [torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, g, w in zip(streams, got, ws):
+            rlk.rlk_attn_diff_backward(p.params, *dev, out, out2, dout, lse, p.cq, -1, *g, w, stream=st)
+    torch.cuda.synchronize()
+    rlk.rlk_attn_check_device_error()
+    for g in got:
+        _same(g, want)
+
+
 def test_empty_batches():
     import torch
     p = Problem([0, 0], [0, 0], 8, 2)
