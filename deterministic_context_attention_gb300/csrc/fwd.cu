@@ -22,11 +22,16 @@
 // time: an item's second map first, whose output waits in the shared memory that
 // half of Q and K leaves free, then its first map, whose epilogue takes lambda
 // times the second from it.  Its fold is the one of fold_max_coeffs: block
-// states leave the softmax as (maximum, sum), O is divided once at the end.  For
-// 4 sequences of 777 to 4096 tokens (32 heads over 8; 367 GFLOP by the formulas)
-// it takes 548 us, 670 TFLOP/s; by the tensor core's own count, P in two parts,
-// 1.1 PFLOP/s, what the plain prefill reaches.  A chunk of rows against a long
-// context: 592 TFLOP/s.
+// states leave the softmax as (maximum, sum), O is divided once at the end.  S
+// and PV are issued by a warp each, S behind the commit of the PV product that
+// read P in its buffer: a single warp is held by its 16 PV products for 1000
+// cycles and by each barrier check for 100 (a chunk of 512 rows against 8000
+// keys: 157 us, 147 so).  FP32 rows leave by a bulk copy of each thread's own row
+// (4 sequences of 777 to 4096 tokens with both outputs: 545 us, 534 so).
+// What bounds it: the chain softmax (1400 cycles) -> PV (1600 with its latency) ->
+// S (1000) of either buffer, 2240 cycles a block where the products take 1280.
+// Those 4 sequences (32 heads over 8; 367 GFLOP by the formulas) take 530 us,
+// 690 TFLOP/s; by the tensor core's own count, P in two parts, 1.15 PFLOP/s.
 //
 // Warp roles (512 threads, four warpgroups):
 //   warps 0-3  correction / epilogue: thread r owns TMEM lane r (row r) and
@@ -42,7 +47,8 @@
 //   warp  9    TMEM allocator and MMA issuer (also zeroes V rows past the
 //              valid length of a partial block)
 //   warps 10-11 idle (registers are granted per warpgroup: warps 8-11 run
-//              with 48, warps 0-3 with 208, the softmax groups with 128)
+//              with 48, warps 0-3 with 208, the softmax groups with 128); in
+//              differential attention warp 9 issues S and warp 11 the PV products
 // TMEM (512 columns): S/P double buffer [0,256), PV double buffer [256,512).
 // Per block the tensor core runs S_{b+1} then PV_b, so the softmax of block
 // b+1 overlaps PV_b and the correction of block b overlaps both.
@@ -66,6 +72,9 @@ constexpr int kRegsCorrection = 208;
 constexpr int kRegsSoftmax = 128;
 constexpr int kRegsProducer = 48;
 static_assert(kRegsCorrection + 2 * kRegsSoftmax + kRegsProducer <= 4 * kRegsLaunch, "register split");
+// Differential attention: 216 for the correction (its epilogue spills with 208:
+// 535 us instead of 530), 120 for the softmax.
+static_assert(216 + 2 * 120 + kRegsProducer <= 4 * kRegsLaunch, "register split");
 
 // DIFF: differential attention, whose items hold one map at a time: 64 of the
 // 128 columns of Q and K.  The freed shared memory keeps the second map's
@@ -97,9 +106,11 @@ struct FwdLayout {
   // epilogue staging: per correction warp 32 rows x 128 B (one column chunk)
   static constexpr int kEpiOff = kPageOff + 2 * kPageWin * 4;
   static constexpr int kEpiBytes = 4 * 32 * 128;
-  // the second map's rows: float4 [32][128 rows]
+  // the rows of either map's output, 16 bytes apart from whole lines (thread r
+  // writes and reads row r alone, without conflicts)
   static constexpr int kParkOff = kEpiOff + kEpiBytes;
-  static constexpr int kTotal = kParkOff + (DIFF ? kTileRows * kHeadDim * 4 : 0);
+  static constexpr int kParkRow = kHeadDim + 4;  // floats
+  static constexpr int kTotal = kParkOff + (DIFF ? kTileRows * kParkRow * 4 : 0);
   static constexpr int kAlloc = kTotal + 1024;
   static_assert(kAlloc <= 232448, "forward shared memory");
   static_assert(kEpiOff % 16 == 0, "staging alignment");
@@ -463,13 +474,14 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (fail || *abort) break;
       }
-    } else if (warp == 9) {
+    } else if (warp == 9 || (DIFF && warp == 11)) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t kIdescS = idesc_bf16(128, B, false, false);
       constexpr uint32_t kIdescPV = idesc_bf16(128, kHeadDim, false, true);
       const Desc qd0 = make_desc(q_addr, 16, 1024);
       const uint32_t leader = elect_one_sync();
       uint32_t k_it = 0, v_it = 0, s_it = 0, pv_it = 0, q_it = 0;
+      const bool do_s = !DIFF || warp == 9;  // (differential: warp 11 issues the PV products)
       // the next item's descriptor (two levels of dependent global loads,
       // ~700 cycles) is read while the current item runs, not between the
       // last PV and the next item's first S
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(512, 1)
       for (int round = 0; snake_item<MODE>(round) < p.num_items; ++round) {
         const ItemInfo it = nxt;
         // with RoPE in the prefill the softmax warps hand over the rotated tile
-        bool ok = mbar_wait(&bars[ROPE ? L::kQRot : L::kQFull], q_it & 1, abort, p.err, 0x201);
+        bool ok = !do_s || mbar_wait(&bars[ROPE ? L::kQRot : L::kQFull], q_it & 1, abort, p.err, 0x201);
         if (!__all_sync(0xffffffffu, ok)) break;
         ++q_it;
         const uint32_t kb = k_it, vb = v_it, sb = s_it, pb = pv_it;
@@ -486,6 +498,10 @@ __global__ void __launch_bounds__(512, 1)
           const uint32_t ki = kb + j;
           const uint32_t stage = ki % SK;
           bool w = mbar_wait(&bars[L::kKFull + stage], (ki / SK) & 1, abort, p.err, 0x202);
+          // with a warp of its own for the PV products, S waits for the one that
+          // read P in its buffer
+          const uint32_t si = sb + j;
+          if (DIFF && si >= 2) w = w && mbar_wait(&bars[L::kPVFull + (si & 1)], ((si - 2) >> 1) & 1, abort, p.err, 0x206);
           if (!__all_sync(0xffffffffu, w)) return false;
           tc_fence_after();
           // the whole warp walks the K-steps (warp-uniform descriptors); the
@@ -507,16 +523,24 @@ __global__ void __launch_bounds__(512, 1)
           __syncwarp();
           return true;
         };
-        if (!issue_s(0)) break;
-        if (snake_item<MODE>(round + 1) < p.num_items) nxt = item_info<MODE>(p, snake_item<MODE>(round + 1));
+        if (!DIFF && !issue_s(0)) break;
+        auto read_ahead = [&]() {
+          if (snake_item<MODE>(round + 1) < p.num_items) nxt = item_info<MODE>(p, snake_item<MODE>(round + 1));
+        };
+        if (!DIFF) read_ahead();
         bool fail = false;
         for (int j = 0; j < it.nb; ++j) {
-          if (j + 1 < it.nb) {
+          if (DIFF && do_s) {
+            if (!issue_s(j)) { fail = true; break; }
+          } else if (!DIFF && j + 1 < it.nb) {
             if (!issue_s(j + 1)) { fail = true; break; }
-          } else {
+          }
+          if (do_s && j + 1 == it.nb) {
             if (leader) umma_commit(&bars[L::kQEmpty]);  // Q no longer read
             __syncwarp();
           }
+          if (DIFF && j == 0) read_ahead();
+          if (DIFF && do_s) continue;
           const uint32_t sidx = sb + j, buf = sidx & 1;
           const uint32_t vi = vb + j, vstage = vi % SV;
           const uint32_t pvi = pb + j, pvbuf = pvi & 1;
@@ -573,6 +597,7 @@ __global__ void __launch_bounds__(512, 1)
     // ------------------------------------------------------------ softmax
     // group h (warps 4-7: h = 0, warps 12-15: h = 1) takes keys
     // [h B/2, (h+1) B/2) of every global block; row r is TMEM lane r in both
+    if (DIFF) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;" ::: "memory");
     constexpr int HB = B / 2, NC = HB / 32;
     const int h = warp >= 12 ? 1 : 0;
     const int r = tid - (h ? 384 : 128);
@@ -660,7 +685,8 @@ __global__ void __launch_bounds__(512, 1)
     }
   } else {
     // ------------------------------------------------------------ correction / epilogue
-    setmaxnreg_inc208();
+    if (DIFF) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+    else setmaxnreg_inc208();
     const int r = tid;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t pv_it = 0, st_it = 0;
@@ -811,32 +837,39 @@ __global__ void __launch_bounds__(512, 1)
             if (tr < it.row_count) store(row_base + static_cast<int64_t>(tr) * p.hq, jj, v);
           }
         };
-        // differential attention: out = O1 - lambda O2, one fma an element;
-        // O2, final a round earlier, waits in shared memory (thread r's own
-        // 16-byte pieces, 128 rows apart)
+        // differential attention: out = O1 - lambda O2, one fma an element.  O2,
+        // final a round earlier, waits in shared memory, from where each thread's
+        // row of either output leaves by a copy of its own, behind the next blocks.
         const bool second = DIFF && map_of<MODE>(round) == 1;
         if (DIFF) {
           const float rl = __frcp_rn(lsum);
 #pragma unroll
           for (int e = 0; e < kHeadDim; ++e) O[e] = __fmul_rn(O[e], rl);
-          float4* park = reinterpret_cast<float4*>(smem + L::kParkOff) + r;
-          if (second) {
-#pragma unroll
-            for (int e = 0; e < kHeadDim; e += 4) park[e / 4 * kTileRows] = make_float4(O[e], O[e + 1], O[e + 2], O[e + 3]);
-          } else {
+          float* row = reinterpret_cast<float*>(smem + L::kParkOff) + r * L::kParkRow;
+          bulk_wait_read();  // the row's last copy has been read
+          if (!second) {
             const float nl = -__ldg(p.lambda + it.head);
 #pragma unroll
             for (int e = 0; e < kHeadDim; e += 4) {
-              const float4 x = park[e / 4 * kTileRows];
+              const float4 x = *reinterpret_cast<const float4*>(row + e);
               O[e] = __fmaf_rn(nl, x.x, O[e]);
               O[e + 1] = __fmaf_rn(nl, x.y, O[e + 1]);
               O[e + 2] = __fmaf_rn(nl, x.z, O[e + 2]);
               O[e + 3] = __fmaf_rn(nl, x.w, O[e + 3]);
             }
           }
+          float* const to = second ? p.out2 : p.out_f32;
+          if (second || to) {
+#pragma unroll
+            for (int e = 0; e < kHeadDim; e += 4)
+              *reinterpret_cast<float4*>(row + e) = make_float4(O[e], O[e + 1], O[e + 2], O[e + 3]);
+          }
+          if (to && valid) {
+            fence_proxy_async_smem();
+            bulk_store(to + (row_base + static_cast<int64_t>(r) * p.hq) * kHeadDim, row, kHeadDim * 4);
+          }
         }
-        float* const out_f32 = second ? p.out2 : p.out_f32;
-        if (out_f32) {
+        if (!DIFF && p.out_f32) {
 #pragma unroll
           for (int c = 0; c < kHeadDim / 32; ++c) {
 #pragma unroll
@@ -845,7 +878,7 @@ __global__ void __launch_bounds__(512, 1)
                   make_float4(O[32 * c + 4 * j], O[32 * c + 4 * j + 1], O[32 * c + 4 * j + 2], O[32 * c + 4 * j + 3]);
             __syncwarp();
             write_chunks([&](int64_t row_idx, int jj, const float4& v) {
-              reinterpret_cast<float4*>(out_f32 + row_idx * kHeadDim + 32 * c)[jj] = v;
+              reinterpret_cast<float4*>(p.out_f32 + row_idx * kHeadDim + 32 * c)[jj] = v;
             });
             __syncwarp();
           }
@@ -894,6 +927,7 @@ __global__ void __launch_bounds__(512, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  if (DIFF) bulk_wait_read();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {

@@ -226,6 +226,15 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32],
       : "r"(taddr)
       : "memory");
 }
+// `bytes` (a multiple of 16) of shared memory to global memory, asynchronously:
+// a group of its own of the calling thread.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The thread's bulk stores have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 // Ties registers written by an earlier tcgen05.ld to a preceding
 // tcgen05.wait::ld (emits no instruction): uses cannot move above it.
 __device__ __forceinline__ void tmem_tie(uint32_t (&r)[32], float& mx) {
