@@ -836,11 +836,10 @@ cudaError_t configure_bwd_kernels() {
   return configure_dbwd_kernels();
 }
 
-// lse and Delta of every query head (of its `maps` maps), transposed; two maps:
-// then the count of items taken
+// lse and Delta of every query head (of its `maps` maps), transposed
 size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu, int maps) {
   const size_t t_pad = static_cast<size_t>(cu[prm->num_seqs]) + 128;
-  return (2 * maps * t_pad * prm->num_q_heads * sizeof(float) + (maps > 1 ? 16 : 0) + 255) / 256 * 256;
+  return (2 * maps * t_pad * prm->num_q_heads * sizeof(float) + 255) / 256 * 256;
 }
 
 rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k, const void* v,
@@ -860,7 +859,8 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   PrepParams pp;
   pp.out2 = diff ? diff->out2 : nullptr;
   pp.lambda = diff ? diff->lambda : nullptr;
-  pp.counter = diff ? reinterpret_cast<unsigned int*>(delta_t + t_pad * prm->num_q_heads * maps) : nullptr;
+  // the count of dQ items lies in the padding of the last row, which nothing else reads or writes
+  pp.counter = diff ? reinterpret_cast<unsigned int*>(delta_t + t_pad * prm->num_q_heads * maps - 4) : nullptr;
   pp.hq = prm->num_q_heads;
   pp.rows = T;
   pp.t_pad = t_pad;
