@@ -9,7 +9,7 @@
 // tile pair the tensor core takes 48 units of a 128 x 128 x 16 product for
 // dK/dV and 32 for dQ (map by map, with dP and dV of each, it is 72 and 40: that
 // form, the plain kernels run over both maps, took 1000 + 700 us for 2 x 4096
-// tokens of 32 heads over 8, this one 740 + 445).  P and dS enter as two BF16
+// tokens of 32 heads over 8, this one 740 to 770 + 445).  P and dS enter as two BF16
 // parts, as in the plain backward.
 //
 // Accumulation.  The tensor core truncates its FP32 sums: 5e-8 of the value a
@@ -41,7 +41,7 @@
 // shared memory, whose bandwidth those take whole; 3160 a step are measured
 // (dQ 1900).  So statistics are in registers before each wait, and the warps
 // that form P and dS spill nothing.  At 2 x 4096 tokens (687 GFLOP by the
-// formulas, dK/dV and dQ together) that is 1185 us, 580 TFLOP/s.
+// formulas) the two take 1190 to 1215 us one after the other, 570 TFLOP/s.
 //
 // The two launches overlap: dK/dV's CTAs, all resident, let dQ's be scheduled at
 // once, and one of those starts on each SM that the former leave (the shared
