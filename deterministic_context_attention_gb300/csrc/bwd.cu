@@ -110,25 +110,9 @@ __global__ void __launch_bounds__(256) rlk_bwd_prep_diff_kernel(const __grid_con
   }
 }
 
-// dlambda[h] = -(sum of Delta_2 over the rows), one CTA a query head: thread t
-// adds rows t, t + 1024, ... in ascending order, then a fixed tree.  add: to
-// what an earlier range of the batch's sequences left.
-__global__ void __launch_bounds__(1024) rlk_bwd_dlambda_kernel(const float* delta_t, int64_t t_pad, int64_t rows,
-                                                               float* dlambda, bool add) {
-  __shared__ float part[32];
-  const float* x = delta_t + (2 * static_cast<int64_t>(blockIdx.x) + 1) * t_pad;
-  float s = 0.f;
-  for (int64_t i = threadIdx.x; i < rows; i += 1024) s = __fadd_rn(s, x[i]);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    s = part[threadIdx.x];
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    if (threadIdx.x == 0) dlambda[blockIdx.x] = add ? __fsub_rn(dlambda[blockIdx.x], s) : -s;
-  }
+// dlambda where no dQ launch forms it (a rank without rows): one warp a query head.
+__global__ void __launch_bounds__(32) rlk_bwd_dlambda_kernel(const __grid_constant__ DLambda p) {
+  dlambda_head(p, blockIdx.x, threadIdx.x);
 }
 
 // ------------------------------------------------------------------ shared layout
@@ -814,6 +798,7 @@ cudaError_t launch_bwd(BwdParams* bp, const std::vector<BwdItem>& tiles, int hea
       // a further launch counts from zero again (the first one's zero is the preprocess's)
       if (KIND == 1 && i0 && (e = cudaMemsetAsync(bp->counter, 0, sizeof(*bp->counter), stream)) != cudaSuccess) return e;
       e = launch_dbwd<KIND>(*bp, grid, mq, mk, mv, mdo, overlap && i0 == 0, stream);
+      if (KIND == 1) bp->dlam.out = nullptr;  // the first dQ launch forms it
     } else {
       rlk_bwd_kernel<KIND><<<grid, 384, BwdLayoutT<KIND>::kAlloc, stream>>>(*bp, mq, mk, mv, mdo);
       e = cudaGetLastError();
@@ -874,7 +859,6 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
     blocks = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * 8);
     if (diff) {
       rlk_bwd_prep_diff_kernel<<<static_cast<int>(blocks), 256, 0, stream>>>(pp);
-      rlk_bwd_dlambda_kernel<<<prm->num_q_heads, 1024, 0, stream>>>(delta_t, t_pad, T, diff->dlambda, diff->add);
     } else {
       rlk_bwd_prep_kernel<<<static_cast<int>(blocks), 256, 0, stream>>>(pp);
     }
@@ -899,6 +883,7 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   bp->delta_t = delta_t;
   bp->lambda = diff ? diff->lambda : nullptr;
   bp->counter = pp.counter;
+  bp->dlam = {nullptr, delta_t, t_pad, T, diff && diff->add};
   bp->dq = dq;
   bp->dk = dk;
   bp->dv = dv;
@@ -937,6 +922,11 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   const bool overlap = !tiles.empty();
   tiles.clear();
   for (auto& x : qi) tiles.push_back(x.second);
+  if (diff) bp->dlam.out = diff->dlambda;
+  if (diff && tiles.empty()) {
+    rlk_bwd_dlambda_kernel<<<prm->num_q_heads, 32, 0, stream>>>(bp->dlam);
+    if (cudaGetLastError() != cudaSuccess) return RLK_ERR_CUDA;
+  }
   auto launch1 = diff ? launch_bwd<1, true> : launch_bwd<1, false>;
   if (!tiles.empty() && launch1(bp.get(), tiles, prm->num_q_heads, mq, mk, mv, mdo, num_sms, overlap, stream) != cudaSuccess)
     return RLK_ERR_CUDA;

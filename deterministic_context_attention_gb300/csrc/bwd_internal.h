@@ -18,6 +18,39 @@ struct alignas(16) BwdItem {
 
 constexpr int kMaxBwdTiles = 1800;
 
+// dlambda[h] = -(sum of Delta_2 over the rows of head h); add: to what an earlier
+// range of the batch's sequences left.
+struct DLambda {
+  float* out;            // [hq], or null: not this launch's
+  const float* delta_t;  // [hq][2 maps][t_pad]
+  int64_t t_pad, rows;
+  bool add;
+};
+
+// One warp a head: lane l adds rows l + 32 i, eight sums side by side (i mod 8) in
+// ascending order, which meet in fixed trees.
+__device__ __forceinline__ void dlambda_head(const DLambda& p, int h, int lane) {
+  const float* x = p.delta_t + (2 * static_cast<int64_t>(h) + 1) * p.t_pad;
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = 0.f;
+  for (int64_t r = lane; r < p.rows; r += 256) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r + 32 * i < p.rows ? __ldg(x + r + 32 * i) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __fadd_rn(s[i], v[i]);
+  }
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) {
+#pragma unroll
+    for (int i = 0; i < off; ++i) s[i] = __fadd_rn(s[i], s[i + off]);
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], off));
+  if (lane == 0) p.out[h] = p.add ? __fsub_rn(p.out[h], s[0]) : -s[0];
+}
+
 // The item list holds tiles; item i is head i mod item_heads of tile
 // i / item_heads (the heads of a tile are adjacent in the longest-first
 // order), so a launch takes kMaxBwdTiles * heads items.
@@ -31,6 +64,7 @@ struct BwdParams {
   const float* delta_t; // [hq][t_pad] (the same)
   const float* lambda;  // differential: [hq]
   unsigned int* counter;  // differential dQ: items taken beyond each CTA's first, 0 at the launch
+  DLambda dlam;         // differential dQ
   float* dq;
   float* dk;
   float* dv;

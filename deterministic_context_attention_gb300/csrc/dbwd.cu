@@ -1,5 +1,5 @@
 // dbwd.cu -- backward of differential attention for sm_103a: dQ, dK, dV (the
-// preprocess and dlambda are in bwd.cu).
+// preprocess is in bwd.cu), and dlambda.
 //
 // With P_m = exp(scale q_m k_m^T - lse_m), dP = dO V^T and Delta_m = dO . O_m:
 //   dV   = (P_1 - lambda P_2)^T dO
@@ -57,7 +57,8 @@
 //   warp  8      TMA producer
 //   warp  9      TMEM allocator, issuer of S and dP; warp 11 of dV, dK, dQ (one
 //                warp for all: dK/dV 813 us, dQ 536)
-//   warp  10     the column statistics of dK/dV
+//   warp  10     dK/dV: the column statistics; dQ: dlambda, a head at a time (a kernel
+//                of its own before dK/dV: 4 us a call)
 //   warps 12-15  accumulators to global memory
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -449,7 +450,11 @@ __global__ void __launch_bounds__(kDBThreads, 1)
         }
         st_it += tiles;
       }
-    } else if (warp == 10 && KIND == 0) {
+    } else if (warp == 10 && KIND == 1) {
+      // ---------------------------------------------------------- dlambda
+      if (p.dlam.out)
+        for (int h = blockIdx.x; h < p.hq; h += gridDim.x) dlambda_head(p.dlam, h, lane);
+    } else if (warp == 10) {
       // ---------------------------------------------------------- column statistics
       // of each streamed tile's queries: lse_m log2 e, Delta_1 and lambda Delta_2, 0
       // past the sequence's end, and -lambda of the tile's head

@@ -429,8 +429,9 @@ rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, v
  * order and split_k.  The decode folds its blocks in segments of 512 keys: its
  * rows are those of the prefill's last row within FP32 rounding, not bit for
  * bit.
- * A score softmax_scale * q_m k_m^T has to be finite in FP32.  Outputs must not
- * overlap inputs or each other.
+ * A score softmax_scale * q_m k_m^T has to be finite in FP32, and v in a row's
+ * last 128-key block too where the row does not see it (its weight is 0, and
+ * 0 * Inf is NaN).  Outputs must not overlap inputs or each other.
  *   lambda: device FP32 [Hq], any finite value;
  *   params: as for rlk_attn_prefill, kv_block_size 128 (RLK_ERR_UNSUPPORTED
  *     otherwise); softmax_scale is usually 1/sqrt(64).

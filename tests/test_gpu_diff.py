@@ -375,6 +375,17 @@ def test_more_tiles_than_one_launch_takes():
         _same(one.backward(sub, alone)[:3], [x[a] for x in grads[:3]], s)
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+def test_every_rank_has_the_whole_dlambda(layout):
+    # ranks without a row of their own among them
+    p = Problem([1, 70], [1, 70], 12, 4, seed=25)
+    dev = p.device()
+    fwd = p.forward(dev)
+    want = p.backward(dev, fwd)[3]
+    for r in range(8):
+        _same([p.backward(dev, fwd, ranks=[r], cp=8, layout=layout)[3]], [want], r)
+
+
 def test_two_backward_calls_at_once():
     # on two streams, each with its own workspace and outputs
     import torch
