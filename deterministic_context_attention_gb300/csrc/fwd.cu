@@ -649,6 +649,7 @@ __global__ void __launch_bounds__(512, 1)
         const bool full = __all_sync(0xffffffffu, !valid || hv == HB);
         uint32_t sv[NC][32];
         float lse_b = -INFINITY, rcp = 0.0f, mc = 0.0f;
+        bool none = false;
         if (warp_rows) xmax[h * kTileRows + r] = half_load<NC>(ta, full, hv, sv);
         mbar_arrive(xbar);
         w = mbar_wait(xbar, x_par, abort, p.err, 0x302);
@@ -656,7 +657,10 @@ __global__ void __launch_bounds__(512, 1)
         if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
         if (warp_rows) {
           const float m = fmaxf(xmax[r], xmax[kTileRows + r]);  // exact
-          mc = has ? __fmul_rn(m, p.scale_log2) : 0.0f;
+          // (differential: a maximum of -inf, of visible keys whose scores are all
+          // NaN or -inf, stays out of the weights, which are then NaN or 0)
+          mc = has && (!DIFF || m != -INFINITY) ? __fmul_rn(m, p.scale_log2) : 0.0f;
+          none = DIFF && m == -INFINITY;
           xsum[h * kTileRows + r] = half_probs<NC>(ta, sv, p.scale_log2, mc);
         }
         // P is in TMEM: the PV product may start while the half sums are
@@ -669,9 +673,11 @@ __global__ void __launch_bounds__(512, 1)
         w = mbar_wait(xbar, x_par, abort, p.err, 0x303);
         x_par ^= 1;
         if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
-        if (DIFF && h == 0 && warp_rows && has) {  // the fold takes mc and the sum as they are
-          lse_b = mc;
+        if (DIFF && h == 0 && warp_rows && has) {
+          // the fold takes mc and the sum as they are; -inf (no key of weight)
+          // lets it pass over the block, which a sum of NaN must not
           rcp = __fadd_rn(xsum[r], xsum[kTileRows + r]);
+          lse_b = none && rcp == 0.0f ? -INFINITY : mc;
         }
         if (!DIFF && h == 0 && warp_rows && has) block_stats(mc, __fadd_rn(xsum[r], xsum[kTileRows + r]), lse_b, rcp);
         if (h == 0) {
