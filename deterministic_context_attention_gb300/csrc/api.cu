@@ -41,7 +41,7 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
                         const float* out_f32, const void* dout, const float* lse,
                         const int32_t* cu, int32_t cp_rank, float* dq, float* dk, float* dv,
                         void* workspace, size_t workspace_bytes, ErrWord* err, int num_sms,
-                        cudaStream_t stream, const DiffBackward* diff);
+                        cudaStream_t stream, const DiffBackward* diff, cudaError_t* error);
 size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu, int maps);
 }  // namespace rlk
 
@@ -74,6 +74,9 @@ rlk_status fail(rlk_status st, const char* fmt, ...) {
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
   g_last_error = buf;
+  // a launch or fill that was refused is this call's error, not one for the next
+  // launch on the thread to find
+  if (st == RLK_ERR_CUDA) (void)cudaGetLastError();
   return st;
 }
 
@@ -1863,14 +1866,15 @@ rlk_status diff_backward_impl(const rlk_attn_params* params, const void* q, cons
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
+  cudaError_t e = cudaSuccess;
   if (T == 0) {  // no row: a gradient of zeros (or nothing to add)
-    cudaError_t e = diff.add ? cudaSuccess : cudaMemsetAsync(diff.dlambda, 0, hq * sizeof(float), stream);
+    e = diff.add ? cudaSuccess : cudaMemsetAsync(diff.dlambda, 0, hq * sizeof(float), stream);
     if (e != cudaSuccess) return fail(RLK_ERR_CUDA, "dlambda fill: %s", cudaGetErrorString(e));
     return ok();
   }
   st = rlk::run_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,
-                         workspace_bytes, dev->err, dev->num_sms, stream, &diff);
-  if (st) return fail(st, "differential backward launch: %s", cudaGetErrorString(cudaPeekAtLastError()));
+                         workspace_bytes, dev->err, dev->num_sms, stream, &diff, &e);
+  if (st) return fail(st, "differential backward launch: %s", cudaGetErrorString(e));
   return ok();
 }
 
@@ -2086,9 +2090,11 @@ rlk_status rlk_attn_backward(const rlk_attn_params* params, const void* q, const
   if (g_dry_run) return ok();
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev))) return st;
+  cudaError_t e = cudaSuccess;
   st = rlk::run_backward(params, q, k, v, out_f32, dout, lse, cu_seqlens, cp_rank, dq, dk, dv, workspace,
-                         workspace_bytes, dev->err, dev->num_sms, stream, nullptr);
-  if (st) return st;
+                         workspace_bytes, dev->err, dev->num_sms, stream, nullptr, &e);
+  if (st == RLK_ERR_CUDA) return fail(st, "backward launch: %s", cudaGetErrorString(e));
+  if (st) return fail(st, "the backward takes KV block 128");
   return ok();
 }
 

@@ -830,8 +830,14 @@ size_t backward_workspace_bytes(const rlk_attn_params* prm, const int32_t* cu, i
 rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k, const void* v,
                         const float* out_f32, const void* dout, const float* lse, const int32_t* cu,
                         int32_t cp_rank, float* dq, float* dk, float* dv, void* workspace, size_t workspace_bytes,
-                        ErrWord* err, int num_sms, cudaStream_t stream, const DiffBackward* diff) {
+                        ErrWord* err, int num_sms, cudaStream_t stream, const DiffBackward* diff,
+                        cudaError_t* error) {
   (void)workspace_bytes;
+  // RLK_ERR_CUDA, and the error itself for the caller's message
+  auto failed = [&](cudaError_t e) {
+    *error = e;
+    return e != cudaSuccess;
+  };
   const int maps = diff ? 2 : 1;
   const int T = cu[prm->num_seqs];
   if (T == 0) return RLK_OK;
@@ -862,13 +868,15 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
     } else {
       rlk_bwd_prep_kernel<<<static_cast<int>(blocks), 256, 0, stream>>>(pp);
     }
-    if (cudaGetLastError() != cudaSuccess) return RLK_ERR_CUDA;
+    if (failed(cudaGetLastError())) return RLK_ERR_CUDA;
   }
 
   CUtensorMap mq, mk, mv, mdo;
   if (!make_map_bwd(&mq, q, prm->num_q_heads, T) || !make_map_bwd(&mk, k, prm->num_kv_heads, T) ||
-      !make_map_bwd(&mv, v, prm->num_kv_heads, T) || !make_map_bwd(&mdo, dout, prm->num_q_heads, T))
+      !make_map_bwd(&mv, v, prm->num_kv_heads, T) || !make_map_bwd(&mdo, dout, prm->num_q_heads, T)) {
+    *error = cudaErrorInvalidValue;
     return RLK_ERR_CUDA;
+  }
 
   auto bp = std::make_unique<BwdParams>();
   std::memset(bp.get(), 0, sizeof(BwdParams));
@@ -917,7 +925,7 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   std::vector<BwdItem> tiles;
   for (auto& x : kv) tiles.push_back(x.second);
   auto launch0 = diff ? launch_bwd<0, true> : launch_bwd<0, false>;
-  if (!tiles.empty() && launch0(bp.get(), tiles, prm->num_kv_heads, mq, mk, mv, mdo, num_sms, false, stream) != cudaSuccess)
+  if (!tiles.empty() && failed(launch0(bp.get(), tiles, prm->num_kv_heads, mq, mk, mv, mdo, num_sms, false, stream)))
     return RLK_ERR_CUDA;
   const bool overlap = !tiles.empty();
   tiles.clear();
@@ -925,10 +933,10 @@ rlk_status run_backward(const rlk_attn_params* prm, const void* q, const void* k
   if (diff) bp->dlam.out = diff->dlambda;
   if (diff && tiles.empty()) {
     rlk_bwd_dlambda_kernel<<<prm->num_q_heads, 32, 0, stream>>>(bp->dlam);
-    if (cudaGetLastError() != cudaSuccess) return RLK_ERR_CUDA;
+    if (failed(cudaGetLastError())) return RLK_ERR_CUDA;
   }
   auto launch1 = diff ? launch_bwd<1, true> : launch_bwd<1, false>;
-  if (!tiles.empty() && launch1(bp.get(), tiles, prm->num_q_heads, mq, mk, mv, mdo, num_sms, overlap, stream) != cudaSuccess)
+  if (!tiles.empty() && failed(launch1(bp.get(), tiles, prm->num_q_heads, mq, mk, mv, mdo, num_sms, overlap, stream)))
     return RLK_ERR_CUDA;
   return RLK_OK;
 }

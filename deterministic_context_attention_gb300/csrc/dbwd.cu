@@ -823,7 +823,9 @@ cudaError_t launch_dbwd(const BwdParams& p, int grid, const CUtensorMap& mq, con
   a.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &a;
   c.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&c, rlk_dbwd_kernel<KIND>, p, mq, mk, mv, mdo);
+  const cudaError_t e = cudaLaunchKernelEx(&c, rlk_dbwd_kernel<KIND>, p, mq, mk, mv, mdo);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // it is returned, not left for the next launch to read
+  return e;
 }
 template cudaError_t launch_dbwd<0>(const BwdParams&, int, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                     const CUtensorMap&, bool, cudaStream_t);
