@@ -1,4 +1,5 @@
-"""Differential attention where values are extreme: scores that are NaN or infinite."""
+"""Differential attention where values are extreme (scores that are NaN or infinite)
+and where sequences are long enough that accumulators leave more than once."""
 import numpy as np
 import pytest
 
@@ -107,3 +108,67 @@ def test_scores_of_minus_infinity_weigh_nothing():
     p.k[:128, :, 0] = p.k[:128, :, 64] = -1e8
     p.k[128:256, :, 0] = p.k[128:256, :, 64] = -1e8
     _same([x[rows] for x in got], [x[rows] for x in p.forward()])
+
+
+# ---------------------------------------------------------------- long sequences
+
+def _definition(p):
+    """Gradients of whole sequences in FP64 on the device, and for dlambda the sums
+    of |dO| |O_2| over a head's rows."""
+    import torch
+    q, k, v, lam = (x.double() for x in p.device())
+    do = torch.from_numpy(p.dout).cuda().double()
+    g = p.hq // p.hkv
+    dq, dk, dv, dlam, size = (torch.zeros_like(x) for x in (q, k, v, lam, lam))
+    for s in range(len(p.q_lens)):
+        a = slice(int(p.cq[s]), int(p.cq[s + 1]))
+        hidden = torch.ones((a.stop - a.start,) * 2, dtype=torch.bool, device="cuda").triu(1)
+        for h in range(p.hq):
+            kv = h // g
+            dp = do[a, h] @ v[a, kv].T
+            for m, c in ((0, 1.0), (1, -float(lam[h]))):
+                at = slice(64 * m, 64 * m + 64)
+                w = torch.softmax((q[a, h, at] @ k[a, kv, at].T * p.scale).masked_fill(hidden, -np.inf), 1)
+                delta = (w * dp).sum(1, keepdim=True)
+                ds = c * w * (dp - delta)
+                dq[a, h, at] = p.scale * (ds @ k[a, kv, at])
+                dk[a, kv, at] += p.scale * (ds.T @ q[a, h, at])
+                dv[a, kv] += c * (w.T @ do[a, h])
+                if m:
+                    dlam[h] -= delta.sum()
+                    size[h] += (do[a, h].norm(dim=1) * (w @ v[a, kv]).norm(dim=1)).sum()
+    return dq, dk, dv, dlam, size
+
+
+# relative 2-norm: an accumulator takes 128 products at the most, each of which may
+# lose 2^-23 of the sum; P and dS in two pieces 2^-18, S and dP of 4 and 8 products,
+# the exponential and the saved log sum (of size 8) less than 2^-18 more.  With the
+# sums of a whole group in one accumulator dV is 5e-5 and more off here.
+GRAD_LONG_REL_L2 = 128 * 2.0 ** -23 + 2.0 ** -17
+
+
+@pytest.mark.parametrize("lens,hq,hkv", [([1024], 8, 1), ([1025], 4, 2), ([1100, 300], 8, 4), ([2200], 8, 1), ([2049, 129], 4, 4)])
+def test_backward_of_long_sequences_is_the_definition(lens, hq, hkv):
+    # dQ leaves its accumulator every 8 key tiles, dV and dK theirs every 8 query tiles of a head
+    p = Problem(lens, lens, hq, hkv, seed=39)
+    got = p.backward()
+    want = _definition(p)
+    for x, w, name in zip(got[:3], want[:3], ("dq", "dk", "dv")):
+        assert float((x - w).norm() / w.norm()) <= GRAD_LONG_REL_L2, name
+        # a lost or doubled tile of any row, head by head, whatever the rows' sizes
+        rows = (x - w).norm(dim=2) / w.norm(dim=2).clamp_min(float(w.norm(dim=2).mean()) * 2.0 ** -4)
+        assert float(rows.max()) <= 16 * GRAD_LONG_REL_L2, name
+    # Delta_2 = dO . O_2: O_2 within 2^-17 of its norm (as in the forward), the sums' roundings less than that
+    assert bool(((got[3] - want[3]).abs() <= 2.0 ** -16 * want[4]).all())
+
+
+@pytest.mark.parametrize("cp,layout", [(2, 1), (3, 0)])
+def test_ranks_of_long_sequences(cp, layout):
+    # query tiles that do not start on a multiple of 128
+    lens = [2200, 1030]
+    p = Problem(lens, lens, 4, 2, seed=40)
+    dev = p.device()
+    fwd = p.forward(dev)
+    want = p.backward(dev, fwd)
+    _same(p.forward(dev, ranks=range(cp), cp=cp, layout=layout), fwd, "forward")
+    _same(p.backward(dev, fwd, ranks=range(cp), cp=cp, layout=layout), want, "backward")
