@@ -1,9 +1,11 @@
 """Differential attention where values are extreme (scores that are NaN or infinite)
-and where sequences are long enough that accumulators leave more than once."""
+and where sequences are long enough that accumulators leave more than once;
+groups of every size in the decode."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_diff import Paged, Problem, _np, _same
+import oracle.diff as od
+from tests.test_gpu_diff import Paged, Problem, _near_prefill, _np, _same, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +174,18 @@ def test_ranks_of_long_sequences(cp, layout):
     want = p.backward(dev, fwd)
     _same(p.forward(dev, ranks=range(cp), cp=cp, layout=layout), fwd, "forward")
     _same(p.backward(dev, fwd, ranks=range(cp), cp=cp, layout=layout), want, "backward")
+
+
+# ---------------------------------------------------------------- groups of the decode
+
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_decode_of_every_group_size(group):
+    c = Paged([300, 1, 1409], 2 * group, 2, 16, seed=41 + group)
+    want = c.decode(1, ws=False)
+    _near_prefill(c, want)
+    for split in (0, 2, 5):
+        _same(c.decode(split), want, split)
+    q, k, v, a, _ = c.p.sequence(0)
+    w, _, wl, t, _, tl = od.forward(q, k, v, c.p.lam, c.p.scale)
+    _within(_np(want[0][a]), w, t, "out")
+    _within(_np(want[2][a]), wl, tl, "lse")
