@@ -426,12 +426,15 @@ rlk_status rlk_attn_cache_append(const rlk_attn_params* params, const void* q, v
  * nearly equal maps would show); out is fma(-lambda, O_2, O_1) in FP32, rounded
  * to BF16 only at the final write.  So the prefill's out has the same bits for
  * every chunking, batch and CP rank, and the decode's for every batch, page
- * order and split_k.  The decode folds its blocks in segments of 512 keys: its
- * rows are those of the prefill's last row within FP32 rounding, not bit for
+ * order and split_k.  The decode folds its blocks in segments of 512 keys and
+ * sums a block's weights in fixed point (each to 2^-27 of the block's largest):
+ * its rows are those of the prefill's last row within FP32 rounding, not bit for
  * bit.
- * A score softmax_scale * q_m k_m^T has to be finite in FP32, and v in a row's
- * last 128-key block too where the row does not see it (its weight is 0, and
- * 0 * Inf is NaN).  Outputs must not overlap inputs or each other.
+ * A score softmax_scale * q_m k_m^T has to be finite and, in the prefill, below
+ * 2^30 in size (a block's weights carry the rounding of its largest score; past
+ * that a row may be NaN).  A NaN score makes its row NaN.  v has to be finite in
+ * a row's last 128-key block too where the row does not see it (its weight is 0,
+ * and 0 * Inf is NaN).  Outputs must not overlap inputs or each other.
  *   lambda: device FP32 [Hq], any finite value;
  *   params: as for rlk_attn_prefill, kv_block_size 128 (RLK_ERR_UNSUPPORTED
  *     otherwise); softmax_scale is usually 1/sqrt(64).
@@ -483,6 +486,8 @@ rlk_status rlk_attn_diff_decode(const rlk_attn_params* params, const void* q, co
  *     dq_m = softmax_scale dS_m k_m,  dk_m = softmax_scale dS_m^T q_m,
  *     dlambda[h] = -(sum of Delta_2 over the rows of head h)
  * with dk and dv summed over a KV head's query heads.
+ * P_m is formed from the saved lse, so it is off by about 2^-22 of |lse|, and
+ * Delta_1, from the saved out, by about 2^-23 of |lambda| |dout| |O_2|.
  *   out_f32, out2, lse: the outputs of rlk_attn_diff_prefill;
  *   dq [T, Hq, 128], dk, dv [T, Hkv, 128], dlambda [Hq]: device FP32;
  *   cp_rank: as in rlk_attn_backward (-1: everything; else the rank's dq rows
