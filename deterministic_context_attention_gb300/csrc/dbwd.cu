@@ -40,14 +40,18 @@
 // TMEM traffic 1650 on their own and 3000 beside products with both operands in
 // shared memory, whose bandwidth those take whole; 3160 a step are measured
 // (dQ 1900).  So statistics are in registers before each wait, and the warps
-// that form P and dS spill nothing.  At 2 x 4096 tokens (687 GFLOP by the
-// formulas) the two take 1190 to 1215 us one after the other, 570 TFLOP/s.
+// that form P and dS keep out of local memory (dK/dV's 128 bytes of spills are the
+// accumulator warps': 4 are left in a build without those, all in one without P and
+// dS).  At 2 x 4096 tokens (687 GFLOP by the formulas) the two take 1190 to 1215 us
+// one after the other, 570 TFLOP/s.  Batches of few or uneven items are bounded by
+// the longest dK/dV item instead, which one SM walks alone: one sequence of 1201
+// tokens, 5 query heads over one KV head, 10 items, takes 166 us, 40 over 8 take 198.
 //
 // The two launches overlap: dK/dV's CTAs, all resident, let dQ's be scheduled at
 // once, and one of those starts on each SM that the former leave (the shared
-// memory holds one).  dQ reads nothing of dK/dV's, takes its items longest first
-// from a counter, so that the SMs end together, and waits for dK/dV before its
-// end.  7 sequences of 5 to 1201 tokens, 40 heads over 8: 343 -> 313 us for the
+// memory holds one).  dQ reads nothing of dK/dV's and waits for it before its end.
+// A dQ CTA's first item is the one of its number, whenever it starts; further ones
+// it takes longest first from a counter as it gets done.  7 sequences of 5 to 1201 tokens, 40 heads over 8: 343 -> 313 us for the
 // whole call, 2 x 4096: 1265 -> 1230 (one kernel with both roles' code: 335 and
 // 1290, its dQ loop 10 % slower).
 //
@@ -56,7 +60,8 @@
 //                64 columns
 //   warp  8      TMA producer
 //   warp  9      TMEM allocator, issuer of S and dP; warp 11 of dV, dK, dQ (one
-//                warp for all: dK/dV 813 us, dQ 536)
+//                warp for all: dK/dV 859 us and dQ 536; two, with dV and dK leaving
+//                half a period apart: 876 and 474)
 //   warp  10     dK/dV: the column statistics; dQ: dlambda, a head at a time (a kernel
 //                of its own before dK/dV: 4 us a call)
 //   warps 12-15  accumulators to global memory

@@ -12,10 +12,12 @@
 // that the low pieces' products are summed on their own and the two sums meet
 // in one FP32 addition.
 //
-// Softmax, all in FP32, per row: a block b of 128 keys gives m_b = max s, p =
+// Softmax in FP32, per row: a block b of 128 keys gives m_b = max s, p =
 // 2^((s - m_b) c), l_b = sum p, O_b = sum p v, c = scale log2(e); blocks are
 // folded left to right into segments of 512 keys (a fixed cut of the sequence),
 // segments left to right into the row, with a running maximum (segments.cuh).
+// l_b alone is summed in fixed point, each p to 2^-27 and p below that not at all:
+// at the worst 2^-20 of l_b, where a tree of FP32 sums has 2^-21.
 // out = O_1 / l_1 - lambda O_2 / l_2.  The result depends on the cached rows and
 // the query alone, not on the batch, the order of the pages or the split.  (Not
 // the log-sum-exp fold of the plain decode: a log sum of 40 and more, as keys of

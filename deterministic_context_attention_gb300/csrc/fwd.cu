@@ -31,7 +31,9 @@
 // What bounds it: the chain softmax (1400 cycles) -> PV (1600 with its latency) ->
 // S (1000) of either buffer, 2240 cycles a block where the products take 1280.
 // Those 4 sequences (32 heads over 8; 367 GFLOP by the formulas) take 530 us,
-// 690 TFLOP/s; by the tensor core's own count, P in two parts, 1.15 PFLOP/s.
+// 690 TFLOP/s; by the tensor core's own count, P in two parts, 1.15 PFLOP/s.  Few
+// rows against a long cache are bounded by one item, both maps of a tile on one SM:
+// of the chunk's 148 us 144 are those of 4 items alone.
 //
 // Warp roles (512 threads, four warpgroups):
 //   warps 0-3  correction / epilogue: thread r owns TMEM lane r (row r) and
