@@ -51,9 +51,9 @@
 // once, and one of those starts on each SM that the former leave (the shared
 // memory holds one).  dQ reads nothing of dK/dV's and waits for it before its end.
 // A dQ CTA's first item is the one of its number, whenever it starts; further ones
-// it takes longest first from a counter as it gets done.  7 sequences of 5 to 1201 tokens, 40 heads over 8: 343 -> 313 us for the
-// whole call, 2 x 4096: 1265 -> 1230 (one kernel with both roles' code: 335 and
-// 1290, its dQ loop 10 % slower).
+// it takes longest first from a counter as it gets done.  7 sequences of 5 to 1201
+// tokens, 40 heads over 8: 343 -> 313 us for the whole call, 2 x 4096: 1265 -> 1230
+// (one kernel with both roles' code: 335 and 1290, its dQ loop 10 % slower).
 //
 // Warp roles (512 threads):
 //   warps 0-7    P and dS: warp w takes TMEM lane quadrant w mod 4 and 32 of the
